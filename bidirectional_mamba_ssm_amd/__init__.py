@@ -5,7 +5,9 @@ only marshals torch tensors (device memory and the current stream) into the
 C ABI declared in include/bimamba.h. It has no compute path of its own and
 raises if the library is not built.
 """
+import contextlib
 import ctypes
+import math
 
 import torch
 
@@ -479,16 +481,26 @@ def _conv_out(out, batch, L, nheads, headdim, ngroups, d_state, dtype, device, n
 
 
 def conv1d(fwd, bwd, nheads, headdim, ngroups, d_state, activation="silu",
-           cu_seqlens=None, init_ctx=None, final_ctx=None, out=None, stream=None):
+           cu_seqlens=None, init_ctx=None, final_ctx=None, out=None, stream=None, dtype=None):
     """Short depthwise convolution of the scan inputs (bimamba_conv1d).
 
     fwd/bwd: dicts of device tensors xbc [b,L,ch] (x | B | C channels, bf16 or
     fp32), weight [ch,W] f32, bias [ch] f32 or None; bwd may be None.
     init_ctx/final_ctx: [b, W-1, ch] in xbc's dtype (may be the same tensor).
     out: optional (fwd_out, bwd_out) dicts of x, B, C to write.
+    xbc may be an Act8 checkpoint of it, in both directions or neither
+    (bimamba_conv1d_act8; no contexts): dtype is then the outputs' (bf16 if
+    not given).
     Returns (fwd_out, bwd_out), each a dict x [b,L,H,P], B, C [b,L,G,N].
     """
     xbc = fwd["xbc"]
+    if isinstance(xbc, Act8):
+        if init_ctx is not None or final_ctx is not None:
+            raise ValueError("a convolution from a checkpoint takes no contexts")
+        return _conv1d_act8(fwd, bwd, (nheads, headdim, ngroups, d_state), activation, cu_seqlens, out,
+                            dtype if dtype is not None else torch.bfloat16, stream)
+    if dtype is not None and dtype != xbc.dtype:
+        raise TypeError(f"dtype {dtype} is not xbc's {xbc.dtype}")
     dev = _cuda_device(xbc)
     if xbc.dim() != 3 or fwd["weight"].dim() != 2:
         raise ValueError("xbc must be [batch, L, channels] and weight [channels, width]")
@@ -546,6 +558,327 @@ def gated_norm(y, z, weight, group_size=None, eps=1e-5, out=None, stream=None):
                                         DTYPES[z.dtype], _ptr(y), _ptr(z), _ptr(weight),
                                         float(eps), _ptr(out), _stream(stream)))
     return out
+
+
+def _on(dev, stream):
+    """The context a call runs in: its tensors' device current, and the given
+    stream too, so that what the call allocates belongs to that stream."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return contextlib.nullcontext()
+
+
+def _out(t, name, shape, dtype, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _check(t, name, shape, dtype, dev)
+    return t
+
+
+def _workspace(query, dev):
+    n = ctypes.c_size_t(0)
+    _abi.check(query(ctypes.byref(n)))
+    ws = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
+    return ws, n.value
+
+
+def _offsets(cu_seqlens):
+    if cu_seqlens is None:
+        return None, 0
+    vals = [int(v) for v in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens)]
+    return (ctypes.c_int32 * len(vals))(*vals), len(vals) - 1
+
+
+class Act8:
+    """An activation kept in 8 bits (include/bimamba.h, bimamba_act8): q int8
+    [..., C] and scale uint8 [..., (C + 31) // 32], the exponent that each 32
+    consecutive channels share. Made by act8_pack or layer_norm; read by
+    act8_unpack and, in place of the tensor, by conv1d, conv1d_bwd,
+    gated_norm_bwd and layer_norm_bwd."""
+
+    __slots__ = ("q", "scale")
+
+    def __init__(self, q, scale):
+        self.q, self.scale = q, scale
+
+    @property
+    def shape(self):
+        return self.q.shape
+
+    @property
+    def device(self):
+        return self.q.device
+
+    @staticmethod
+    def empty(shape, device):
+        shape = tuple(shape)
+        return Act8(torch.empty(shape, dtype=torch.int8, device=device),
+                    torch.empty(shape[:-1] + ((shape[-1] + 31) // 32,), dtype=torch.uint8, device=device))
+
+    def _ptrs(self, name, shape, dev):
+        shape = tuple(shape)
+        _check(self.q, f"{name}.q", shape, torch.int8, dev)
+        _check(self.scale, f"{name}.scale", shape[:-1] + ((shape[-1] + 31) // 32,), torch.uint8, dev)
+        return _abi.Act8Ptrs(self.q.data_ptr(), self.scale.data_ptr())
+
+
+def _rows(shape):
+    """(rows, channels) of [..., channels]."""
+    if not len(shape) or not shape[-1]:
+        raise ValueError(f"shape {tuple(shape)} has no channels")
+    return math.prod(shape[:-1]), shape[-1]
+
+
+def _kept(t, name, shape, dtype, dev):
+    """(data, scale) pointers of a tensor or of its 8-bit checkpoint."""
+    if isinstance(t, Act8):
+        p = t._ptrs(name, shape, dev)
+        return ctypes.c_void_p(p.q), ctypes.c_void_p(p.scale)
+    _check(t, name, tuple(shape), dtype, dev)
+    return _ptr(t), None
+
+
+def act8_pack(x, out=None, stream=None):
+    """x [..., C] (bf16 or fp32) as an 8-bit checkpoint (bimamba_act8_pack).
+    out: an Act8 to write. Returns the Act8."""
+    dev = _cuda_device(x)
+    if x.dtype not in DTYPES:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    _check(x, "x", tuple(x.shape), x.dtype, dev)
+    rows, C = _rows(x.shape)
+    with _on(dev, stream):
+        if out is None:
+            out = Act8.empty(x.shape, dev)
+        p = out._ptrs("out", x.shape, dev)
+        _abi.check(lib().bimamba_act8_pack(rows, C, DTYPES[x.dtype], _ptr(x), ctypes.byref(p), _stream(stream)))
+    return out
+
+
+def act8_unpack(a, dtype=torch.bfloat16, out=None, stream=None):
+    """The values an Act8 stands for, as bf16 or fp32 (bimamba_act8_unpack)."""
+    dev = _cuda_device(a)
+    if dtype not in DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    p = a._ptrs("a", a.shape, dev)
+    rows, C = _rows(a.shape)
+    with _on(dev, stream):
+        out = _out(out, "out", tuple(a.shape), dtype, dev)
+        _abi.check(lib().bimamba_act8_unpack(rows, C, DTYPES[dtype], ctypes.byref(p), _ptr(out), _stream(stream)))
+    return out
+
+
+def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, checkpoint=False, out=None,
+               sum_out=None, stream=None):
+    """Layer norm over the last dimension (bimamba_layer_norm) of h = x, or of
+    h = x + residual rounded to x's dtype. x, residual [..., C] bf16 or fp32,
+    C in 8..16384; weight, bias float32 [C] or None.
+
+    checkpoint: keep h in 8 bits too (True, or an Act8 to write). sum_out:
+    where to write h with a residual (may be residual or x itself). Returns a
+    dict: out, sum (h; x itself without a residual), mean and rstd (float32
+    [...], for layer_norm_bwd), ckpt (Act8 or None)."""
+    dev = _cuda_device(x)
+    if x.dtype not in DTYPES:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    shape = tuple(x.shape)
+    _check(x, "x", shape, x.dtype, dev)
+    rows, C = _rows(shape)
+    if residual is not None:
+        _check(residual, "residual", shape, x.dtype, dev)
+    elif sum_out is not None:
+        raise ValueError("sum_out goes with a residual")
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _check(t, name, (C,), torch.float32, dev)
+    with _on(dev, stream):
+        out = _out(out, "out", shape, x.dtype, dev)
+        if residual is not None:
+            sum_out = _out(sum_out, "sum_out", shape, x.dtype, dev)
+        stats = torch.empty((2,) + shape[:-1], dtype=torch.float32, device=dev)
+        mean, rstd = stats[0], stats[1]
+        ckpt = None
+        if checkpoint is not False and checkpoint is not None:
+            ckpt = Act8.empty(shape, dev) if checkpoint is True else checkpoint
+        p = ckpt._ptrs("checkpoint", shape, dev) if ckpt is not None else None
+        _abi.check(lib().bimamba_layer_norm(
+            rows, C, DTYPES[x.dtype], _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), float(eps), _ptr(out),
+            _ptr(sum_out), _ptr(mean), _ptr(rstd), ctypes.byref(p) if p is not None else None, _stream(stream)))
+    return dict(out=out, sum=x if residual is None else sum_out, mean=mean, rstd=rstd, ckpt=ckpt)
+
+
+def layer_norm_bwd(dout, x, mean, rstd, weight=None, dsum=None, wgrad=True, dx=None, stream=None):
+    """Gradient of layer_norm (bimamba_layer_norm_bwd). dout [..., C]; x: what
+    layer_norm returned as sum (dout's dtype) or its Act8 checkpoint; mean,
+    rstd float32 [...]; dsum: the gradient reaching sum along the residual
+    stream, added to dx (dx may be dsum itself). Returns (dx, dweight, dbias):
+    dx in dout's dtype (the gradient of x and of residual), the other two
+    float32 [C], None with wgrad=False."""
+    dev = _cuda_device(dout)
+    dt = dout.dtype
+    if dt not in DTYPES:
+        raise TypeError(f"unsupported dtype {dt}")
+    shape = tuple(dout.shape)
+    _check(dout, "dout", shape, dt, dev)
+    rows, C = _rows(shape)
+    xp, xs = _kept(x, "x", shape, dt, dev)
+    _check(mean, "mean", shape[:-1], torch.float32, dev)
+    _check(rstd, "rstd", shape[:-1], torch.float32, dev)
+    if weight is not None:
+        _check(weight, "weight", (C,), torch.float32, dev)
+    if dsum is not None:
+        _check(dsum, "dsum", shape, dt, dev)
+    with _on(dev, stream):
+        dx = _out(dx, "dx", shape, dt, dev)
+        dw = db = ws = None
+        nbytes = 0
+        if wgrad:
+            dw = torch.empty(C, dtype=torch.float32, device=dev)
+            db = torch.empty(C, dtype=torch.float32, device=dev)
+            ws, nbytes = _workspace(
+                lambda n: lib().bimamba_layer_norm_bwd_workspace_size(rows, C, DTYPES[dt], n), dev)
+        _abi.check(lib().bimamba_layer_norm_bwd(
+            rows, C, DTYPES[dt], xp, xs, _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dout), _ptr(dsum), _ptr(dx),
+            _ptr(dw), _ptr(db), _ptr(ws), nbytes, _stream(stream)))
+    return dx, dw, db
+
+
+def gated_norm_bwd(dout, y, z, weight, group_size=None, eps=1e-5, wgrad=True, dy=None, dz=None, stream=None):
+    """Gradient of gated_norm (bimamba_gated_norm_bwd): dout [..., C] in z's
+    dtype, y float32 and z [..., C] (each the tensor or its Act8 checkpoint).
+    Returns (dy float32, dz in dout's dtype, dweight float32 [C] or None)."""
+    dev = _cuda_device(dout)
+    dt = dout.dtype
+    if dt not in DTYPES:
+        raise TypeError(f"unsupported dtype {dt}")
+    shape = tuple(dout.shape)
+    _check(dout, "dout", shape, dt, dev)
+    rows, C = _rows(shape)
+    gs = C if group_size is None else int(group_size)
+    yp, ys = _kept(y, "y", shape, torch.float32, dev)
+    zp, zs = _kept(z, "z", shape, dt, dev)
+    _check(weight, "weight", (C,), torch.float32, dev)
+    with _on(dev, stream):
+        dy = _out(dy, "dy", shape, torch.float32, dev)
+        dz = _out(dz, "dz", shape, dt, dev)
+        dw = ws = None
+        nbytes = 0
+        if wgrad:
+            dw = torch.empty(C, dtype=torch.float32, device=dev)
+            ws, nbytes = _workspace(
+                lambda n: lib().bimamba_gated_norm_bwd_workspace_size(rows, C, gs, DTYPES[dt], n), dev)
+        _abi.check(lib().bimamba_gated_norm_bwd(
+            rows, C, gs, DTYPES[dt], yp, ys, zp, zs, _ptr(weight), float(eps), _ptr(dout), _ptr(dy), _ptr(dz),
+            _ptr(dw), _ptr(ws), nbytes, _stream(stream)))
+    return dy, dz, dw
+
+
+def _conv_dims(d, dims, dtype):
+    """(batch, L, ch, W) of a direction whose xbc is a tensor or an Act8."""
+    xbc, w = d["xbc"], d["weight"]
+    if len(xbc.shape) != 3 or w.dim() != 2:
+        raise ValueError("xbc must be [batch, L, channels] and weight [channels, width]")
+    batch, L, ch = xbc.shape
+    if ch != conv_channels(*dims):
+        raise ValueError(f"xbc has {ch} channels, expected nheads*headdim + 2*ngroups*d_state")
+    if dtype not in DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return batch, L, ch, w.shape[1]
+
+
+def _conv1d_act8(fwd, bwd, dims, activation, cu_seqlens, out, dtype, stream):
+    dev = _cuda_device(fwd["xbc"])
+    batch, L, ch, W = _conv_dims(fwd, dims, dtype)
+    H, P, G, N = dims
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation {activation!r} is not one of {sorted(map(str, ACTIVATIONS))}")
+    outs = list(out) if out is not None else [None, None]
+    shape = _abi.ConvShape(batch, L, H, P, N, G, W, DTYPES[dtype], ACTIVATIONS[activation], 0)
+    cu_arr, nseq = _offsets(cu_seqlens)
+    with _on(dev, stream):
+        res, args = [None, None], []
+        for i, (d, name) in enumerate(((fwd, "fwd"), (bwd, "bwd"))):
+            if d is None:
+                args += [None, None]
+                continue
+            if not isinstance(d["xbc"], Act8):
+                raise TypeError("both directions' xbc must be Act8, or neither")
+            p = d["xbc"]._ptrs(f"{name}.xbc", (batch, L, ch), dev)
+            _check(d["weight"], f"{name}.weight", (ch, W), torch.float32, dev)
+            bias = d.get("bias")
+            if bias is not None:
+                _check(bias, f"{name}.bias", (ch,), torch.float32, dev)
+            o = res[i] = _conv_out(outs[i], batch, L, H, P, G, N, dtype, dev, name)
+            args += [_abi.ConvDir(None, d["weight"].data_ptr(), bias.data_ptr() if bias is not None else None,
+                                  o["x"].data_ptr(), o["B"].data_ptr(), o["C"].data_ptr()), p]
+        ws, nbytes = _workspace(
+            lambda n: lib().bimamba_conv1d_workspace_size(ctypes.byref(shape), nseq, n), dev)
+        _abi.check(lib().bimamba_conv1d_act8(
+            ctypes.byref(shape), *[ctypes.byref(v) if v is not None else None for v in args], cu_arr, nseq,
+            _ptr(ws), nbytes, _stream(stream)))
+    return res[0], res[1]
+
+
+def conv1d_bwd(fwd, bwd, gfwd, gbwd, nheads, headdim, ngroups, d_state, activation="silu",
+               cu_seqlens=None, out=None, stream=None, dtype=None):
+    """Gradient of conv1d (bimamba_conv1d_bwd), both directions in one call.
+
+    fwd/bwd: the forward's dicts, xbc [b,L,ch] (or its Act8 checkpoint, in
+    both directions or neither), weight [ch,W] f32, bias [ch] f32 or None;
+    bwd may be None. gfwd/gbwd: float32 gradients of its outputs, dicts with
+    x [b,L,H,P], B and C [b,L,G,N] (ssd_bwd's results serve as they are).
+    dtype: of the returned xbc gradients; xbc's own unless xbc is a
+    checkpoint (then bf16 if not given). out: optional (fwd, bwd) tensors for
+    the xbc gradients. Returns (fwd, bwd) dicts: xbc [b,L,ch] in that dtype,
+    weight [ch,W] and bias [ch] (None without a bias) float32; bwd None if
+    not given."""
+    xbc = fwd["xbc"]
+    dev = _cuda_device(xbc)
+    q8 = isinstance(xbc, Act8)
+    if dtype is None:
+        dtype = torch.bfloat16 if q8 else xbc.dtype
+    elif not q8 and dtype != xbc.dtype:
+        raise TypeError(f"dtype {dtype} is not xbc's {xbc.dtype}")
+    H, P, G, N = nheads, headdim, ngroups, d_state
+    batch, L, ch, W = _conv_dims(fwd, (H, P, G, N), dtype)
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation {activation!r} is not one of {sorted(map(str, ACTIVATIONS))}")
+    if (bwd is None) != (gbwd is None):
+        raise ValueError("bwd and gbwd come together")
+    shape = _abi.ConvShape(batch, L, H, P, N, G, W, DTYPES[dtype], ACTIVATIONS[activation], 0)
+    cu_arr, nseq = _offsets(cu_seqlens)
+    outs = list(out) if out is not None else [None, None]
+    with _on(dev, stream):
+        res, args = [None, None], [None, None]
+        for i, (d, g, name) in enumerate(((fwd, gfwd, "fwd"), (bwd, gbwd, "bwd"))):
+            if d is None:
+                continue
+            if isinstance(d["xbc"], Act8) != q8:
+                raise TypeError("both directions' xbc must be Act8, or neither")
+            xp, xs = _kept(d["xbc"], f"{name}.xbc", (batch, L, ch), dtype, dev)
+            _check(d["weight"], f"{name}.weight", (ch, W), torch.float32, dev)
+            bias = d.get("bias")
+            if bias is not None:
+                _check(bias, f"{name}.bias", (ch,), torch.float32, dev)
+            _check(g["x"], f"{name}_grad.x", (batch, L, H, P), torch.float32, dev)
+            _check(g["B"], f"{name}_grad.B", (batch, L, G, N), torch.float32, dev)
+            _check(g["C"], f"{name}_grad.C", (batch, L, G, N), torch.float32, dev)
+            dxbc = _out(outs[i], f"{name}_out", (batch, L, ch), dtype, dev)
+            dw = torch.empty(ch, W, dtype=torch.float32, device=dev)
+            db = torch.empty(ch, dtype=torch.float32, device=dev) if bias is not None else None
+            res[i] = dict(xbc=dxbc, weight=dw, bias=db)
+            args[i] = _abi.ConvGrad(xp, xs, _ptr(d["weight"]), _ptr(bias), _ptr(g["x"]), _ptr(g["B"]),
+                                    _ptr(g["C"]), _ptr(dxbc), _ptr(dw), _ptr(db))
+        ws, nbytes = _workspace(
+            lambda n: lib().bimamba_conv1d_bwd_workspace_size(ctypes.byref(shape), int(bwd is not None), nseq, n),
+            dev)
+        _abi.check(lib().bimamba_conv1d_bwd(
+            ctypes.byref(shape), ctypes.byref(args[0]), ctypes.byref(args[1]) if bwd is not None else None,
+            cu_arr, nseq, _ptr(ws), nbytes, _stream(stream)))
+    return res[0], res[1]
 
 
 def seq_index(cu_seqlens, device="cuda", stream=None):

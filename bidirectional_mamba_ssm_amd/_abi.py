@@ -24,6 +24,10 @@ EXPORTS = (
     "bimamba_ssd_bwd_workspace_size", "bimamba_ssd_bwd", "bimamba_gated_norm",
     "bimamba_ssd_fwd_streams", "bimamba_merge_linear", "bimamba_ssd_fwd_noalloc",
     "bimamba_state_alloc_conv", "bimamba_state_conv_ctx", "bimamba_block_step_conv",
+    "bimamba_act8_pack", "bimamba_act8_unpack", "bimamba_conv1d_act8",
+    "bimamba_conv1d_bwd_workspace_size", "bimamba_conv1d_bwd",
+    "bimamba_gated_norm_bwd_workspace_size", "bimamba_gated_norm_bwd", "bimamba_layer_norm",
+    "bimamba_layer_norm_bwd_workspace_size", "bimamba_layer_norm_bwd",
 )
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -64,6 +68,17 @@ class ConvDir(ctypes.Structure):
     _fields_ = [("xbc", ctypes.c_void_p), ("weight", ctypes.c_void_p),
                 ("bias", ctypes.c_void_p), ("x", ctypes.c_void_p),
                 ("B", ctypes.c_void_p), ("C", ctypes.c_void_p)]
+
+
+class Act8Ptrs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class ConvGrad(ctypes.Structure):
+    _fields_ = [("xbc", ctypes.c_void_p), ("xbc_scale", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p), ("dB", ctypes.c_void_p), ("dC", ctypes.c_void_p),
+                ("dxbc", ctypes.c_void_p), ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p)]
 
 
 _LIB = None
@@ -123,6 +138,18 @@ def load():
     lib.bimamba_state_conv_ctx.argtypes = [vp]
     lib.bimamba_state_conv_ctx.restype = vp
     lib.bimamba_block_step_conv.argtypes = [vp, csp, cdp, cdp, sp, dp, dp, ctypes.c_int, vp, vp]
+    ll, ci, cf, size = ctypes.c_longlong, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    ap, cgp, np_ = ctypes.POINTER(Act8Ptrs), ctypes.POINTER(ConvGrad), ctypes.POINTER(size)
+    lib.bimamba_act8_pack.argtypes = [ll, ll, ci, vp, ap, vp]
+    lib.bimamba_act8_unpack.argtypes = [ll, ll, ci, ap, vp, vp]
+    lib.bimamba_conv1d_act8.argtypes = [csp, cdp, ap, cdp, ap, i32p, ci, vp, size, vp]
+    lib.bimamba_conv1d_bwd_workspace_size.argtypes = [csp, ci, ci, np_]
+    lib.bimamba_conv1d_bwd.argtypes = [csp, cgp, cgp, i32p, ci, vp, size, vp]
+    lib.bimamba_gated_norm_bwd_workspace_size.argtypes = [ll, ci, ci, ci, np_]
+    lib.bimamba_gated_norm_bwd.argtypes = [ll, ci, ci, ci, vp, vp, vp, vp, vp, cf, vp, vp, vp, vp, vp, size, vp]
+    lib.bimamba_layer_norm.argtypes = [ll, ci, ci, vp, vp, vp, vp, cf, vp, vp, vp, vp, ap, vp]
+    lib.bimamba_layer_norm_bwd_workspace_size.argtypes = [ll, ci, ci, np_]
+    lib.bimamba_layer_norm_bwd.argtypes = [ll, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, size, vp]
     for name in EXPORTS:
         getattr(lib, name).restype = getattr(lib, name).restype or ctypes.c_int
     _LIB = lib

@@ -196,6 +196,82 @@ int check_conv_dir(const bimamba_conv_dir *d, const char *name, bool empty) {
     return BIMAMBA_OK;
 }
 
+// the conditions that a direction's 8-bit checkpoint of the convolution's
+// input is given, and the arrays that bimamba_conv1d and _bwd share
+int check_act8(const bimamba_act8 *a, const char *name, bool empty) {
+    if (!a) return fail(BIMAMBA_EINVAL, "%s: the checkpoint is NULL", name);
+    if (empty) return BIMAMBA_OK;
+    if (!a->q || !a->scale) return fail(BIMAMBA_EINVAL, "%s: the checkpoint's q and scale are required", name);
+    if (!aligned16(a->q)) return fail(BIMAMBA_EINVAL, "%s: the checkpoint's q must be 16-byte aligned", name);
+    return BIMAMBA_OK;
+}
+
+int check_conv_grad(const bimamba_conv_grad *d, const char *name, bool empty) {
+    if (!d) return fail(BIMAMBA_EINVAL, "%s direction is NULL", name);
+    if (!d->weight || !d->dweight) return fail(BIMAMBA_EINVAL, "%s: weight and dweight are required", name);
+    if (((uintptr_t)d->weight | (uintptr_t)d->bias | (uintptr_t)d->dweight | (uintptr_t)d->dbias) & 3u)
+        return fail(BIMAMBA_EINVAL, "%s: weight, bias and their gradients must be 4-byte aligned", name);
+    if (empty) return BIMAMBA_OK;
+    if (!d->xbc || !d->dx || !d->dB || !d->dC || !d->dxbc)
+        return fail(BIMAMBA_EINVAL, "%s: xbc, dx, dB, dC and dxbc are required", name);
+    if (!aligned16(d->xbc) || !aligned16(d->dx) || !aligned16(d->dB) || !aligned16(d->dC) || !aligned16(d->dxbc))
+        return fail(BIMAMBA_EINVAL, "%s: xbc, dx, dB, dC and dxbc must be 16-byte aligned", name);
+    return BIMAMBA_OK;
+}
+
+int check_workspace(const void *ws, size_t have, size_t need) {
+    if (!need) return BIMAMBA_OK;
+    if (!ws) return fail(BIMAMBA_EWORKSPACE, "workspace of %zu bytes required", need);
+    if (have < need) return fail(BIMAMBA_EWORKSPACE, "workspace %zu bytes < %zu required", have, need);
+    if ((uintptr_t)ws & 255u) return fail(BIMAMBA_EINVAL, "workspace must be 256-byte aligned");
+    return BIMAMBA_OK;
+}
+
+// rows of an array of activations: element indexes stay far inside 63 bits
+int check_rows(long long rows, int dtype) {
+    if (dtype != BIMAMBA_F32 && dtype != BIMAMBA_BF16)
+        return fail(BIMAMBA_EINVAL, "dtype %d is not BIMAMBA_F32 or BIMAMBA_BF16", dtype);
+    if (rows < 0) return fail(BIMAMBA_EINVAL, "rows %lld < 0", rows);
+    if (rows > (1LL << 31) - 1) return fail(BIMAMBA_EUNSUPPORTED, "rows %lld exceed 2^31-1", rows);
+    return BIMAMBA_OK;
+}
+bool aligned_to(const void *p, int dtype) { return ((uintptr_t)p & (dtype == BIMAMBA_BF16 ? 1u : 3u)) == 0; }
+
+int check_layer_norm(long long rows, int channels, int dtype) {
+    int rc = check_rows(rows, dtype);
+    if (rc) return rc;
+    if (channels < 8 || channels > 16384)
+        return fail(BIMAMBA_EUNSUPPORTED, "channels %d not in [8, 16384]", channels);
+    return BIMAMBA_OK;
+}
+
+int check_gated_norm(long long rows, int channels, int group_size, int dtype) {
+    int rc = check_rows(rows, dtype);
+    if (rc) return rc;
+    if (channels <= 0 || channels % 256 || channels > 8192)
+        return fail(BIMAMBA_EUNSUPPORTED, "channels %d: need a multiple of 256 up to 8192", channels);
+    if (group_size <= 0 || group_size % 256 || channels % group_size)
+        return fail(BIMAMBA_EINVAL, "group_size %d: need a multiple of 256 dividing %d", group_size, channels);
+    return BIMAMBA_OK;
+}
+
+int check_conv_bwd_shape(const bimamba_conv_shape *s) {
+    int rc = check_conv_shape(s);
+    if (rc) return rc;
+    // a run's positions, rounded up to its workgroup, are counted in int32
+    if (s->seqlen > (1 << 30)) return fail(BIMAMBA_EUNSUPPORTED, "seqlen %d exceeds 2^30", s->seqlen);
+    const long long ch = (long long)s->nheads * s->headdim + 2LL * s->ngroups * s->d_state;
+    if ((ch + 63) / 64 * ((long long)s->seqlen / 64 + 1) * s->batch * 2 > (1LL << 31) - 1)
+        return fail(BIMAMBA_EUNSUPPORTED, "%d x %d tokens of %lld channels are too many for one launch", s->batch,
+                    s->seqlen, ch);
+    return BIMAMBA_OK;
+}
+
+size_t conv_bwd_dir_bytes(const bimamba_conv_shape *s, int ndir) {
+    return align256(4 * conv_bwd_part(s->batch, s->seqlen, s->nheads * s->headdim, s->ngroups * s->d_state, s->width,
+                                      ndir));
+}
+
 // packed rows: the per-token sequence index
 int check_grad(const bimamba_grad *g, const char *name, bool empty) {
     if (!g) return fail(BIMAMBA_EINVAL, "%s gradients are NULL", name);
@@ -819,6 +895,281 @@ int bimamba_merge_linear(long long rows, int cin, int cout, const float *y_fwd,
     a.out = out;
     hipError_t e = launch_merge(a, (hipStream_t)stream);
     return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the merge");
+}
+
+int bimamba_conv1d_act8(const bimamba_conv_shape *s, const bimamba_conv_dir *fwd,
+                        const bimamba_act8 *xbc_fwd, const bimamba_conv_dir *bwd,
+                        const bimamba_act8 *xbc_bwd, const int32_t *cu_seqlens, int nseq,
+                        void *workspace, size_t workspace_bytes, bimamba_stream stream) {
+    int rc = check_conv_shape(s);
+    if (rc) return rc;
+    const bool empty = s->seqlen == 0;
+    const bimamba_conv_dir *dirs[2] = {fwd, bwd};
+    const bimamba_act8 *kept[2] = {xbc_fwd, xbc_bwd};
+    ConvArgs a;
+    memset(&a, 0, sizeof a);
+    ConvDirPtrs *ptrs[2] = {&a.fwd, &a.bwd};
+    for (int i = 0; i < (bwd ? 2 : 1); ++i) {
+        const char *name = i ? "reverse" : "forward";
+        if (!dirs[i]) return fail(BIMAMBA_EINVAL, "%s direction is NULL", name);
+        if ((rc = check_act8(kept[i], name, empty))) return rc;
+        if (dirs[i]->xbc) return fail(BIMAMBA_EINVAL, "%s: xbc must be NULL, the checkpoint stands for it", name);
+        bimamba_conv_dir d = *dirs[i];
+        d.xbc = kept[i]->q;
+        if ((rc = check_conv_dir(&d, name, empty))) return rc;
+        ptrs[i]->xbc = d.xbc;
+        ptrs[i]->xscale = (const uint8_t *)kept[i]->scale;
+        ptrs[i]->weight = d.weight;
+        ptrs[i]->bias = d.bias;
+        ptrs[i]->x = d.x;
+        ptrs[i]->B = d.B;
+        ptrs[i]->C = d.C;
+    }
+    if (!bwd && xbc_bwd) return fail(BIMAMBA_EINVAL, "a reverse checkpoint is given without the reverse direction");
+    if (cu_seqlens) {
+        if (s->batch != 1) return fail(BIMAMBA_EINVAL, "cu_seqlens requires batch == 1");
+        if ((rc = check_offsets(cu_seqlens, nseq, s->seqlen))) return rc;
+    } else if (nseq != 0) {
+        return fail(BIMAMBA_EINVAL, "nseq %d given without cu_seqlens", nseq);
+    }
+    if ((rc = check_workspace(workspace, workspace_bytes, conv_workspace(cu_seqlens ? nseq : 0, s->seqlen)))) return rc;
+    if (empty) return BIMAMBA_OK;
+    a.batch = s->batch;
+    a.L = s->seqlen;
+    a.hp = s->nheads * s->headdim;
+    a.gn = s->ngroups * s->d_state;
+    a.ch = a.hp + 2 * a.gn;
+    a.W = s->width;
+    a.ndir = bwd ? 2 : 1;
+    a.act = s->activation;
+    hipStream_t st = (hipStream_t)stream;
+    hipError_t e;
+    if (cu_seqlens) {
+        int32_t *seq = (int32_t *)workspace;
+        if ((e = launch_seq_index(cu_seqlens, nseq, s->seqlen, seq, st)) != hipSuccess)
+            return hip_fail(e, "building sequence index");
+        a.seq = seq;
+    }
+    if ((e = launch_conv(a, s->dtype == BIMAMBA_BF16, st)) != hipSuccess)
+        return hip_fail(e, "launching conv1d");
+    return BIMAMBA_OK;
+}
+
+int bimamba_conv1d_bwd_workspace_size(const bimamba_conv_shape *s, int has_bwd, int nseq, size_t *bytes) {
+    int rc = check_conv_bwd_shape(s);
+    if (rc) return rc;
+    if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
+    if (nseq < 0) return fail(BIMAMBA_EINVAL, "nseq %d < 0", nseq);
+    const int ndir = has_bwd ? 2 : 1;
+    *bytes = align256(conv_workspace(nseq, s->seqlen)) + ndir * conv_bwd_dir_bytes(s, ndir);
+    return BIMAMBA_OK;
+}
+
+int bimamba_conv1d_bwd(const bimamba_conv_shape *s, const bimamba_conv_grad *fwd, const bimamba_conv_grad *bwd,
+                       const int32_t *cu_seqlens, int nseq, void *workspace, size_t workspace_bytes,
+                       bimamba_stream stream) {
+    int rc = check_conv_bwd_shape(s);
+    if (rc) return rc;
+    const bool empty = s->seqlen == 0;
+    if ((rc = check_conv_grad(fwd, "forward", empty))) return rc;
+    if (bwd && (rc = check_conv_grad(bwd, "reverse", empty))) return rc;
+    if (bwd && !empty && !fwd->xbc_scale != !bwd->xbc_scale)
+        return fail(BIMAMBA_EUNSUPPORTED, "both directions' inputs must be checkpoints, or neither");
+    if (cu_seqlens) {
+        if (s->batch != 1) return fail(BIMAMBA_EINVAL, "cu_seqlens requires batch == 1");
+        if ((rc = check_offsets(cu_seqlens, nseq, s->seqlen))) return rc;
+    } else if (nseq != 0) {
+        return fail(BIMAMBA_EINVAL, "nseq %d given without cu_seqlens", nseq);
+    }
+    const int ndir = bwd ? 2 : 1;
+    const size_t seq_bytes = align256(conv_workspace(cu_seqlens ? nseq : 0, s->seqlen));
+    const size_t dir_bytes = conv_bwd_dir_bytes(s, ndir);
+    if ((rc = check_workspace(workspace, workspace_bytes, seq_bytes + ndir * dir_bytes))) return rc;
+    ConvBwdArgs a;
+    memset(&a, 0, sizeof a);
+    const bimamba_conv_grad *dirs[2] = {fwd, bwd};
+    for (int i = 0; i < ndir; ++i) {
+        a.dir[i].xbc = dirs[i]->xbc;
+        a.dir[i].xscale = dirs[i]->xbc_scale;
+        a.dir[i].weight = dirs[i]->weight;
+        a.dir[i].bias = dirs[i]->bias;
+        a.dir[i].dx = dirs[i]->dx;
+        a.dir[i].dB = dirs[i]->dB;
+        a.dir[i].dC = dirs[i]->dC;
+        a.dir[i].dxbc = dirs[i]->dxbc;
+        a.dir[i].dw = dirs[i]->dweight;
+        a.dir[i].db = dirs[i]->dbias;
+        a.dir[i].part = (float *)((char *)workspace + seq_bytes + i * dir_bytes);
+    }
+    a.batch = s->batch;
+    a.L = s->seqlen;
+    a.hp = s->nheads * s->headdim;
+    a.gn = s->ngroups * s->d_state;
+    a.ch = a.hp + 2 * a.gn;
+    a.W = s->width;
+    a.ndir = ndir;
+    a.act = s->activation;
+    hipStream_t st = (hipStream_t)stream;
+    hipError_t e;
+    if (cu_seqlens && !empty) {
+        int32_t *seq = (int32_t *)workspace;
+        if ((e = launch_seq_index(cu_seqlens, nseq, s->seqlen, seq, st)) != hipSuccess)
+            return hip_fail(e, "building sequence index");
+        a.seq = seq;
+    }
+    e = launch_conv_bwd(a, s->dtype == BIMAMBA_BF16, st);
+    return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the convolution's gradient");
+}
+
+int bimamba_gated_norm_bwd_workspace_size(long long rows, int channels, int group_size, int dtype, size_t *bytes) {
+    int rc = check_gated_norm(rows, channels, group_size, dtype);
+    if (rc) return rc;
+    if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
+    *bytes = (size_t)gated_norm_bwd_wgs(rows) * channels * 4;
+    return BIMAMBA_OK;
+}
+
+int bimamba_gated_norm_bwd(long long rows, int channels, int group_size, int dtype, const void *y,
+                           const uint8_t *y_scale, const void *z, const uint8_t *z_scale, const float *weight,
+                           float eps, const void *dout, float *dy, void *dz, float *dweight, void *workspace,
+                           size_t workspace_bytes, bimamba_stream stream) {
+    int rc = check_gated_norm(rows, channels, group_size, dtype);
+    if (rc) return rc;
+    if (!(eps >= 0.f) || eps > 3.0e38f) return fail(BIMAMBA_EINVAL, "eps must be finite and >= 0");
+    if (rows == 0 && !dweight) return BIMAMBA_OK;
+    if (rows > 0) {
+        if (!y || !z || !weight || !dout || !dy || !dz)
+            return fail(BIMAMBA_EINVAL, "y, z, weight, dout, dy and dz are required");
+        if (!aligned16(y) || !aligned16(z) || !aligned16(weight) || !aligned16(dout) || !aligned16(dy) || !aligned16(dz))
+            return fail(BIMAMBA_EINVAL, "y, z, weight, dout, dy and dz must be 16-byte aligned");
+    }
+    if ((uintptr_t)dweight & 3u) return fail(BIMAMBA_EINVAL, "dweight must be 4-byte aligned");
+    const size_t need = dweight ? (size_t)gated_norm_bwd_wgs(rows) * channels * 4 : 0;
+    if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+    EpiBwdArgs a;
+    memset(&a, 0, sizeof a);
+    a.rows = rows;
+    a.C = channels;
+    a.gs = group_size;
+    a.eps = eps;
+    a.y = y;
+    a.yscale = y_scale;
+    a.z = z;
+    a.zscale = z_scale;
+    a.w = weight;
+    a.dout = dout;
+    a.dy = dy;
+    a.dz = dz;
+    a.dw = dweight;
+    a.part = need ? (float *)workspace : nullptr;
+    hipError_t e = launch_gated_norm_bwd(a, dtype == BIMAMBA_BF16, (hipStream_t)stream);
+    return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the gated norm's gradient");
+}
+
+int bimamba_layer_norm(long long rows, int channels, int dtype, const void *x, const void *residual,
+                       const float *weight, const float *bias, float eps, void *out, void *sum, float *mean,
+                       float *rstd, const bimamba_act8 *ckpt, bimamba_stream stream) {
+    int rc = check_layer_norm(rows, channels, dtype);
+    if (rc) return rc;
+    if (!(eps >= 0.f) || eps > 3.0e38f) return fail(BIMAMBA_EINVAL, "eps must be finite and >= 0");
+    if (rows == 0) return BIMAMBA_OK;
+    if (!x || !out) return fail(BIMAMBA_EINVAL, "x and out are required");
+    if (!residual != !sum) return fail(BIMAMBA_EINVAL, "residual and sum come together");
+    if (ckpt && (!ckpt->q || !ckpt->scale))
+        return fail(BIMAMBA_EINVAL, "the checkpoint's q and scale are required");
+    if (!aligned_to(x, dtype) || !aligned_to(residual, dtype) || !aligned_to(out, dtype) || !aligned_to(sum, dtype))
+        return fail(BIMAMBA_EINVAL, "x, residual, out and sum must be aligned to their elements");
+    if (((uintptr_t)weight | (uintptr_t)bias | (uintptr_t)mean | (uintptr_t)rstd) & 3u)
+        return fail(BIMAMBA_EINVAL, "weight, bias, mean and rstd must be 4-byte aligned");
+    LnArgs a;
+    memset(&a, 0, sizeof a);
+    a.rows = rows;
+    a.C = channels;
+    a.eps = eps;
+    a.x = x;
+    a.res = residual;
+    a.w = weight;
+    a.b = bias;
+    a.out = out;
+    a.sum = sum;
+    a.mean = mean;
+    a.rstd = rstd;
+    if (ckpt) {
+        a.q = (int8_t *)ckpt->q;
+        a.scale = (uint8_t *)ckpt->scale;
+    }
+    hipError_t e = launch_layer_norm(a, dtype == BIMAMBA_BF16, (hipStream_t)stream);
+    return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the layer norm");
+}
+
+int bimamba_layer_norm_bwd_workspace_size(long long rows, int channels, int dtype, size_t *bytes) {
+    int rc = check_layer_norm(rows, channels, dtype);
+    if (rc) return rc;
+    if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
+    *bytes = (size_t)layer_norm_bwd_wgs(rows, channels) * 2 * channels * 4;
+    return BIMAMBA_OK;
+}
+
+int bimamba_layer_norm_bwd(long long rows, int channels, int dtype, const void *x, const uint8_t *x_scale,
+                           const float *mean, const float *rstd, const float *weight, const void *dout,
+                           const void *dsum, void *dx, float *dweight, float *dbias, void *workspace,
+                           size_t workspace_bytes, bimamba_stream stream) {
+    int rc = check_layer_norm(rows, channels, dtype);
+    if (rc) return rc;
+    const bool wgrad = dweight || dbias;
+    if (rows == 0 && !wgrad) return BIMAMBA_OK;
+    if (rows > 0) {
+        if (!x || !mean || !rstd || !dout || !dx)
+            return fail(BIMAMBA_EINVAL, "x, mean, rstd, dout and dx are required");
+        if ((!x_scale && !aligned_to(x, dtype)) || !aligned_to(dout, dtype) || !aligned_to(dsum, dtype) ||
+            !aligned_to(dx, dtype))
+            return fail(BIMAMBA_EINVAL, "x, dout, dsum and dx must be aligned to their elements");
+    }
+    if (((uintptr_t)weight | (uintptr_t)mean | (uintptr_t)rstd | (uintptr_t)dweight | (uintptr_t)dbias) & 3u)
+        return fail(BIMAMBA_EINVAL, "weight, mean, rstd, dweight and dbias must be 4-byte aligned");
+    const size_t need = wgrad ? (size_t)layer_norm_bwd_wgs(rows, channels) * 2 * channels * 4 : 0;
+    if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+    LnBwdArgs a;
+    memset(&a, 0, sizeof a);
+    a.rows = rows;
+    a.C = channels;
+    a.x = x;
+    a.xscale = x_scale;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.w = weight;
+    a.dout = dout;
+    a.dsum = dsum;
+    a.dx = dx;
+    a.dw = dweight;
+    a.db = dbias;
+    a.part = need ? (float *)workspace : nullptr;
+    hipError_t e = launch_layer_norm_bwd(a, dtype == BIMAMBA_BF16, (hipStream_t)stream);
+    return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the layer norm's gradient");
+}
+
+static int act8_call(long long rows, long long channels, int dtype, const void *x, const bimamba_act8 *a, bool pack,
+                     bimamba_stream stream) {
+    int rc = check_rows(rows, dtype);
+    if (rc) return rc;
+    if (channels < 1 || channels > (1LL << 31) - 1)
+        return fail(BIMAMBA_EUNSUPPORTED, "channels %lld not in [1, 2^31-1]", channels);
+    if (rows == 0) return BIMAMBA_OK;
+    if (!x || !a || !a->q || !a->scale) return fail(BIMAMBA_EINVAL, "x, q and scale are required");
+    if (!aligned_to(x, dtype)) return fail(BIMAMBA_EINVAL, "x must be aligned to its elements");
+    Act8Args p{rows, channels, const_cast<void *>(x), (int8_t *)a->q, (uint8_t *)a->scale};
+    hipError_t e = launch_act8(p, dtype == BIMAMBA_BF16, pack, (hipStream_t)stream);
+    return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the 8-bit checkpoint");
+}
+
+int bimamba_act8_pack(long long rows, long long channels, int dtype, const void *x, const bimamba_act8 *out,
+                      bimamba_stream stream) {
+    return act8_call(rows, channels, dtype, x, out, true, stream);
+}
+
+int bimamba_act8_unpack(long long rows, long long channels, int dtype, const bimamba_act8 *in, void *x,
+                        bimamba_stream stream) {
+    return act8_call(rows, channels, dtype, x, in, false, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,305 @@
+// Gradient of the short convolution (conv1d.hip) of both directions. In scan
+// positions p (token p forward, token L-1-p reverse) both directions are the
+// same causal filter u_p = b + sum_k w_k in_{p-(W-1)+k}; given the output's
+// gradient dout (fp32, as bimamba_ssd_bwd leaves it):
+//   du_p = dout_p act'(u_p),   act' = sig(u) (1 + u (1 - sig(u))) for SiLU
+//   din_p = sum_k w_k du_{p+(W-1)-k},
+//   dw_k = sum_p du_p in_{p-(W-1)+k},   db = sum_p du_p
+// terms across a row's or a packed sequence's ends left out. The input may be
+// read from its 8-bit checkpoint (rows.hpp).
+//
+// A stream bounded by HBM: input and dout read once, din written once. A lane
+// owns four adjacent channels and walks a run of positions with the last W-1
+// inputs and du in registers: u_p and du_p are computed as p comes in, and
+// din_{p-(W-1)}, whose last term du_p is, goes out. A run starts W-1
+// positions early with its inputs and ends W-1 late with its du; four waves
+// of a workgroup take adjacent runs. Rows are loaded kBatch positions ahead.
+// dw and db stay in the lane's registers over the run, are joined over the
+// workgroup through LDS and over workgroups by col_sum.hip.
+#include "internal.hpp"
+#include "rows.hpp"
+
+namespace bm {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kBatch = 4;   // positions loaded and worked on together, >= W - 1
+
+typedef uint32_t w2 __attribute__((ext_vector_type(2)));
+
+// VEC channels of one row of the input
+template <typename T, bool Q8, int VEC> struct In;
+template <> struct In<float, false, 4> {
+    rvec r;
+    __device__ __forceinline__ void load(const void *p, const uint8_t *, size_t row, int ch, int, int c) {
+        r = *(const rvec *)((const float *)p + row * ch + c);
+    }
+    __device__ __forceinline__ float get(int j) const { return __uint_as_float(r[j]); }
+};
+template <> struct In<uint16_t, false, 4> {
+    w2 r;
+    __device__ __forceinline__ void load(const void *p, const uint8_t *, size_t row, int ch, int, int c) {
+        r = *(const w2 *)((const uint16_t *)p + row * ch + c);
+    }
+    __device__ __forceinline__ float get(int j) const {
+        return __uint_as_float((j & 1) ? (r[j >> 1] & 0xffff0000u) : (r[j >> 1] << 16));
+    }
+};
+template <typename T> struct In<T, false, 1> {
+    T r;
+    __device__ __forceinline__ void load(const void *p, const uint8_t *, size_t row, int ch, int, int c) {
+        r = ((const T *)p)[row * ch + c];
+    }
+    __device__ __forceinline__ float get(int) const { return Elem<T>::load(&r, 0); }
+};
+template <typename T> struct In<T, true, 4> {
+    uint32_t r, e;
+    __device__ __forceinline__ void load(const void *p, const uint8_t *scale, size_t row, int ch, int nblk, int c) {
+        r = *(const uint32_t *)((const int8_t *)p + row * ch + c);
+        e = scale[row * nblk + c / 32];
+    }
+    __device__ __forceinline__ float get(int j) const { return (float)Bytes<4>::get(r, j) * act8_unit(e); }
+};
+template <typename T> struct In<T, true, 1> {
+    int r;
+    uint32_t e;
+    __device__ __forceinline__ void load(const void *p, const uint8_t *scale, size_t row, int ch, int nblk, int c) {
+        r = ((const int8_t *)p)[row * ch + c];
+        e = scale[row * nblk + c / 32];
+    }
+    __device__ __forceinline__ float get(int) const { return (float)r * act8_unit(e); }
+};
+
+template <int VEC>
+__device__ __forceinline__ void load_grad(const float *p, float (&v)[VEC]) {
+    if constexpr (VEC == 4) {
+        const float4 q = *(const float4 *)p;
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+        v[0] = *p;
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void store_in(float *p, const float (&v)[VEC]) {
+    if constexpr (VEC == 4) *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]);
+    else *p = v[0];
+}
+template <int VEC>
+__device__ __forceinline__ void store_in(uint16_t *p, const float (&v)[VEC]) {
+    if constexpr (VEC == 4) {
+        const rf2 a = {v[0], v[1]}, b = {v[2], v[3]};
+        w2 o;
+        o[0] = __builtin_bit_cast(uint32_t, __builtin_convertvector(a, rbf2));
+        o[1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(b, rbf2));
+        *(w2 *)p = o;
+    } else {
+        *p = __builtin_bit_cast(uint16_t, (__bf16)v[0]);
+    }
+}
+
+template <typename T, bool Q8, int VEC, int W, bool PACKED>
+__global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvBwdArgs a) {
+    constexpr int H = W - 1, N = H + kBatch;
+    __shared__ float join[kWaves][VEC * (W + 1)][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // workgroup -> (row and direction, tile of runs, channel slab)
+    const int slab = blockIdx.x % a.slabs;
+    const int rest = blockIdx.x / a.slabs;
+    const int tile = rest % a.tiles, unit = rest / a.tiles;
+    const bool rev = unit % a.ndir != 0;
+    const int b = unit / a.ndir;
+    const ConvBwdDir d = rev ? a.dir[1] : a.dir[0];
+    const int L = a.L, ch = a.ch, nblk = (ch + 31) / 32;
+    const int cv = slab * 64 + lane;
+    const bool chan_ok = cv < a.nvec;
+    const int c0 = (chan_ok ? cv : a.nvec - 1) * VEC;   // lanes past the end store nothing
+
+    float w[VEC][W], bias[VEC], aw[VEC][W], ab[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            w[j][k] = d.weight[(size_t)(c0 + j) * W + k];
+            aw[j][k] = 0.f;
+        }
+        bias[j] = d.bias ? d.bias[c0 + j] : 0.f;
+        ab[j] = 0.f;
+    }
+    // dout array of the lane: x, B or C
+    const float *g;
+    int gs;
+    if (c0 < a.hp) {
+        g = d.dx + c0; gs = a.hp;
+    } else if (c0 < a.hp + a.gn) {
+        g = d.dB + (c0 - a.hp); gs = a.gn;
+    } else {
+        g = d.dC + (c0 - a.hp - a.gn); gs = a.gn;
+    }
+    const size_t row0 = (size_t)b * L;
+    const int p0 = (tile * kWaves + wave) * a.run;
+    const int p1 = min(p0 + a.run, L);
+    auto token = [&](int p) { return rev ? L - 1 - p : p; };
+
+    if (p0 < L) {
+        float win[N][VEC], du[N][VEC];
+        int sid[N];
+        In<T, Q8, VEC> next[kBatch];
+        float gnext[kBatch][VEC];
+        int snext[kBatch];
+        auto fetch = [&](int p) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int t = token(min(p + i, L - 1));   // positions past the end: masked when used
+                next[i].load(d.xbc, d.xscale, row0 + t, ch, nblk, c0);
+                load_grad<VEC>(g + (row0 + t) * gs, gnext[i]);
+                if constexpr (PACKED) snext[i] = a.seq[t];
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const int p = p0 - H + i;
+            In<T, Q8, VEC> v;
+            v.load(d.xbc, d.xscale, row0 + token(max(p, 0)), ch, nblk, c0);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                win[i][j] = p >= 0 ? v.get(j) : 0.f;
+                du[i][j] = 0.f;
+            }
+            if constexpr (PACKED) sid[i] = p >= 0 ? a.seq[token(p)] : -1;
+        }
+        fetch(p0);
+        for (int p = p0; p < p1 + H; p += kBatch) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const bool live = p + i < L;
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    win[H + i][j] = live ? next[i].get(j) : 0.f;
+                    du[H + i][j] = live ? gnext[i][j] : 0.f;
+                }
+                if constexpr (PACKED) sid[H + i] = live ? snext[i] : -1;
+            }
+            if (p + kBatch < p1 + H) fetch(p + kBatch);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const bool own = p + i < p1;
+                const int s = p + i - H;
+                const bool out = s >= p0 && s < p1;
+                float o[VEC];
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    float tap[W];
+                    float u = bias[j];
+#pragma unroll
+                    for (int k = 0; k < W; ++k) {
+                        tap[k] = !PACKED || sid[i + k] == sid[i + H] ? win[i + k][j] : 0.f;
+                        u = fmaf(w[j][k], tap[k], u);
+                    }
+                    const float sg = __builtin_amdgcn_rcpf(1.0f + __expf(-u));
+                    const float slope = a.act ? sg * fmaf(u, 1.0f - sg, 1.0f) : 1.0f;
+                    // a position past the end has no gradient, whatever its slope
+                    const float v = p + i < L ? du[H + i][j] * slope : 0.f;
+                    du[H + i][j] = v;
+                    const float m = own ? v : 0.f;
+                    ab[j] += m;
+#pragma unroll
+                    for (int k = 0; k < W; ++k) aw[j][k] = fmaf(m, tap[k], aw[j][k]);
+                    o[j] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < W; ++k)
+                        o[j] = fmaf(w[j][H - k], !PACKED || sid[i + k] == sid[i] ? du[i + k][j] : 0.f, o[j]);
+                }
+                if (out && chan_ok) store_in<VEC>((T *)d.dxbc + (row0 + token(s)) * ch + c0, o);
+            }
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    win[i][j] = win[kBatch + i][j];
+                    du[i][j] = du[kBatch + i][j];
+                }
+                if constexpr (PACKED) sid[i] = sid[kBatch + i];
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) join[wave][k * VEC + j][lane] = aw[j][k];
+        join[wave][W * VEC + j][lane] = ab[j];
+    }
+    __syncthreads();
+    // wave v joins taps v, v + 4 (tap W is the bias)
+    float *part = d.part + (size_t)(b * a.tiles + tile) * (W + 1) * ch;
+    for (int k = wave; k <= W; k += kWaves) {
+        float o[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            o[j] = 0.f;
+#pragma unroll
+            for (int v = 0; v < kWaves; ++v) o[j] += join[v][k * VEC + j][lane];
+        }
+        if (chan_ok) store_in<VEC>(part + (size_t)k * ch + c0, o);
+    }
+}
+
+template <typename T, bool Q8, int VEC, int W>
+hipError_t launch_w(const ConvBwdArgs &a, hipStream_t s) {
+    const dim3 grid((unsigned)((long long)a.slabs * a.tiles * a.batch * a.ndir));
+    if (a.seq) BM_LAUNCH("conv1d_bwd_packed", (k_conv_bwd<T, Q8, VEC, W, true>), grid, dim3(64 * kWaves), 0, s, a);
+    else BM_LAUNCH("conv1d_bwd", (k_conv_bwd<T, Q8, VEC, W, false>), grid, dim3(64 * kWaves), 0, s, a);
+    return hipGetLastError();
+}
+template <typename T, bool Q8, int VEC>
+hipError_t launch_v(const ConvBwdArgs &a, hipStream_t s) {
+    switch (a.W) {
+        case 2: return launch_w<T, Q8, VEC, 2>(a, s);
+        case 3: return launch_w<T, Q8, VEC, 3>(a, s);
+        case 4: return launch_w<T, Q8, VEC, 4>(a, s);
+    }
+    return hipErrorInvalidValue;
+}
+template <typename T>
+hipError_t launch_t(const ConvBwdArgs &a, bool vec, hipStream_t s) {
+    if (a.dir[0].xscale) return vec ? launch_v<T, true, 4>(a, s) : launch_v<T, true, 1>(a, s);
+    return vec ? launch_v<T, false, 4>(a, s) : launch_v<T, false, 1>(a, s);
+}
+
+// positions a wave walks: long runs repeat few halo rows, short ones give
+// the chip enough waves
+int run_length(int batch, int L, int slabs, int ndir) {
+    int run = 64;
+    while (run > 16 && (long long)((L + run - 1) / run) * slabs * batch * ndir < 2048) run /= 2;
+    return run;
+}
+int tiles_of(int L, int run) { return (L + run * kWaves - 1) / (run * kWaves); }
+int slabs_of(int hp, int gn, int *nvec) {
+    *nvec = (hp + 2 * gn) / (conv_vectorized(true, hp, gn) ? 4 : 1);
+    return (*nvec + 63) / 64;
+}
+
+}  // namespace
+
+size_t conv_bwd_part(int batch, int L, int hp, int gn, int W, int ndir) {
+    int nvec;
+    const int slabs = slabs_of(hp, gn, &nvec);
+    return (size_t)batch * tiles_of(L, run_length(batch, L, slabs, ndir)) * (W + 1) * (hp + 2 * gn);
+}
+
+hipError_t launch_conv_bwd(ConvBwdArgs a, bool bf16, hipStream_t s) {
+    a.slabs = slabs_of(a.hp, a.gn, &a.nvec);
+    a.run = run_length(a.batch, a.L, a.slabs, a.ndir);
+    a.tiles = tiles_of(a.L, a.run);
+    if (a.L > 0) {
+        const bool vec = conv_vectorized(bf16, a.hp, a.gn);
+        hipError_t e = bf16 ? launch_t<uint16_t>(a, vec, s) : launch_t<float>(a, vec, s);
+        if (e != hipSuccess) return e;
+    }
+    ColSum sets[2];
+    for (int i = 0; i < a.ndir; ++i)
+        sets[i] = ColSum{a.dir[i].part, a.batch * a.tiles, a.ch, a.W, 1, a.dir[i].dw, a.dir[i].db};
+    return launch_col_sum(sets, a.ndir, s);
+}
+
+}  // namespace bm

@@ -118,7 +118,8 @@ hipError_t launch_gated_norm(const EpiArgs &a, bool bf16, hipStream_t s);
 
 // conv1d.hip: short depthwise convolution of the x | B | C channels
 struct ConvDirPtrs {
-    const void *xbc;           // [batch][L][ch]
+    const void *xbc;           // [batch][L][ch], int8 with xscale
+    const uint8_t *xscale;     // [batch][L][(ch + 31) / 32] or nullptr (both directions alike)
     const float *weight;       // [ch][W]
     const float *bias;         // [ch] or nullptr
     void *x, *B, *C;           // outputs [batch][L][hp], [batch][L][gn] x2
@@ -137,5 +138,88 @@ bool conv_vectorized(bool bf16, int hp, int gn);
 hipError_t launch_conv(ConvArgs a, bool bf16, hipStream_t s);
 // dst[i] = src ? src[i] : 0 for n 16-bit words (context of an empty row)
 hipError_t launch_ctx_copy(const void *src, void *dst, size_t n, hipStream_t s);
+
+// col_sum.hip: columns of partial sums (weight gradients)
+struct ColSum {
+    const float *part;         // [n][taps + bias][ch]
+    int n, ch, taps, bias;     // bias: 1 if the last ch columns are the bias's, else 0
+    float *w;                  // [ch][taps] or nullptr
+    float *b;                  // [ch] or nullptr
+};
+hipError_t launch_col_sum(const ColSum *sets, int nsets, hipStream_t s);   // 1 or 2 of one shape
+
+// layer_norm.hip
+struct LnArgs {
+    long long rows;
+    int C;                     // 8 .. 16384
+    float eps;
+    const void *x, *res;       // [rows][C]; res may be nullptr
+    const float *w, *b;        // [C] or nullptr
+    void *out, *sum;           // [rows][C]; sum only with res
+    float *mean, *rstd;        // [rows] or nullptr
+    int8_t *q;                 // 8-bit checkpoint of x + res, or nullptr
+    uint8_t *scale;
+};
+hipError_t launch_layer_norm(const LnArgs &a, bool bf16, hipStream_t s);
+struct LnBwdArgs {
+    long long rows;
+    int C;
+    const void *x;             // dtype, or int8 with xscale
+    const uint8_t *xscale;
+    const float *mean, *rstd, *w;   // w may be nullptr
+    const void *dout, *dsum;   // dsum may be nullptr
+    void *dx;
+    float *dw, *db;            // [C] or nullptr
+    float *part;               // workspace, or nullptr with neither dw nor db
+};
+int layer_norm_bwd_wgs(long long rows, int C);
+hipError_t launch_layer_norm_bwd(const LnBwdArgs &a, bool bf16, hipStream_t s);
+
+// gated_norm_bwd.hip
+struct EpiBwdArgs {
+    long long rows;
+    int C, gs;
+    float eps;
+    const void *y;             // float, or int8 with yscale
+    const uint8_t *yscale;
+    const void *z;             // dtype, or int8 with zscale
+    const uint8_t *zscale;
+    const float *w;
+    const void *dout;          // dtype
+    float *dy;
+    void *dz;                  // dtype
+    float *dw;                 // [C] or nullptr
+    float *part;
+};
+int gated_norm_bwd_wgs(long long rows);
+hipError_t launch_gated_norm_bwd(const EpiBwdArgs &a, bool bf16, hipStream_t s);
+
+// act8.hip
+struct Act8Args {
+    long long rows, C;
+    void *x;                   // read when packing, written when unpacking
+    int8_t *q;
+    uint8_t *scale;
+};
+hipError_t launch_act8(Act8Args a, bool bf16, bool pack, hipStream_t s);
+
+// conv1d_bwd.hip: gradient of the short convolution
+struct ConvBwdDir {
+    const void *xbc;           // [batch][L][ch] dtype, or int8 with xscale
+    const uint8_t *xscale;     // [batch][L][(ch + 31) / 32] or nullptr
+    const float *weight, *bias;
+    const float *dx, *dB, *dC; // gradients of the outputs
+    void *dxbc;                // dtype
+    float *dw, *db;            // [ch][W], [ch] or nullptr
+    float *part;               // workspace [batch * tiles][W + 1][ch]
+};
+struct ConvBwdArgs {
+    ConvBwdDir dir[2];
+    int batch, L, hp, gn, ch, W, ndir, act;
+    int nvec, slabs, tiles, run;   // set by launch_conv_bwd
+    const int32_t *seq;
+};
+size_t conv_bwd_part(int batch, int L, int hp, int gn, int W, int ndir);   // floats per direction
+hipError_t launch_conv_bwd(ConvBwdArgs a, bool bf16, hipStream_t s);
 
 }  // namespace bm

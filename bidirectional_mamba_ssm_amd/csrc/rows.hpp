@@ -1,0 +1,140 @@
+// Device helpers of the row-wise training kernels (norms, 8-bit checkpoints):
+// 16-byte lane vectors of a row, sums over a wave by DPP lane moves, and the
+// 8-bit checkpoint code.
+//
+// 8-bit checkpoints (bimamba_act8): 32 consecutive channels of a row share
+// one power of two. With E the largest fp32 exponent field among them, an
+// element v is kept as the integer q = clamp(round(v 2^(133-E)), -127, 127)
+// (nearest, ties to even) and stands for q 2^(E-133). Scaling by a power of
+// two is exact, so the one rounding is the integer's: half a unit, 2^(E-134),
+// at most 2^-7 of the block's largest magnitude (one unit, as much, where the
+// clamp takes effect). q has 7 bits, so a decoded value is exact in bf16.
+// A block that holds an infinity or a NaN has E = 255 and decodes as NaN.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+
+namespace bm {
+
+// Rows of any length start at any multiple of the element size; gfx950 takes
+// vector loads and stores at such addresses (unaligned access is the
+// target's default), so these types promise only the element's alignment.
+typedef uint32_t u4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u4_a4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u2_a1 __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u1_a1 __attribute__((aligned(1)));
+typedef uint32_t rvec __attribute__((ext_vector_type(4)));
+typedef __bf16 rbf2 __attribute__((ext_vector_type(2)));
+typedef float rf2 __attribute__((ext_vector_type(2)));
+
+// one lane's vector of a row: 16 bytes, V elements
+template <typename T> struct Lane;
+template <> struct Lane<uint16_t> {
+    static constexpr int V = 8;
+    __device__ __forceinline__ static rvec load(const uint16_t *p) { return *(const u4_a2 *)p; }
+    __device__ __forceinline__ static float get(rvec r, int j) {
+        const uint32_t w = r[j >> 1];
+        return __uint_as_float((j & 1) ? (w & 0xffff0000u) : (w << 16));
+    }
+    // round to nearest even (hardware conversion)
+    __device__ __forceinline__ static rvec pack(const float *v) {
+        rvec r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const rf2 p = {v[2 * j], v[2 * j + 1]};
+            r[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, rbf2));
+        }
+        return r;
+    }
+    __device__ __forceinline__ static void store(uint16_t *p, rvec r) { *(u4_a2 *)p = r; }
+};
+template <> struct Lane<float> {
+    static constexpr int V = 4;
+    __device__ __forceinline__ static rvec load(const float *p) { return *(const u4_a4 *)p; }
+    __device__ __forceinline__ static float get(rvec r, int j) { return __uint_as_float(r[j]); }
+    __device__ __forceinline__ static rvec pack(const float *v) {
+        rvec r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = __float_as_uint(v[j]);
+        return r;
+    }
+    __device__ __forceinline__ static void store(float *p, rvec r) { *(u4_a4 *)p = r; }
+};
+
+// V bytes of an 8-bit checkpoint
+template <int V> struct Bytes;
+template <> struct Bytes<8> {
+    typedef uint32_t type __attribute__((ext_vector_type(2)));
+    __device__ __forceinline__ static type load(const int8_t *p) { return *(const u2_a1 *)p; }
+    __device__ __forceinline__ static void store(int8_t *p, type r) { *(u2_a1 *)p = r; }
+    __device__ __forceinline__ static int get(type r, int j) {
+        return (int)(r[j >> 2] << (24 - 8 * (j & 3))) >> 24;
+    }
+    __device__ __forceinline__ static type pack(const int *q) {
+        type r;
+        r[0] = (uint32_t)(q[0] & 255) | (uint32_t)(q[1] & 255) << 8 | (uint32_t)(q[2] & 255) << 16 |
+               (uint32_t)q[3] << 24;
+        r[1] = (uint32_t)(q[4] & 255) | (uint32_t)(q[5] & 255) << 8 | (uint32_t)(q[6] & 255) << 16 |
+               (uint32_t)q[7] << 24;
+        return r;
+    }
+};
+template <> struct Bytes<4> {
+    typedef uint32_t type;
+    __device__ __forceinline__ static type load(const int8_t *p) { return *(const u1_a1 *)p; }
+    __device__ __forceinline__ static void store(int8_t *p, type r) { *(u1_a1 *)p = r; }
+    __device__ __forceinline__ static int get(type r, int j) { return (int)(r << (24 - 8 * j)) >> 24; }
+    __device__ __forceinline__ static type pack(const int *q) {
+        return (uint32_t)(q[0] & 255) | (uint32_t)(q[1] & 255) << 8 | (uint32_t)(q[2] & 255) << 16 |
+               (uint32_t)q[3] << 24;
+    }
+};
+
+// 2^(e-133) for a block's exponent field e; NaN for 255. 2^(e-127) is the
+// field itself as a float, except that field 0 means 2^-127 (a subnormal) and
+// 255 a NaN: both have the mantissa's top bit set. Times 2^-6, exact down to
+// the subnormal 2^-133.
+__device__ __forceinline__ float act8_unit(uint32_t e) {
+    const uint32_t top = (e == 0 || e == 255) ? 0x00400000u : 0u;
+    return __uint_as_float((e << 23) | top) * 0.015625f;
+}
+// the integer kept for v in a block of exponent field e (0 in a NaN block)
+__device__ __forceinline__ int act8_code(float v, int e) {
+    const float m = rintf(__builtin_ldexpf(v, 133 - e));
+    const int q = (int)fminf(fmaxf(m, -127.f), 127.f);
+    return e == 255 ? 0 : q;
+}
+// exponent field of the largest of V magnitudes (bit patterns order as the
+// magnitudes do, infinities and NaN above all)
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+template <int CTRL, int ROW = 0xf, int BANK = 0xf, bool BOUND = true>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROW, BANK, BOUND);
+}
+template <int CTRL, int ROW = 0xf>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __uint_as_float(dpp<CTRL, ROW>(__float_as_uint(v)));
+}
+// largest over the LANES (2, 4 or 8) adjacent lanes that hold one block
+template <int LANES>
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
+    v = max(v, dpp<0xB1>(v));                     // quad_perm [1,0,3,2]
+    if constexpr (LANES > 2) v = max(v, dpp<0x4E>(v));   // quad_perm [2,3,0,1]
+    if constexpr (LANES > 4) v = max(v, dpp<0x141>(v));  // row_half_mirror
+    return v;
+}
+// sum over the wave's 64 lanes, the same in every lane; a fixed order
+__device__ __forceinline__ float wave_total(float v) {
+    v = dpp_add<0xB1>(v);                         // lanes 1 apart
+    v = dpp_add<0x4E>(v);                         // 2 apart
+    v = dpp_add<0x141>(v);                        // the other quad of 8
+    v = dpp_add<0x140>(v);                        // the other half of 16
+    v = dpp_add<0x142, 0xa>(v);                   // row 0 into 1, 2 into 3
+    v = dpp_add<0x143, 0xc>(v);                   // rows 0..1 into 2..3
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+
+}  // namespace bm

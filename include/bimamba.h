@@ -379,6 +379,126 @@ int bimamba_block_step_conv(bimamba_state *st, const bimamba_conv_shape *cs,
                             const bimamba_shape *s, const bimamba_dir *fwd,
                             const bimamba_dir *bwd, int commit, float *y,
                             bimamba_stream stream);
+/* ---- 8-bit activation checkpoints -----------------------------------------
+ *
+ * What a training step keeps for its backward pass, at 1 + 1/32 bytes an
+ * element: 32 consecutive channels of a row (the last block of a row may be
+ * shorter) share a power of two. With E the largest fp32 exponent field among
+ * a block's elements, an element v is kept as the signed integer
+ * q = clamp(round(v * 2^(133-E)), -127, 127) (to nearest, ties to even) and
+ * stands for q * 2^(E-133): within 2^-7 of the block's largest magnitude.
+ * E = 0 (zeros and fp32 subnormals) is kept as such; a block that holds an
+ * infinity or a NaN has E = 255 and stands for NaNs. Values read back are
+ * exact in either dtype. bimamba_conv1d_act8, bimamba_conv1d_bwd,
+ * bimamba_gated_norm_bwd and bimamba_layer_norm_bwd read a checkpoint where
+ * they would read the array, without a full-size copy in between. */
+typedef struct {
+    void *q;      /* int8 [rows][channels]                                     */
+    void *scale;  /* uint8 [rows][(channels + 31) / 32], the blocks' E          */
+} bimamba_act8;
+/* x: dtype [rows][channels], aligned to its elements (as are q and scale
+ * here: to one byte). rows >= 0, channels in [1, 2^31-1]. Arrays may not
+ * overlap. */
+int bimamba_act8_pack(long long rows, long long channels, int dtype, const void *x,
+                      const bimamba_act8 *out, bimamba_stream stream);
+int bimamba_act8_unpack(long long rows, long long channels, int dtype, const bimamba_act8 *in,
+                        void *x, bimamba_stream stream);
+
+/* ---- Training: the steps around the scan ------------------------------------
+ *
+ * With bimamba_ssd_bwd these are the backward pass of a mixer layer; the
+ * norm in front of the block and its residual stream are the plain pre-norm
+ * block's (each block of the DiffuMamba stack is a norm, the bidirectional
+ * mixer and a residual add; blog, "network architecture"). Gradients of
+ * weights are summed over tokens in a fixed order (fp32 within a workgroup,
+ * fp64 over them): the same inputs give the same bits. */
+
+/* bimamba_conv1d with each direction's input in an 8-bit checkpoint (rows =
+ * batch * seqlen, channels as in bimamba_conv1d; q 16-byte aligned): the
+ * scan's inputs rebuilt in the backward pass. fwd->xbc and bwd->xbc must be
+ * NULL; xbc_bwd goes with bwd. s->dtype is the outputs'. No contexts. The
+ * workspace is bimamba_conv1d_workspace_size(). */
+int bimamba_conv1d_act8(const bimamba_conv_shape *s, const bimamba_conv_dir *fwd,
+                        const bimamba_act8 *xbc_fwd, const bimamba_conv_dir *bwd,
+                        const bimamba_act8 *xbc_bwd, const int32_t *cu_seqlens, int nseq,
+                        void *workspace, size_t workspace_bytes, bimamba_stream stream);
+
+/* Gradient of bimamba_conv1d (without contexts, as rows start in training),
+ * both directions in one call. The reverse direction in forward time order. */
+typedef struct {
+    const void *xbc;          /* [batch][seqlen][channels] dtype, the forward's
+                                 input; int8 with xbc_scale                      */
+    const uint8_t *xbc_scale; /* NULL, or the scales of xbc's 8-bit checkpoint
+                                 (for both directions or neither)                */
+    const float *weight;      /* [channels][width]                               */
+    const float *bias;        /* [channels] or NULL, as in the forward           */
+    const float *dx, *dB, *dC;/* float gradients of x, B and C
+                                 (bimamba_ssd_bwd's)                              */
+    void *dxbc;               /* out [batch][seqlen][channels] dtype (rounded to
+                                 nearest even for bf16)                          */
+    float *dweight;           /* out [channels][width]                           */
+    float *dbias;             /* out [channels], or NULL                         */
+} bimamba_conv_grad;
+int bimamba_conv1d_bwd_workspace_size(const bimamba_conv_shape *s, int has_bwd, int nseq, size_t *bytes);
+/* cu_seqlens and nseq as in bimamba_conv1d. seqlen at most 2^30. xbc, dx, dB,
+ * dC and dxbc 16-byte aligned, workspace 256-byte aligned. Outputs must not
+ * overlap each other or an input; with no token the weights' gradients are 0. */
+int bimamba_conv1d_bwd(const bimamba_conv_shape *s, const bimamba_conv_grad *fwd, const bimamba_conv_grad *bwd,
+                       const int32_t *cu_seqlens, int nseq, void *workspace, size_t workspace_bytes,
+                       bimamba_stream stream);
+
+/* Gradient of bimamba_gated_norm. rows, channels, group_size, dtype, weight
+ * and eps as there.
+ *  y         float [rows][channels], or int8 with y_scale (8-bit checkpoint)
+ *  z         dtype [rows][channels], or int8 with z_scale
+ *  dout      dtype [rows][channels]
+ *  dy        out float [rows][channels] (bimamba_ssd_bwd's dy)
+ *  dz        out dtype [rows][channels]
+ *  dweight   out float [channels], or NULL if not wanted
+ * The workspace is needed with dweight only. Pointers 16-byte aligned (scales
+ * to one byte, dweight to 4), workspace 256-byte aligned; outputs must not
+ * overlap each other or an input. With no row dweight is 0. */
+int bimamba_gated_norm_bwd_workspace_size(long long rows, int channels, int group_size, int dtype, size_t *bytes);
+int bimamba_gated_norm_bwd(long long rows, int channels, int group_size, int dtype, const void *y,
+                           const uint8_t *y_scale, const void *z, const uint8_t *z_scale, const float *weight,
+                           float eps, const void *dout, float *dy, void *dz, float *dweight, void *workspace,
+                           size_t workspace_bytes, bimamba_stream stream);
+
+/* Layer norm of each row, optionally after a residual add:
+ *
+ *   h = x + residual,  out = (h - mean h) * rstd * weight + bias,
+ *   rstd = 1 / sqrt(mean (h - mean h)^2 + eps)
+ *
+ *  channels  8..16384
+ *  x         dtype [rows][channels]
+ *  residual  dtype [rows][channels], or NULL (h = x)
+ *  weight    float [channels], or NULL (1);  bias likewise, NULL: 0
+ *  out       dtype [rows][channels]
+ *  sum       dtype [rows][channels]: h rounded to the dtype, which is what the
+ *            norm then sees; with residual only (NULL without). May be x or
+ *            residual itself; no other overlap is allowed.
+ *  mean, rstd float [rows] for the gradient, or NULL
+ *  ckpt      NULL, or where to keep h in 8 bits (the same pass)
+ * Arrays are aligned to their elements. Computed in fp32. */
+int bimamba_layer_norm(long long rows, int channels, int dtype, const void *x, const void *residual,
+                       const float *weight, const float *bias, float eps, void *out, void *sum, float *mean,
+                       float *rstd, const bimamba_act8 *ckpt, bimamba_stream stream);
+/* Its gradient, with mean and rstd from the forward pass:
+ *  x         h: dtype [rows][channels], or int8 with x_scale (8-bit checkpoint)
+ *  dout      dtype [rows][channels]
+ *  dsum      dtype [rows][channels], the gradient that reaches h along the
+ *            residual stream, added to dx; or NULL
+ *  dx        out dtype [rows][channels], the gradient of x and of residual;
+ *            may be dsum itself, no other overlap is allowed
+ *  dweight, dbias  out float [channels], or NULL if not wanted
+ * The workspace is needed with dweight or dbias only (256-byte aligned). With
+ * no row dweight and dbias are 0. */
+int bimamba_layer_norm_bwd_workspace_size(long long rows, int channels, int dtype, size_t *bytes);
+int bimamba_layer_norm_bwd(long long rows, int channels, int dtype, const void *x, const uint8_t *x_scale,
+                           const float *mean, const float *rstd, const float *weight, const void *dout,
+                           const void *dsum, void *dx, float *dweight, float *dbias, void *workspace,
+                           size_t workspace_bytes, bimamba_stream stream);
+
 /* Per-kernel timing for benchmarks and profilers, per calling thread.
  * Between bimamba_profile_begin() and bimamba_profile_end(), every kernel the
  * library launches from this thread is bracketed by two hipEvents recorded on
