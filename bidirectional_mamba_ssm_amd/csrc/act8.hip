@@ -47,10 +47,9 @@ __global__ __launch_bounds__(kThreads) void k_act8(Act8Args a) {
             uint32_t top = 0;
 #pragma unroll
             for (int j = 0; j < V; ++j) top = max(top, abs_bits(v[j]));
-            const int e = (int)(block_max<LB>(top) >> 23);
-            int code[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) code[j] = act8_code(v[j], e);
+            top = block_max<LB>(top);
+            uint32_t code[V];
+            act8_codes<V>(v, top, code);
             if (n == V) {
                 Bytes<V>::store(a.q + at, Bytes<V>::pack(code));
             } else {
@@ -58,16 +57,14 @@ __global__ __launch_bounds__(kThreads) void k_act8(Act8Args a) {
                 for (int j = 0; j < V; ++j)
                     if (j < n) a.q[at + j] = (int8_t)code[j];
             }
-            if (in && l % LB == 0) a.scale[sat] = (uint8_t)e;
+            if (in && l % LB == 0) a.scale[sat] = (uint8_t)(top >> 23);
         } else {
             if (n == 0) continue;
             const float unit = act8_unit(a.scale[sat]);
             T *x = (T *)a.x + at;
             if (n == V) {
-                const typename Bytes<V>::type q = Bytes<V>::load(a.q + at);
                 float v[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) v[j] = (float)Bytes<V>::get(q, j) * unit;
+                Bytes<V>::values(Bytes<V>::load(a.q + at), unit, v);
                 L::store(x, L::pack(v));
             } else {
                 for (int j = 0; j < n; ++j) {

@@ -1025,7 +1025,7 @@ int bimamba_gated_norm_bwd_workspace_size(long long rows, int channels, int grou
     int rc = check_gated_norm(rows, channels, group_size, dtype);
     if (rc) return rc;
     if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
-    *bytes = (size_t)gated_norm_bwd_wgs(rows) * channels * 4;
+    *bytes = (size_t)gated_norm_bwd_wgs(rows, channels) * channels * 4;
     return BIMAMBA_OK;
 }
 
@@ -1044,7 +1044,7 @@ int bimamba_gated_norm_bwd(long long rows, int channels, int group_size, int dty
             return fail(BIMAMBA_EINVAL, "y, z, weight, dout, dy and dz must be 16-byte aligned");
     }
     if ((uintptr_t)dweight & 3u) return fail(BIMAMBA_EINVAL, "dweight must be 4-byte aligned");
-    const size_t need = dweight ? (size_t)gated_norm_bwd_wgs(rows) * channels * 4 : 0;
+    const size_t need = dweight ? (size_t)gated_norm_bwd_wgs(rows, channels) * channels * 4 : 0;
     if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
     EpiBwdArgs a;
     memset(&a, 0, sizeof a);
@@ -1106,7 +1106,7 @@ int bimamba_layer_norm_bwd_workspace_size(long long rows, int channels, int dtyp
     int rc = check_layer_norm(rows, channels, dtype);
     if (rc) return rc;
     if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
-    *bytes = (size_t)layer_norm_bwd_wgs(rows, channels) * 2 * channels * 4;
+    *bytes = (size_t)layer_norm_bwd_wgs(rows, channels, dtype == BIMAMBA_BF16) * 2 * channels * 4;
     return BIMAMBA_OK;
 }
 
@@ -1127,7 +1127,7 @@ int bimamba_layer_norm_bwd(long long rows, int channels, int dtype, const void *
     }
     if (((uintptr_t)weight | (uintptr_t)mean | (uintptr_t)rstd | (uintptr_t)dweight | (uintptr_t)dbias) & 3u)
         return fail(BIMAMBA_EINVAL, "weight, mean, rstd, dweight and dbias must be 4-byte aligned");
-    const size_t need = wgrad ? (size_t)layer_norm_bwd_wgs(rows, channels) * 2 * channels * 4 : 0;
+    const size_t need = wgrad ? (size_t)layer_norm_bwd_wgs(rows, channels, dtype == BIMAMBA_BF16) * 2 * channels * 4 : 0;
     if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
     LnBwdArgs a;
     memset(&a, 0, sizeof a);

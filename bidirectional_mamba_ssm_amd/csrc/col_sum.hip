@@ -5,33 +5,35 @@
 // workgroups does not show in the result's accuracy).
 //
 // Columns are [taps][channels], and [channels] more where there is a bias:
-// column (k, c) goes to w[c * taps + k], column (taps, c) to b[c]. A workgroup takes 64 columns, its 16 waves 16
-// interleaved slices of the rows, joined through LDS.
+// column (k, c) goes to w[c * taps + k], column (taps, c) to b[c]. A workgroup takes 32 columns (128-byte
+// runs of a row) and 32 interleaved slices of the rows, joined through LDS.
 #include "internal.hpp"
 
 namespace bm {
 namespace {
 
-constexpr int kSlices = 16;
+constexpr int kCols = 32, kSlices = 32;
 
 struct ColSums {
     ColSum set[2];
 };
 
-__global__ __launch_bounds__(64 * kSlices) void k_col_sum(ColSums all) {
+__global__ __launch_bounds__(kCols * kSlices) void k_col_sum(ColSums all) {
     const ColSum a = all.set[blockIdx.y];
-    __shared__ double part[kSlices][64];
-    const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
+    __shared__ double part[kSlices][kCols];
+    const int lane = threadIdx.x % kCols, slice = threadIdx.x / kCols;
     const long long cols = (long long)(a.taps + a.bias) * a.ch;
-    const long long col = (long long)blockIdx.x * 64 + lane;
+    const long long col = (long long)blockIdx.x * kCols + lane;
     double s = 0.0;
     if (col < cols) {
         const float *p = a.part + col;
         int r = slice;
-        for (; r + 3 * kSlices < a.n; r += 4 * kSlices) {
-            const float v0 = p[(size_t)r * cols], v1 = p[(size_t)(r + kSlices) * cols];
-            const float v2 = p[(size_t)(r + 2 * kSlices) * cols], v3 = p[(size_t)(r + 3 * kSlices) * cols];
-            s += ((double)v0 + (double)v1) + ((double)v2 + (double)v3);
+        for (; r + 7 * kSlices < a.n; r += 8 * kSlices) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = p[(size_t)(r + i * kSlices) * cols];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += (double)v[i];
         }
         for (; r < a.n; r += kSlices) s += (double)p[(size_t)r * cols];
     }
@@ -56,7 +58,8 @@ hipError_t launch_col_sum(const ColSum *sets, int nsets, hipStream_t s) {
     all.set[0] = sets[0];
     all.set[1] = sets[nsets - 1];
     const long long cols = (long long)(sets[0].taps + sets[0].bias) * sets[0].ch;
-    BM_LAUNCH("col_sum", k_col_sum, dim3((unsigned)((cols + 63) / 64), nsets), dim3(64 * kSlices), 0, s, all);
+    BM_LAUNCH("col_sum", k_col_sum, dim3((unsigned)((cols + kCols - 1) / kCols), nsets),
+              dim3(kCols * kSlices), 0, s, all);
     return hipGetLastError();
 }
 

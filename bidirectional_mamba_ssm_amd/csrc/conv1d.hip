@@ -75,14 +75,16 @@ __device__ __forceinline__ Pack<T, VEC> load_row(const ConvDirPtrs &d, const T *
     if constexpr (!Q8) {
         return *(const Pack<T, VEC> *)p;
     } else {
-        const Pack<int8_t, VEC> q = *(const Pack<int8_t, VEC> *)((const int8_t *)d.xbc + row * ch + c0);
+        const int8_t *q = (const int8_t *)d.xbc + row * ch + c0;
         const float unit = act8_unit(d.xscale[row * ((ch + 31) / 32) + c0 / 32]);
+        float v[VEC];
+        if constexpr (VEC == 4) values4(*(const uint32_t *)q, unit, v);
+        else v[0] = (float)*q * unit;
         Pack<T, VEC> o;
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-            const float v = (float)q.v[j] * unit;
-            if constexpr (sizeof(T) == 2) o.v[j] = (T)(__float_as_uint(v) >> 16);
-            else o.v[j] = v;
+            if constexpr (sizeof(T) == 2) o.v[j] = (T)(__float_as_uint(v[j]) >> 16);
+            else o.v[j] = v[j];
         }
         return o;
     }

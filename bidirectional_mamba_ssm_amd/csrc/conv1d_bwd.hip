@@ -58,7 +58,11 @@ template <typename T> struct In<T, true, 4> {
         r = *(const uint32_t *)((const int8_t *)p + row * ch + c);
         e = scale[row * nblk + c / 32];
     }
-    __device__ __forceinline__ float get(int j) const { return (float)Bytes<4>::get(r, j) * act8_unit(e); }
+    __device__ __forceinline__ float get(int j) const {
+        float v[4];
+        values4(r, act8_unit(e), v);
+        return v[j];
+    }
 };
 template <typename T> struct In<T, true, 1> {
     int r;

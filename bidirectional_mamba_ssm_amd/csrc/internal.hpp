@@ -172,7 +172,7 @@ struct LnBwdArgs {
     float *dw, *db;            // [C] or nullptr
     float *part;               // workspace, or nullptr with neither dw nor db
 };
-int layer_norm_bwd_wgs(long long rows, int C);
+int layer_norm_bwd_wgs(long long rows, int C, bool bf16);
 hipError_t launch_layer_norm_bwd(const LnBwdArgs &a, bool bf16, hipStream_t s);
 
 // gated_norm_bwd.hip
@@ -191,7 +191,7 @@ struct EpiBwdArgs {
     float *dw;                 // [C] or nullptr
     float *part;
 };
-int gated_norm_bwd_wgs(long long rows);
+int gated_norm_bwd_wgs(long long rows, int C);
 hipError_t launch_gated_norm_bwd(const EpiBwdArgs &a, bool bf16, hipStream_t s);
 
 // act8.hip

@@ -10,12 +10,15 @@
 // h may be read back from its 8-bit checkpoint (rows.hpp), which the forward
 // pass can write as it goes.
 //
-// Both are streams bounded by HBM. A row lives in the registers of 64 to 512
-// lanes (32 elements each at most, 16-byte vectors), so every array is
-// read or written once; the sums over a row are DPP lane moves, and LDS only
-// where a row has more than one wave. dw and db are summed in registers over
-// the rows a workgroup walks, then over the workgroups in a fixed order by a
-// second launch (col_sum.hip): no atomics, the same bits every time.
+// Both are streams bounded by HBM. A row lives in the registers of one wave
+// or of the waves of one workgroup, NV 16-byte vectors a lane, so every array
+// is read or written once; the next row's loads are under way while a row is
+// worked on. Sums over a row are DPP lane moves, and one exchange through LDS
+// where it has several waves: the forward pass sends each wave's mean and sum
+// of squares about it, which join exactly, so the variance is never a
+// difference of large numbers. dw and db are summed in registers over the rows
+// a workgroup walks, then over workgroups in a fixed order by a second launch
+// (col_sum.hip): no atomics, the same bits every time.
 //
 // The last vector of a row whose length is no multiple of it starts at C - V
 // instead: it overlaps its neighbour, its first `skip` elements count in no
@@ -26,118 +29,164 @@
 namespace bm {
 namespace {
 
-// sums of N values over the TPR lanes of a row; `part` has 2 * TPR/64 * N
-// floats, its halves used in turn (`flip`), so one barrier a sum is enough
-template <int TPR, int N>
-__device__ __forceinline__ void row_totals(float (&v)[N], float *part, int &flip) {
+constexpr int kMaxWaves = 8;   // of a row
+
+// Where a lane's vectors lie in a row of C channels shared by `waves` waves:
+// vector k starts at channel c[k]. has[k] is 0 for a lane past the end (it
+// reads the row's last vector again). In vector kt (-1: none) some lane's
+// first `skip` elements belong to the vector before.
+template <int V, int NV>
+struct Place {
+    int c[NV];
+    float has[NV];
+    int kt, skip;
+    float count;   // elements of this wave
+    __device__ __forceinline__ Place(int C, int t, int lanes) {
+        kt = C % V ? C / (V * lanes) : -1;
+        skip = 0;
+        int n = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = wave_total(v[i]);
-    if constexpr (TPR > 64) {
-        constexpr int NW = TPR / 64;
-        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-        float *p = part + flip * NW * N;
-        flip ^= 1;
-        if (lane == 0) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) p[wave * N + i] = v[i];
+        for (int k = 0; k < NV; ++k) {
+            const int at = (k * lanes + t) * V;
+            c[k] = min(at, C - V);
+            has[k] = at < C ? 1.f : 0.f;
+            if (at < C && at != c[k]) skip = at - c[k];
+            const int first = (k * lanes + (t & ~63)) * V;
+            n += max(0, min(64 * V, C - first));
         }
-        __syncthreads();
+        count = (float)n;
+    }
+    // v's element j of vector k counts: all do but the overlapped ones
+    __device__ __forceinline__ float own(int k, int j, float v) const { return k == kt && j < skip ? 0.f : v; }
+};
+
+template <int V>
+__device__ __forceinline__ void load_w(const float *p, int c, float none, float *v) {
+    if (p) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float s = 0.f;
+        for (int i = 0; i < V / 4; ++i) {
+            const rvec r = *(const u4_a4 *)(p + c + 4 * i);
 #pragma unroll
-            for (int w = 0; w < NW; ++w) s += p[w * N + i];
-            v[i] = s;
+            for (int j = 0; j < 4; ++j) v[4 * i + j] = __uint_as_float(r[j]);
         }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = none;
     }
 }
 
-// Where a lane's vectors lie in a row of C channels: vector k starts at
-// channel c[k]; its elements below skip[k] belong to the vector before
-// (V: the lane has none).
-template <int V, int NV, int TPR>
-struct Place {
-    int c[NV], skip[NV];
-    uint32_t full;   // bit k: every lane of the wave has all of vector k
-    __device__ __forceinline__ Place(int C) {
-        const int t = threadIdx.x & (TPR - 1);
-        full = 0;
+// The forward pass: one wave a row, kRows of them a workgroup, or MULTI: the
+// whole workgroup a row.
+constexpr int kRows = 4;
+
+template <typename T, int NV, bool MULTI, bool RES, bool CK>
+__global__ __launch_bounds__(MULTI ? 64 * kMaxWaves : 64 * kRows) void k_layer_norm(LnArgs a) {
+    using L = Lane<T>;
+    constexpr int V = L::V;
+    __shared__ float2 part[MULTI ? 2 : 1][MULTI ? kMaxWaves : 1];
+    const int C = a.C;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t = MULTI ? threadIdx.x : threadIdx.x & 63, lanes = MULTI ? blockDim.x : 64;
+    const Place<V, NV> at(C, t, lanes);
+    const float n = (float)C;
+    float w[NV][V], b[NV][V];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        load_w<V>(a.w, at.c[k], 1.f, w[k]);
+        load_w<V>(a.b, at.c[k], 0.f, b[k]);
+    }
+    const long long step = (long long)gridDim.x * (MULTI ? 1 : kRows);
+    long long row = (long long)blockIdx.x * (MULTI ? 1 : kRows) + (MULTI ? 0 : wave);
+    rvec nx[NV], nr[RES ? NV : 1];
+    auto fetch = [&](long long r) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int at = (k * TPR + t) * V;
-            c[k] = min(at, C - V);
-            skip[k] = min(at - c[k], V);
-            if (__all(skip[k] == 0)) full |= 1u << k;
+            nx[k] = L::load((const T *)a.x + r * C + at.c[k]);
+            if constexpr (RES) nr[k] = L::load((const T *)a.res + r * C + at.c[k]);
         }
-    }
-};
-
-template <typename T, int E, int TPR, bool RES, bool CK>
-__global__ __launch_bounds__(TPR > 64 ? TPR : 256) void k_layer_norm(LnArgs a) {
-    using L = Lane<T>;
-    constexpr int V = L::V, NV = E / V;
-    __shared__ float part[TPR > 64 ? 2 * TPR / 64 : 1];
-    const int C = a.C;
-    const Place<V, NV, TPR> at(C);
-    const int slot = TPR > 64 ? 0 : threadIdx.x >> 6;
-    constexpr int RPW = TPR > 64 ? 1 : 4;
-    const float n = (float)C;
-    int flip = 0;
-    for (long long row = (long long)blockIdx.x * RPW + slot; row < a.rows; row += (long long)gridDim.x * RPW) {
-        const T *x = (const T *)a.x + row * C;
+    };
+    constexpr bool kAhead = NV * V <= 16;   // wider lanes have no registers for it
+    if (kAhead && row < a.rows) fetch(row);
+    for (int flip = 0; row < a.rows; row += step, flip ^= 1) {
+        if (!kAhead) fetch(row);
         rvec r[NV];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) r[k] = L::load(x + at.c[k]);
-        if constexpr (RES) {
-            const T *s = (const T *)a.res + row * C;
-            rvec q[NV];
-#pragma unroll
-            for (int k = 0; k < NV; ++k) q[k] = L::load(s + at.c[k]);
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
+        for (int k = 0; k < NV; ++k) {
+            r[k] = nx[k];
+            if constexpr (RES) {
                 float h[V];
 #pragma unroll
-                for (int j = 0; j < V; ++j) h[j] = L::get(r[k], j) + L::get(q[k], j);
+                for (int j = 0; j < V; ++j) h[j] = L::get(nx[k], j) + L::get(nr[k], j);
                 r[k] = L::pack(h);   // the stream is kept in its dtype, and the norm sees what is kept
             }
         }
-        float m[1] = {0.f};
+        if (kAhead && row + step < a.rows) fetch(row + step);
+        float m = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (at.full >> k & 1) {
+            float s = 0.f;
 #pragma unroll
-                for (int j = 0; j < V; ++j) m[0] += L::get(r[k], j);
-            } else {
+            for (int j = 0; j < V; ++j) s += L::get(r[k], j);
+            if (k == at.kt) {
+                s = 0.f;
 #pragma unroll
-                for (int j = 0; j < V; ++j) m[0] += j >= at.skip[k] ? L::get(r[k], j) : 0.f;
+                for (int j = 0; j < V; ++j) s += at.own(k, j, L::get(r[k], j));
             }
+            m = fmaf(at.has[k], s, m);
         }
-        row_totals<TPR>(m, part, flip);
-        const float mean = m[0] / n;   // exact for a constant row whose sum is
-        float q[1] = {0.f};
+        // this wave's mean (exact for a constant row whose sum is) and squares about it
+        const float cnt = MULTI ? at.count : n;
+        float mean = wave_total(m) / fmaxf(cnt, 1.f);
+        float q = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
+            float s = 0.f;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float d = L::get(r[k], j) - mean;
-                const float dd = (at.full >> k & 1) || j >= at.skip[k] ? d : 0.f;
-                q[0] = fmaf(dd, dd, q[0]);
+                s = fmaf(d, d, s);
             }
+            if (k == at.kt) {
+                s = 0.f;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float d = at.own(k, j, L::get(r[k], j) - mean);
+                    s = fmaf(d, d, s);
+                }
+            }
+            q = fmaf(at.has[k], s, q);
         }
-        row_totals<TPR>(q, part, flip);
-        const float rstd = 1.0f / sqrtf(q[0] / n + a.eps);
+        q = wave_total(q);
+        if constexpr (MULTI) {
+            if ((t & 63) == 0) part[flip][wave] = make_float2(mean, q);
+            __syncthreads();
+            // lane i takes wave i's share; waves hold 64 V elements of each
+            // vector but where the row ends
+            const int i = t & 63, nw = lanes >> 6;
+            float mi = 0.f, qi = 0.f, ci = 0.f;
+            if (i < nw) {
+                const float2 p = part[flip][i];
+                mi = p.x;
+                qi = p.y;
+#pragma unroll
+                for (int k = 0; k < NV; ++k) ci += (float)max(0, min(64 * V, C - (k * lanes + 64 * i) * V));
+            }
+            mean = wave_total(ci * mi) / n;
+            const float d = mi - mean;
+            q = wave_total(fmaf(ci * d, d, qi));
+        }
+        const float rstd = 1.0f / sqrtf(q / n + a.eps);
         T *out = (T *)a.out + row * C;
         T *sum = (T *)a.sum + row * C;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const bool ok = at.skip[k] < V;
-            float o[V];
+            float h[V], o[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                o[j] = (L::get(r[k], j) - mean) * rstd;
-                if (a.w) o[j] *= a.w[at.c[k] + j];
-                if (a.b) o[j] += a.b[at.c[k] + j];
+                h[j] = L::get(r[k], j);
+                o[j] = fmaf((h[j] - mean) * rstd, w[k][j], b[k][j]);
             }
+            const bool ok = at.has[k] != 0.f;
             if (ok) {
                 L::store(out + at.c[k], L::pack(o));
                 if constexpr (RES) L::store(sum + at.c[k], r[k]);
@@ -145,183 +194,278 @@ __global__ __launch_bounds__(TPR > 64 ? TPR : 256) void k_layer_norm(LnArgs a) {
             if constexpr (CK) {
                 uint32_t top = 0;
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    top = max(top, j >= at.skip[k] ? abs_bits(L::get(r[k], j)) : 0u);
-                const int e = (int)(block_max<32 / V>(top) >> 23);
-                int8_t *cq = a.q + row * C;
-                int code[V];
+                for (int j = 0; j < V; ++j) top = max(top, abs_bits(h[j]));
+                if (k == at.kt) {
+                    top = 0;
 #pragma unroll
-                for (int j = 0; j < V; ++j) code[j] = act8_code(L::get(r[k], j), e);
-                if (at.skip[k] == 0) {
-                    Bytes<V>::store(cq + at.c[k], Bytes<V>::pack(code));
-                } else {
+                    for (int j = 0; j < V; ++j) top = max(top, abs_bits(at.own(k, j, h[j])));
+                }
+                top = block_max<32 / V>(ok ? top : 0u);
+                uint32_t code[V];
+                act8_codes<V>(h, top, code);
+                int8_t *cq = a.q + row * C + at.c[k];
+                const int skip = k == at.kt ? at.skip : 0;
+                if (ok && skip == 0) {
+                    Bytes<V>::store(cq, Bytes<V>::pack(code));
+                } else if (ok) {
                     // the overlapped elements may lie in another block
 #pragma unroll
                     for (int j = 0; j < V; ++j)
-                        if (j >= at.skip[k]) cq[at.c[k] + j] = (int8_t)code[j];
+                        if (j >= skip) cq[j] = (int8_t)code[j];
                 }
-                const int c0 = at.c[k] + at.skip[k];
-                if (ok && (c0 & 31) == 0) a.scale[row * ((C + 31) / 32) + c0 / 32] = (uint8_t)e;
+                const int c0 = at.c[k] + skip;
+                if (ok && (c0 & 31) == 0) a.scale[row * ((C + 31) / 32) + c0 / 32] = (uint8_t)(top >> 23);
             }
         }
-        if ((threadIdx.x & (TPR - 1)) == 0) {
+        if (t == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
     }
 }
 
-template <typename T, int E, int TPR, bool Q8, bool DSUM>
-__global__ __launch_bounds__(TPR > 64 ? TPR : 256) void k_layer_norm_bwd(LnBwdArgs a) {
+// The gradient's workgroups have kBwdWaves waves at least, so that few of them
+// (and few rows of partial sums) fill the chip: R rows at a time of W waves
+// each, MULTI if W > 1.
+constexpr int kBwdWaves = 8;
+
+template <typename T, int NV, bool MULTI, bool Q8, bool DSUM>
+__global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, int W, int R) {
     using L = Lane<T>;
-    constexpr int V = L::V, NV = E / V;
-    __shared__ float part[TPR > 64 ? 4 * TPR / 64 : 1];
+    constexpr int V = L::V, E = V * NV;
+    __shared__ float2 part[MULTI ? 2 : 1][MULTI ? kBwdWaves : 1];
+    // sums to join: W E 64 of dw and of db, where R > 1 (then W <= 4)
+    __shared__ float sum[E > 16 ? 1 : MULTI ? 2 * E * 256 : 2 * E * 64];
     const int C = a.C;
-    const Place<V, NV, TPR> at(C);
-    const int slot = TPR > 64 ? 0 : threadIdx.x >> 6;
-    constexpr int RPW = TPR > 64 ? 1 : 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int sub = MULTI ? wave / W : wave, lanes = MULTI ? 64 * W : 64;
+    const int t = threadIdx.x - sub * lanes;
+    const Place<V, NV> at(C, t, lanes);
     const float inv = 1.0f / (float)C;
     const int nblk = (C + 31) / 32;
-    int flip = 0;
     float w[NV][V], dw[NV][V], db[NV][V];
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+        load_w<V>(a.w, at.c[k], 1.f, w[k]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            w[k][j] = a.w ? a.w[at.c[k] + j] : 1.f;
-            dw[k][j] = db[k][j] = 0.f;
-        }
-    for (long long row = (long long)blockIdx.x * RPW + slot; row < a.rows; row += (long long)gridDim.x * RPW) {
-        const float mean = a.mean[row], rstd = a.rstd[row];
-        const T *dout = (const T *)a.dout + row * C;
-        const T *ds = (const T *)a.dsum + row * C;
+        for (int j = 0; j < V; ++j) dw[k][j] = db[k][j] = 0.f;
+    }
+    struct Row {
         rvec g[NV], s[DSUM ? NV : 1], x[Q8 ? 1 : NV];
         typename Bytes<V>::type q[Q8 ? NV : 1];
         uint32_t e[Q8 ? NV : 1];
+        float mean, rstd;
+    };
+    auto fetch = [&](Row &o, long long r) {
+        o.mean = a.mean[r];
+        o.rstd = a.rstd[r];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            g[k] = L::load(dout + at.c[k]);
+            o.g[k] = L::load((const T *)a.dout + r * C + at.c[k]);
             if constexpr (Q8) {
-                q[k] = Bytes<V>::load((const int8_t *)a.x + row * C + at.c[k]);
+                o.q[k] = Bytes<V>::load((const int8_t *)a.x + r * C + at.c[k]);
                 // the block of the lane's own elements; overlapped ones are not used
-                e[k] = a.xscale[row * nblk + min(at.c[k] + at.skip[k], C - 1) / 32];
+                o.e[k] = a.xscale[r * nblk + (at.c[k] + (k == at.kt ? at.skip : 0)) / 32];
             } else {
-                x[k] = L::load((const T *)a.x + row * C + at.c[k]);
+                o.x[k] = L::load((const T *)a.x + r * C + at.c[k]);
             }
-            if constexpr (DSUM) s[k] = L::load(ds + at.c[k]);
+            if constexpr (DSUM) o.s[k] = L::load((const T *)a.dsum + r * C + at.c[k]);
         }
-        auto xhat = [&](int k, int j) {
-            float v;
-            if constexpr (Q8) v = (float)Bytes<V>::get(q[k], j) * act8_unit(e[k]);
-            else v = L::get(x[k], j);
-            return (v - mean) * rstd;
-        };
-        float t[2] = {0.f, 0.f};
+    };
+    // all waves make the same turns (the barrier); one without a row reads the
+    // last one and uses nothing of it
+    const long long step = (long long)gridDim.x * R, last = a.rows - 1;
+    long long base = (long long)blockIdx.x * R;
+    constexpr bool kAhead = E <= 16;   // wider lanes have no registers for it
+    Row next;
+    if (kAhead) fetch(next, min(base + sub, last));
+    for (int flip = 0; base < a.rows; base += step, flip ^= 1) {
+        const long long row = base + sub;
+        const bool live = row < a.rows;
+        if (!MULTI && !live) break;
+        if (!kAhead) fetch(next, min(row, last));
+        const Row r = next;
+        if (kAhead) fetch(next, min(row + step, last));
+        float xh[NV][V];
+        float t1 = 0.f, t2 = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
+            if constexpr (Q8) {
+                Bytes<V>::values(r.q[k], act8_unit(r.e[k]), xh[k]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) xh[k][j] = L::get(r.x[k], j);
+            }
+            float s1 = 0.f, s2 = 0.f;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float d = L::get(g[k], j);
-                const float xh = xhat(k, j);
-                db[k][j] += d;
-                dw[k][j] = fmaf(d, xh, dw[k][j]);
-                const float gw = (at.full >> k & 1) || j >= at.skip[k] ? d * w[k][j] : 0.f;
-                t[0] += gw;
-                t[1] = fmaf(gw, xh, t[1]);
+                const float d = L::get(r.g[k], j);
+                xh[k][j] = (xh[k][j] - r.mean) * r.rstd;
+                if (!MULTI || live) {
+                    db[k][j] += d;
+                    dw[k][j] = fmaf(d, xh[k][j], dw[k][j]);
+                }
+                const float gw = d * w[k][j];
+                s1 += gw;
+                s2 = fmaf(gw, xh[k][j], s2);
             }
+            if (k == at.kt) {
+                s1 = s2 = 0.f;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float gw = at.own(k, j, L::get(r.g[k], j) * w[k][j]);
+                    s1 += gw;
+                    s2 = fmaf(gw, at.own(k, j, xh[k][j]), s2);
+                }
+            }
+            t1 = fmaf(at.has[k], s1, t1);
+            t2 = fmaf(at.has[k], s2, t2);
         }
-        row_totals<TPR>(t, part, flip);
-        const float m1 = t[0] * inv, m2 = t[1] * inv;
+        t1 = wave_total(t1);
+        t2 = wave_total(t2);
+        if constexpr (MULTI) {
+            if ((t & 63) == 0) part[flip][wave] = make_float2(t1, t2);
+            __syncthreads();
+            t1 = t2 = 0.f;
+            for (int i = 0; i < W; ++i) {
+                const float2 p = part[flip][sub * W + i];
+                t1 += p.x;
+                t2 += p.y;
+            }
+            if (!live) continue;
+        }
+        const float m1 = t1 * inv, m2 = t2 * inv;
         T *dx = (T *)a.dx + row * C;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             float o[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                o[j] = rstd * (fmaf(L::get(g[k], j), w[k][j], -m1) - xhat(k, j) * m2);
-                if constexpr (DSUM) o[j] += L::get(s[k], j);
+                const float d = fmaf(-xh[k][j], m2, fmaf(L::get(r.g[k], j), w[k][j], -m1));
+                if constexpr (DSUM) o[j] = fmaf(r.rstd, d, L::get(r.s[k], j));
+                else o[j] = r.rstd * d;
             }
-            if (Q8 ? at.skip[k] == 0 : at.skip[k] < V) {
-                L::store(dx + at.c[k], L::pack(o));
-            } else if (Q8 && at.skip[k] < V) {
-                const rvec p = L::pack(o);
+            if (at.has[k] == 0.f) continue;
+            const rvec p = L::pack(o);
+            const int skip = k == at.kt ? at.skip : 0;
+            if (!Q8 || skip == 0) {
+                L::store(dx + at.c[k], p);
+            } else {
+                // an overlapped element was decoded with another block's unit
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    if (j < at.skip[k]) continue;
-                    if constexpr (sizeof(T) == 2)
-                        dx[at.c[k] + j] = (T)(p[j >> 1] >> (16 * (j & 1)));
-                    else
-                        dx[at.c[k] + j] = __uint_as_float(p[j]);
+                    if (j < skip) continue;
+                    if constexpr (sizeof(T) == 2) dx[at.c[k] + j] = (T)(p[j >> 1] >> (16 * (j & 1)));
+                    else dx[at.c[k] + j] = __uint_as_float(p[j]);
                 }
             }
         }
     }
     if (!a.part) return;
-    // this workgroup's share of dw | db; several waves of one row each hold
-    // other channels, four waves of four rows the same ones (added in order)
+    // this workgroup's share of dw | db: the R rows' sums added in order
     float *out = a.part + (size_t)blockIdx.x * 2 * C;
-    if constexpr (TPR == 64) {
-        __shared__ float sum[2 * E * 64];
-        const int lane = threadIdx.x & 63;
-        for (int s = 0; s < 4; ++s) {
-            if (slot == s) {
+    if constexpr (E <= 16) {
+        for (int s = 0; s < R && R > 1; ++s) {
+            if (sub == s) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
-                        const int i = (k * V + j) * 64 + lane;
+                        float *p = sum + (k * V + j) * lanes + t, *q = p + E * lanes;
                         if (s > 0) {
-                            dw[k][j] += sum[i];
-                            db[k][j] += sum[E * 64 + i];
+                            dw[k][j] += *p;
+                            db[k][j] += *q;
                         }
-                        if (s < 3) {
-                            sum[i] = dw[k][j];
-                            sum[E * 64 + i] = db[k][j];
+                        if (s < R - 1) {
+                            *p = dw[k][j];
+                            *q = db[k][j];
                         }
                     }
             }
             __syncthreads();
         }
-        if (slot != 3) return;
+        if (sub != R - 1) return;
     }
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+        const int skip = k == at.kt ? at.skip : 0;
+        if (at.has[k] == 0.f) continue;
+        if (skip == 0) {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (j >= at.skip[k]) {
-                out[at.c[k] + j] = dw[k][j];
-                out[C + at.c[k] + j] = db[k][j];
+            for (int i = 0; i < V / 4; ++i) {
+                Lane<float>::store(out + at.c[k] + 4 * i, Lane<float>::pack(dw[k] + 4 * i));
+                Lane<float>::store(out + C + at.c[k] + 4 * i, Lane<float>::pack(db[k] + 4 * i));
             }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (j >= skip) {
+                    out[at.c[k] + j] = dw[k][j];
+                    out[C + at.c[k] + j] = db[k][j];
+                }
+        }
+    }
 }
 
-// lanes and elements per lane of a row: the fewest that hold it
-#define BM_ROW_FORMS(DO) DO(8, 64) DO(16, 64) DO(32, 64) DO(32, 128) DO(32, 256) DO(32, 512)
+// How a row is held: nv vectors a lane of `waves` waves. `lane` elements a lane
+// where that is enough, the fewest otherwise that kMaxWaves waves can do with.
+struct Form {
+    int nv, waves;
+};
+template <typename T>
+Form row_form(int C, int lane) {
+    const int V = 16 / (int)sizeof(T);
+    const int units = (C + 64 * V - 1) / (64 * V);          // vectors of a row, in waves
+    Form f;
+    f.nv = 1;
+    while (f.nv * V < lane && f.nv < units) f.nv *= 2;
+    while (f.nv * kMaxWaves < units) f.nv *= 2;
+    f.waves = (units + f.nv - 1) / f.nv;
+    return f;
+}
+template <typename T>
+Form bwd_form(int C) { return row_form<T>(C, 8); }
+inline int bwd_rows(const Form &f) { return f.waves >= kBwdWaves ? 1 : kBwdWaves / f.waves; }
+template <typename T>
+int bwd_wgs(long long rows, int C) {
+    const Form f = bwd_form<T>(C);
+    const int r = bwd_rows(f), most = f.nv * (16 / (int)sizeof(T)) > 8 ? 256 : 512;
+    const long long wgs = (rows + r - 1) / r;
+    return (int)(wgs < most ? wgs : most);
+}
 
 template <typename T, bool RES, bool CK>
 hipError_t launch_fwd(const LnArgs &a, hipStream_t s) {
-#define DO(E, TPR)                                                                              \
-    if (a.C <= E * TPR) {                                                                       \
-        const long long per = TPR > 64 ? 1 : 4, wgs = (a.rows + per - 1) / per;                  \
-        const dim3 grid((unsigned)(wgs < 4096 ? wgs : 4096));                                    \
-        BM_LAUNCH("layer_norm", (k_layer_norm<T, E, TPR, RES, CK>), grid,                        \
-                  dim3(TPR > 64 ? TPR : 256), 0, s, a);                                          \
-        return hipGetLastError();                                                               \
+    const Form f = row_form<T>(a.C, 16);
+    const bool multi = f.waves > 1;
+    const long long per = multi ? 1 : kRows, wgs = (a.rows + per - 1) / per;
+    const dim3 grid((unsigned)(wgs < 2048 ? wgs : 2048)), block(multi ? 64 * f.waves : 64 * kRows);
+#define GO(NV)                                                                                              \
+    if (f.nv == NV) {                                                                                       \
+        if (multi) BM_LAUNCH("layer_norm", (k_layer_norm<T, NV, true, RES, CK>), grid, block, 0, s, a);       \
+        else BM_LAUNCH("layer_norm", (k_layer_norm<T, NV, false, RES, CK>), grid, block, 0, s, a);            \
+        return hipGetLastError();                                                                           \
     }
-    BM_ROW_FORMS(DO)
-#undef DO
+    GO(1) GO(2) GO(4)
+    if constexpr (sizeof(T) == 4) { GO(8) }
+#undef GO
     return hipErrorInvalidValue;
 }
 
 template <typename T, bool Q8, bool DSUM>
-hipError_t launch_b(const LnBwdArgs &a, int wgs, hipStream_t s) {
-#define DO(E, TPR)                                                                              \
-    if (a.C <= E * TPR) {                                                                       \
-        BM_LAUNCH("layer_norm_bwd", (k_layer_norm_bwd<T, E, TPR, Q8, DSUM>), dim3((unsigned)wgs),  \
-                  dim3(TPR > 64 ? TPR : 256), 0, s, a);                                          \
-        return hipGetLastError();                                                               \
+hipError_t launch_b(const LnBwdArgs &a, hipStream_t s) {
+    const Form f = bwd_form<T>(a.C);
+    const int R = bwd_rows(f);
+    const dim3 grid((unsigned)bwd_wgs<T>(a.rows, a.C)), block(64 * f.waves * R);
+#define GO(NV, MULTI)                                                                                    \
+    if (f.nv == NV && (f.waves > 1) == MULTI) {                                                          \
+        BM_LAUNCH("layer_norm_bwd", (k_layer_norm_bwd<T, NV, MULTI, Q8, DSUM>), grid, block, 0, s, a,      \
+                  f.waves, R);                                                                           \
+        return hipGetLastError();                                                                        \
     }
-    BM_ROW_FORMS(DO)
-#undef DO
+    GO(1, false) GO(2, true) GO(4, true)
+    if constexpr (sizeof(T) == 4) { GO(2, false) GO(8, true) } else { GO(1, true) }
+#undef GO
     return hipErrorInvalidValue;
 }
 
@@ -331,9 +475,9 @@ hipError_t launch_fwd_t(const LnArgs &a, hipStream_t s) {
     return a.q ? launch_fwd<T, false, true>(a, s) : launch_fwd<T, false, false>(a, s);
 }
 template <typename T>
-hipError_t launch_b_t(const LnBwdArgs &a, int wgs, hipStream_t s) {
-    if (a.xscale) return a.dsum ? launch_b<T, true, true>(a, wgs, s) : launch_b<T, true, false>(a, wgs, s);
-    return a.dsum ? launch_b<T, false, true>(a, wgs, s) : launch_b<T, false, false>(a, wgs, s);
+hipError_t launch_b_t(const LnBwdArgs &a, hipStream_t s) {
+    if (a.xscale) return a.dsum ? launch_b<T, true, true>(a, s) : launch_b<T, true, false>(a, s);
+    return a.dsum ? launch_b<T, false, true>(a, s) : launch_b<T, false, false>(a, s);
 }
 
 }  // namespace
@@ -344,19 +488,17 @@ hipError_t launch_layer_norm(const LnArgs &a, bool bf16, hipStream_t s) {
 }
 
 // workgroups of the gradient: each leaves one row of 2 C partial sums
-int layer_norm_bwd_wgs(long long rows, int C) {
-    const long long per = C > 2048 ? 1 : 4, wgs = (rows + per - 1) / per;
-    return (int)(wgs < 512 ? wgs : 512);
+int layer_norm_bwd_wgs(long long rows, int C, bool bf16) {
+    return bf16 ? bwd_wgs<uint16_t>(rows, C) : bwd_wgs<float>(rows, C);
 }
 
 hipError_t launch_layer_norm_bwd(const LnBwdArgs &a, bool bf16, hipStream_t s) {
-    const int wgs = layer_norm_bwd_wgs(a.rows, a.C);
     if (a.rows > 0) {
-        hipError_t e = bf16 ? launch_b_t<uint16_t>(a, wgs, s) : launch_b_t<float>(a, wgs, s);
+        hipError_t e = bf16 ? launch_b_t<uint16_t>(a, s) : launch_b_t<float>(a, s);
         if (e != hipSuccess) return e;
     }
     if (!a.dw && !a.db) return hipSuccess;
-    const ColSum c{a.part, wgs, a.C, 1, 1, a.dw, a.db};
+    const ColSum c{a.part, layer_norm_bwd_wgs(a.rows, a.C, bf16), a.C, 1, 1, a.dw, a.db};
     return launch_col_sum(&c, 1, s);
 }
 

@@ -63,33 +63,37 @@ template <> struct Lane<float> {
     __device__ __forceinline__ static void store(float *p, rvec r) { *(u4_a4 *)p = r; }
 };
 
+// the low bytes of four words
+__device__ __forceinline__ uint32_t bytes4(const uint32_t *q) {
+    const uint32_t lo = __builtin_amdgcn_perm(q[1], q[0], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(q[3], q[2], 0x04000c0cu);
+    return lo | hi;
+}
+// q unit of four signed bytes (a sign-extending byte select and conversion,
+// one instruction, and a product)
+__device__ __forceinline__ void values4(uint32_t r, float unit, float *v) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = (float)(int8_t)(r >> (8 * j)) * unit;
+}
+
 // V bytes of an 8-bit checkpoint
 template <int V> struct Bytes;
 template <> struct Bytes<8> {
     typedef uint32_t type __attribute__((ext_vector_type(2)));
     __device__ __forceinline__ static type load(const int8_t *p) { return *(const u2_a1 *)p; }
     __device__ __forceinline__ static void store(int8_t *p, type r) { *(u2_a1 *)p = r; }
-    __device__ __forceinline__ static int get(type r, int j) {
-        return (int)(r[j >> 2] << (24 - 8 * (j & 3))) >> 24;
-    }
-    __device__ __forceinline__ static type pack(const int *q) {
-        type r;
-        r[0] = (uint32_t)(q[0] & 255) | (uint32_t)(q[1] & 255) << 8 | (uint32_t)(q[2] & 255) << 16 |
-               (uint32_t)q[3] << 24;
-        r[1] = (uint32_t)(q[4] & 255) | (uint32_t)(q[5] & 255) << 8 | (uint32_t)(q[6] & 255) << 16 |
-               (uint32_t)q[7] << 24;
-        return r;
+    __device__ __forceinline__ static type pack(const uint32_t *q) { return type{bytes4(q), bytes4(q + 4)}; }
+    __device__ __forceinline__ static void values(type r, float unit, float *v) {
+        values4(r[0], unit, v);
+        values4(r[1], unit, v + 4);
     }
 };
 template <> struct Bytes<4> {
     typedef uint32_t type;
     __device__ __forceinline__ static type load(const int8_t *p) { return *(const u1_a1 *)p; }
     __device__ __forceinline__ static void store(int8_t *p, type r) { *(u1_a1 *)p = r; }
-    __device__ __forceinline__ static int get(type r, int j) { return (int)(r << (24 - 8 * j)) >> 24; }
-    __device__ __forceinline__ static type pack(const int *q) {
-        return (uint32_t)(q[0] & 255) | (uint32_t)(q[1] & 255) << 8 | (uint32_t)(q[2] & 255) << 16 |
-               (uint32_t)q[3] << 24;
-    }
+    __device__ __forceinline__ static type pack(const uint32_t *q) { return bytes4(q); }
+    __device__ __forceinline__ static void values(type r, float unit, float *v) { values4(r, unit, v); }
 };
 
 // 2^(e-133) for a block's exponent field e; NaN for 255. 2^(e-127) is the
@@ -100,14 +104,34 @@ __device__ __forceinline__ float act8_unit(uint32_t e) {
     const uint32_t top = (e == 0 || e == 255) ? 0x00400000u : 0u;
     return __uint_as_float((e << 23) | top) * 0.015625f;
 }
-// the integer kept for v in a block of exponent field e (0 in a NaN block)
-__device__ __forceinline__ int act8_code(float v, int e) {
-    const float m = rintf(__builtin_ldexpf(v, 133 - e));
-    const int q = (int)fminf(fmaxf(m, -127.f), 127.f);
-    return e == 255 ? 0 : q;
+// The integers kept for V values of a block whose largest magnitude has the
+// bits `top`, in the low bytes of code[]. 1.5 2^23 + m holds round(m), ties to
+// even, in its low bits, so one fma scales and rounds. Its factor 2^(133-E)
+// overflows for E < 6, below 2^-121: there (but for zeros, whose factor does
+// not matter) the scaling is a separate, also exact, step.
+template <int V>
+__device__ __forceinline__ void act8_codes(const float *v, uint32_t top, uint32_t *code) {
+    constexpr float kInt = 12582912.f;
+    const int e = (int)(top >> 23);
+    const bool far = e < 6 && top != 0;
+    const float s = __uint_as_float((uint32_t)(133 - max(e, 6) + 127) << 23);
+    if (__any(far)) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float m = far ? __builtin_ldexpf(v[j], 133 - e) + kInt : fmaf(v[j], s, kInt);
+            code[j] = __float_as_uint(fminf(fmaxf(m, kInt - 127.f), kInt + 127.f));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            code[j] = __float_as_uint(__builtin_amdgcn_fmed3f(fmaf(v[j], s, kInt), kInt - 127.f, kInt + 127.f));
+    }
+    if (__any(e == 255)) {   // a NaN block holds zeros
+#pragma unroll
+        for (int j = 0; j < V; ++j) code[j] = e == 255 ? 0u : code[j];
+    }
 }
-// exponent field of the largest of V magnitudes (bit patterns order as the
-// magnitudes do, infinities and NaN above all)
+// bits of a magnitude: they order as magnitudes do, infinities and NaN above all
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 template <int CTRL, int ROW = 0xf, int BANK = 0xf, bool BOUND = true>
