@@ -255,7 +255,7 @@ int check_gated_norm(long long rows, int channels, int group_size, int dtype) {
     return BIMAMBA_OK;
 }
 
-int check_conv_bwd_shape(const bimamba_conv_shape *s) {
+int check_conv_train_shape(const bimamba_conv_shape *s) {
     int rc = check_conv_shape(s);
     if (rc) return rc;
     // a run's positions, rounded up to its workgroup, are counted in int32
@@ -901,14 +901,13 @@ int bimamba_conv1d_act8(const bimamba_conv_shape *s, const bimamba_conv_dir *fwd
                         const bimamba_act8 *xbc_fwd, const bimamba_conv_dir *bwd,
                         const bimamba_act8 *xbc_bwd, const int32_t *cu_seqlens, int nseq,
                         void *workspace, size_t workspace_bytes, bimamba_stream stream) {
-    int rc = check_conv_shape(s);
+    int rc = check_conv_train_shape(s);
     if (rc) return rc;
     const bool empty = s->seqlen == 0;
     const bimamba_conv_dir *dirs[2] = {fwd, bwd};
     const bimamba_act8 *kept[2] = {xbc_fwd, xbc_bwd};
-    ConvArgs a;
+    ConvAct8Args a;
     memset(&a, 0, sizeof a);
-    ConvDirPtrs *ptrs[2] = {&a.fwd, &a.bwd};
     for (int i = 0; i < (bwd ? 2 : 1); ++i) {
         const char *name = i ? "reverse" : "forward";
         if (!dirs[i]) return fail(BIMAMBA_EINVAL, "%s direction is NULL", name);
@@ -917,13 +916,13 @@ int bimamba_conv1d_act8(const bimamba_conv_shape *s, const bimamba_conv_dir *fwd
         bimamba_conv_dir d = *dirs[i];
         d.xbc = kept[i]->q;
         if ((rc = check_conv_dir(&d, name, empty))) return rc;
-        ptrs[i]->xbc = d.xbc;
-        ptrs[i]->xscale = (const uint8_t *)kept[i]->scale;
-        ptrs[i]->weight = d.weight;
-        ptrs[i]->bias = d.bias;
-        ptrs[i]->x = d.x;
-        ptrs[i]->B = d.B;
-        ptrs[i]->C = d.C;
+        a.dir[i].q = (const int8_t *)kept[i]->q;
+        a.dir[i].scale = (const uint8_t *)kept[i]->scale;
+        a.dir[i].weight = d.weight;
+        a.dir[i].bias = d.bias;
+        a.dir[i].x = d.x;
+        a.dir[i].B = d.B;
+        a.dir[i].C = d.C;
     }
     if (!bwd && xbc_bwd) return fail(BIMAMBA_EINVAL, "a reverse checkpoint is given without the reverse direction");
     if (cu_seqlens) {
@@ -950,13 +949,13 @@ int bimamba_conv1d_act8(const bimamba_conv_shape *s, const bimamba_conv_dir *fwd
             return hip_fail(e, "building sequence index");
         a.seq = seq;
     }
-    if ((e = launch_conv(a, s->dtype == BIMAMBA_BF16, st)) != hipSuccess)
+    if ((e = launch_conv_act8(a, s->dtype == BIMAMBA_BF16, st)) != hipSuccess)
         return hip_fail(e, "launching conv1d");
     return BIMAMBA_OK;
 }
 
 int bimamba_conv1d_bwd_workspace_size(const bimamba_conv_shape *s, int has_bwd, int nseq, size_t *bytes) {
-    int rc = check_conv_bwd_shape(s);
+    int rc = check_conv_train_shape(s);
     if (rc) return rc;
     if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
     if (nseq < 0) return fail(BIMAMBA_EINVAL, "nseq %d < 0", nseq);
@@ -968,7 +967,7 @@ int bimamba_conv1d_bwd_workspace_size(const bimamba_conv_shape *s, int has_bwd, 
 int bimamba_conv1d_bwd(const bimamba_conv_shape *s, const bimamba_conv_grad *fwd, const bimamba_conv_grad *bwd,
                        const int32_t *cu_seqlens, int nseq, void *workspace, size_t workspace_bytes,
                        bimamba_stream stream) {
-    int rc = check_conv_bwd_shape(s);
+    int rc = check_conv_train_shape(s);
     if (rc) return rc;
     const bool empty = s->seqlen == 0;
     if ((rc = check_conv_grad(fwd, "forward", empty))) return rc;

@@ -19,8 +19,8 @@
 // No LDS, no barriers (except one when the context is updated in place).
 // Channel vectors never straddle the x | B | C boundaries, so each lane
 // writes one output array with vector stores.
+#include "common.hpp"
 #include "internal.hpp"
-#include "rows.hpp"
 
 namespace bm {
 namespace {
@@ -68,30 +68,8 @@ __device__ __forceinline__ float silu(float v) {
     return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
 }
 
-// VEC channels from c0 of one row of the input (at p). From an 8-bit checkpoint (rows.hpp)
-// they are decoded to T as they come in, which is exact for both types.
-template <typename T, int VEC, bool Q8>
-__device__ __forceinline__ Pack<T, VEC> load_row(const ConvDirPtrs &d, const T *p, long long row, int ch, int c0) {
-    if constexpr (!Q8) {
-        return *(const Pack<T, VEC> *)p;
-    } else {
-        const int8_t *q = (const int8_t *)d.xbc + row * ch + c0;
-        const float unit = act8_unit(d.xscale[row * ((ch + 31) / 32) + c0 / 32]);
-        float v[VEC];
-        if constexpr (VEC == 4) values4(*(const uint32_t *)q, unit, v);
-        else v[0] = (float)*q * unit;
-        Pack<T, VEC> o;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-            if constexpr (sizeof(T) == 2) o.v[j] = (T)(__float_as_uint(v[j]) >> 16);
-            else o.v[j] = v[j];
-        }
-        return o;
-    }
-}
-
 // One direction (REV: the reverse stream) of batch row b.
-template <typename T, int VEC, int W, bool PACKED, int kTok, bool REV, bool Q8>
+template <typename T, int VEC, int W, bool PACKED, int kTok, bool REV>
 __device__ __forceinline__ void conv_dir(const ConvArgs &a, int b) {
     using P = Pack<T, VEC>;
     constexpr int R = kTok + W - 1;          // rows held per lane
@@ -136,13 +114,13 @@ __device__ __forceinline__ void conv_dir(const ConvArgs &a, int b) {
         if (base >= 0 && base + R <= a.L) {
             // interior run: every row exists, all loads issued back to back
 #pragma unroll
-            for (int i = 0; i < R; ++i) raw[i] = load_row<T, VEC, Q8>(d, prow + (long long)i * a.ch, (long long)row0 + base + i, a.ch, c0);
+            for (int i = 0; i < R; ++i) raw[i] = *(const P *)(prow + (long long)i * a.ch);
         } else {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int r = base + i;
                 if (r >= 0 && r < a.L) {
-                    raw[i] = load_row<T, VEC, Q8>(d, prow + (long long)i * a.ch, (long long)row0 + r, a.ch, c0);
+                    raw[i] = *(const P *)(prow + (long long)i * a.ch);
                 } else if (r < 0 && a.init) {
                     raw[i] = *(const P *)((const T *)a.init +
                                           ((size_t)b * (W - 1) + (W - 1) + r) * a.ch + c0);
@@ -212,48 +190,43 @@ __device__ __forceinline__ void conv_dir(const ConvArgs &a, int b) {
 
 // kTok: tokens per wave (16 for long rows; 8 for small problems, where the
 // grid would not fill the chip and the per-wave chain is the latency)
-template <typename T, int VEC, int W, bool PACKED, int kTok, bool Q8>
+template <typename T, int VEC, int W, bool PACKED, int kTok>
 __global__ __launch_bounds__(64 * kWaves) void k_conv(ConvArgs a) {
     const int dir = (int)(blockIdx.z % (unsigned)a.ndir);
     const int b = (int)(blockIdx.z / (unsigned)a.ndir);
     if (dir == 1)
-        conv_dir<T, VEC, W, PACKED, kTok, true, Q8>(a, b);
+        conv_dir<T, VEC, W, PACKED, kTok, true>(a, b);
     else
-        conv_dir<T, VEC, W, PACKED, kTok, false, Q8>(a, b);
+        conv_dir<T, VEC, W, PACKED, kTok, false>(a, b);
 }
 
-template <typename T, int VEC, int W, int TOK, bool Q8>
+template <typename T, int VEC, int W, int TOK>
 hipError_t launch_t(const ConvArgs &a, hipStream_t s) {
     const int tiles = (a.L + TOK * kWaves - 1) / (TOK * kWaves);
     // in place: one workgroup per (row, channel slab) walks the row in order,
     // so the initial context is read before the final one is written
     const dim3 grid(a.inplace ? 1 : tiles, (a.nvec + 63) / 64, a.batch * a.ndir);
     if (a.seq)
-        BM_LAUNCH("conv1d_packed", (k_conv<T, VEC, W, true, TOK, Q8>), grid, dim3(64, kWaves), 0, s, a);
+        BM_LAUNCH("conv1d_packed", (k_conv<T, VEC, W, true, TOK>), grid, dim3(64, kWaves), 0, s, a);
     else
-        BM_LAUNCH("conv1d", (k_conv<T, VEC, W, false, TOK, Q8>), grid, dim3(64, kWaves), 0, s, a);
+        BM_LAUNCH("conv1d", (k_conv<T, VEC, W, false, TOK>), grid, dim3(64, kWaves), 0, s, a);
     return hipGetLastError();
 }
 
-template <typename T, int VEC, int W, bool Q8>
+template <typename T, int VEC, int W>
 hipError_t launch_w(const ConvArgs &a, hipStream_t s) {
-    return (long long)a.batch * a.L <= 4096 ? launch_t<T, VEC, W, 8, Q8>(a, s)
-                                             : launch_t<T, VEC, W, 16, Q8>(a, s);
-}
-
-template <typename T, int VEC, bool Q8>
-hipError_t launch_q(const ConvArgs &a, hipStream_t s) {
-    switch (a.W) {
-        case 2: return launch_w<T, VEC, 2, Q8>(a, s);
-        case 3: return launch_w<T, VEC, 3, Q8>(a, s);
-        case 4: return launch_w<T, VEC, 4, Q8>(a, s);
-    }
-    return hipErrorInvalidValue;
+    return (long long)a.batch * a.L <= 4096 ? launch_t<T, VEC, W, 8>(a, s)
+                                             : launch_t<T, VEC, W, 16>(a, s);
 }
 
 template <typename T, int VEC>
 hipError_t launch_v(const ConvArgs &a, hipStream_t s) {
-    return a.fwd.xscale ? launch_q<T, VEC, true>(a, s) : launch_q<T, VEC, false>(a, s);
+    switch (a.W) {
+        case 2: return launch_w<T, VEC, 2>(a, s);
+        case 3: return launch_w<T, VEC, 3>(a, s);
+        case 4: return launch_w<T, VEC, 4>(a, s);
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace

@@ -16,6 +16,8 @@
 // of a workgroup take adjacent runs. Rows are loaded kBatch positions ahead.
 // dw and db stay in the lane's registers over the run, are joined over the
 // workgroup through LDS and over workgroups by col_sum.hip.
+#include <type_traits>
+
 #include "internal.hpp"
 #include "rows.hpp"
 
@@ -34,15 +36,19 @@ template <> struct In<float, false, 4> {
     __device__ __forceinline__ void load(const void *p, const uint8_t *, size_t row, int ch, int, int c) {
         r = *(const rvec *)((const float *)p + row * ch + c);
     }
-    __device__ __forceinline__ float get(int j) const { return __uint_as_float(r[j]); }
+    __device__ __forceinline__ void values(float *v) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(r[j]);
+    }
 };
 template <> struct In<uint16_t, false, 4> {
     w2 r;
     __device__ __forceinline__ void load(const void *p, const uint8_t *, size_t row, int ch, int, int c) {
         r = *(const w2 *)((const uint16_t *)p + row * ch + c);
     }
-    __device__ __forceinline__ float get(int j) const {
-        return __uint_as_float((j & 1) ? (r[j >> 1] & 0xffff0000u) : (r[j >> 1] << 16));
+    __device__ __forceinline__ void values(float *v) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __uint_as_float((j & 1) ? (r[j >> 1] & 0xffff0000u) : (r[j >> 1] << 16));
     }
 };
 template <typename T> struct In<T, false, 1> {
@@ -50,7 +56,7 @@ template <typename T> struct In<T, false, 1> {
     __device__ __forceinline__ void load(const void *p, const uint8_t *, size_t row, int ch, int, int c) {
         r = ((const T *)p)[row * ch + c];
     }
-    __device__ __forceinline__ float get(int) const { return Elem<T>::load(&r, 0); }
+    __device__ __forceinline__ void values(float *v) const { v[0] = Elem<T>::load(&r, 0); }
 };
 template <typename T> struct In<T, true, 4> {
     uint32_t r, e;
@@ -58,11 +64,7 @@ template <typename T> struct In<T, true, 4> {
         r = *(const uint32_t *)((const int8_t *)p + row * ch + c);
         e = scale[row * nblk + c / 32];
     }
-    __device__ __forceinline__ float get(int j) const {
-        float v[4];
-        values4(r, act8_unit(e), v);
-        return v[j];
-    }
+    __device__ __forceinline__ void values(float *v) const { values4(r, act8_unit(e), v); }
 };
 template <typename T> struct In<T, true, 1> {
     int r;
@@ -71,7 +73,7 @@ template <typename T> struct In<T, true, 1> {
         r = ((const int8_t *)p)[row * ch + c];
         e = scale[row * nblk + c / 32];
     }
-    __device__ __forceinline__ float get(int) const { return (float)r * act8_unit(e); }
+    __device__ __forceinline__ void values(float *v) const { v[0] = (float)r * act8_unit(e); }
 };
 
 template <int VEC>
@@ -107,9 +109,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvBwdArgs a) {
     __shared__ float join[kWaves][VEC * (W + 1)][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // workgroup -> (row and direction, tile of runs, channel slab)
-    const int slab = blockIdx.x % a.slabs;
-    const int rest = blockIdx.x / a.slabs;
+    // workgroup -> (row and direction, tile of runs, channel slab). Workgroups
+    // go round robin over the 8 XCDs; each takes one stretch of the work, so
+    // that adjacent tiles meet in one L2.
+    const int per = (int)((gridDim.x + 7) / 8);
+    const int work = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+    if (work >= a.wgs) return;
+    const int slab = work % a.slabs;
+    const int rest = work / a.slabs;
     const int tile = rest % a.tiles, unit = rest / a.tiles;
     const bool rev = unit % a.ndir != 0;
     const int b = unit / a.ndir;
@@ -147,49 +154,67 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvBwdArgs a) {
 
     if (p0 < L) {
         float win[N][VEC], du[N][VEC];
-        int sid[N];
         In<T, Q8, VEC> next[kBatch];
         float gnext[kBatch][VEC];
-        int snext[kBatch];
         auto fetch = [&](int p) {
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const int t = token(min(p + i, L - 1));   // positions past the end: masked when used
+                const int t = token(min(p + i, L - 1));   // positions past the end: zeroed when used
                 next[i].load(d.xbc, d.xscale, row0 + t, ch, nblk, c0);
                 load_grad<VEC>(g + (row0 + t) * gs, gnext[i]);
-                if constexpr (PACKED) snext[i] = a.seq[t];
             }
+        };
+        // packed: bit m tells that position p0 - H + m is a sequence's first
+        uint64_t starts[2] = {0, 0};
+        if constexpr (PACKED) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int p = p0 - H + 64 * h + lane;
+                const bool in = p > 0 && p < L;
+                const int t = token(in ? p : 0), u = token(in ? p - 1 : 0);
+                starts[h] = __ballot(in && a.seq[t] != a.seq[u]);
+            }
+        }
+        // the bits of the window of the batch from p
+        auto window = [&](int p) -> uint32_t {
+            if constexpr (!PACKED) return 0u;
+            const int m = p - p0;
+            const uint64_t w = m >= 64 ? starts[1] >> (m - 64)
+                                       : starts[0] >> m | (m ? starts[1] << (64 - m) : 0);
+            return (uint32_t)w & ((1u << N) - 1);
         };
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             const int p = p0 - H + i;
             In<T, Q8, VEC> v;
             v.load(d.xbc, d.xscale, row0 + token(max(p, 0)), ch, nblk, c0);
+            v.values(win[i]);
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
-                win[i][j] = p >= 0 ? v.get(j) : 0.f;
+                if (p < 0) win[i][j] = 0.f;
                 du[i][j] = 0.f;
             }
-            if constexpr (PACKED) sid[i] = p >= 0 ? a.seq[token(p)] : -1;
         }
-        fetch(p0);
-        for (int p = p0; p < p1 + H; p += kBatch) {
+        // kBatch positions from p. EDGE: some of them lie past the run's or the
+        // row's end, some outputs before the run, or sequences meet (`first`);
+        // elsewhere nothing is asked.
+        auto batch = [&](int p, auto edge, uint32_t first) {
+            constexpr bool EDGE = decltype(edge)::value;
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const bool live = p + i < L;
+                next[i].values(win[H + i]);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
-                    win[H + i][j] = live ? next[i].get(j) : 0.f;
-                    du[H + i][j] = live ? gnext[i][j] : 0.f;
+                    du[H + i][j] = gnext[i][j];
+                    // a row past the end was read from the last one
+                    if (EDGE && p + i >= L) win[H + i][j] = 0.f;
                 }
-                if constexpr (PACKED) sid[H + i] = live ? snext[i] : -1;
             }
-            if (p + kBatch < p1 + H) fetch(p + kBatch);
+            if (!EDGE || p + kBatch < p1 + H) fetch(p + kBatch);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const bool own = p + i < p1;
+                const bool own = !EDGE || p + i < p1, live = !EDGE || p + i < L;
                 const int s = p + i - H;
-                const bool out = s >= p0 && s < p1;
                 float o[VEC];
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
@@ -197,13 +222,16 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvBwdArgs a) {
                     float u = bias[j];
 #pragma unroll
                     for (int k = 0; k < W; ++k) {
-                        tap[k] = !PACKED || sid[i + k] == sid[i + H] ? win[i + k][j] : 0.f;
+                        // no start among window positions i + k + 1 .. i + H
+                        const bool same = !PACKED || !EDGE || !(first >> (i + k + 1) & ((1u << (H - k)) - 1));
+                        tap[k] = same ? win[i + k][j] : 0.f;
                         u = fmaf(w[j][k], tap[k], u);
                     }
                     const float sg = __builtin_amdgcn_rcpf(1.0f + __expf(-u));
-                    const float slope = a.act ? sg * fmaf(u, 1.0f - sg, 1.0f) : 1.0f;
+                    const float slope = sg * fmaf(u, 1.0f - sg, 1.0f);
+                    float v = du[H + i][j] * (a.act ? slope : 1.0f);
                     // a position past the end has no gradient, whatever its slope
-                    const float v = p + i < L ? du[H + i][j] * slope : 0.f;
+                    if (!live) v = 0.f;
                     du[H + i][j] = v;
                     const float m = own ? v : 0.f;
                     ab[j] += m;
@@ -211,21 +239,35 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvBwdArgs a) {
                     for (int k = 0; k < W; ++k) aw[j][k] = fmaf(m, tap[k], aw[j][k]);
                     o[j] = 0.f;
 #pragma unroll
-                    for (int k = 0; k < W; ++k)
-                        o[j] = fmaf(w[j][H - k], !PACKED || sid[i + k] == sid[i] ? du[i + k][j] : 0.f, o[j]);
+                    for (int k = 0; k < W; ++k) {
+                        // no start among window positions i + 1 .. i + k
+                        const bool same = !PACKED || !EDGE || !(first >> (i + 1) & ((1u << k) - 1));
+                        o[j] = fmaf(w[j][H - k], same ? du[i + k][j] : 0.f, o[j]);
+                    }
                 }
-                if (out && chan_ok) store_in<VEC>((T *)d.dxbc + (row0 + token(s)) * ch + c0, o);
+                // lanes past the last channel vector hold its very values
+                if (!EDGE || (s >= p0 && s < p1))
+                    store_in<VEC>((T *)d.dxbc + (row0 + token(s)) * ch + c0, o);
             }
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
+            for (int i = 0; i < H; ++i)
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
                     win[i][j] = win[kBatch + i][j];
                     du[i][j] = du[kBatch + i][j];
                 }
-                if constexpr (PACKED) sid[i] = sid[kBatch + i];
-            }
-        }
+        };
+        fetch(p0);
+        int p = p0;
+        do {
+            batch(p, std::true_type(), window(p));
+            p += kBatch;
+            // Loads and stores share a counter. With everything arrived here,
+            // each turn of the inner loop waits for the loads of the turn
+            // before and leaves that turn's stores, which come after them, alone.
+            __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
+            for (; p + kBatch <= p1 && window(p) == 0; p += kBatch) batch(p, std::false_type(), 0u);
+        } while (p < p1 + H);
     }
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
@@ -250,7 +292,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvBwdArgs a) {
 
 template <typename T, bool Q8, int VEC, int W>
 hipError_t launch_w(const ConvBwdArgs &a, hipStream_t s) {
-    const dim3 grid((unsigned)((long long)a.slabs * a.tiles * a.batch * a.ndir));
+    const dim3 grid((unsigned)((a.wgs + 7) / 8 * 8));
     if (a.seq) BM_LAUNCH("conv1d_bwd_packed", (k_conv_bwd<T, Q8, VEC, W, true>), grid, dim3(64 * kWaves), 0, s, a);
     else BM_LAUNCH("conv1d_bwd", (k_conv_bwd<T, Q8, VEC, W, false>), grid, dim3(64 * kWaves), 0, s, a);
     return hipGetLastError();
@@ -273,7 +315,7 @@ hipError_t launch_t(const ConvBwdArgs &a, bool vec, hipStream_t s) {
 // positions a wave walks: long runs repeat few halo rows, short ones give
 // the chip enough waves
 int run_length(int batch, int L, int slabs, int ndir) {
-    int run = 64;
+    int run = 32;
     while (run > 16 && (long long)((L + run - 1) / run) * slabs * batch * ndir < 2048) run /= 2;
     return run;
 }
@@ -295,6 +337,7 @@ hipError_t launch_conv_bwd(ConvBwdArgs a, bool bf16, hipStream_t s) {
     a.slabs = slabs_of(a.hp, a.gn, &a.nvec);
     a.run = run_length(a.batch, a.L, a.slabs, a.ndir);
     a.tiles = tiles_of(a.L, a.run);
+    a.wgs = a.slabs * a.tiles * a.batch * a.ndir;
     if (a.L > 0) {
         const bool vec = conv_vectorized(bf16, a.hp, a.gn);
         hipError_t e = bf16 ? launch_t<uint16_t>(a, vec, s) : launch_t<float>(a, vec, s);

@@ -118,8 +118,7 @@ hipError_t launch_gated_norm(const EpiArgs &a, bool bf16, hipStream_t s);
 
 // conv1d.hip: short depthwise convolution of the x | B | C channels
 struct ConvDirPtrs {
-    const void *xbc;           // [batch][L][ch], int8 with xscale
-    const uint8_t *xscale;     // [batch][L][(ch + 31) / 32] or nullptr (both directions alike)
+    const void *xbc;           // [batch][L][ch]
     const float *weight;       // [ch][W]
     const float *bias;         // [ch] or nullptr
     void *x, *B, *C;           // outputs [batch][L][hp], [batch][L][gn] x2
@@ -203,6 +202,21 @@ struct Act8Args {
 };
 hipError_t launch_act8(Act8Args a, bool bf16, bool pack, hipStream_t s);
 
+// conv1d_act8.hip: the short convolution from 8-bit checkpoints
+struct ConvAct8Dir {
+    const int8_t *q;           // [batch][L][ch]
+    const uint8_t *scale;      // [batch][L][(ch + 31) / 32]
+    const float *weight, *bias;
+    void *x, *B, *C;           // outputs, as in ConvDirPtrs
+};
+struct ConvAct8Args {
+    ConvAct8Dir dir[2];
+    int batch, L, hp, gn, ch, W, ndir, act;
+    int nvec, slabs, tiles, run, wgs;   // set by launch_conv_act8
+    const int32_t *seq;
+};
+hipError_t launch_conv_act8(ConvAct8Args a, bool bf16, hipStream_t s);
+
 // conv1d_bwd.hip: gradient of the short convolution
 struct ConvBwdDir {
     const void *xbc;           // [batch][L][ch] dtype, or int8 with xscale
@@ -216,7 +230,7 @@ struct ConvBwdDir {
 struct ConvBwdArgs {
     ConvBwdDir dir[2];
     int batch, L, hp, gn, ch, W, ndir, act;
-    int nvec, slabs, tiles, run;   // set by launch_conv_bwd
+    int nvec, slabs, tiles, run, wgs;   // set by launch_conv_bwd
     const int32_t *seq;
 };
 size_t conv_bwd_part(int batch, int L, int hp, int gn, int W, int ndir);   // floats per direction

@@ -439,7 +439,8 @@ hipError_t launch_fwd(const LnArgs &a, hipStream_t s) {
     const Form f = row_form<T>(a.C, 16);
     const bool multi = f.waves > 1;
     const long long per = multi ? 1 : kRows, wgs = (a.rows + per - 1) / per;
-    const dim3 grid((unsigned)(wgs < 2048 ? wgs : 2048)), block(multi ? 64 * f.waves : 64 * kRows);
+    // two rows (or kRows pairs) a workgroup, more only if that leaves too few
+    const dim3 grid((unsigned)(wgs < 2048 ? wgs : wgs < 4096 ? 2048 : (wgs + 1) / 2)), block(multi ? 64 * f.waves : 64 * kRows);
 #define GO(NV)                                                                                              \
     if (f.nv == NV) {                                                                                       \
         if (multi) BM_LAUNCH("layer_norm", (k_layer_norm<T, NV, true, RES, CK>), grid, block, 0, s, a);       \
