@@ -5,8 +5,8 @@ only marshals torch tensors (device memory and the current stream) into the
 C ABI declared in include/bimamba.h. It has no compute path of its own and
 raises if the library is not built.
 """
-import contextlib
 import ctypes
+import functools
 import math
 
 import torch
@@ -34,6 +34,9 @@ def _ptr(t):
 def _check(t, name, shape, dtype, device):
     """The library sees plain pointers: every tensor's device, dtype, shape and
     layout is checked here, before anything is launched."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous() \
+            and t.device == device:
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -560,30 +563,60 @@ def gated_norm(y, z, weight, group_size=None, eps=1e-5, out=None, stream=None):
     return out
 
 
+# The calls of the training steps are short next to their own overhead, so
+# they take the current stream's handle and device without the objects that
+# torch.cuda makes of them, and pass addresses as plain integers.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _elsewhere(dev, stream):
+    """Whether a call has to run under _on() first."""
+    return stream is not None or dev.index != _current_device()
+
+
 def _on(dev, stream):
-    """The context a call runs in: its tensors' device current, and the given
-    stream too, so that what the call allocates belongs to that stream."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
+    """The context of a call on another stream than the current one, or on
+    tensors of another device than the current one: both are made current, so
+    that what the call allocates belongs to the stream it is used on."""
+    if stream is None:
         return torch.cuda.device(dev)
-    return contextlib.nullcontext()
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
 
 
-def _out(t, name, shape, dtype, dev):
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _out(t, name, shape, dtype, dev, like=None):
+    """The caller's output, checked, or a new one; like: a tensor of just that
+    kind, which is the quicker way to one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty_like(like) if like is not None else torch.empty(shape, dtype=dtype, device=dev)
     _check(t, name, shape, dtype, dev)
     return t
 
 
-def _workspace(query, dev):
+@functools.lru_cache(maxsize=4096)
+def _size(query, *sizes):
+    """What a workspace query (an entry point's name) says of plain sizes."""
     n = ctypes.c_size_t(0)
-    _abi.check(query(ctypes.byref(n)))
-    ws = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
-    return ws, n.value
+    _abi.check(getattr(lib(), query)(*sizes, ctypes.byref(n)))
+    return n.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _conv_size(query, shape, *sizes):
+    n = ctypes.c_size_t(0)
+    _abi.check(getattr(lib(), query)(ctypes.byref(_abi.ConvShape(*shape)), *sizes, ctypes.byref(n)))
+    return n.value
+
+
+def _workspace(nbytes, dev):
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
 
 
 def _offsets(cu_seqlens):
@@ -619,55 +652,73 @@ class Act8:
         return Act8(torch.empty(shape, dtype=torch.int8, device=device),
                     torch.empty(shape[:-1] + ((shape[-1] + 31) // 32,), dtype=torch.uint8, device=device))
 
+    def _checked(self, name, shape, dev):
+        """The addresses of q and scale."""
+        _check(self.q, name + ".q", shape, torch.int8, dev)
+        _check(self.scale, name + ".scale", shape[:-1] + ((shape[-1] + 31) // 32,), torch.uint8, dev)
+        return self.q.data_ptr(), self.scale.data_ptr()
+
     def _ptrs(self, name, shape, dev):
-        shape = tuple(shape)
-        _check(self.q, f"{name}.q", shape, torch.int8, dev)
-        _check(self.scale, f"{name}.scale", shape[:-1] + ((shape[-1] + 31) // 32,), torch.uint8, dev)
-        return _abi.Act8Ptrs(self.q.data_ptr(), self.scale.data_ptr())
+        return _abi.Act8Ptrs(*self._checked(name, tuple(shape), dev))
 
 
 def _rows(shape):
     """(rows, channels) of [..., channels]."""
-    if not len(shape) or not shape[-1]:
+    if not shape or not shape[-1]:
         raise ValueError(f"shape {tuple(shape)} has no channels")
     return math.prod(shape[:-1]), shape[-1]
 
 
 def _kept(t, name, shape, dtype, dev):
-    """(data, scale) pointers of a tensor or of its 8-bit checkpoint."""
+    """The addresses (data, scale) of a tensor (scale None) or of its 8-bit
+    checkpoint."""
     if isinstance(t, Act8):
-        p = t._ptrs(name, shape, dev)
-        return ctypes.c_void_p(p.q), ctypes.c_void_p(p.scale)
-    _check(t, name, tuple(shape), dtype, dev)
-    return _ptr(t), None
+        return t._checked(name, shape, dev)
+    _check(t, name, shape, dtype, dev)
+    return t.data_ptr(), None
+
+
+def _dtype_code(dtype):
+    code = DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
 
 
 def act8_pack(x, out=None, stream=None):
     """x [..., C] (bf16 or fp32) as an 8-bit checkpoint (bimamba_act8_pack).
     out: an Act8 to write. Returns the Act8."""
     dev = _cuda_device(x)
-    if x.dtype not in DTYPES:
-        raise TypeError(f"unsupported dtype {x.dtype}")
-    _check(x, "x", tuple(x.shape), x.dtype, dev)
-    rows, C = _rows(x.shape)
-    with _on(dev, stream):
-        if out is None:
-            out = Act8.empty(x.shape, dev)
-        p = out._ptrs("out", x.shape, dev)
-        _abi.check(lib().bimamba_act8_pack(rows, C, DTYPES[x.dtype], _ptr(x), ctypes.byref(p), _stream(stream)))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return act8_pack(x, out)
+    code, shape = _dtype_code(x.dtype), tuple(x.shape)
+    _check(x, "x", shape, x.dtype, dev)
+    rows, C = _rows(shape)
+    if out is None:
+        out = Act8.empty(shape, dev)
+        p = _abi.Act8Ptrs(out.q.data_ptr(), out.scale.data_ptr())
+    else:
+        p = out._ptrs("out", shape, dev)
+    rc = lib().bimamba_act8_pack(rows, C, code, x.data_ptr(), ctypes.byref(p), _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
     return out
 
 
 def act8_unpack(a, dtype=torch.bfloat16, out=None, stream=None):
     """The values an Act8 stands for, as bf16 or fp32 (bimamba_act8_unpack)."""
     dev = _cuda_device(a)
-    if dtype not in DTYPES:
-        raise TypeError(f"unsupported dtype {dtype}")
-    p = a._ptrs("a", a.shape, dev)
-    rows, C = _rows(a.shape)
-    with _on(dev, stream):
-        out = _out(out, "out", tuple(a.shape), dtype, dev)
-        _abi.check(lib().bimamba_act8_unpack(rows, C, DTYPES[dtype], ctypes.byref(p), _ptr(out), _stream(stream)))
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return act8_unpack(a, dtype, out)
+    code, shape = _dtype_code(dtype), tuple(a.shape)
+    rows, C = _rows(shape)
+    p = a._ptrs("a", shape, dev)
+    out = _out(out, "out", shape, dtype, dev)
+    rc = lib().bimamba_act8_unpack(rows, C, code, ctypes.byref(p), out.data_ptr(), _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
     return out
 
 
@@ -682,31 +733,34 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, checkpoint=Fa
     dict: out, sum (h; x itself without a residual), mean and rstd (float32
     [...], for layer_norm_bwd), ckpt (Act8 or None)."""
     dev = _cuda_device(x)
-    if x.dtype not in DTYPES:
-        raise TypeError(f"unsupported dtype {x.dtype}")
-    shape = tuple(x.shape)
-    _check(x, "x", shape, x.dtype, dev)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return layer_norm(x, weight, bias, residual, eps, checkpoint, out, sum_out)
+    dt, shape = x.dtype, tuple(x.shape)
+    code = _dtype_code(dt)
+    _check(x, "x", shape, dt, dev)
     rows, C = _rows(shape)
     if residual is not None:
-        _check(residual, "residual", shape, x.dtype, dev)
+        _check(residual, "residual", shape, dt, dev)
     elif sum_out is not None:
         raise ValueError("sum_out goes with a residual")
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is not None:
-            _check(t, name, (C,), torch.float32, dev)
-    with _on(dev, stream):
-        out = _out(out, "out", shape, x.dtype, dev)
-        if residual is not None:
-            sum_out = _out(sum_out, "sum_out", shape, x.dtype, dev)
-        stats = torch.empty((2,) + shape[:-1], dtype=torch.float32, device=dev)
-        mean, rstd = stats[0], stats[1]
-        ckpt = None
-        if checkpoint is not False and checkpoint is not None:
-            ckpt = Act8.empty(shape, dev) if checkpoint is True else checkpoint
-        p = ckpt._ptrs("checkpoint", shape, dev) if ckpt is not None else None
-        _abi.check(lib().bimamba_layer_norm(
-            rows, C, DTYPES[x.dtype], _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), float(eps), _ptr(out),
-            _ptr(sum_out), _ptr(mean), _ptr(rstd), ctypes.byref(p) if p is not None else None, _stream(stream)))
+    if weight is not None:
+        _check(weight, "weight", (C,), torch.float32, dev)
+    if bias is not None:
+        _check(bias, "bias", (C,), torch.float32, dev)
+    out = _out(out, "out", shape, dt, dev, x)
+    if residual is not None:
+        sum_out = _out(sum_out, "sum_out", shape, dt, dev, x)
+    mean, rstd = torch.empty((2,) + shape[:-1], dtype=torch.float32, device=dev).unbind(0)
+    ckpt = p = None
+    if checkpoint is not False and checkpoint is not None:
+        ckpt = Act8.empty(shape, dev) if checkpoint is True else checkpoint
+        p = ctypes.byref(ckpt._ptrs("checkpoint", shape, dev))
+    rc = lib().bimamba_layer_norm(
+        rows, C, code, x.data_ptr(), _adr(residual), _adr(weight), _adr(bias), eps, out.data_ptr(), _adr(sum_out),
+        mean.data_ptr(), rstd.data_ptr(), p, _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
     return dict(out=out, sum=x if residual is None else sum_out, mean=mean, rstd=rstd, ckpt=ckpt)
 
 
@@ -718,10 +772,11 @@ def layer_norm_bwd(dout, x, mean, rstd, weight=None, dsum=None, wgrad=True, dx=N
     dx in dout's dtype (the gradient of x and of residual), the other two
     float32 [C], None with wgrad=False."""
     dev = _cuda_device(dout)
-    dt = dout.dtype
-    if dt not in DTYPES:
-        raise TypeError(f"unsupported dtype {dt}")
-    shape = tuple(dout.shape)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return layer_norm_bwd(dout, x, mean, rstd, weight, dsum, wgrad, dx)
+    dt, shape = dout.dtype, tuple(dout.shape)
+    code = _dtype_code(dt)
     _check(dout, "dout", shape, dt, dev)
     rows, C = _rows(shape)
     xp, xs = _kept(x, "x", shape, dt, dev)
@@ -731,18 +786,18 @@ def layer_norm_bwd(dout, x, mean, rstd, weight=None, dsum=None, wgrad=True, dx=N
         _check(weight, "weight", (C,), torch.float32, dev)
     if dsum is not None:
         _check(dsum, "dsum", shape, dt, dev)
-    with _on(dev, stream):
-        dx = _out(dx, "dx", shape, dt, dev)
-        dw = db = ws = None
-        nbytes = 0
-        if wgrad:
-            dw = torch.empty(C, dtype=torch.float32, device=dev)
-            db = torch.empty(C, dtype=torch.float32, device=dev)
-            ws, nbytes = _workspace(
-                lambda n: lib().bimamba_layer_norm_bwd_workspace_size(rows, C, DTYPES[dt], n), dev)
-        _abi.check(lib().bimamba_layer_norm_bwd(
-            rows, C, DTYPES[dt], xp, xs, _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dout), _ptr(dsum), _ptr(dx),
-            _ptr(dw), _ptr(db), _ptr(ws), nbytes, _stream(stream)))
+    dx = _out(dx, "dx", shape, dt, dev, dout)
+    dw = db = ws = None
+    nbytes = 0
+    if wgrad:
+        dw, db = torch.empty((2, C), dtype=torch.float32, device=dev).unbind(0)
+        nbytes = _size("bimamba_layer_norm_bwd_workspace_size", rows, C, code)
+        ws = _workspace(nbytes, dev)
+    rc = lib().bimamba_layer_norm_bwd(
+        rows, C, code, xp, xs, mean.data_ptr(), rstd.data_ptr(), _adr(weight), dout.data_ptr(), _adr(dsum),
+        dx.data_ptr(), _adr(dw), _adr(db), _adr(ws), nbytes, _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
     return dx, dw, db
 
 
@@ -751,74 +806,80 @@ def gated_norm_bwd(dout, y, z, weight, group_size=None, eps=1e-5, wgrad=True, dy
     dtype, y float32 and z [..., C] (each the tensor or its Act8 checkpoint).
     Returns (dy float32, dz in dout's dtype, dweight float32 [C] or None)."""
     dev = _cuda_device(dout)
-    dt = dout.dtype
-    if dt not in DTYPES:
-        raise TypeError(f"unsupported dtype {dt}")
-    shape = tuple(dout.shape)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return gated_norm_bwd(dout, y, z, weight, group_size, eps, wgrad, dy, dz)
+    dt, shape = dout.dtype, tuple(dout.shape)
+    code = _dtype_code(dt)
     _check(dout, "dout", shape, dt, dev)
     rows, C = _rows(shape)
     gs = C if group_size is None else int(group_size)
     yp, ys = _kept(y, "y", shape, torch.float32, dev)
     zp, zs = _kept(z, "z", shape, dt, dev)
     _check(weight, "weight", (C,), torch.float32, dev)
-    with _on(dev, stream):
-        dy = _out(dy, "dy", shape, torch.float32, dev)
-        dz = _out(dz, "dz", shape, dt, dev)
-        dw = ws = None
-        nbytes = 0
-        if wgrad:
-            dw = torch.empty(C, dtype=torch.float32, device=dev)
-            ws, nbytes = _workspace(
-                lambda n: lib().bimamba_gated_norm_bwd_workspace_size(rows, C, gs, DTYPES[dt], n), dev)
-        _abi.check(lib().bimamba_gated_norm_bwd(
-            rows, C, gs, DTYPES[dt], yp, ys, zp, zs, _ptr(weight), float(eps), _ptr(dout), _ptr(dy), _ptr(dz),
-            _ptr(dw), _ptr(ws), nbytes, _stream(stream)))
+    dy = _out(dy, "dy", shape, torch.float32, dev)
+    dz = _out(dz, "dz", shape, dt, dev, dout)
+    dw = ws = None
+    nbytes = 0
+    if wgrad:
+        dw = torch.empty(C, dtype=torch.float32, device=dev)
+        nbytes = _size("bimamba_gated_norm_bwd_workspace_size", rows, C, gs, code)
+        ws = _workspace(nbytes, dev)
+    rc = lib().bimamba_gated_norm_bwd(
+        rows, C, gs, code, yp, ys, zp, zs, weight.data_ptr(), eps, dout.data_ptr(), dy.data_ptr(), dz.data_ptr(),
+        _adr(dw), _adr(ws), nbytes, _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
     return dy, dz, dw
 
 
-def _conv_dims(d, dims, dtype):
-    """(batch, L, ch, W) of a direction whose xbc is a tensor or an Act8."""
-    xbc, w = d["xbc"], d["weight"]
-    if len(xbc.shape) != 3 or w.dim() != 2:
+def _conv_plan(xbc, weight, dims, activation, dtype):
+    """The plain sizes of a bimamba_conv_shape, for an xbc that is a tensor or
+    an Act8."""
+    if len(xbc.shape) != 3 or weight.dim() != 2:
         raise ValueError("xbc must be [batch, L, channels] and weight [channels, width]")
     batch, L, ch = xbc.shape
-    if ch != conv_channels(*dims):
+    H, P, G, N = dims
+    if ch != conv_channels(H, P, G, N):
         raise ValueError(f"xbc has {ch} channels, expected nheads*headdim + 2*ngroups*d_state")
-    if dtype not in DTYPES:
-        raise TypeError(f"unsupported dtype {dtype}")
-    return batch, L, ch, w.shape[1]
+    code = _dtype_code(dtype)
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation {activation!r} is not one of {sorted(map(str, ACTIVATIONS))}")
+    return (batch, L, H, P, N, G, weight.shape[1], code, ACTIVATIONS[activation], 0), ch
 
 
 def _conv1d_act8(fwd, bwd, dims, activation, cu_seqlens, out, dtype, stream):
-    dev = _cuda_device(fwd["xbc"])
-    batch, L, ch, W = _conv_dims(fwd, dims, dtype)
+    xbc = fwd["xbc"]
+    dev = _cuda_device(xbc)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return _conv1d_act8(fwd, bwd, dims, activation, cu_seqlens, out, dtype, None)
+    sizes, ch = _conv_plan(xbc, fwd["weight"], dims, activation, dtype)
+    batch, L, W = sizes[0], sizes[1], sizes[6]
     H, P, G, N = dims
-    if activation not in ACTIVATIONS:
-        raise ValueError(f"activation {activation!r} is not one of {sorted(map(str, ACTIVATIONS))}")
-    outs = list(out) if out is not None else [None, None]
-    shape = _abi.ConvShape(batch, L, H, P, N, G, W, DTYPES[dtype], ACTIVATIONS[activation], 0)
+    outs = out if out is not None else (None, None)
     cu_arr, nseq = _offsets(cu_seqlens)
-    with _on(dev, stream):
-        res, args = [None, None], []
-        for i, (d, name) in enumerate(((fwd, "fwd"), (bwd, "bwd"))):
-            if d is None:
-                args += [None, None]
-                continue
-            if not isinstance(d["xbc"], Act8):
-                raise TypeError("both directions' xbc must be Act8, or neither")
-            p = d["xbc"]._ptrs(f"{name}.xbc", (batch, L, ch), dev)
-            _check(d["weight"], f"{name}.weight", (ch, W), torch.float32, dev)
-            bias = d.get("bias")
-            if bias is not None:
-                _check(bias, f"{name}.bias", (ch,), torch.float32, dev)
-            o = res[i] = _conv_out(outs[i], batch, L, H, P, G, N, dtype, dev, name)
-            args += [_abi.ConvDir(None, d["weight"].data_ptr(), bias.data_ptr() if bias is not None else None,
-                                  o["x"].data_ptr(), o["B"].data_ptr(), o["C"].data_ptr()), p]
-        ws, nbytes = _workspace(
-            lambda n: lib().bimamba_conv1d_workspace_size(ctypes.byref(shape), nseq, n), dev)
-        _abi.check(lib().bimamba_conv1d_act8(
-            ctypes.byref(shape), *[ctypes.byref(v) if v is not None else None for v in args], cu_arr, nseq,
-            _ptr(ws), nbytes, _stream(stream)))
+    res, args = [None, None], [None, None, None, None]
+    for i, (d, name) in enumerate(((fwd, "fwd"), (bwd, "bwd"))):
+        if d is None:
+            continue
+        if not isinstance(d["xbc"], Act8):
+            raise TypeError("both directions' xbc must be Act8, or neither")
+        q, scale = d["xbc"]._checked(name + ".xbc", (batch, L, ch), dev)
+        _check(d["weight"], name + ".weight", (ch, W), torch.float32, dev)
+        bias = d.get("bias")
+        if bias is not None:
+            _check(bias, name + ".bias", (ch,), torch.float32, dev)
+        o = res[i] = _conv_out(outs[i], batch, L, H, P, G, N, dtype, dev, name)
+        args[2 * i] = ctypes.byref(_abi.ConvDir(None, d["weight"].data_ptr(), _adr(bias), o["x"].data_ptr(),
+                                                o["B"].data_ptr(), o["C"].data_ptr()))
+        args[2 * i + 1] = ctypes.byref(_abi.Act8Ptrs(q, scale))
+    nbytes = _conv_size("bimamba_conv1d_workspace_size", sizes, nseq) if nseq else 0
+    ws = _workspace(nbytes, dev)
+    rc = lib().bimamba_conv1d_act8(ctypes.byref(_abi.ConvShape(*sizes)), *args, cu_arr, nseq, _adr(ws), nbytes,
+                                   _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
     return res[0], res[1]
 
 
@@ -837,47 +898,50 @@ def conv1d_bwd(fwd, bwd, gfwd, gbwd, nheads, headdim, ngroups, d_state, activati
     not given."""
     xbc = fwd["xbc"]
     dev = _cuda_device(xbc)
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return conv1d_bwd(fwd, bwd, gfwd, gbwd, nheads, headdim, ngroups, d_state, activation, cu_seqlens, out,
+                              None, dtype)
     q8 = isinstance(xbc, Act8)
     if dtype is None:
         dtype = torch.bfloat16 if q8 else xbc.dtype
     elif not q8 and dtype != xbc.dtype:
         raise TypeError(f"dtype {dtype} is not xbc's {xbc.dtype}")
     H, P, G, N = nheads, headdim, ngroups, d_state
-    batch, L, ch, W = _conv_dims(fwd, (H, P, G, N), dtype)
-    if activation not in ACTIVATIONS:
-        raise ValueError(f"activation {activation!r} is not one of {sorted(map(str, ACTIVATIONS))}")
+    sizes, ch = _conv_plan(xbc, fwd["weight"], (H, P, G, N), activation, dtype)
+    batch, L, W = sizes[0], sizes[1], sizes[6]
     if (bwd is None) != (gbwd is None):
         raise ValueError("bwd and gbwd come together")
-    shape = _abi.ConvShape(batch, L, H, P, N, G, W, DTYPES[dtype], ACTIVATIONS[activation], 0)
     cu_arr, nseq = _offsets(cu_seqlens)
-    outs = list(out) if out is not None else [None, None]
-    with _on(dev, stream):
-        res, args = [None, None], [None, None]
-        for i, (d, g, name) in enumerate(((fwd, gfwd, "fwd"), (bwd, gbwd, "bwd"))):
-            if d is None:
-                continue
-            if isinstance(d["xbc"], Act8) != q8:
-                raise TypeError("both directions' xbc must be Act8, or neither")
-            xp, xs = _kept(d["xbc"], f"{name}.xbc", (batch, L, ch), dtype, dev)
-            _check(d["weight"], f"{name}.weight", (ch, W), torch.float32, dev)
-            bias = d.get("bias")
-            if bias is not None:
-                _check(bias, f"{name}.bias", (ch,), torch.float32, dev)
-            _check(g["x"], f"{name}_grad.x", (batch, L, H, P), torch.float32, dev)
-            _check(g["B"], f"{name}_grad.B", (batch, L, G, N), torch.float32, dev)
-            _check(g["C"], f"{name}_grad.C", (batch, L, G, N), torch.float32, dev)
-            dxbc = _out(outs[i], f"{name}_out", (batch, L, ch), dtype, dev)
-            dw = torch.empty(ch, W, dtype=torch.float32, device=dev)
-            db = torch.empty(ch, dtype=torch.float32, device=dev) if bias is not None else None
-            res[i] = dict(xbc=dxbc, weight=dw, bias=db)
-            args[i] = _abi.ConvGrad(xp, xs, _ptr(d["weight"]), _ptr(bias), _ptr(g["x"]), _ptr(g["B"]),
-                                    _ptr(g["C"]), _ptr(dxbc), _ptr(dw), _ptr(db))
-        ws, nbytes = _workspace(
-            lambda n: lib().bimamba_conv1d_bwd_workspace_size(ctypes.byref(shape), int(bwd is not None), nseq, n),
-            dev)
-        _abi.check(lib().bimamba_conv1d_bwd(
-            ctypes.byref(shape), ctypes.byref(args[0]), ctypes.byref(args[1]) if bwd is not None else None,
-            cu_arr, nseq, _ptr(ws), nbytes, _stream(stream)))
+    outs = out if out is not None else (None, None)
+    f32 = torch.float32
+    res, args = [None, None], [None, None]
+    for i, (d, g, name) in enumerate(((fwd, gfwd, "fwd"), (bwd, gbwd, "bwd"))):
+        if d is None:
+            continue
+        if isinstance(d["xbc"], Act8) != q8:
+            raise TypeError("both directions' xbc must be Act8, or neither")
+        xp, xs = _kept(d["xbc"], name + ".xbc", (batch, L, ch), dtype, dev)
+        w, bias, gx, gB, gC = d["weight"], d.get("bias"), g["x"], g["B"], g["C"]
+        _check(w, name + ".weight", (ch, W), f32, dev)
+        _check(gx, name + "_grad.x", (batch, L, H, P), f32, dev)
+        _check(gB, name + "_grad.B", (batch, L, G, N), f32, dev)
+        _check(gC, name + "_grad.C", (batch, L, G, N), f32, dev)
+        dxbc = _out(outs[i], name + "_out", (batch, L, ch), dtype, dev, None if q8 else d["xbc"])
+        dw = torch.empty((ch, W), dtype=f32, device=dev)
+        db = None
+        if bias is not None:
+            _check(bias, name + ".bias", (ch,), f32, dev)
+            db = torch.empty(ch, dtype=f32, device=dev)
+        res[i] = dict(xbc=dxbc, weight=dw, bias=db)
+        args[i] = ctypes.byref(_abi.ConvGrad(xp, xs, w.data_ptr(), _adr(bias), gx.data_ptr(), gB.data_ptr(),
+                                             gC.data_ptr(), dxbc.data_ptr(), dw.data_ptr(), _adr(db)))
+    nbytes = _conv_size("bimamba_conv1d_bwd_workspace_size", sizes, 0 if bwd is None else 1, nseq)
+    ws = _workspace(nbytes, dev)
+    rc = lib().bimamba_conv1d_bwd(ctypes.byref(_abi.ConvShape(*sizes)), args[0], args[1], cu_arr, nseq, _adr(ws),
+                                  nbytes, _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
     return res[0], res[1]
 
 
