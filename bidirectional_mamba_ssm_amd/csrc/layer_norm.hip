@@ -10,9 +10,9 @@
 // h may be read back from its 8-bit checkpoint (rows.hpp), which the forward
 // pass can write as it goes.
 //
-// Both are streams bounded by HBM. A row lives in the registers of one wave
-// or of the waves of one workgroup, NV 16-byte vectors a lane, so every array
-// is read or written once; the next row's loads are under way while a row is
+// Both are streams bounded by HBM. A row lives in the registers of 8, 16, 32
+// or 64 lanes of a wave (narrow rows share one) or of several waves of a
+// workgroup, NV 16-byte vectors a lane, so every array is read or written once; the next row's loads are under way while a row is
 // worked on. Sums over a row are DPP lane moves, and one exchange through LDS
 // where it has several waves: the forward pass sends each wave's mean and sum
 // of squares about it, which join exactly, so the variance is never a
@@ -75,18 +75,26 @@ __device__ __forceinline__ void load_w(const float *p, int c, float none, float 
     }
 }
 
-// The forward pass: one wave a row, kRows of them a workgroup, or MULTI: the
-// whole workgroup a row.
+// Lanes of a row: G of a wave, or (G = 0) several waves.
+// The forward pass has workgroups of kRows waves, or (G = 0) one row each.
 constexpr int kRows = 4;
 
-template <typename T, int NV, bool MULTI, bool RES, bool CK>
-__global__ __launch_bounds__(MULTI ? 64 * kMaxWaves : 64 * kRows) void k_layer_norm(LnArgs a) {
+template <int G>
+__device__ __forceinline__ float lanes_total(float v) {
+    if constexpr (G == 0 || G == 64) return wave_total(v);
+    else return group_total<G>(v);
+}
+
+template <typename T, int NV, int G, bool RES, bool CK>
+__global__ __launch_bounds__(G == 0 ? 64 * kMaxWaves : 64 * kRows) void k_layer_norm(LnArgs a) {
     using L = Lane<T>;
     constexpr int V = L::V;
+    constexpr bool MULTI = G == 0;
+    constexpr int kShare = MULTI ? 1 : 64 / G;   // rows of a wave
     __shared__ float2 part[MULTI ? 2 : 1][MULTI ? kMaxWaves : 1];
     const int C = a.C;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int t = MULTI ? threadIdx.x : threadIdx.x & 63, lanes = MULTI ? blockDim.x : 64;
+    const int t = MULTI ? threadIdx.x : threadIdx.x & (G - 1), lanes = MULTI ? blockDim.x : G;
     const Place<V, NV> at(C, t, lanes);
     const float n = (float)C;
     float w[NV][V], b[NV][V];
@@ -95,8 +103,9 @@ __global__ __launch_bounds__(MULTI ? 64 * kMaxWaves : 64 * kRows) void k_layer_n
         load_w<V>(a.w, at.c[k], 1.f, w[k]);
         load_w<V>(a.b, at.c[k], 0.f, b[k]);
     }
-    const long long step = (long long)gridDim.x * (MULTI ? 1 : kRows);
-    long long row = (long long)blockIdx.x * (MULTI ? 1 : kRows) + (MULTI ? 0 : wave);
+    const long long step = (long long)gridDim.x * (MULTI ? 1 : kRows * kShare);
+    long long row = (long long)blockIdx.x * (MULTI ? 1 : kRows * kShare) + (MULTI ? 0 : wave * kShare);
+    if (kShare > 1) row += (threadIdx.x & 63) / (MULTI ? 64 : G);
     rvec nx[NV], nr[RES ? NV : 1];
     auto fetch = [&](long long r) {
 #pragma unroll
@@ -136,7 +145,7 @@ __global__ __launch_bounds__(MULTI ? 64 * kMaxWaves : 64 * kRows) void k_layer_n
         }
         // this wave's mean (exact for a constant row whose sum is) and squares about it
         const float cnt = MULTI ? at.count : n;
-        float mean = wave_total(m) / fmaxf(cnt, 1.f);
+        float mean = lanes_total<G>(m) / fmaxf(cnt, 1.f);
         float q = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -156,7 +165,7 @@ __global__ __launch_bounds__(MULTI ? 64 * kMaxWaves : 64 * kRows) void k_layer_n
             }
             q = fmaf(at.has[k], s, q);
         }
-        q = wave_total(q);
+        q = lanes_total<G>(q);
         if constexpr (MULTI) {
             if ((t & 63) == 0) part[flip][wave] = make_float2(mean, q);
             __syncthreads();
@@ -229,17 +238,20 @@ __global__ __launch_bounds__(MULTI ? 64 * kMaxWaves : 64 * kRows) void k_layer_n
 // each, MULTI if W > 1.
 constexpr int kBwdWaves = 8;
 
-template <typename T, int NV, bool MULTI, bool Q8, bool DSUM>
+template <typename T, int NV, int G, bool Q8, bool DSUM>
 __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, int W, int R) {
     using L = Lane<T>;
     constexpr int V = L::V, E = V * NV;
+    constexpr bool MULTI = G == 0;
+    constexpr int kShare = MULTI ? 1 : 64 / G;   // rows of a wave
     __shared__ float2 part[MULTI ? 2 : 1][MULTI ? kBwdWaves : 1];
     // sums to join: W E 64 of dw and of db, where R > 1 (then W <= 4)
     __shared__ float sum[E > 16 ? 1 : MULTI ? 2 * E * 256 : 2 * E * 64];
     const int C = a.C;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int sub = MULTI ? wave / W : wave, lanes = MULTI ? 64 * W : 64;
-    const int t = threadIdx.x - sub * lanes;
+    const int sub = MULTI ? wave / W : wave, lanes = MULTI ? 64 * W : G;
+    const int t = MULTI ? threadIdx.x - sub * lanes : threadIdx.x & (G - 1);
+    const int slot = sub * kShare + (kShare > 1 ? (threadIdx.x & 63) / (MULTI ? 64 : G) : 0);
     const Place<V, NV> at(C, t, lanes);
     const float inv = 1.0f / (float)C;
     const int nblk = (C + 31) / 32;
@@ -278,9 +290,9 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
     long long base = (long long)blockIdx.x * R;
     constexpr bool kAhead = E <= 16;   // wider lanes have no registers for it
     Row next;
-    if (kAhead) fetch(next, min(base + sub, last));
+    if (kAhead) fetch(next, min(base + slot, last));
     for (int flip = 0; base < a.rows; base += step, flip ^= 1) {
-        const long long row = base + sub;
+        const long long row = base + slot;
         const bool live = row < a.rows;
         if (!MULTI && !live) break;
         if (!kAhead) fetch(next, min(row, last));
@@ -321,8 +333,8 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
             t1 = fmaf(at.has[k], s1, t1);
             t2 = fmaf(at.has[k], s2, t2);
         }
-        t1 = wave_total(t1);
-        t2 = wave_total(t2);
+        t1 = lanes_total<G>(t1);
+        t2 = lanes_total<G>(t2);
         if constexpr (MULTI) {
             if ((t & 63) == 0) part[flip][wave] = make_float2(t1, t2);
             __syncthreads();
@@ -362,10 +374,23 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
         }
     }
     if (!a.part) return;
-    // this workgroup's share of dw | db: the R rows' sums added in order
+    // this workgroup's share of dw | db: the sums of the R rows at a time added in order
     float *out = a.part + (size_t)blockIdx.x * 2 * C;
+    if constexpr (kShare > 1) {
+        // the rows that share a wave first
+#pragma unroll
+        for (int off = G; off < 64; off *= 2)
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    dw[k][j] += __shfl_xor(dw[k][j], off);
+                    db[k][j] += __shfl_xor(db[k][j], off);
+                }
+    }
     if constexpr (E <= 16) {
-        for (int s = 0; s < R && R > 1; ++s) {
+        const int n = R / kShare;   // waves, or (G = 0) rows
+        for (int s = 0; s < n && n > 1; ++s) {
             if (sub == s) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
@@ -376,7 +401,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
                             dw[k][j] += *p;
                             db[k][j] += *q;
                         }
-                        if (s < R - 1) {
+                        if (s < n - 1) {
                             *p = dw[k][j];
                             *q = db[k][j];
                         }
@@ -384,7 +409,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
             }
             __syncthreads();
         }
-        if (sub != R - 1) return;
+        if (sub != n - 1) return;
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -407,28 +432,42 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
     }
 }
 
-// How a row is held: nv vectors a lane of `waves` waves. `lane` elements a lane
-// where that is enough, the fewest otherwise that kMaxWaves waves can do with.
+// How a row is held: G lanes of one wave or (G = 0) `waves` waves, nv vectors
+// a lane. Rows of up to 512 channels take the fewest lanes, 8 elements each (a
+// wave a row instead costs 60 000 x 64 bf16 rows 27 us for 8); wider ones
+// `lane` elements a lane, or the fewest that kMaxWaves waves can do with.
 struct Form {
-    int nv, waves;
+    int nv, waves, G;
 };
 template <typename T>
 Form row_form(int C, int lane) {
     const int V = 16 / (int)sizeof(T);
-    const int units = (C + 64 * V - 1) / (64 * V);          // vectors of a row, in waves
     Form f;
     f.nv = 1;
+    f.waves = 1;
+    f.G = 64;
+    if (C <= 256) {
+        f.nv = 8 / V;
+        f.G = C <= 64 ? 8 : C <= 128 ? 16 : 32;
+        return f;
+    }
+    const int units = (C + 64 * V - 1) / (64 * V);          // vectors of a row, in waves
     while (f.nv * V < lane && f.nv < units) f.nv *= 2;
     while (f.nv * kMaxWaves < units) f.nv *= 2;
     f.waves = (units + f.nv - 1) / f.nv;
+    if (f.waves > 1) f.G = 0;
     return f;
 }
 template <typename T>
 Form bwd_form(int C) { return row_form<T>(C, 8); }
-inline int bwd_rows(const Form &f) { return f.waves >= kBwdWaves ? 1 : kBwdWaves / f.waves; }
+// rows that a workgroup of the gradient takes at a time
+inline int bwd_rows(const Form &f) {
+    return f.G ? kBwdWaves * (64 / f.G) : f.waves >= kBwdWaves ? 1 : kBwdWaves / f.waves;
+}
 template <typename T>
 int bwd_wgs(long long rows, int C) {
     const Form f = bwd_form<T>(C);
+    // two workgroups of 8 waves a CU, or the one that its registers allow
     const int r = bwd_rows(f), most = f.nv * (16 / (int)sizeof(T)) > 8 ? 256 : 512;
     const long long wgs = (rows + r - 1) / r;
     return (int)(wgs < most ? wgs : most);
@@ -437,18 +476,18 @@ int bwd_wgs(long long rows, int C) {
 template <typename T, bool RES, bool CK>
 hipError_t launch_fwd(const LnArgs &a, hipStream_t s) {
     const Form f = row_form<T>(a.C, 16);
-    const bool multi = f.waves > 1;
-    const long long per = multi ? 1 : kRows, wgs = (a.rows + per - 1) / per;
-    // two rows (or kRows pairs) a workgroup, more only if that leaves too few
-    const dim3 grid((unsigned)(wgs < 2048 ? wgs : wgs < 4096 ? 2048 : (wgs + 1) / 2)), block(multi ? 64 * f.waves : 64 * kRows);
-#define GO(NV)                                                                                              \
-    if (f.nv == NV) {                                                                                       \
-        if (multi) BM_LAUNCH("layer_norm", (k_layer_norm<T, NV, true, RES, CK>), grid, block, 0, s, a);       \
-        else BM_LAUNCH("layer_norm", (k_layer_norm<T, NV, false, RES, CK>), grid, block, 0, s, a);            \
+    const long long per = f.G ? kRows * (64 / f.G) : 1, wgs = (a.rows + per - 1) / per;
+    // two turns a workgroup, more only if that leaves too few
+    const dim3 grid((unsigned)(wgs < 2048 ? wgs : wgs < 4096 ? 2048 : (wgs + 1) / 2));
+    const dim3 block(64 * (f.G ? kRows : f.waves));
+#define GO(NV, G_)                                                                                          \
+    if (f.nv == NV && f.G == G_) {                                                                          \
+        BM_LAUNCH("layer_norm", (k_layer_norm<T, NV, G_, RES, CK>), grid, block, 0, s, a);                    \
         return hipGetLastError();                                                                           \
     }
-    GO(1) GO(2) GO(4)
-    if constexpr (sizeof(T) == 4) { GO(8) }
+    constexpr int N8 = 8 * sizeof(T) / 16;   // vectors that make 8 elements
+    GO(N8, 8) GO(N8, 16) GO(N8, 32)
+    GO(N8, 64) GO(2 * N8, 64) GO(2 * N8, 0) GO(4 * N8, 0)
 #undef GO
     return hipErrorInvalidValue;
 }
@@ -457,15 +496,15 @@ template <typename T, bool Q8, bool DSUM>
 hipError_t launch_b(const LnBwdArgs &a, hipStream_t s) {
     const Form f = bwd_form<T>(a.C);
     const int R = bwd_rows(f);
-    const dim3 grid((unsigned)bwd_wgs<T>(a.rows, a.C)), block(64 * f.waves * R);
-#define GO(NV, MULTI)                                                                                    \
-    if (f.nv == NV && (f.waves > 1) == MULTI) {                                                          \
-        BM_LAUNCH("layer_norm_bwd", (k_layer_norm_bwd<T, NV, MULTI, Q8, DSUM>), grid, block, 0, s, a,      \
+    const dim3 grid((unsigned)bwd_wgs<T>(a.rows, a.C)), block(64 * (f.G ? kBwdWaves : f.waves * R));
+#define GO(NV, G_)                                                                                       \
+    if (f.nv == NV && f.G == G_) {                                                                       \
+        BM_LAUNCH("layer_norm_bwd", (k_layer_norm_bwd<T, NV, G_, Q8, DSUM>), grid, block, 0, s, a,         \
                   f.waves, R);                                                                           \
         return hipGetLastError();                                                                        \
     }
-    GO(1, false) GO(2, true) GO(4, true)
-    if constexpr (sizeof(T) == 4) { GO(2, false) GO(8, true) } else { GO(1, true) }
+    constexpr int N8 = 8 * sizeof(T) / 16;   // vectors that make 8 elements
+    GO(N8, 8) GO(N8, 16) GO(N8, 32) GO(N8, 64) GO(N8, 0) GO(2 * N8, 0) GO(4 * N8, 0)
 #undef GO
     return hipErrorInvalidValue;
 }

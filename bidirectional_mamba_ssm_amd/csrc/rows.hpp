@@ -150,6 +150,16 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v) {
     if constexpr (LANES > 4) v = max(v, dpp<0x141>(v));  // row_half_mirror
     return v;
 }
+// sum over each G adjacent lanes (8, 16 or 32), the same in each of them
+template <int G>
+__device__ __forceinline__ float group_total(float v) {
+    v = dpp_add<0xB1>(v);
+    v = dpp_add<0x4E>(v);
+    v = dpp_add<0x141>(v);
+    if constexpr (G > 8) v = dpp_add<0x140>(v);
+    if constexpr (G > 16) v += __shfl_xor(v, 16);
+    return v;
+}
 // sum over the wave's 64 lanes, the same in every lane; a fixed order
 __device__ __forceinline__ float wave_total(float v) {
     v = dpp_add<0xB1>(v);                         // lanes 1 apart
