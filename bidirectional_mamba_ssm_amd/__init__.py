@@ -874,7 +874,7 @@ def _conv1d_act8(fwd, bwd, dims, activation, cu_seqlens, out, dtype, stream):
         args[2 * i] = ctypes.byref(_abi.ConvDir(None, d["weight"].data_ptr(), _adr(bias), o["x"].data_ptr(),
                                                 o["B"].data_ptr(), o["C"].data_ptr()))
         args[2 * i + 1] = ctypes.byref(_abi.Act8Ptrs(q, scale))
-    nbytes = _conv_size("bimamba_conv1d_workspace_size", sizes, nseq) if nseq else 0
+    nbytes = _conv_size("bimamba_conv1d_act8_workspace_size", sizes, nseq)
     ws = _workspace(nbytes, dev)
     rc = lib().bimamba_conv1d_act8(ctypes.byref(_abi.ConvShape(*sizes)), *args, cu_arr, nseq, _adr(ws), nbytes,
                                    _raw_stream(dev.index))

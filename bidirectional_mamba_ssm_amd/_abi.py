@@ -24,7 +24,7 @@ EXPORTS = (
     "bimamba_ssd_bwd_workspace_size", "bimamba_ssd_bwd", "bimamba_gated_norm",
     "bimamba_ssd_fwd_streams", "bimamba_merge_linear", "bimamba_ssd_fwd_noalloc",
     "bimamba_state_alloc_conv", "bimamba_state_conv_ctx", "bimamba_block_step_conv",
-    "bimamba_act8_pack", "bimamba_act8_unpack", "bimamba_conv1d_act8",
+    "bimamba_act8_pack", "bimamba_act8_unpack", "bimamba_conv1d_act8_workspace_size", "bimamba_conv1d_act8",
     "bimamba_conv1d_bwd_workspace_size", "bimamba_conv1d_bwd",
     "bimamba_gated_norm_bwd_workspace_size", "bimamba_gated_norm_bwd", "bimamba_layer_norm",
     "bimamba_layer_norm_bwd_workspace_size", "bimamba_layer_norm_bwd",
@@ -142,6 +142,7 @@ def load():
     ap, cgp, np_ = ctypes.POINTER(Act8Ptrs), ctypes.POINTER(ConvGrad), ctypes.POINTER(size)
     lib.bimamba_act8_pack.argtypes = [ll, ll, ci, vp, ap, vp]
     lib.bimamba_act8_unpack.argtypes = [ll, ll, ci, ap, vp, vp]
+    lib.bimamba_conv1d_act8_workspace_size.argtypes = [csp, ci, np_]
     lib.bimamba_conv1d_act8.argtypes = [csp, cdp, ap, cdp, ap, i32p, ci, vp, size, vp]
     lib.bimamba_conv1d_bwd_workspace_size.argtypes = [csp, ci, ci, np_]
     lib.bimamba_conv1d_bwd.argtypes = [csp, cgp, cgp, i32p, ci, vp, size, vp]

@@ -267,6 +267,25 @@ int check_conv_train_shape(const bimamba_conv_shape *s) {
     return BIMAMBA_OK;
 }
 
+// packed sequences of a training-step convolution (the index table in `table`
+// where there are many)
+hipError_t set_packed(ConvSeqs &p, const int32_t *cu, int nseq, int seqlen, void *table, hipStream_t st) {
+    p.seq = nullptr;
+    p.count = 0;
+    if (!cu) return hipSuccess;
+    if (nseq <= ConvSeqs::kMost) {
+        p.count = nseq + 1;
+        memcpy(p.off, cu, sizeof(int32_t) * (nseq + 1));
+        return hipSuccess;
+    }
+    p.seq = (const int32_t *)table;
+    return launch_seq_index(cu, nseq, seqlen, (int32_t *)table, st);
+}
+// its workspace
+size_t seqs_workspace(int nseq, int seqlen) {
+    return nseq > ConvSeqs::kMost ? align256(sizeof(int32_t) * (size_t)(seqlen > 0 ? seqlen : 1)) : 0;
+}
+
 size_t conv_bwd_dir_bytes(const bimamba_conv_shape *s, int ndir) {
     return align256(4 * conv_bwd_part(s->batch, s->seqlen, s->nheads * s->headdim, s->ngroups * s->d_state, s->width,
                                       ndir));
@@ -897,6 +916,15 @@ int bimamba_merge_linear(long long rows, int cin, int cout, const float *y_fwd,
     return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the merge");
 }
 
+int bimamba_conv1d_act8_workspace_size(const bimamba_conv_shape *s, int nseq, size_t *bytes) {
+    int rc = check_conv_train_shape(s);
+    if (rc) return rc;
+    if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
+    if (nseq < 0) return fail(BIMAMBA_EINVAL, "nseq %d < 0", nseq);
+    *bytes = seqs_workspace(nseq, s->seqlen);
+    return BIMAMBA_OK;
+}
+
 int bimamba_conv1d_act8(const bimamba_conv_shape *s, const bimamba_conv_dir *fwd,
                         const bimamba_act8 *xbc_fwd, const bimamba_conv_dir *bwd,
                         const bimamba_act8 *xbc_bwd, const int32_t *cu_seqlens, int nseq,
@@ -931,7 +959,7 @@ int bimamba_conv1d_act8(const bimamba_conv_shape *s, const bimamba_conv_dir *fwd
     } else if (nseq != 0) {
         return fail(BIMAMBA_EINVAL, "nseq %d given without cu_seqlens", nseq);
     }
-    if ((rc = check_workspace(workspace, workspace_bytes, conv_workspace(cu_seqlens ? nseq : 0, s->seqlen)))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, seqs_workspace(cu_seqlens ? nseq : 0, s->seqlen)))) return rc;
     if (empty) return BIMAMBA_OK;
     a.batch = s->batch;
     a.L = s->seqlen;
@@ -943,12 +971,8 @@ int bimamba_conv1d_act8(const bimamba_conv_shape *s, const bimamba_conv_dir *fwd
     a.act = s->activation;
     hipStream_t st = (hipStream_t)stream;
     hipError_t e;
-    if (cu_seqlens) {
-        int32_t *seq = (int32_t *)workspace;
-        if ((e = launch_seq_index(cu_seqlens, nseq, s->seqlen, seq, st)) != hipSuccess)
-            return hip_fail(e, "building sequence index");
-        a.seq = seq;
-    }
+    if ((e = set_packed(a.packed, cu_seqlens, nseq, s->seqlen, workspace, st)) != hipSuccess)
+        return hip_fail(e, "building sequence index");
     if ((e = launch_conv_act8(a, s->dtype == BIMAMBA_BF16, st)) != hipSuccess)
         return hip_fail(e, "launching conv1d");
     return BIMAMBA_OK;
@@ -960,7 +984,7 @@ int bimamba_conv1d_bwd_workspace_size(const bimamba_conv_shape *s, int has_bwd, 
     if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
     if (nseq < 0) return fail(BIMAMBA_EINVAL, "nseq %d < 0", nseq);
     const int ndir = has_bwd ? 2 : 1;
-    *bytes = align256(conv_workspace(nseq, s->seqlen)) + ndir * conv_bwd_dir_bytes(s, ndir);
+    *bytes = seqs_workspace(nseq, s->seqlen) + ndir * conv_bwd_dir_bytes(s, ndir);
     return BIMAMBA_OK;
 }
 
@@ -981,7 +1005,7 @@ int bimamba_conv1d_bwd(const bimamba_conv_shape *s, const bimamba_conv_grad *fwd
         return fail(BIMAMBA_EINVAL, "nseq %d given without cu_seqlens", nseq);
     }
     const int ndir = bwd ? 2 : 1;
-    const size_t seq_bytes = align256(conv_workspace(cu_seqlens ? nseq : 0, s->seqlen));
+    const size_t seq_bytes = seqs_workspace(cu_seqlens ? nseq : 0, s->seqlen);
     const size_t dir_bytes = conv_bwd_dir_bytes(s, ndir);
     if ((rc = check_workspace(workspace, workspace_bytes, seq_bytes + ndir * dir_bytes))) return rc;
     ConvBwdArgs a;
@@ -1010,12 +1034,8 @@ int bimamba_conv1d_bwd(const bimamba_conv_shape *s, const bimamba_conv_grad *fwd
     a.act = s->activation;
     hipStream_t st = (hipStream_t)stream;
     hipError_t e;
-    if (cu_seqlens && !empty) {
-        int32_t *seq = (int32_t *)workspace;
-        if ((e = launch_seq_index(cu_seqlens, nseq, s->seqlen, seq, st)) != hipSuccess)
-            return hip_fail(e, "building sequence index");
-        a.seq = seq;
-    }
+    if ((e = set_packed(a.packed, empty ? nullptr : cu_seqlens, nseq, s->seqlen, workspace, st)) != hipSuccess)
+        return hip_fail(e, "building sequence index");
     e = launch_conv_bwd(a, s->dtype == BIMAMBA_BF16, st);
     return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the convolution's gradient");
 }

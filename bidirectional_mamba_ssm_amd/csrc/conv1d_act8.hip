@@ -19,6 +19,7 @@
 // lane need 180 registers and ran 66 us; runs of 16 or 64 positions 50.
 #include <type_traits>
 
+#include "conv_seqs.hpp"
 #include "internal.hpp"
 #include "rows.hpp"
 
@@ -125,23 +126,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_act8(ConvAct8Args a) {
             sc += more ? ss : 0;
         }
     };
-    // packed: bit m tells that position p0 - H + m is a sequence's first
-    uint64_t starts[2] = {0, 0};
-    if constexpr (PACKED) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int p = p0 - H + 64 * h + lane;
-            const bool in = p > 0 && p < L;
-            const int t = token(in ? p : 0), u = token(in ? p - 1 : 0);
-            starts[h] = __ballot(in && a.seq[t] != a.seq[u]);
-        }
-    }
-    auto window = [&](int p) -> uint32_t {
-        if constexpr (!PACKED) return 0u;
-        const int m = p - p0;
-        const uint64_t s = m >= 64 ? starts[1] >> (m - 64) : starts[0] >> m | (m ? starts[1] << (64 - m) : 0);
-        return (uint32_t)s & ((1u << N) - 1);
-    };
+    // where the window of the batch from p has sequence starts
+    StartBits starts;
+    if constexpr (PACKED) starts = StartBits(a.packed, p0 - H, L, rev);
+    auto window = [&](int p) -> uint32_t { return PACKED ? starts.from(p - p0, N) : 0u; };
 #pragma unroll
     for (int i = 0; i < H; ++i) {
         const int p = p0 - H + i;
@@ -197,11 +185,12 @@ hipError_t launch_w(const ConvAct8Args &a, hipStream_t s) {
     const dim3 grid((unsigned)((a.wgs + 7) / 8 * 8));
 #define GO(PACKED, ACT) \
     BM_LAUNCH("conv1d_act8", (k_conv_act8<T, VEC, W, PACKED, ACT>), grid, dim3(64 * kWaves), 0, s, a)
+    const bool packed = a.packed.seq || a.packed.count;
     if (a.act) {
-        if (a.seq) GO(true, true);
+        if (packed) GO(true, true);
         else GO(false, true);
     } else {
-        if (a.seq) GO(true, false);
+        if (packed) GO(true, false);
         else GO(false, false);
     }
 #undef GO

@@ -18,6 +18,7 @@
 // workgroup through LDS and over workgroups by col_sum.hip.
 #include <type_traits>
 
+#include "conv_seqs.hpp"
 #include "internal.hpp"
 #include "rows.hpp"
 
@@ -164,25 +165,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvBwdArgs a) {
                 load_grad<VEC>(g + (row0 + t) * gs, gnext[i]);
             }
         };
-        // packed: bit m tells that position p0 - H + m is a sequence's first
-        uint64_t starts[2] = {0, 0};
-        if constexpr (PACKED) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int p = p0 - H + 64 * h + lane;
-                const bool in = p > 0 && p < L;
-                const int t = token(in ? p : 0), u = token(in ? p - 1 : 0);
-                starts[h] = __ballot(in && a.seq[t] != a.seq[u]);
-            }
-        }
-        // the bits of the window of the batch from p
-        auto window = [&](int p) -> uint32_t {
-            if constexpr (!PACKED) return 0u;
-            const int m = p - p0;
-            const uint64_t w = m >= 64 ? starts[1] >> (m - 64)
-                                       : starts[0] >> m | (m ? starts[1] << (64 - m) : 0);
-            return (uint32_t)w & ((1u << N) - 1);
-        };
+        // where the window of the batch from p has sequence starts
+        StartBits starts;
+        if constexpr (PACKED) starts = StartBits(a.packed, p0 - H, L, rev);
+        auto window = [&](int p) -> uint32_t { return PACKED ? starts.from(p - p0, N) : 0u; };
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             const int p = p0 - H + i;
@@ -293,7 +279,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvBwdArgs a) {
 template <typename T, bool Q8, int VEC, int W>
 hipError_t launch_w(const ConvBwdArgs &a, hipStream_t s) {
     const dim3 grid((unsigned)((a.wgs + 7) / 8 * 8));
-    if (a.seq) BM_LAUNCH("conv1d_bwd_packed", (k_conv_bwd<T, Q8, VEC, W, true>), grid, dim3(64 * kWaves), 0, s, a);
+    if (a.packed.seq || a.packed.count) BM_LAUNCH("conv1d_bwd_packed", (k_conv_bwd<T, Q8, VEC, W, true>), grid, dim3(64 * kWaves), 0, s, a);
     else BM_LAUNCH("conv1d_bwd", (k_conv_bwd<T, Q8, VEC, W, false>), grid, dim3(64 * kWaves), 0, s, a);
     return hipGetLastError();
 }
@@ -312,11 +298,15 @@ hipError_t launch_t(const ConvBwdArgs &a, bool vec, hipStream_t s) {
     return vec ? launch_v<T, false, 4>(a, s) : launch_v<T, false, 1>(a, s);
 }
 
-// positions a wave walks: long runs repeat few halo rows, short ones give
-// the chip enough waves
+// Positions a wave walks: 32, or fewer where that leaves the chip short of
+// waves (a run repeats W - 1 rows at either end; 8 x 1024 tokens of 4352
+// channels: 32 122 us, 64 131, 96 145, 16 125; 2500 x 96: 8 8.6 us, 16 11.4,
+// 16384 x 96, 2048 waves of 16: 14, of 8: 16.5).
 int run_length(int batch, int L, int slabs, int ndir) {
     int run = 32;
-    while (run > 16 && (long long)((L + run - 1) / run) * slabs * batch * ndir < 2048) run /= 2;
+    auto waves = [&] { return (long long)((L + run - 1) / run) * slabs * batch * ndir; };
+    while (run > 16 && waves() < 2048) run /= 2;
+    if (waves() < 1024) run /= 2;
     return run;
 }
 int tiles_of(int L, int run) { return (L + run * kWaves - 1) / (run * kWaves); }

@@ -202,6 +202,15 @@ struct Act8Args {
 };
 hipError_t launch_act8(Act8Args a, bool bf16, bool pack, hipStream_t s);
 
+// Packed sequences of a training-step convolution: their offsets by value up
+// to kMost sequences, the per-token index beyond.
+struct ConvSeqs {
+    static constexpr int kMost = 128;
+    const int32_t *seq;        // [L] or nullptr
+    int count;                 // offsets in off; 0 with seq, or if not packed
+    int32_t off[kMost + 1];
+};
+
 // conv1d_act8.hip: the short convolution from 8-bit checkpoints
 struct ConvAct8Dir {
     const int8_t *q;           // [batch][L][ch]
@@ -213,7 +222,7 @@ struct ConvAct8Args {
     ConvAct8Dir dir[2];
     int batch, L, hp, gn, ch, W, ndir, act;
     int nvec, slabs, tiles, run, wgs;   // set by launch_conv_act8
-    const int32_t *seq;
+    ConvSeqs packed;
 };
 hipError_t launch_conv_act8(ConvAct8Args a, bool bf16, hipStream_t s);
 
@@ -231,7 +240,7 @@ struct ConvBwdArgs {
     ConvBwdDir dir[2];
     int batch, L, hp, gn, ch, W, ndir, act;
     int nvec, slabs, tiles, run, wgs;   // set by launch_conv_bwd
-    const int32_t *seq;
+    ConvSeqs packed;
 };
 size_t conv_bwd_part(int batch, int L, int hp, int gn, int W, int ndir);   // floats per direction
 hipError_t launch_conv_bwd(ConvBwdArgs a, bool bf16, hipStream_t s);

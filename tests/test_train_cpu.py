@@ -285,7 +285,12 @@ def test_conv_act8_refused(lib):
     assert call(d, a, d, None) == E
     assert call(d, a, None, a) == E
     assert call(d, a, nseq=1) == E
-    assert call(d, a, cu=[0, 4, 8], nseq=2) == _abi.EWORKSPACE
+    many = [0] * 129 + [8]   # beyond what goes by value: a table in the workspace
+    assert call(d, a, cu=many, nseq=129) == _abi.EWORKSPACE
+    n = ctypes.c_size_t(0)
+    assert lib.bimamba_conv1d_act8_workspace_size(ctypes.byref(s), 129, ctypes.byref(n)) == 0 and n.value >= 32
+    assert lib.bimamba_conv1d_act8_workspace_size(ctypes.byref(s), 128, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.bimamba_conv1d_act8_workspace_size(ctypes.byref(s), -1, ctypes.byref(n)) == E
 
 
 def test_act8_refused(lib):

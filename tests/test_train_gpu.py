@@ -151,6 +151,11 @@ LN_CASES = [
     (3, 16383, "bf16", True, False, False, False),
     (5000, 96, "bf16", True, True, True, True),
     (9001, 40, "f32", False, False, True, True),
+    (4097, 16, "bf16", True, True, True, True),
+    (3001, 130, "f32", True, True, False, True),
+    (2000, 200, "bf16", False, True, True, False),
+    (1500, 256, "f32", True, False, True, True),
+    (129, 257, "bf16", True, True, True, True),
 ]
 
 
@@ -414,6 +419,9 @@ CONV_CASES = [
     (1, None, 3, 7, 1, 3, 4, "f32", "silu", True, True, True, (1, 1, 1, 63, 2, 64, 128)),
     (1, None, 2, 16, 1, 16, 2, "f32", "none", True, True, False, (0, 5, 0)),
     (1, None, 8, 64, 1, 128, 3, "bf16", "silu", True, False, True, (700, 33, 512, 260)),
+    (1, None, 2, 16, 1, 16, 4, "f32", "silu", True, True, True, (3, 0, 5, 1, 30, 64) * 21),
+    (1, None, 2, 16, 1, 16, 4, "bf16", "silu", True, True, True, (1, 2, 0, 70) * 33),
+    (1, None, 2, 16, 1, 16, 3, "f32", "silu", True, True, False, (1,) * 300),
 ]
 
 
@@ -439,7 +447,7 @@ def _conv_inputs(case, seed):
     return dirs, grads, cu, L, ch
 
 
-@pytest.mark.parametrize("case", CONV_CASES, ids=lambda c: "-".join(str(v).replace(" ", "") for v in c))
+@pytest.mark.parametrize("case", CONV_CASES, ids=lambda c: "-".join(str(v).replace(" ", "")[:32] for v in c))
 def test_conv1d_bwd(case):
     batch, _, H, P, G, N, W, dtype, act, both, bias, ckpt, lens = case
     print(f"case {case}", flush=True)
