@@ -666,6 +666,8 @@ def _rows(shape):
     """(rows, channels) of [..., channels]."""
     if not shape or not shape[-1]:
         raise ValueError(f"shape {tuple(shape)} has no channels")
+    if shape[-1] >= 2 ** 31:
+        raise ValueError(f"{shape[-1]} channels are beyond 2^31 - 1")
     return math.prod(shape[:-1]), shape[-1]
 
 
@@ -753,11 +755,11 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, checkpoint=Fa
         sum_out = _out(sum_out, "sum_out", shape, dt, dev, x)
     mean, rstd = torch.empty((2,) + shape[:-1], dtype=torch.float32, device=dev).unbind(0)
     ckpt = p = None
-    if checkpoint is not False and checkpoint is not None:
-        ckpt = Act8.empty(shape, dev) if checkpoint is True else checkpoint
+    if checkpoint:
+        ckpt = checkpoint if isinstance(checkpoint, Act8) else Act8.empty(shape, dev)
         p = ctypes.byref(ckpt._ptrs("checkpoint", shape, dev))
     rc = lib().bimamba_layer_norm(
-        rows, C, code, x.data_ptr(), _adr(residual), _adr(weight), _adr(bias), eps, out.data_ptr(), _adr(sum_out),
+        rows, C, code, x.data_ptr(), _adr(residual), _adr(weight), _adr(bias), float(eps), out.data_ptr(), _adr(sum_out),
         mean.data_ptr(), rstd.data_ptr(), p, _raw_stream(dev.index))
     if rc:
         _abi.check(rc)
@@ -826,7 +828,7 @@ def gated_norm_bwd(dout, y, z, weight, group_size=None, eps=1e-5, wgrad=True, dy
         nbytes = _size("bimamba_gated_norm_bwd_workspace_size", rows, C, gs, code)
         ws = _workspace(nbytes, dev)
     rc = lib().bimamba_gated_norm_bwd(
-        rows, C, gs, code, yp, ys, zp, zs, weight.data_ptr(), eps, dout.data_ptr(), dy.data_ptr(), dz.data_ptr(),
+        rows, C, gs, code, yp, ys, zp, zs, weight.data_ptr(), float(eps), dout.data_ptr(), dy.data_ptr(), dz.data_ptr(),
         _adr(dw), _adr(ws), nbytes, _raw_stream(dev.index))
     if rc:
         _abi.check(rc)
@@ -842,6 +844,8 @@ def _conv_plan(xbc, weight, dims, activation, dtype):
     H, P, G, N = dims
     if ch != conv_channels(H, P, G, N):
         raise ValueError(f"xbc has {ch} channels, expected nheads*headdim + 2*ngroups*d_state")
+    if max(batch, L, ch) >= 2 ** 31:
+        raise ValueError(f"xbc's shape {tuple(xbc.shape)} is beyond 2^31 - 1")
     code = _dtype_code(dtype)
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation {activation!r} is not one of {sorted(map(str, ACTIVATIONS))}")

@@ -260,10 +260,13 @@ int check_conv_train_shape(const bimamba_conv_shape *s) {
     if (rc) return rc;
     // a run's positions, rounded up to its workgroup, are counted in int32
     if (s->seqlen > (1 << 30)) return fail(BIMAMBA_EUNSUPPORTED, "seqlen %d exceeds 2^30", s->seqlen);
-    const long long ch = (long long)s->nheads * s->headdim + 2LL * s->ngroups * s->d_state;
-    if ((ch + 63) / 64 * ((long long)s->seqlen / 64 + 1) * s->batch * 2 > (1LL << 31) - 1)
+    // a launch has fewer than 2^32 threads: workgroups of 256, each 64 tokens
+    // at least (fewer only in small problems) of 64 channel vectors
+    const long long hp = (long long)s->nheads * s->headdim, gn = (long long)s->ngroups * s->d_state;
+    const long long vecs = (hp + 2 * gn) / (conv_vectorized(true, (int)hp, (int)gn) ? 4 : 1);
+    if ((vecs + 63) / 64 * ((long long)s->seqlen / 64 + 1) * s->batch * 2 > (1LL << 24) - 8)
         return fail(BIMAMBA_EUNSUPPORTED, "%d x %d tokens of %lld channels are too many for one launch", s->batch,
-                    s->seqlen, ch);
+                    s->seqlen, hp + 2 * gn);
     return BIMAMBA_OK;
 }
 

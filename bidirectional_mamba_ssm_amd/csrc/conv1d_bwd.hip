@@ -14,8 +14,16 @@
 // din_{p-(W-1)}, whose last term du_p is, goes out. A run starts W-1
 // positions early with its inputs and ends W-1 late with its du; four waves
 // of a workgroup take adjacent runs. Rows are loaded kBatch positions ahead.
-// dw and db stay in the lane's registers over the run, are joined over the
+// The inner batches ask nothing and never wait for their own stores. dw and db
+// stay in the lane's registers over the run, are joined over the
 // workgroup through LDS and over workgroups by col_sum.hip.
+//
+// Measured (8 x 1024 tokens, 4352 channels, width 4, bf16, SiLU, both
+// directions): 119 us, 571 MB at 4.8 TB/s, and 5 us for the sums; 2500 packed
+// tokens of 96 channels in fp32 9.5 us. Tests in every batch 131; the inner
+// batches' code shared with a store under a branch, which made each batch wait
+// for the stores of the one before, 138. The arithmetic (432 vector
+// instructions for 16 elements a lane) would take 60.
 #include <type_traits>
 
 #include "conv_seqs.hpp"

@@ -11,6 +11,11 @@
 // needs, of v^2 and of g v, come from one walk over the registers and cost
 // one barrier, and the next row's loads are under way meanwhile. dw stays in
 // registers over the rows that a workgroup walks and is joined by col_sum.hip.
+//
+// Measured (bf16): 8192 x 4096, one group, 90 us, 470 MB at 5.2 TB/s, and 5 us
+// for the sums; 3001 x 5120, groups of 1280, both checkpoints, 34 us, 155 MB at
+// 4.5 TB/s. Four chunks a wave need 210 registers, so that 5-wave workgroups
+// took two rounds (44 us); loads of eight passes for five chunks 62.
 #include "internal.hpp"
 #include "rows.hpp"
 

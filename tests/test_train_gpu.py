@@ -736,3 +736,16 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("C", [100, 600, 2500])
+def test_layer_norm_overflowing_variance(C):
+    """Where the variance passes fp32's range rstd is 0, and so is the output
+    (plus the bias); lanes past the row's end add nothing to that."""
+    x = torch.zeros(3, C, device=DEV)
+    x[1, C - 1] = 1e30
+    x[2, 0] = -1e30
+    b = torch.full((C,), 0.5, device=DEV)
+    o = bm.layer_norm(x, None, b)
+    assert torch.equal(o["out"], torch.full_like(x, 0.5))
+    assert torch.equal(o["rstd"][1:], torch.zeros(2, device=DEV))
