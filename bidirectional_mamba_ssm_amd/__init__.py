@@ -824,7 +824,7 @@ def gated_norm_bwd(dout, y, z, weight, group_size=None, eps=1e-5, wgrad=True, dy
     dw = ws = None
     nbytes = 0
     if wgrad:
-        dw = torch.empty(C, dtype=torch.float32, device=dev)
+        dw = torch.empty_like(weight)
         nbytes = _size("bimamba_gated_norm_bwd_workspace_size", rows, C, gs, code)
         ws = _workspace(nbytes, dev)
     rc = lib().bimamba_gated_norm_bwd(
@@ -932,11 +932,11 @@ def conv1d_bwd(fwd, bwd, gfwd, gbwd, nheads, headdim, ngroups, d_state, activati
         _check(gB, name + "_grad.B", (batch, L, G, N), f32, dev)
         _check(gC, name + "_grad.C", (batch, L, G, N), f32, dev)
         dxbc = _out(outs[i], name + "_out", (batch, L, ch), dtype, dev, None if q8 else d["xbc"])
-        dw = torch.empty((ch, W), dtype=f32, device=dev)
+        dw = torch.empty_like(w)
         db = None
         if bias is not None:
             _check(bias, name + ".bias", (ch,), f32, dev)
-            db = torch.empty(ch, dtype=f32, device=dev)
+            db = torch.empty_like(bias)
         res[i] = dict(xbc=dxbc, weight=dw, bias=db)
         args[i] = ctypes.byref(_abi.ConvGrad(xp, xs, w.data_ptr(), _adr(bias), gx.data_ptr(), gB.data_ptr(),
                                              gC.data_ptr(), dxbc.data_ptr(), dw.data_ptr(), _adr(db)))

@@ -5,7 +5,8 @@
 // workgroups does not show in the result's accuracy).
 //
 // Columns are [taps][channels], and [channels] more where there is a bias:
-// column (k, c) goes to w[c * taps + k], column (taps, c) to b[c]. A workgroup takes 32 columns (128-byte
+// column (k, c) goes to w[c * taps + k], column (taps, c) to b[c]. A workgroup
+// takes 32 columns (128-byte
 // runs of a row) and 32 interleaved slices of the rows, joined through LDS,
 // or, where there are columns enough for every CU, 128 and 8: more work a
 // thread and fewer joins (2 x 21 760 columns of 64 rows 9.5 -> 5 us).

@@ -10,13 +10,14 @@
 // kBatch positions ahead, and a run starts W-1 positions early.
 //
 // At 8 x 1024 tokens of 4352 channels, width 4, bf16, SiLU, both directions:
-// 44 us, 216 MB at 4.9 TB/s (the convolution from bf16 input: 54 us, 285 MB).
-// Its arithmetic alone takes some 38 us (233 vector instructions for 16
+// 43 us, 216 MB at 5.0 TB/s (the convolution from bf16 input: 54 us, 285 MB).
+// Its arithmetic alone takes some 35 us (212 vector instructions for 16
 // elements a lane, 32 of them exp and rcp at a quarter of the rate), so what
 // it spends elsewhere shows: pointers that walk with the rows instead of a
-// product each, no test of the activation, 62 -> 44 us together with the walk
-// itself (the bf16 kernel's form, with a decoding load, took 62). 8 channels a
-// lane need 180 registers and ran 66 us; runs of 16 or 64 positions 50.
+// product each, no test of the activation, a window that is not moved, 62 ->
+// 43 us together with the walk itself (the bf16 kernel's form, with a decoding
+// load, took 62), and 50 where the clock has just risen from idle. 8 channels
+// a lane need 180 registers and ran 66 us; runs of 16 or 64 positions 50.
 #include <type_traits>
 
 #include "conv_seqs.hpp"
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_act8(ConvAct8Args a) {
     o += (long long)(row0 + token(p0)) * os;
     if (rev) os = -os;
 
-    float win[N][VEC];
+    float win[8][VEC];   // a ring where batches come in pairs
     Codes<VEC> next[kBatch];
     // so do the rows to load next
     const long long qs = rev ? -ch : ch, ss = rev ? -nblk : nblk;
@@ -141,12 +142,14 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_act8(ConvAct8Args a) {
         for (int j = 0; j < VEC; ++j)
             if (p < 0) win[i][j] = 0.f;
     }
-    // EDGE: the run ends in this batch or the next, or sequences meet in its
-    // window; elsewhere nothing is asked
-    auto batch = [&](int p, auto edge, uint32_t first) {
+    // The batch from p, its window in the ring from slot AT on. EDGE: the run
+    // ends in this batch or the next, or sequences meet in its window; elsewhere
+    // nothing is asked.
+    auto batch = [&](int p, auto edge, auto slot, uint32_t first) {
         constexpr bool EDGE = decltype(edge)::value;
+        constexpr int AT = decltype(slot)::value;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) next[i].values(win[H + i]);
+        for (int i = 0; i < kBatch; ++i) next[i].values(win[(AT + H + i) & 7]);
         if (!EDGE || p + kBatch < p1) fetch(p + kBatch);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -158,25 +161,42 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_act8(ConvAct8Args a) {
                 for (int k = 0; k < W; ++k) {
                     // no start among window positions i + k + 1 .. i + H
                     const bool same = !PACKED || !EDGE || !(first >> (i + k + 1) & ((1u << (H - k)) - 1));
-                    u = fmaf(w[j][k], same ? win[i + k][j] : 0.f, u);
+                    u = fmaf(w[j][k], same ? win[(AT + i + k) & 7][j] : 0.f, u);
                 }
                 v[j] = ACT ? u * __builtin_amdgcn_rcpf(1.0f + __expf(-u)) : u;
             }
             if (!EDGE || p + i < p1) store_out<T, VEC>(o, v);
             o += os;
         }
+    };
+    using Even = std::integral_constant<int, 0>;
+    using Odd = std::integral_constant<int, kBatch>;
+    fetch(p0);
+    int p = p0;
+    auto back = [&] {   // the last H inputs to the window's start
 #pragma unroll
         for (int i = 0; i < H; ++i)
 #pragma unroll
             for (int j = 0; j < VEC; ++j) win[i][j] = win[kBatch + i][j];
-    };
-    fetch(p0);
-    int p = p0;
-    do {
-        batch(p, std::true_type(), window(p));
         p += kBatch;
+    };
+    do {
+        batch(p, std::true_type(), Even(), window(p));
+        back();
         __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): as in conv1d_bwd.hip
-        for (; p + 2 * kBatch <= p1 && window(p) == 0; p += kBatch) batch(p, std::false_type(), 0u);
+        if constexpr (PACKED) {
+            for (; p + 2 * kBatch <= p1 && window(p) == 0;) {
+                batch(p, std::false_type(), Even(), 0u);
+                back();
+            }
+        } else {
+            // two batches go once round the ring, and nothing is moved (with
+            // sequences as well it takes registers that cost a wave: 50 -> 53 us)
+            for (; p + 3 * kBatch <= p1; p += 2 * kBatch) {
+                batch(p, std::false_type(), Even(), 0u);
+                batch(p + kBatch, std::false_type(), Odd(), 0u);
+            }
+        }
     } while (p < p1);
 }
 

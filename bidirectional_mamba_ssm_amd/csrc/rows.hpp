@@ -96,13 +96,11 @@ template <> struct Bytes<4> {
     __device__ __forceinline__ static void values(type r, float unit, float *v) { values4(r, unit, v); }
 };
 
-// 2^(e-133) for a block's exponent field e; NaN for 255. 2^(e-127) is the
-// field itself as a float, except that field 0 means 2^-127 (a subnormal) and
-// 255 a NaN: both have the mantissa's top bit set. Times 2^-6, exact down to
-// the subnormal 2^-133.
+// 2^(e-133) for a block's exponent field e, down to the subnormal 2^-133; NaN
+// for 255
 __device__ __forceinline__ float act8_unit(uint32_t e) {
-    const uint32_t top = (e == 0 || e == 255) ? 0x00400000u : 0u;
-    return __uint_as_float((e << 23) | top) * 0.015625f;
+    const float u = __builtin_ldexpf(1.0f, (int)e - 133);
+    return e == 255 ? __uint_as_float(0x7fc00000u) : u;
 }
 // The integers kept for V values of a block whose largest magnitude has the
 // bits `top`, in the low bytes of code[]. 1.5 2^23 + m holds round(m), ties to

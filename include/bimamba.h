@@ -25,7 +25,8 @@
  *  - Work is enqueued asynchronously on `stream` (a hipStream_t; NULL is the
  *    null stream). Nothing synchronizes. A failed launch returns BIMAMBA_EHIP.
  *  - Results are deterministic: the same inputs give the same bits.
- *  - x, B, C, y and the state arrays must be 16-byte aligned.
+ *  - x, B, C, y and the state arrays must be 16-byte aligned (the layer norm's
+ *    arrays and 8-bit checkpoints of other arrays: to their elements).
  */
 #ifndef BIMAMBA_H
 #define BIMAMBA_H
