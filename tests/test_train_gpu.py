@@ -749,3 +749,54 @@ def test_layer_norm_overflowing_variance(C):
     o = bm.layer_norm(x, None, b)
     assert torch.equal(o["out"], torch.full_like(x, 0.5))
     assert torch.equal(o["rstd"][1:], torch.zeros(2, device=DEV))
+
+
+# ---- offsets past 32 bits --------------------------------------------------------------------------
+# Arrays of more than 2^31 elements: their last rows must come out as they do
+# alone (rows, or a filter's width of them, are all that a result depends on).
+
+BIG_ROWS, BIG_C, TAIL = 263000, 8192, 5   # 2.15e9 elements
+
+
+def test_norms_past_32_bits():
+    g = _gen(51)
+    x = torch.empty(BIG_ROWS, BIG_C, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    tail = x[-TAIL:].clone()
+    o, s = bm.layer_norm(x, checkpoint=True), bm.layer_norm(tail, checkpoint=True)
+    assert torch.equal(o["out"][-TAIL:], s["out"]) and torch.equal(o["ckpt"].q[-TAIL:], s["ckpt"].q)
+    assert torch.equal(o["ckpt"].scale[-TAIL:], s["ckpt"].scale) and torch.equal(o["rstd"][-TAIL:], s["rstd"])
+    back = bm.act8_unpack(o["ckpt"])
+    assert torch.equal(back[-TAIL:], bm.act8_unpack(s["ckpt"]))
+    del back
+    a = bm.act8_pack(x)
+    assert torch.equal(a.q[-TAIL:], s["ckpt"].q) and torch.equal(a.scale[-TAIL:], s["ckpt"].scale)
+    # x serves as the gradient, too
+    dx = bm.layer_norm_bwd(x, a, o["mean"], o["rstd"], dsum=x)[0]
+    ds = bm.layer_norm_bwd(tail, s["ckpt"], s["mean"], s["rstd"], dsum=tail)[0]
+    assert torch.equal(dx[-TAIL:], ds)
+    del dx, o
+    w = torch.ones(BIG_C, device=DEV)
+    dy, dz, _ = bm.gated_norm_bwd(x, a, a, w)
+    ey, ez, _ = bm.gated_norm_bwd(tail, s["ckpt"], s["ckpt"], w)
+    assert torch.equal(dy[-TAIL:], ey) and torch.equal(dz[-TAIL:], ez)
+
+
+def test_convolution_past_32_bits():
+    g = _gen(52)
+    L, H, P, G, N = 525000, 64, 64, 1, 16
+    ch, tail = H * P + 2 * N, 200
+    d = dict(xbc=torch.empty(1, L, ch, dtype=torch.bfloat16, device=DEV).normal_(generator=g),
+             weight=_randn(g, ch, 4) * 0.5, bias=_randn(g, ch))
+    gr = dict(x=torch.empty(1, L, H, P, device=DEV).normal_(generator=g), B=_randn(g, 1, L, G, N),
+              C=_randn(g, 1, L, G, N))
+    d["xbc"] = bm.act8_pack(d["xbc"])
+
+    def cut(v):
+        return v[:, -tail:].contiguous()
+    sd = dict(d, xbc=bm.Act8(cut(d["xbc"].q), cut(d["xbc"].scale)))
+    sg = {k: cut(v) for k, v in gr.items()}
+    for big, small in zip(bm.conv1d_bwd(d, d, gr, gr, H, P, G, N), bm.conv1d_bwd(sd, sd, sg, sg, H, P, G, N)):
+        assert torch.equal(big["xbc"][:, -100:], small["xbc"][:, -100:])
+    for big, small in zip(bm.conv1d(d, d, H, P, G, N), bm.conv1d(sd, sd, H, P, G, N)):
+        for k in ("x", "B", "C"):
+            assert torch.equal(big[k][:, -100:], small[k][:, -100:]), k
