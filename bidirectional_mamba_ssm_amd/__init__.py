@@ -35,7 +35,7 @@ def _check(t, name, shape, dtype, device):
     """The library sees plain pointers: every tensor's device, dtype, shape and
     layout is checked here, before anything is launched."""
     if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous() \
-            and t.device == device:
+            and t.get_device() == device.index:
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -610,9 +610,12 @@ def _size(query, *sizes):
 
 @functools.lru_cache(maxsize=4096)
 def _conv_size(query, shape, *sizes):
+    """(the workspace, the bimamba_conv_shape to pass, which the library only
+    reads) for plain sizes."""
     n = ctypes.c_size_t(0)
-    _abi.check(getattr(lib(), query)(ctypes.byref(_abi.ConvShape(*shape)), *sizes, ctypes.byref(n)))
-    return n.value
+    cshape = ctypes.byref(_abi.ConvShape(*shape))
+    _abi.check(getattr(lib(), query)(cshape, *sizes, ctypes.byref(n)))
+    return n.value, cshape
 
 
 def _workspace(nbytes, dev):
@@ -792,7 +795,10 @@ def layer_norm_bwd(dout, x, mean, rstd, weight=None, dsum=None, wgrad=True, dx=N
     dw = db = ws = None
     nbytes = 0
     if wgrad:
-        dw, db = torch.empty((2, C), dtype=torch.float32, device=dev).unbind(0)
+        if weight is not None:
+            dw, db = torch.empty_like(weight), torch.empty_like(weight)
+        else:
+            dw, db = torch.empty((2, C), dtype=torch.float32, device=dev).unbind(0)
         nbytes = _size("bimamba_layer_norm_bwd_workspace_size", rows, C, code)
         ws = _workspace(nbytes, dev)
     rc = lib().bimamba_layer_norm_bwd(
@@ -874,13 +880,20 @@ def _conv1d_act8(fwd, bwd, dims, activation, cu_seqlens, out, dtype, stream):
         bias = d.get("bias")
         if bias is not None:
             _check(bias, name + ".bias", (ch,), torch.float32, dev)
-        o = res[i] = _conv_out(outs[i], batch, L, H, P, G, N, dtype, dev, name)
+        o = outs[i]
+        if o is None:
+            o = dict(x=torch.empty((batch, L, H, P), dtype=dtype, device=dev),
+                     B=torch.empty((batch, L, G, N), dtype=dtype, device=dev))
+            o["C"] = torch.empty_like(o["B"])
+        else:
+            _conv_out(o, batch, L, H, P, G, N, dtype, dev, name)
+        res[i] = o
         args[2 * i] = ctypes.byref(_abi.ConvDir(None, d["weight"].data_ptr(), _adr(bias), o["x"].data_ptr(),
                                                 o["B"].data_ptr(), o["C"].data_ptr()))
         args[2 * i + 1] = ctypes.byref(_abi.Act8Ptrs(q, scale))
-    nbytes = _conv_size("bimamba_conv1d_act8_workspace_size", sizes, nseq)
+    nbytes, cshape = _conv_size("bimamba_conv1d_act8_workspace_size", sizes, nseq)
     ws = _workspace(nbytes, dev)
-    rc = lib().bimamba_conv1d_act8(ctypes.byref(_abi.ConvShape(*sizes)), *args, cu_arr, nseq, _adr(ws), nbytes,
+    rc = lib().bimamba_conv1d_act8(cshape, *args, cu_arr, nseq, _adr(ws), nbytes,
                                    _raw_stream(dev.index))
     if rc:
         _abi.check(rc)
@@ -940,9 +953,9 @@ def conv1d_bwd(fwd, bwd, gfwd, gbwd, nheads, headdim, ngroups, d_state, activati
         res[i] = dict(xbc=dxbc, weight=dw, bias=db)
         args[i] = ctypes.byref(_abi.ConvGrad(xp, xs, w.data_ptr(), _adr(bias), gx.data_ptr(), gB.data_ptr(),
                                              gC.data_ptr(), dxbc.data_ptr(), dw.data_ptr(), _adr(db)))
-    nbytes = _conv_size("bimamba_conv1d_bwd_workspace_size", sizes, 0 if bwd is None else 1, nseq)
+    nbytes, cshape = _conv_size("bimamba_conv1d_bwd_workspace_size", sizes, 0 if bwd is None else 1, nseq)
     ws = _workspace(nbytes, dev)
-    rc = lib().bimamba_conv1d_bwd(ctypes.byref(_abi.ConvShape(*sizes)), args[0], args[1], cu_arr, nseq, _adr(ws),
+    rc = lib().bimamba_conv1d_bwd(cshape, args[0], args[1], cu_arr, nseq, _adr(ws),
                                   nbytes, _raw_stream(dev.index))
     if rc:
         _abi.check(rc)
