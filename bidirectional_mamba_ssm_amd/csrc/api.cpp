@@ -1001,6 +1001,9 @@ int bimamba_conv1d_bwd(const bimamba_conv_shape *s, const bimamba_conv_grad *fwd
     if (bwd && (rc = check_conv_grad(bwd, "reverse", empty))) return rc;
     if (bwd && !empty && !fwd->xbc_scale != !bwd->xbc_scale)
         return fail(BIMAMBA_EUNSUPPORTED, "both directions' inputs must be checkpoints, or neither");
+    if (bwd && (fwd->dweight == bwd->dweight || (fwd->dbias && fwd->dbias == bwd->dbias) ||
+                (!empty && fwd->dxbc == bwd->dxbc)))
+        return fail(BIMAMBA_EINVAL, "the two directions' gradients must be different arrays");
     if (cu_seqlens) {
         if (s->batch != 1) return fail(BIMAMBA_EINVAL, "cu_seqlens requires batch == 1");
         if ((rc = check_offsets(cu_seqlens, nseq, s->seqlen))) return rc;

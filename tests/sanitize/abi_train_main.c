@@ -48,7 +48,8 @@ int main(void) {
 
     EXPECT(BIMAMBA_EINVAL, bimamba_conv1d_bwd(0, &g, 0, 0, 0, 0, 0, 0));
     EXPECT(BIMAMBA_EINVAL, bimamba_conv1d_bwd(&s, 0, 0, 0, 0, 0, 0, 0));
-    EXPECT(BIMAMBA_EWORKSPACE, bimamba_conv1d_bwd(&s, &g, &g, 0, 0, 0, 0, 0));
+    EXPECT(BIMAMBA_EWORKSPACE, bimamba_conv1d_bwd(&s, &g, 0, 0, 0, 0, 0, 0));
+    EXPECT(BIMAMBA_EINVAL, bimamba_conv1d_bwd(&s, &g, &g, 0, 0, 0, 0, 0));
     EXPECT(BIMAMBA_EINVAL, bimamba_conv1d_bwd(&s, &g, 0, 0, 1, 0, 0, 0));
     EXPECT(BIMAMBA_EWORKSPACE, bimamba_conv1d_bwd(&s, &g, 0, cu, 130, p, 16, 0));
     EXPECT(BIMAMBA_OK, bimamba_conv1d_bwd_workspace_size(&s, 1, 130, &n));

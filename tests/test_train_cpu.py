@@ -253,6 +253,11 @@ def test_conv_bwd_refused(lib):
         assert _cb(lib, f=_cgrad(**{name: FAKE + 2})) == E, name
     assert _cb(lib, f=_cgrad(xbc_scale=FAKE), b=_cgrad()) == U
     assert _cb(lib, b=_cgrad(dC=None)) == E
+    other = dict(dxbc=FAKE * 2, dweight=FAKE * 2, dbias=FAKE * 2)
+    assert _cb(lib, b=_cgrad(**other)) == K
+    for name in other:   # one array for both directions
+        assert _cb(lib, b=_cgrad(**dict(other, **{name: FAKE}))) == E, name
+    assert _cb(lib, f=_cgrad(dbias=None), b=_cgrad(**dict(other, dbias=None))) == K
     assert _cb(lib, nseq=2) == E
     assert _cb(lib, cu=[0, 3, 7], nseq=2) == E
     assert _cb(lib, cu=[0, 5, 4, 8], nseq=3) == E
@@ -262,7 +267,7 @@ def test_conv_bwd_refused(lib):
     assert lib.bimamba_conv1d_bwd_workspace_size(ctypes.byref(s), 1, 0, None) == E
     assert lib.bimamba_conv1d_bwd_workspace_size(ctypes.byref(s), 1, -1, ctypes.byref(n)) == E
     assert lib.bimamba_conv1d_bwd_workspace_size(ctypes.byref(s), 1, 2, ctypes.byref(n)) == 0
-    assert _cb(lib, b=_cgrad(), cu=[0, 3, 8], nseq=2, ws=FAKE, wsb=n.value - 1) == K
+    assert _cb(lib, b=_cgrad(**other), cu=[0, 3, 8], nseq=2, ws=FAKE, wsb=n.value - 1) == K
 
 
 def test_conv_act8_refused(lib):
