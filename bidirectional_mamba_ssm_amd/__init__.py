@@ -910,9 +910,10 @@ def conv1d_bwd(fwd, bwd, gfwd, gbwd, nheads, headdim, ngroups, d_state, activati
     x [b,L,H,P], B and C [b,L,G,N] (ssd_bwd's results serve as they are).
     dtype: of the returned xbc gradients; xbc's own unless xbc is a
     checkpoint (then bf16 if not given). out: optional (fwd, bwd) tensors for
-    the xbc gradients. Returns (fwd, bwd) dicts: xbc [b,L,ch] in that dtype,
-    weight [ch,W] and bias [ch] (None without a bias) float32; bwd None if
-    not given."""
+    the xbc gradients; they may not overlap each other or an input (xbc
+    itself least of all: a token's gradient is made from its neighbours').
+    Returns (fwd, bwd) dicts: xbc [b,L,ch] in that dtype, weight [ch,W] and
+    bias [ch] (None without a bias) float32; bwd None if not given."""
     xbc = fwd["xbc"]
     dev = _cuda_device(xbc)
     if _elsewhere(dev, stream):

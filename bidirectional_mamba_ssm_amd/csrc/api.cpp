@@ -6,6 +6,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <initializer_list>
 #include <string>
 #include <vector>
 
@@ -226,6 +227,30 @@ int check_workspace(const void *ws, size_t have, size_t need) {
     if ((uintptr_t)ws & 255u) return fail(BIMAMBA_EINVAL, "workspace must be 256-byte aligned");
     return BIMAMBA_OK;
 }
+
+// The arrays of a training step, by which calls whose results would depend on
+// the order of reads and writes are refused.
+struct Array {
+    const char *name;
+    const void *p;             // NULL: not given
+    size_t bytes;
+};
+bool overlap(const Array &a, const Array &b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x && y && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+// none of the arrays written may overlap another one or an array read
+int check_apart(std::initializer_list<Array> written, std::initializer_list<Array> read) {
+    for (const Array *w = written.begin(); w != written.end(); ++w) {
+        for (const Array *v = w + 1; v != written.end(); ++v)
+            if (overlap(*w, *v)) return fail(BIMAMBA_EINVAL, "%s overlaps %s", w->name, v->name);
+        for (const Array &r : read)
+            if (overlap(*w, r)) return fail(BIMAMBA_EINVAL, "%s overlaps %s", w->name, r.name);
+    }
+    return BIMAMBA_OK;
+}
+size_t elem_size(int dtype) { return dtype == BIMAMBA_BF16 ? 2 : 4; }
+size_t act8_blocks(long long channels) { return (size_t)((channels + 31) / 32); }
 
 // rows of an array of activations: element indexes stay far inside 63 bits
 int check_rows(long long rows, int dtype) {
@@ -1014,6 +1039,24 @@ int bimamba_conv1d_bwd(const bimamba_conv_shape *s, const bimamba_conv_grad *fwd
     const size_t seq_bytes = seqs_workspace(cu_seqlens ? nseq : 0, s->seqlen);
     const size_t dir_bytes = conv_bwd_dir_bytes(s, ndir);
     if ((rc = check_workspace(workspace, workspace_bytes, seq_bytes + ndir * dir_bytes))) return rc;
+    // a run reads rows of xbc before and after its own, which other waves write
+    const size_t tok = (size_t)s->batch * s->seqlen;
+    const size_t hp = (size_t)s->nheads * s->headdim, gn = (size_t)s->ngroups * s->d_state, ch = hp + 2 * gn;
+    const size_t e = elem_size(s->dtype), ex = fwd->xbc_scale ? 1 : e, nb = act8_blocks((long long)ch);
+    const bimamba_conv_grad none = {}, &f = *fwd, &r = bwd ? *bwd : none;
+    if ((rc = check_apart({{"the forward dxbc", f.dxbc, tok * ch * e}, {"the forward dweight", f.dweight, ch * s->width * 4},
+                           {"the forward dbias", f.dbias, ch * 4}, {"the reverse dxbc", r.dxbc, tok * ch * e},
+                           {"the reverse dweight", r.dweight, ch * s->width * 4}, {"the reverse dbias", r.dbias, ch * 4},
+                           {"the workspace", workspace, seq_bytes + ndir * dir_bytes}},
+                          {{"the forward xbc", f.xbc, tok * ch * ex}, {"the forward xbc_scale", f.xbc_scale, tok * nb},
+                           {"the forward weight", f.weight, ch * s->width * 4}, {"the forward bias", f.bias, ch * 4},
+                           {"the forward dx", f.dx, tok * hp * 4}, {"the forward dB", f.dB, tok * gn * 4},
+                           {"the forward dC", f.dC, tok * gn * 4}, {"the reverse xbc", r.xbc, tok * ch * ex},
+                           {"the reverse xbc_scale", r.xbc_scale, tok * nb},
+                           {"the reverse weight", r.weight, ch * s->width * 4}, {"the reverse bias", r.bias, ch * 4},
+                           {"the reverse dx", r.dx, tok * hp * 4}, {"the reverse dB", r.dB, tok * gn * 4},
+                           {"the reverse dC", r.dC, tok * gn * 4}})))
+        return rc;
     ConvBwdArgs a;
     memset(&a, 0, sizeof a);
     const bimamba_conv_grad *dirs[2] = {fwd, bwd};
@@ -1039,11 +1082,11 @@ int bimamba_conv1d_bwd(const bimamba_conv_shape *s, const bimamba_conv_grad *fwd
     a.ndir = ndir;
     a.act = s->activation;
     hipStream_t st = (hipStream_t)stream;
-    hipError_t e;
-    if ((e = set_packed(a.packed, empty ? nullptr : cu_seqlens, nseq, s->seqlen, workspace, st)) != hipSuccess)
-        return hip_fail(e, "building sequence index");
-    e = launch_conv_bwd(a, s->dtype == BIMAMBA_BF16, st);
-    return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the convolution's gradient");
+    hipError_t err;
+    if ((err = set_packed(a.packed, empty ? nullptr : cu_seqlens, nseq, s->seqlen, workspace, st)) != hipSuccess)
+        return hip_fail(err, "building sequence index");
+    err = launch_conv_bwd(a, s->dtype == BIMAMBA_BF16, st);
+    return err == hipSuccess ? BIMAMBA_OK : hip_fail(err, "launching the convolution's gradient");
 }
 
 int bimamba_gated_norm_bwd_workspace_size(long long rows, int channels, int group_size, int dtype, size_t *bytes) {

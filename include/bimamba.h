@@ -443,8 +443,9 @@ typedef struct {
 } bimamba_conv_grad;
 int bimamba_conv1d_bwd_workspace_size(const bimamba_conv_shape *s, int has_bwd, int nseq, size_t *bytes);
 /* cu_seqlens and nseq as in bimamba_conv1d. seqlen at most 2^30. xbc, dx, dB,
- * dC and dxbc 16-byte aligned, workspace 256-byte aligned. Outputs must not
- * overlap each other or an input; with no token the weights' gradients are 0. */
+ * dC and dxbc 16-byte aligned, workspace 256-byte aligned. Calls whose outputs
+ * or workspace overlap each other or an input are refused; with no token the
+ * weights' gradients are 0. */
 int bimamba_conv1d_bwd(const bimamba_conv_shape *s, const bimamba_conv_grad *fwd, const bimamba_conv_grad *bwd,
                        const int32_t *cu_seqlens, int nseq, void *workspace, size_t workspace_bytes,
                        bimamba_stream stream);

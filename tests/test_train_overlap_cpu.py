@@ -1,0 +1,107 @@
+"""Arrays of the training steps that overlap where a result would depend on
+the order of reads and writes: such calls are refused before any HIP call.
+CPU only, on addresses that are never dereferenced."""
+import ctypes
+import os
+
+import pytest
+
+from bidirectional_mamba_ssm_amd import _abi
+
+STEP = 1 << 24   # further apart than any array here is long
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(_abi.LIB_PATH):
+        from bidirectional_mamba_ssm_amd import build
+        build.build()
+    return _abi.load()
+
+
+class Places:
+    """Addresses of named arrays, each in a place of its own."""
+
+    def __init__(self):
+        self.used = {}
+
+    def __call__(self, name):
+        return self.used.setdefault(name, STEP * (len(self.used) + 1))
+
+
+def _refused(lib, rc, *names):
+    assert rc == _abi.EINVAL, (rc, lib.bimamba_last_error())
+    msg = lib.bimamba_last_error().decode()
+    assert "overlaps" in msg and all(n in msg for n in names), msg
+
+
+# ---- the convolution's gradient ---------------------------------------------------
+
+B_, L_, H_, P_, N_, G_, W_ = 2, 50, 2, 16, 16, 1, 4
+CH = H_ * P_ + 2 * G_ * N_
+TOK = B_ * L_
+# bytes of each array (bf16) and whether the call writes it
+CONV = dict(xbc=(TOK * CH * 2, False), weight=(CH * W_ * 4, False), bias=(CH * 4, False),
+            dx=(TOK * H_ * P_ * 4, False), dB=(TOK * N_ * 4, False), dC=(TOK * N_ * 4, False),
+            dxbc=(TOK * CH * 2, True), dweight=(CH * W_ * 4, True), dbias=(CH * 4, True))
+
+
+def _conv_bwd(lib, at, q8=False):
+    s = _abi.ConvShape(B_, L_, H_, P_, N_, G_, W_, _abi.BF16, 1, 0)
+    n = ctypes.c_size_t(0)
+    assert lib.bimamba_conv1d_bwd_workspace_size(ctypes.byref(s), 1, 0, ctypes.byref(n)) == 0
+    dirs = [_abi.ConvGrad(at[r + "xbc"], at[r + "scale"] if q8 else None, at[r + "weight"], at[r + "bias"],
+                          at[r + "dx"], at[r + "dB"], at[r + "dC"], at[r + "dxbc"], at[r + "dweight"],
+                          at[r + "dbias"]) for r in "fr"]
+    return lib.bimamba_conv1d_bwd(ctypes.byref(s), ctypes.byref(dirs[0]), ctypes.byref(dirs[1]), None, 0, at["ws"],
+                                  n.value, None)
+
+
+def _conv_places():
+    p = Places()
+    at = {r + k: p(r + k) for r in "fr" for k in list(CONV) + ["scale"]}
+    at["ws"] = p("ws")
+    return at
+
+
+@pytest.mark.parametrize("out", ["fdxbc", "rdxbc"])
+@pytest.mark.parametrize("src", ["fxbc", "rxbc"])
+def test_conv_bwd_onto_its_input(lib, out, src):
+    at = _conv_places()
+    at[out] = at[src]
+    _refused(lib, _conv_bwd(lib, at), "dxbc", "xbc")
+
+
+@pytest.mark.parametrize("src", sorted(CONV))
+def test_conv_bwd_partial_overlaps(lib, src):
+    """An output that begins inside another array's last bytes, and one that
+    ends in another's first ones."""
+    nbytes = CONV[src][0]
+    for r in "fr":
+        at = _conv_places()
+        if r + src != "fdxbc":
+            at["fdxbc"] = at[r + src] + (nbytes - 1) // 16 * 16
+            _refused(lib, _conv_bwd(lib, at), "the forward dxbc")
+            at = _conv_places()
+            at["fdxbc"] = at[r + src] - (CONV["dxbc"][0] - 16)
+            _refused(lib, _conv_bwd(lib, at), "the forward dxbc")
+        if r + src != "rdweight":
+            at = _conv_places()
+            at["rdweight"] = at[r + src] + nbytes - 4
+            _refused(lib, _conv_bwd(lib, at), "the reverse dweight")
+
+
+def test_conv_bwd_checkpoints_and_workspace(lib):
+    for out, size in (("fdxbc", 16), ("rdxbc", 16), ("fdweight", 4), ("rdbias", 4)):
+        at = _conv_places()
+        at[out] = at["rscale"] + (TOK * 2 - 1) // size * size
+        _refused(lib, _conv_bwd(lib, at, q8=True), "the reverse xbc_scale")
+        at = _conv_places()
+        at[out] = at["fxbc"] + TOK * CH - size   # a byte an element
+        _refused(lib, _conv_bwd(lib, at, q8=True), "the forward xbc")
+        at = _conv_places()
+        at[out] = at["ws"]
+        _refused(lib, _conv_bwd(lib, at), "the workspace")
+    at = _conv_places()
+    at["rdC"] = at["ws"]
+    _refused(lib, _conv_bwd(lib, at), "the workspace", "the reverse dC")
