@@ -987,7 +987,21 @@ int bimamba_conv1d_act8(const bimamba_conv_shape *s, const bimamba_conv_dir *fwd
     } else if (nseq != 0) {
         return fail(BIMAMBA_EINVAL, "nseq %d given without cu_seqlens", nseq);
     }
-    if ((rc = check_workspace(workspace, workspace_bytes, seqs_workspace(cu_seqlens ? nseq : 0, s->seqlen)))) return rc;
+    const size_t seq_bytes = seqs_workspace(cu_seqlens ? nseq : 0, s->seqlen);
+    if ((rc = check_workspace(workspace, workspace_bytes, seq_bytes))) return rc;
+    const size_t tok = (size_t)s->batch * s->seqlen;
+    const size_t hp = (size_t)s->nheads * s->headdim, gn = (size_t)s->ngroups * s->d_state, ch = hp + 2 * gn;
+    const size_t el = elem_size(s->dtype), nb = act8_blocks((long long)ch);
+    const ConvAct8Dir &f = a.dir[0], &r = a.dir[1];
+    if ((rc = check_apart({{"the forward x", f.x, tok * hp * el}, {"the forward B", f.B, tok * gn * el},
+                           {"the forward C", f.C, tok * gn * el}, {"the reverse x", r.x, tok * hp * el},
+                           {"the reverse B", r.B, tok * gn * el}, {"the reverse C", r.C, tok * gn * el},
+                           {"the workspace", workspace, seq_bytes}},
+                          {{"the forward q", f.q, tok * ch}, {"the forward scale", f.scale, tok * nb},
+                           {"the forward weight", f.weight, ch * s->width * 4}, {"the forward bias", f.bias, ch * 4},
+                           {"the reverse q", r.q, tok * ch}, {"the reverse scale", r.scale, tok * nb},
+                           {"the reverse weight", r.weight, ch * s->width * 4}, {"the reverse bias", r.bias, ch * 4}})))
+        return rc;
     if (empty) return BIMAMBA_OK;
     a.batch = s->batch;
     a.L = s->seqlen;

@@ -418,7 +418,8 @@ int bimamba_act8_unpack(long long rows, long long channels, int dtype, const bim
  * batch * seqlen, channels as in bimamba_conv1d; q 16-byte aligned): the
  * scan's inputs rebuilt in the backward pass. fwd->xbc and bwd->xbc must be
  * NULL; xbc_bwd goes with bwd. s->dtype is the outputs'. No contexts. seqlen
- * at most 2^30. A workspace is needed with more than 128 packed sequences. */
+ * at most 2^30. A workspace is needed with more than 128 packed sequences.
+ * Outputs that overlap each other or an input are refused. */
 int bimamba_conv1d_act8_workspace_size(const bimamba_conv_shape *s, int nseq, size_t *bytes);
 int bimamba_conv1d_act8(const bimamba_conv_shape *s, const bimamba_conv_dir *fwd,
                         const bimamba_act8 *xbc_fwd, const bimamba_conv_dir *bwd,

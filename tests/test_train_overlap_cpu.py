@@ -105,3 +105,42 @@ def test_conv_bwd_checkpoints_and_workspace(lib):
     at = _conv_places()
     at["rdC"] = at["ws"]
     _refused(lib, _conv_bwd(lib, at), "the workspace", "the reverse dC")
+
+
+# ---- the convolution from checkpoints ----------------------------------------------
+
+C8_OUT = dict(x=TOK * H_ * P_ * 2, B=TOK * N_ * 2, C=TOK * N_ * 2)
+C8_IN = dict(q=TOK * CH, scale=TOK * 2, weight=CH * W_ * 4, bias=CH * 4)
+
+
+def _conv_act8(lib, at):
+    s = _abi.ConvShape(B_, L_, H_, P_, N_, G_, W_, _abi.BF16, 1, 0)
+    dirs = [_abi.ConvDir(None, at[r + "weight"], at[r + "bias"], at[r + "x"], at[r + "B"], at[r + "C"]) for r in "fr"]
+    kept = [_abi.Act8Ptrs(at[r + "q"], at[r + "scale"]) for r in "fr"]
+    return lib.bimamba_conv1d_act8(ctypes.byref(s), ctypes.byref(dirs[0]), ctypes.byref(kept[0]), ctypes.byref(dirs[1]),
+                                   ctypes.byref(kept[1]), None, 0, None, 0, None)
+
+
+@pytest.mark.parametrize("out", [r + k for r in "fr" for k in C8_OUT])
+def test_conv_from_checkpoint_overlaps(lib, out):
+    p = Places()
+    places = {r + k: p(r + k) for r in "fr" for k in list(C8_OUT) + list(C8_IN)}
+    for other, place in places.items():
+        if other == out:
+            continue
+        nbytes = (C8_OUT | C8_IN)[other[1:]]
+        for at in (place, place + (nbytes - 1) // 16 * 16, place - C8_OUT[out[1:]] + 16):
+            _refused(lib, _conv_act8(lib, dict(places, **{out: at})))
+
+
+def test_conv_from_checkpoint_onto_its_sequence_table(lib):
+    s = _abi.ConvShape(1, L_, H_, P_, N_, G_, W_, _abi.BF16, 1, 0)
+    p = Places()
+    d = _abi.ConvDir(None, p("weight"), p("bias"), p("x"), p("B"), p("C"))
+    kept = _abi.Act8Ptrs(p("q"), p("scale"))
+    cu = (ctypes.c_int32 * 201)(*[min(i, L_) for i in range(201)])
+    n = ctypes.c_size_t(0)
+    assert lib.bimamba_conv1d_act8_workspace_size(ctypes.byref(s), 200, ctypes.byref(n)) == 0
+    rc = lib.bimamba_conv1d_act8(ctypes.byref(s), ctypes.byref(d), ctypes.byref(kept), None, None, cu, 200, p("C"),
+                                 n.value, None)
+    _refused(lib, rc, "the forward C", "the workspace")
