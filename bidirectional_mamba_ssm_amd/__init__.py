@@ -734,9 +734,11 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, checkpoint=Fa
     C in 8..16384; weight, bias float32 [C] or None.
 
     checkpoint: keep h in 8 bits too (True, or an Act8 to write). sum_out:
-    where to write h with a residual (may be residual or x itself). Returns a
-    dict: out, sum (h; x itself without a residual), mean and rstd (float32
-    [...], for layer_norm_bwd), ckpt (Act8 or None)."""
+    where to write h with a residual. sum_out may be residual or x itself,
+    and so may out with a residual (without one x is what sum returns). Other
+    overlaps are refused. Returns a dict: out, sum (h; x itself without a
+    residual), mean and rstd (float32 [...], for layer_norm_bwd), ckpt (Act8
+    or None)."""
     dev = _cuda_device(x)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
@@ -753,7 +755,12 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, checkpoint=Fa
         _check(weight, "weight", (C,), torch.float32, dev)
     if bias is not None:
         _check(bias, "bias", (C,), torch.float32, dev)
-    out = _out(out, "out", shape, dt, dev, x)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _check(out, "out", shape, dt, dev)
+        if residual is None and rows and out.data_ptr() == x.data_ptr():
+            raise ValueError("out overlaps x, which is returned as sum without a residual")
     if residual is not None:
         sum_out = _out(sum_out, "sum_out", shape, dt, dev, x)
     mean, rstd = torch.empty((2,) + shape[:-1], dtype=torch.float32, device=dev).unbind(0)

@@ -1163,6 +1163,16 @@ int bimamba_layer_norm(long long rows, int channels, int dtype, const void *x, c
         return fail(BIMAMBA_EINVAL, "x, residual, out and sum must be aligned to their elements");
     if (((uintptr_t)weight | (uintptr_t)bias | (uintptr_t)mean | (uintptr_t)rstd) & 3u)
         return fail(BIMAMBA_EINVAL, "weight, bias, mean and rstd must be 4-byte aligned");
+    // x and residual may each be out or sum itself: a row is read before it is
+    // written, and by its own lanes. An input that is an output is tested as that.
+    const size_t C = channels, bytes = rows * C * elem_size(dtype), stat = (size_t)rows * 4;
+    auto apart = [&](const void *in) { return in == out || in == sum ? nullptr : in; };
+    if ((rc = check_apart({{"out", out, bytes}, {"sum", sum, bytes}, {"mean", mean, stat}, {"rstd", rstd, stat},
+                           {"the checkpoint's q", ckpt ? ckpt->q : nullptr, rows * C},
+                           {"the checkpoint's scale", ckpt ? ckpt->scale : nullptr, rows * act8_blocks(channels)}},
+                          {{"x", apart(x), bytes}, {"residual", apart(residual), bytes}, {"weight", weight, C * 4},
+                           {"bias", bias, C * 4}})))
+        return rc;
     LnArgs a;
     memset(&a, 0, sizeof a);
     a.rows = rows;

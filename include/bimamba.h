@@ -479,11 +479,12 @@ int bimamba_gated_norm_bwd(long long rows, int channels, int group_size, int dty
  *  weight    float [channels], or NULL (1);  bias likewise, NULL: 0
  *  out       dtype [rows][channels]
  *  sum       dtype [rows][channels]: h rounded to the dtype, which is what the
- *            norm then sees; with residual only (NULL without). May be x or
- *            residual itself; no other overlap is allowed.
+ *            norm then sees; with residual only (NULL without)
  *  mean, rstd float [rows] for the gradient, or NULL
  *  ckpt      NULL, or where to keep h in 8 bits (the same pass)
- * Arrays are aligned to their elements. Computed in fp32. */
+ * out and sum may each be x or residual itself; calls whose outputs overlap
+ * each other, or an input in any other way, are refused. Arrays are aligned
+ * to their elements. Computed in fp32. */
 int bimamba_layer_norm(long long rows, int channels, int dtype, const void *x, const void *residual,
                        const float *weight, const float *bias, float eps, void *out, void *sum, float *mean,
                        float *rstd, const bimamba_act8 *ckpt, bimamba_stream stream);

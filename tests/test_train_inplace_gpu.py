@@ -1,0 +1,55 @@
+"""Training steps whose results go into one of their own inputs: what the
+documentation allows gives the bits of separate arrays, and what it does not
+allow is refused. Widths at which a row's last vector overlaps a vector of
+another wave are among them."""
+import pytest
+import torch
+
+import bidirectional_mamba_ssm_amd as bm
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+# 2500: neighbours in one wave; the others: in two (bf16 and fp32, forward and gradient)
+WIDTHS = [100, 257, 513, 1025, 1537, 2049, 2500, 4097, 8193]
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _arrays(rows, C, dtype, seed, n):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return [torch.randn(rows, C, generator=g, device=DEV).to(DT[dtype]) for _ in range(n)]
+
+
+def _same(a, b):
+    return all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layer_norm_into_its_inputs(C, dtype):
+    rows = 700
+    print(f"rows {rows} C {C} {dtype}", flush=True)
+    x, r = _arrays(rows, C, dtype, C, 2)
+    want = bm.layer_norm(x, residual=r, checkpoint=True)
+    for into in ((0, None), (1, None), (None, 0), (None, 1), (0, 1), (1, 0)):
+        a = [x.clone(), r.clone()]
+        out, s = (None if i is None else a[i] for i in into)
+        o = bm.layer_norm(a[0], residual=a[1], out=out, sum_out=s, checkpoint=True)
+        assert out is None or o["out"] is out
+        assert s is None or o["sum"] is s
+        assert _same([o["out"], o["sum"], o["mean"], o["rstd"], o["ckpt"].q, o["ckpt"].scale],
+                     [want["out"], want["sum"], want["mean"], want["rstd"], want["ckpt"].q, want["ckpt"].scale]), into
+
+
+def test_layer_norm_refusals():
+    x, r, t = _arrays(6, 200, "bf16", 1, 3)
+    with pytest.raises(bm.BimambaError, match="overlaps"):
+        bm.layer_norm(x, residual=r, out=t, sum_out=t)
+    with pytest.raises(bm.BimambaError, match="overlaps"):
+        bm.layer_norm(x, residual=r, out=x, sum_out=x)
+    with pytest.raises(ValueError, match="overlaps"):
+        bm.layer_norm(x, out=x)
+    buf = torch.zeros(7, 200, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(bm.BimambaError, match="overlaps"):
+        bm.layer_norm(buf[:6], out=buf[1:])
+    bm.layer_norm(x[:0], out=x[:0])   # no row, nothing to overlap

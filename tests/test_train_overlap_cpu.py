@@ -144,3 +144,45 @@ def test_conv_from_checkpoint_onto_its_sequence_table(lib):
     rc = lib.bimamba_conv1d_act8(ctypes.byref(s), ctypes.byref(d), ctypes.byref(kept), None, None, cu, 200, p("C"),
                                  n.value, None)
     _refused(lib, rc, "the forward C", "the workspace")
+
+
+# ---- layer norm -------------------------------------------------------------------------
+
+ROWS, CHS = 9, 72
+LN_OUT = dict(out=ROWS * CHS * 2, sum=ROWS * CHS * 2, mean=ROWS * 4, rstd=ROWS * 4, q=ROWS * CHS, scale=ROWS * 3)
+LN_IN = dict(x=ROWS * CHS * 2, residual=ROWS * CHS * 2, weight=CHS * 4, bias=CHS * 4)
+
+
+def _ln_places():
+    p = Places()
+    return {k: p(k) for k in list(LN_OUT) + list(LN_IN)}
+
+
+def _layer_norm(lib, at):
+    ck = _abi.Act8Ptrs(at["q"], at["scale"])
+    return lib.bimamba_layer_norm(ROWS, CHS, _abi.BF16, at["x"], at["residual"], at["weight"], at["bias"], 1e-5,
+                                  at["out"], at["sum"], at["mean"], at["rstd"], ctypes.byref(ck), None)
+
+
+@pytest.mark.parametrize("out", sorted(LN_OUT))
+def test_layer_norm_overlaps(lib, out):
+    for other, nbytes in (LN_OUT | LN_IN).items():
+        if other == out:
+            continue
+        places = _ln_places()
+        whole = (out in ("out", "sum") and other in ("x", "residual"))   # in place, see below
+        for at in ([] if whole else [places[other]]) + [places[other] + (nbytes - 1) // 4 * 4,
+                                                        places[other] - LN_OUT[out] + 4]:
+            _refused(lib, _layer_norm(lib, dict(places, **{out: at})))
+
+
+@pytest.mark.parametrize("src", ["x", "residual"])
+def test_layer_norm_sum_is_not_out(lib, src):
+    """One array for both results, a place of its own or an input's."""
+    places = _ln_places()
+    _refused(lib, _layer_norm(lib, dict(places, sum=places["out"])), "out", "sum")
+    _refused(lib, _layer_norm(lib, dict(places, sum=places[src], out=places[src])), "out", "sum")
+    # an input that is an output keeps the other outputs away, too
+    for out in ("out", "sum"):
+        for k in ("mean", "q"):
+            _refused(lib, _layer_norm(lib, dict(places, **{out: places[src], k: places[src] + 64})), k)
