@@ -780,7 +780,8 @@ def layer_norm_bwd(dout, x, mean, rstd, weight=None, dsum=None, wgrad=True, dx=N
     """Gradient of layer_norm (bimamba_layer_norm_bwd). dout [..., C]; x: what
     layer_norm returned as sum (dout's dtype) or its Act8 checkpoint; mean,
     rstd float32 [...]; dsum: the gradient reaching sum along the residual
-    stream, added to dx (dx may be dsum itself). Returns (dx, dweight, dbias):
+    stream, added to dx. dx (where to write it) may be dout, dsum or the
+    tensor x itself; other overlaps are refused. Returns (dx, dweight, dbias):
     dx in dout's dtype (the gradient of x and of residual), the other two
     float32 [C], None with wgrad=False."""
     dev = _cuda_device(dout)

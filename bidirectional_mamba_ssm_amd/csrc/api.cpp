@@ -1221,6 +1221,16 @@ int bimamba_layer_norm_bwd(long long rows, int channels, int dtype, const void *
         return fail(BIMAMBA_EINVAL, "weight, mean, rstd, dweight and dbias must be 4-byte aligned");
     const size_t need = wgrad ? (size_t)layer_norm_bwd_wgs(rows, channels, dtype == BIMAMBA_BF16) * 2 * channels * 4 : 0;
     if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+    // dx may be dout, dsum or x itself (x as an array: a checkpoint's bytes lie
+    // elsewhere): a row is read before it is written, and by its own lanes
+    const size_t C = channels, bytes = rows * C * elem_size(dtype), stat = (size_t)rows * 4;
+    auto apart = [&](const void *in) { return in == dx ? nullptr : in; };
+    if ((rc = check_apart({{"dx", dx, bytes}, {"dweight", dweight, C * 4}, {"dbias", dbias, C * 4},
+                           {"the workspace", workspace, need}},
+                          {{"x", x_scale ? x : apart(x), x_scale ? rows * C : bytes},
+                           {"x_scale", x_scale, rows * act8_blocks(channels)}, {"mean", mean, stat}, {"rstd", rstd, stat},
+                           {"weight", weight, C * 4}, {"dout", apart(dout), bytes}, {"dsum", apart(dsum), bytes}})))
+        return rc;
     LnBwdArgs a;
     memset(&a, 0, sizeof a);
     a.rows = rows;

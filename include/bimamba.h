@@ -493,11 +493,12 @@ int bimamba_layer_norm(long long rows, int channels, int dtype, const void *x, c
  *  dout      dtype [rows][channels]
  *  dsum      dtype [rows][channels], the gradient that reaches h along the
  *            residual stream, added to dx; or NULL
- *  dx        out dtype [rows][channels], the gradient of x and of residual;
- *            may be dsum itself, no other overlap is allowed
+ *  dx        out dtype [rows][channels], the gradient of x and of residual
  *  dweight, dbias  out float [channels], or NULL if not wanted
- * The workspace is needed with dweight or dbias only (256-byte aligned). With
- * no row dweight and dbias are 0. */
+ * dx may be dout, dsum or (an array, not a checkpoint) x itself; calls whose
+ * outputs or workspace overlap each other, or an input in any other way, are
+ * refused. The workspace is needed with dweight or dbias only (256-byte
+ * aligned). With no row dweight and dbias are 0. */
 int bimamba_layer_norm_bwd_workspace_size(long long rows, int channels, int dtype, size_t *bytes);
 int bimamba_layer_norm_bwd(long long rows, int channels, int dtype, const void *x, const uint8_t *x_scale,
                            const float *mean, const float *rstd, const float *weight, const void *dout,

@@ -53,3 +53,29 @@ def test_layer_norm_refusals():
     with pytest.raises(bm.BimambaError, match="overlaps"):
         bm.layer_norm(buf[:6], out=buf[1:])
     bm.layer_norm(x[:0], out=x[:0])   # no row, nothing to overlap
+
+
+@pytest.mark.parametrize("C", WIDTHS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layer_norm_bwd_into_its_inputs(C, dtype):
+    rows = 700
+    print(f"rows {rows} C {C} {dtype}", flush=True)
+    x, dout, dsum = _arrays(rows, C, dtype, C, 3)
+    o = bm.layer_norm(x, checkpoint=True)
+    for kept in (x, o["ckpt"]):
+        want = bm.layer_norm_bwd(dout, kept, o["mean"], o["rstd"], dsum=dsum)
+        for into in ("dout", "dsum") + (("x",) if kept is x else ()):
+            a = dict(dout=dout.clone(), dsum=dsum.clone(), x=x.clone())
+            got = bm.layer_norm_bwd(a["dout"], a["x"] if kept is x else kept, o["mean"], o["rstd"], dsum=a["dsum"],
+                                    dx=a[into])
+            assert got[0] is a[into] and _same(got, want), into
+
+
+def test_layer_norm_bwd_refusals():
+    x, dout = _arrays(6, 256, "bf16", 2, 2)
+    o = bm.layer_norm(x, checkpoint=True)
+    buf = torch.zeros(7, 256, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(bm.BimambaError, match="overlaps"):
+        bm.layer_norm_bwd(buf[:6], x, o["mean"], o["rstd"], dx=buf[1:])
+    with pytest.raises(bm.BimambaError, match="overlaps"):
+        bm.layer_norm_bwd(dout, x, o["mean"], o["rstd"], weight=buf.flatten()[:512].view(torch.float32), dx=buf[:6])

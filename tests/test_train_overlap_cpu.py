@@ -186,3 +186,46 @@ def test_layer_norm_sum_is_not_out(lib, src):
     for out in ("out", "sum"):
         for k in ("mean", "q"):
             _refused(lib, _layer_norm(lib, dict(places, **{out: places[src], k: places[src] + 64})), k)
+
+
+# ---- layer norm's gradient ---------------------------------------------------------------
+
+LNB_IN = dict(x=ROWS * CHS * 2, mean=ROWS * 4, rstd=ROWS * 4, weight=CHS * 4, dout=ROWS * CHS * 2, dsum=ROWS * CHS * 2)
+LNB_OUT = dict(dx=ROWS * CHS * 2, dweight=CHS * 4, dbias=CHS * 4)
+
+
+def _lnb_places():
+    p = Places()
+    return {k: p(k) for k in list(LNB_OUT) + list(LNB_IN) + ["scale", "ws"]}
+
+
+def _layer_norm_bwd(lib, at, q8=False):
+    n = ctypes.c_size_t(0)
+    assert lib.bimamba_layer_norm_bwd_workspace_size(ROWS, CHS, _abi.BF16, ctypes.byref(n)) == 0
+    return lib.bimamba_layer_norm_bwd(ROWS, CHS, _abi.BF16, at["x"], at["scale"] if q8 else None, at["mean"], at["rstd"],
+                                      at["weight"], at["dout"], at["dsum"], at["dx"], at["dweight"], at["dbias"],
+                                      at["ws"], n.value, None)
+
+
+@pytest.mark.parametrize("out", sorted(LNB_OUT))
+def test_layer_norm_bwd_overlaps(lib, out):
+    for other, nbytes in (LNB_OUT | LNB_IN).items():
+        if other == out:
+            continue
+        places = _lnb_places()
+        whole = out == "dx" and other in ("x", "dout", "dsum")   # in place
+        for at in ([] if whole else [places[other]]) + [places[other] + (nbytes - 1) // 4 * 4,
+                                                        places[other] - LNB_OUT[out] + 4]:
+            _refused(lib, _layer_norm_bwd(lib, dict(places, **{out: at})))
+    places = _lnb_places()
+    _refused(lib, _layer_norm_bwd(lib, dict(places, **{out: places["ws"]})), "the workspace")
+    for k in ("x", "scale"):
+        _refused(lib, _layer_norm_bwd(lib, dict(places, **{out: places[k]}), q8=True), "x")
+
+
+@pytest.mark.parametrize("src", ["dout", "dsum", "x"])
+def test_layer_norm_bwd_in_place_keeps_others_away(lib, src):
+    places = _lnb_places()
+    places["dx"] = places[src]
+    _refused(lib, _layer_norm_bwd(lib, dict(places, dweight=places[src] + 8)), "dweight")
+    _refused(lib, _layer_norm_bwd(lib, dict(places, rstd=places[src] + 8)), "rstd")
