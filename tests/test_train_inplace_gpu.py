@@ -79,3 +79,28 @@ def test_layer_norm_bwd_refusals():
         bm.layer_norm_bwd(buf[:6], x, o["mean"], o["rstd"], dx=buf[1:])
     with pytest.raises(bm.BimambaError, match="overlaps"):
         bm.layer_norm_bwd(dout, x, o["mean"], o["rstd"], weight=buf.flatten()[:512].view(torch.float32), dx=buf[:6])
+
+
+@pytest.mark.parametrize("C,group", [(256, 256), (1280, 256), (2048, 2048), (5120, 1280), (8192, 8192)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gated_norm_bwd_into_its_inputs(C, group, dtype):
+    rows = 1500
+    print(f"rows {rows} C {C} group {group} {dtype}", flush=True)
+    z, dout = _arrays(rows, C, dtype, C, 2)
+    y, = _arrays(rows, C, "f32", C + 1, 1)
+    w = torch.rand(C, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV) + 0.5
+    want = bm.gated_norm_bwd(dout, y, z, w, group_size=group)
+    for into_y in (False, True):
+        for into_z in (None, "z", "dout"):
+            a = dict(y=y.clone(), z=z.clone(), dout=dout.clone())
+            got = bm.gated_norm_bwd(a["dout"], a["y"], a["z"], w, group_size=group, dy=a["y"] if into_y else None,
+                                    dz=a[into_z] if into_z else None)
+            assert _same(got, want), (into_y, into_z)
+
+
+def test_gated_norm_bwd_refusals():
+    y, z, dout = _arrays(6, 256, "f32", 4, 3)
+    w = torch.ones(256, device=DEV)
+    for kw in (dict(dy=dout), dict(dy=z), dict(dz=y), dict(dy=y, dz=y)):
+        with pytest.raises(bm.BimambaError, match="overlaps"):
+            bm.gated_norm_bwd(dout, y, z, w, **kw)

@@ -229,3 +229,39 @@ def test_layer_norm_bwd_in_place_keeps_others_away(lib, src):
     places["dx"] = places[src]
     _refused(lib, _layer_norm_bwd(lib, dict(places, dweight=places[src] + 8)), "dweight")
     _refused(lib, _layer_norm_bwd(lib, dict(places, rstd=places[src] + 8)), "rstd")
+
+
+# ---- the gated norm's gradient -----------------------------------------------------------
+
+GC = 512
+GN_IN = dict(y=ROWS * GC * 4, z=ROWS * GC * 2, weight=GC * 4, dout=ROWS * GC * 2)
+GN_OUT = dict(dy=ROWS * GC * 4, dz=ROWS * GC * 2, dweight=GC * 4)
+
+
+def _gn_places():
+    p = Places()
+    return {k: p(k) for k in list(GN_OUT) + list(GN_IN) + ["ys", "zs", "ws"]}
+
+
+def _gated_norm_bwd(lib, at, q8=False):
+    n = ctypes.c_size_t(0)
+    assert lib.bimamba_gated_norm_bwd_workspace_size(ROWS, GC, 256, _abi.BF16, ctypes.byref(n)) == 0
+    return lib.bimamba_gated_norm_bwd(ROWS, GC, 256, _abi.BF16, at["y"], at["ys"] if q8 else None, at["z"],
+                                      at["zs"] if q8 else None, at["weight"], 1e-5, at["dout"], at["dy"], at["dz"],
+                                      at["dweight"], at["ws"], n.value, None)
+
+
+@pytest.mark.parametrize("out", sorted(GN_OUT))
+def test_gated_norm_bwd_overlaps(lib, out):
+    for other, nbytes in (GN_OUT | GN_IN).items():
+        if other == out:
+            continue
+        places = _gn_places()
+        whole = (out, other) in (("dy", "y"), ("dz", "z"), ("dz", "dout"))   # in place
+        for at in ([] if whole else [places[other]]) + [places[other] + (nbytes - 1) // 16 * 16,
+                                                        places[other] - GN_OUT[out] + 16]:
+            _refused(lib, _gated_norm_bwd(lib, dict(places, **{out: at})))
+    places = _gn_places()
+    for k in ("y", "z", "ys", "zs"):
+        _refused(lib, _gated_norm_bwd(lib, dict(places, **{out: places[k]}), q8=True), k[0])
+    _refused(lib, _gated_norm_bwd(lib, dict(places, **{out: places["ws"]})), "the workspace")
