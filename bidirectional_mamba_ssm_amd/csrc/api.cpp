@@ -1268,6 +1268,10 @@ static int act8_call(long long rows, long long channels, int dtype, const void *
     if (rows == 0) return BIMAMBA_OK;
     if (!x || !a || !a->q || !a->scale) return fail(BIMAMBA_EINVAL, "x, q and scale are required");
     if (!aligned_to(x, dtype)) return fail(BIMAMBA_EINVAL, "x must be aligned to its elements");
+    const size_t n = (size_t)rows * channels;
+    const Array ax = {"x", x, n * elem_size(dtype)}, aq = {"q", a->q, n},
+                as = {"scale", a->scale, rows * act8_blocks(channels)};
+    if ((rc = pack ? check_apart({aq, as}, {ax}) : check_apart({ax}, {aq, as}))) return rc;
     Act8Args p{rows, channels, const_cast<void *>(x), (int8_t *)a->q, (uint8_t *)a->scale};
     hipError_t e = launch_act8(p, dtype == BIMAMBA_BF16, pack, (hipStream_t)stream);
     return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the 8-bit checkpoint");

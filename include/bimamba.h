@@ -398,8 +398,8 @@ typedef struct {
     void *scale;  /* uint8 [rows][(channels + 31) / 32], the blocks' E          */
 } bimamba_act8;
 /* x: dtype [rows][channels], aligned to its elements (as are q and scale
- * here: to one byte). rows >= 0, channels in [1, 2^31-1]. Arrays may not
- * overlap. */
+ * here: to one byte). rows >= 0, channels in [1, 2^31-1]. Calls whose arrays
+ * written overlap each other or one read are refused. */
 int bimamba_act8_pack(long long rows, long long channels, int dtype, const void *x,
                       const bimamba_act8 *out, bimamba_stream stream);
 int bimamba_act8_unpack(long long rows, long long channels, int dtype, const bimamba_act8 *in,

@@ -104,3 +104,36 @@ def test_gated_norm_bwd_refusals():
     for kw in (dict(dy=dout), dict(dy=z), dict(dz=y), dict(dy=y, dz=y)):
         with pytest.raises(bm.BimambaError, match="overlaps"):
             bm.gated_norm_bwd(dout, y, z, w, **kw)
+
+
+def test_act8_refusals():
+    buf = torch.zeros(4, 128, device=DEV)
+    a = bm.Act8(buf.view(torch.int8)[:, 128:256].contiguous(), torch.zeros(4, 4, dtype=torch.uint8, device=DEV))
+    bm.act8_pack(buf, out=a)
+    over = bm.Act8(buf.view(torch.int8).flatten()[:512].view(4, 128), a.scale)
+    with pytest.raises(bm.BimambaError, match="overlaps"):
+        bm.act8_pack(buf, out=over)
+    with pytest.raises(bm.BimambaError, match="overlaps"):
+        bm.act8_unpack(over, dtype=torch.float32, out=buf)
+
+
+def test_conv1d_refusals():
+    """The convolution's gradient onto its input, and outputs of one array."""
+    batch, L, H, P, G, N = 1, 200, 2, 16, 1, 16
+    ch = H * P + 2 * G * N
+    x = [torch.zeros(batch, L, ch, device=DEV) for _ in range(2)]
+    dirs = [dict(xbc=t, weight=torch.zeros(ch, 4, device=DEV)) for t in x]
+    g = dict(x=torch.zeros(batch, L, H, P, device=DEV), B=torch.zeros(batch, L, G, N, device=DEV),
+             C=torch.zeros(batch, L, G, N, device=DEV))
+    t = torch.zeros_like(x[0])
+    for out in ((x[0], None), (x[1], None), (None, x[0]), (None, x[1]), (t, t)):
+        with pytest.raises(bm.BimambaError, match="overlaps|different arrays"):
+            bm.conv1d_bwd(dirs[0], dirs[1], g, g, H, P, G, N, out=out)
+    kept = [dict(d, xbc=bm.act8_pack(d["xbc"])) for d in dirs]
+    o = dict(x=torch.zeros_like(g["x"]), B=torch.zeros_like(g["B"]), C=torch.zeros_like(g["C"]))
+    for out in ((o, o), (dict(o, C=o["B"]), None)):
+        with pytest.raises(bm.BimambaError, match="overlaps"):
+            bm.conv1d(kept[0], kept[1], H, P, G, N, out=out, dtype=torch.float32)
+    # the same input, weights or gradients for both directions are no overlap
+    want = bm.conv1d_bwd(dirs[0], dict(dirs[0]), g, g, H, P, G, N, out=(t, torch.zeros_like(t)))
+    assert want[0]["xbc"] is t

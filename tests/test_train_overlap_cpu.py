@@ -265,3 +265,24 @@ def test_gated_norm_bwd_overlaps(lib, out):
     for k in ("y", "z", "ys", "zs"):
         _refused(lib, _gated_norm_bwd(lib, dict(places, **{out: places[k]}), q8=True), k[0])
     _refused(lib, _gated_norm_bwd(lib, dict(places, **{out: places["ws"]})), "the workspace")
+
+
+# ---- 8-bit checkpoints ---------------------------------------------------------------------
+
+def test_act8_overlaps(lib):
+    nbytes = dict(x=ROWS * 33 * 4, q=ROWS * 33, scale=ROWS * 2)
+    p = Places()
+    places = {k: p(k) for k in nbytes}
+    for pack in (True, False):
+        for a in nbytes:
+            for b in nbytes:
+                if a == b or (not pack and "x" not in (a, b)):
+                    continue   # an array read may overlap another that is read
+                for at in (places[b], places[b] + (nbytes[b] - 1) // 4 * 4, places[b] - nbytes[a] // 4 * 4 + 4):
+                    q = dict(places, **{a: at})
+                    ck = _abi.Act8Ptrs(q["q"], q["scale"])
+                    if pack:
+                        rc = lib.bimamba_act8_pack(ROWS, 33, _abi.F32, q["x"], ctypes.byref(ck), None)
+                    else:
+                        rc = lib.bimamba_act8_unpack(ROWS, 33, _abi.F32, ctypes.byref(ck), q["x"], None)
+                    _refused(lib, rc)
