@@ -49,6 +49,22 @@ def _check(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _int32s(vals, name):
+    """A C array of integers for the library. ctypes keeps the low 32 bits of a
+    larger number without a word, so that is refused here."""
+    if vals and not (-2 ** 31 <= min(vals) and max(vals) < 2 ** 31):
+        raise ValueError(f"{name} goes beyond 32 bits ({min(vals)} .. {max(vals)})")
+    return (ctypes.c_int32 * len(vals))(*vals)
+
+
+def _offsets(cu_seqlens):
+    """(the C array, the number of sequences) of packed-sequence offsets."""
+    if cu_seqlens is None:
+        return None, 0
+    vals = [int(v) for v in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens)]
+    return _int32s(vals, "cu_seqlens"), len(vals) - 1
+
+
 def _cuda_device(x):
     if x.device.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, not {x.device}")
@@ -114,11 +130,7 @@ def ssd_fwd(fwd, bwd=None, chunk=256, cu_seqlens=None, init_state=None,
     dev = _cuda_device(x)
     fd = _dir(fwd, dtype, dims, dev, "fwd")
     bd = _dir(bwd, dtype, dims, dev, "bwd") if bwd is not None else None
-    cu_arr, nseq = None, 0
-    if cu_seqlens is not None:
-        vals = [int(v) for v in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens)]
-        nseq = len(vals) - 1
-        cu_arr = (ctypes.c_int32 * len(vals))(*vals)
+    cu_arr, nseq = _offsets(cu_seqlens)
     units = nseq if cu_seqlens is not None else batch
     for t, name in ((init_state, "init_state"), (final_state, "final_state")):
         if t is not None:
@@ -203,11 +215,7 @@ def ssd_fwd_noalloc(fwd, bwd, y, chunk=256, cu_seqlens=None, init_state=None,
     dev = _cuda_device(x)
     fd = _dir(fwd, x.dtype, dims, dev, "fwd")
     bd = _dir(bwd, x.dtype, dims, dev, "bwd") if bwd is not None else None
-    cu_arr, nseq = None, 0
-    if cu_seqlens is not None:
-        vals = [int(v) for v in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens)]
-        nseq = len(vals) - 1
-        cu_arr = (ctypes.c_int32 * len(vals))(*vals)
+    cu_arr, nseq = _offsets(cu_seqlens)
     units = nseq if cu_seqlens is not None else batch
     for t, name in ((init_state, "init_state"), (final_state, "final_state")):
         if t is not None:
@@ -230,11 +238,7 @@ def ssd_fwd_streams(fwd, bwd, chunk=256, cu_seqlens=None, init_state=None,
     dev = _cuda_device(x)
     fd = _dir(fwd, x.dtype, dims, dev, "fwd")
     bd = _dir(bwd, x.dtype, dims, dev, "bwd")
-    cu_arr, nseq = None, 0
-    if cu_seqlens is not None:
-        vals = [int(v) for v in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens)]
-        nseq = len(vals) - 1
-        cu_arr = (ctypes.c_int32 * len(vals))(*vals)
+    cu_arr, nseq = _offsets(cu_seqlens)
     units = nseq if cu_seqlens is not None else batch
     for t, name in ((init_state, "init_state"), (final_state, "final_state")):
         if t is not None:
@@ -523,11 +527,7 @@ def conv1d(fwd, bwd, nheads, headdim, ngroups, d_state, activation="silu",
     if bwd is not None:
         bo = _conv_out(outs[1], batch, L, nheads, headdim, ngroups, d_state, xbc.dtype, dev, "bwd")
         bd = _conv_dir(bwd, dims, xbc.dtype, dev, bo, "bwd")
-    cu_arr, nseq = None, 0
-    if cu_seqlens is not None:
-        vals = [int(v) for v in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens)]
-        nseq = len(vals) - 1
-        cu_arr = (ctypes.c_int32 * len(vals))(*vals)
+    cu_arr, nseq = _offsets(cu_seqlens)
     for t, name in ((init_ctx, "init_ctx"), (final_ctx, "final_ctx")):
         if t is not None:
             _check(t, name, (batch, W - 1, ch), xbc.dtype, dev)
@@ -620,13 +620,6 @@ def _conv_size(query, shape, *sizes):
 
 def _workspace(nbytes, dev):
     return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-
-
-def _offsets(cu_seqlens):
-    if cu_seqlens is None:
-        return None, 0
-    vals = [int(v) for v in (cu_seqlens.tolist() if hasattr(cu_seqlens, "tolist") else cu_seqlens)]
-    return (ctypes.c_int32 * len(vals))(*vals), len(vals) - 1
 
 
 class Act8:
@@ -975,13 +968,12 @@ def conv1d_bwd(fwd, bwd, gfwd, gbwd, nheads, headdim, ngroups, d_state, activati
 
 def seq_index(cu_seqlens, device="cuda", stream=None):
     """Per-token packed-sequence index built on the GPU (int32 [total])."""
-    vals = [int(v) for v in cu_seqlens]
-    total = vals[-1]
+    arr, nseq = _offsets(cu_seqlens)
+    total = arr[nseq]
     if torch.device(device).type != "cuda":
         raise ValueError(f"device must be a CUDA device, not {device}")
     out = torch.empty(max(total, 1), dtype=torch.int32, device=device)
-    arr = (ctypes.c_int32 * len(vals))(*vals)
-    _abi.check(lib().bimamba_seq_index(arr, len(vals) - 1, total, _ptr(out), _stream(stream)))
+    _abi.check(lib().bimamba_seq_index(arr, nseq, total, _ptr(out), _stream(stream)))
     return out[:total]
 
 

@@ -1,0 +1,44 @@
+"""Numbers beyond 32 bits are refused by every entry point that takes them
+(the low 32 bits of each make a valid call, which is not the one asked for)."""
+import pytest
+import torch
+
+import bidirectional_mamba_ssm_amd as bm
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+FAR = 2 ** 32
+L, H, P, G, N = 40, 2, 16, 1, 16
+CH = H * P + 2 * G * N
+
+
+def _z(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype, device=DEV)
+
+
+def _scan():
+    return dict(x=_z(1, L, H, P), dt=_z(1, L, H), A=_z(H), B=_z(1, L, G, N), C=_z(1, L, G, N), D=_z(H))
+
+
+def _conv(kept=False):
+    x = _z(1, L, CH)
+    return dict(xbc=bm.act8_pack(x) if kept else x, weight=_z(CH, 4))
+
+
+@pytest.mark.parametrize("cu", [[0, FAR + 7, L], [0, 7, FAR + L]], ids=["inner", "last"])
+def test_offsets(cu):
+    s, c, k, dims = _scan(), _conv(), _conv(True), (H, P, G, N)
+    calls = dict(
+        ssd_fwd=lambda cu: bm.ssd_fwd(s, s, chunk=64, cu_seqlens=cu),
+        ssd_fwd_noalloc=lambda cu: bm.ssd_fwd_noalloc(s, s, _z(1, L, H, P), chunk=64, cu_seqlens=cu),
+        ssd_fwd_streams=lambda cu: bm.ssd_fwd_streams(s, s, chunk=64, cu_seqlens=cu),
+        conv1d=lambda cu: bm.conv1d(c, c, *dims, cu_seqlens=cu),
+        conv1d_act8=lambda cu: bm.conv1d(k, k, *dims, cu_seqlens=cu),
+        conv1d_bwd=lambda cu: bm.conv1d_bwd(c, c, s, s, *dims, cu_seqlens=cu),
+        seq_index=lambda cu: bm.seq_index(cu))
+    for name, call in calls.items():
+        print(name, flush=True)
+        call([v % FAR for v in cu])
+        with pytest.raises(ValueError, match="cu_seqlens.*32 bits"):
+            call(cu)
