@@ -57,6 +57,14 @@ def _int32s(vals, name):
     return (ctypes.c_int32 * len(vals))(*vals)
 
 
+def _int32(v, name):
+    """An integer for the library, refused beyond 32 bits (as in _int32s)."""
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:
+        raise ValueError(f"{name} {v} is beyond 32 bits")
+    return v
+
+
 def _offsets(cu_seqlens):
     """(the C array, the number of sequences) of packed-sequence offsets."""
     if cu_seqlens is None:
@@ -557,9 +565,9 @@ def gated_norm(y, z, weight, group_size=None, eps=1e-5, out=None, stream=None):
     if out is None:
         out = torch.empty(y.shape, dtype=z.dtype, device=dev)
     _check(out, "out", tuple(y.shape), z.dtype, dev)
-    _abi.check(lib().bimamba_gated_norm(rows, C, C if group_size is None else int(group_size),
-                                        DTYPES[z.dtype], _ptr(y), _ptr(z), _ptr(weight),
-                                        float(eps), _ptr(out), _stream(stream)))
+    gs = _int32(C if group_size is None else group_size, "group_size")
+    _abi.check(lib().bimamba_gated_norm(rows, C, gs, DTYPES[z.dtype], _ptr(y), _ptr(z), _ptr(weight), float(eps),
+                                        _ptr(out), _stream(stream)))
     return out
 
 
@@ -824,7 +832,7 @@ def gated_norm_bwd(dout, y, z, weight, group_size=None, eps=1e-5, wgrad=True, dy
     code = _dtype_code(dt)
     _check(dout, "dout", shape, dt, dev)
     rows, C = _rows(shape)
-    gs = C if group_size is None else int(group_size)
+    gs = C if group_size is None else _int32(group_size, "group_size")
     yp, ys = _kept(y, "y", shape, torch.float32, dev)
     zp, zs = _kept(z, "z", shape, dt, dev)
     _check(weight, "weight", (C,), torch.float32, dev)

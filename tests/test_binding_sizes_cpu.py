@@ -30,3 +30,11 @@ def test_offsets_within_32_bits():
 def test_seq_index_beyond_32_bits():
     with pytest.raises(ValueError, match="32 bits"):
         bm.seq_index([0, FAR + 4], device="cpu")
+
+
+def test_int32():
+    for v in (-2 ** 31, -1, 0, 256, 2 ** 31 - 1):
+        assert bm._int32(v, "n") == v
+    for v in (-2 ** 31 - 1, 2 ** 31, FAR + 256, 10 ** 30):
+        with pytest.raises(ValueError, match="group_size.*32 bits"):
+            bm._int32(v, "group_size")

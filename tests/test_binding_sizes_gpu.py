@@ -42,3 +42,14 @@ def test_offsets(cu):
         call([v % FAR for v in cu])
         with pytest.raises(ValueError, match="cu_seqlens.*32 bits"):
             call(cu)
+
+
+def test_group_size():
+    y, w = _z(4, 512), torch.ones(512, device=DEV)
+    bm.gated_norm(y, y, w, group_size=256)
+    bm.gated_norm_bwd(y, y, y, w, group_size=256)
+    for gs in (FAR + 256, 256 - FAR):
+        with pytest.raises(ValueError, match="group_size.*32 bits"):
+            bm.gated_norm(y, y, w, group_size=gs)
+        with pytest.raises(ValueError, match="group_size.*32 bits"):
+            bm.gated_norm_bwd(y, y, y, w, group_size=gs)
