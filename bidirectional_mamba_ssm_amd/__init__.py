@@ -49,16 +49,21 @@ def _check(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _int32s(vals, name):
-    """A C array of integers for the library. ctypes keeps the low 32 bits of a
-    larger number without a word, so that is refused here."""
+def _within_32_bits(vals, name):
+    """ctypes passes on the low 32 bits of a larger number without a word, so
+    every integer that the library takes as a C int is checked first."""
     if vals and not (-2 ** 31 <= min(vals) and max(vals) < 2 ** 31):
         raise ValueError(f"{name} goes beyond 32 bits ({min(vals)} .. {max(vals)})")
+
+
+def _int32s(vals, name):
+    """A C array of integers for the library."""
+    _within_32_bits(vals, name)
     return (ctypes.c_int32 * len(vals))(*vals)
 
 
 def _int32(v, name):
-    """An integer for the library, refused beyond 32 bits (as in _int32s)."""
+    """An integer for the library."""
     v = int(v)
     if not -2 ** 31 <= v < 2 ** 31:
         raise ValueError(f"{name} {v} is beyond 32 bits")
@@ -111,8 +116,14 @@ def make_shape(x, B, chunk, seqlen=None, dt_softplus=False):
     G, N = B.shape[2], B.shape[3]
     if x.dtype not in DTYPES:
         raise TypeError(f"unsupported dtype {x.dtype}")
-    return _abi.Shape(batch, L if seqlen is None else seqlen, H, P, N, G, chunk,
-                      DTYPES[x.dtype], _abi.DT_SOFTPLUS if dt_softplus else 0)
+    sizes = (batch, L if seqlen is None else seqlen, H, P, N, G, chunk)
+    _within_32_bits(sizes, "the problem's shape")
+    return _abi.Shape(*sizes, DTYPES[x.dtype], _abi.DT_SOFTPLUS if dt_softplus else 0)
+
+
+def _conv_shape(*sizes):
+    _within_32_bits(sizes, "the convolution's shape")
+    return _abi.ConvShape(*sizes)
 
 
 def workspace_size(shape, nseq=0):
@@ -285,6 +296,7 @@ def merge_linear(y_fwd, y_bwd, weight, bias=None, out=None, stream=None):
     if out is None:
         out = torch.empty(oshape, dtype=torch.float32, device=dev)
     _check(out, "out", oshape, torch.float32, dev)
+    _within_32_bits((cin, cout), "the merge's channels")
     _abi.check(lib().bimamba_merge_linear(rows, cin, cout, _ptr(y_fwd), _ptr(y_bwd), _ptr(weight),
                                           _ptr(bias), _ptr(out), _stream(stream)))
     return out
@@ -298,6 +310,8 @@ class State:
     def __init__(self, nslots, nheads, headdim, d_state, conv=None):
         self._h = ctypes.c_void_p()
         self.conv = None
+        _within_32_bits((nslots, nheads, headdim, d_state) + tuple(conv[:2] if conv is not None else ()),
+                        "the state's shape")
         if conv is None:
             _abi.check(lib().bimamba_state_alloc(ctypes.byref(self._h), nslots, nheads,
                                                  headdim, d_state))
@@ -347,7 +361,7 @@ class State:
         if slots is not None:
             slots = [int(s) for s in slots]
             n = len(slots)
-            arr = (ctypes.c_int32 * max(n, 1))(*slots)
+            arr = _int32s(slots or [0], "slots")
         _abi.check(lib().bimamba_state_reset(self._h, arr, n, _stream(stream)))
 
     def free(self):
@@ -423,7 +437,7 @@ def block_step_conv(state, fwd, bwd, conv_fwd, conv_bwd, commit=False, chunk=64,
     if y is None:
         y = torch.empty((batch, L, H, P), dtype=torch.float32, device=dev)
     _check(y, "y", (batch, L, H, P), torch.float32, dev)
-    cshape = _abi.ConvShape(batch, L, H, P, N, ngroups, W, DTYPES[xbc.dtype], ACTIVATIONS[activation], 0)
+    cshape = _conv_shape(batch, L, H, P, N, ngroups, W, DTYPES[xbc.dtype], ACTIVATIONS[activation], 0)
     _abi.check(lib().bimamba_block_step_conv(
         state.handle, ctypes.byref(cshape), ctypes.byref(cfd), ctypes.byref(cbd),
         ctypes.byref(shape), ctypes.byref(fd), ctypes.byref(bd), int(bool(commit)), _ptr(y),
@@ -539,8 +553,8 @@ def conv1d(fwd, bwd, nheads, headdim, ngroups, d_state, activation="silu",
     for t, name in ((init_ctx, "init_ctx"), (final_ctx, "final_ctx")):
         if t is not None:
             _check(t, name, (batch, W - 1, ch), xbc.dtype, dev)
-    shape = _abi.ConvShape(batch, L, nheads, headdim, d_state, ngroups, W,
-                           DTYPES[xbc.dtype], ACTIVATIONS[activation], 0)
+    shape = _conv_shape(batch, L, nheads, headdim, d_state, ngroups, W,
+                        DTYPES[xbc.dtype], ACTIVATIONS[activation], 0)
     n = ctypes.c_size_t(0)
     _abi.check(lib().bimamba_conv1d_workspace_size(ctypes.byref(shape), nseq, ctypes.byref(n)))
     ws = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
@@ -566,7 +580,7 @@ def gated_norm(y, z, weight, group_size=None, eps=1e-5, out=None, stream=None):
         out = torch.empty(y.shape, dtype=z.dtype, device=dev)
     _check(out, "out", tuple(y.shape), z.dtype, dev)
     gs = _int32(C if group_size is None else group_size, "group_size")
-    _abi.check(lib().bimamba_gated_norm(rows, C, gs, DTYPES[z.dtype], _ptr(y), _ptr(z), _ptr(weight), float(eps),
+    _abi.check(lib().bimamba_gated_norm(rows, _int32(C, "channels"), gs, DTYPES[z.dtype], _ptr(y), _ptr(z), _ptr(weight), float(eps),
                                         _ptr(out), _stream(stream)))
     return out
 
@@ -621,7 +635,7 @@ def _conv_size(query, shape, *sizes):
     """(the workspace, the bimamba_conv_shape to pass, which the library only
     reads) for plain sizes."""
     n = ctypes.c_size_t(0)
-    cshape = ctypes.byref(_abi.ConvShape(*shape))
+    cshape = ctypes.byref(_conv_shape(*shape))
     _abi.check(getattr(lib(), query)(cshape, *sizes, ctypes.byref(n)))
     return n.value, cshape
 

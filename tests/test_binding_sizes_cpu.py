@@ -38,3 +38,30 @@ def test_int32():
     for v in (-2 ** 31 - 1, 2 ** 31, FAR + 256, 10 ** 30):
         with pytest.raises(ValueError, match="group_size.*32 bits"):
             bm._int32(v, "group_size")
+
+
+def test_shapes_beyond_32_bits():
+    x, B = torch.zeros(1, 4, 2, 16), torch.zeros(1, 4, 1, 16)
+    assert bm.make_shape(x, B, 64).chunk == 64
+    for kw in (dict(chunk=FAR + 64), dict(chunk=64, seqlen=FAR + 4)):
+        with pytest.raises(ValueError, match="32 bits"):
+            bm.make_shape(x, B, **kw)
+    # a row of more tokens than fit (no memory behind it)
+    far = torch.empty(1, device="meta").expand(1, FAR + 8, 1, 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        bm.make_shape(far, far, 64)
+    ok = (1, 8, 2, 16, 16, 1, 4, 0, 1, 0)
+    assert bm._conv_shape(*ok).nheads == 2
+    for i in range(7):
+        with pytest.raises(ValueError, match="32 bits"):
+            bm._conv_shape(*[v + (FAR if j == i else 0) for j, v in enumerate(ok)])
+
+
+def test_state_beyond_32_bits():
+    """A cache of one slot whose view would have 2^32 + 1."""
+    for dims in ((FAR + 1, 2, 16, 16), (1, FAR + 2, 16, 16), (1, 2, FAR + 16, 16), (1, 2, 16, FAR + 16)):
+        with pytest.raises(ValueError, match="32 bits"):
+            bm.State(*dims)
+    for conv in ((FAR + 1, 4, torch.float32), (1, FAR + 4, torch.float32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            bm.State(1, 2, 16, 16, conv=conv)

@@ -53,3 +53,31 @@ def test_group_size():
             bm.gated_norm(y, y, w, group_size=gs)
         with pytest.raises(ValueError, match="group_size.*32 bits"):
             bm.gated_norm_bwd(y, y, y, w, group_size=gs)
+
+
+def test_other_sizes():
+    s, c, k = _scan(), _conv(), _conv(True)
+    for chunk in (FAR + 64, 64 - FAR):
+        for call in (lambda: bm.ssd_fwd(s, s, chunk=chunk), lambda: bm.ssd_fwd_streams(s, s, chunk=chunk),
+                     lambda: bm.ssd_fwd_noalloc(s, s, _z(1, L, H, P), chunk=chunk)):
+            with pytest.raises(ValueError, match="32 bits"):
+                call()
+    # head and state sizes that come out at the same number of channels
+    far = (2 - FAR, 16, 1, 2 ** 35 + 16)
+    assert bm.conv_channels(*far) == CH
+    for call in (lambda: bm.conv1d(c, None, *far, out=({k: v for k, v in s.items()}, None)),
+                 lambda: bm.conv1d(k, None, *far), lambda: bm.conv1d_bwd(c, None, s, None, *far)):
+        with pytest.raises((ValueError, RuntimeError)):
+            call()
+    st = bm.State(2, H, P, N)
+    try:
+        st.tensor().fill_(1.0)
+        with pytest.raises(ValueError, match="slots.*32 bits"):
+            st.reset([FAR + 1])
+        st.reset([])
+        assert (st.tensor() == 1.0).all()
+        st.reset([1])
+        torch.cuda.synchronize()
+        assert (st.tensor()[0] == 1.0).all() and (st.tensor()[1] == 0.0).all()
+    finally:
+        st.free()
