@@ -227,10 +227,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvBwdArgs a) {
                     // a position past the end has no gradient, whatever its slope
                     if (!live) v = 0.f;
                     du[H + i][j] = v;
-                    const float m = own ? v : 0.f;
-                    ab[j] += m;
+                    // another run's position counts there: its taps may be
+                    // infinite, and a zero times that is no zero
+                    if (own) {
+                        ab[j] += v;
 #pragma unroll
-                    for (int k = 0; k < W; ++k) aw[j][k] = fmaf(m, tap[k], aw[j][k]);
+                        for (int k = 0; k < W; ++k) aw[j][k] = fmaf(v, tap[k], aw[j][k]);
+                    }
                     o[j] = 0.f;
 #pragma unroll
                     for (int k = 0; k < W; ++k) {
