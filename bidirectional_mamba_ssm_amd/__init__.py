@@ -5,6 +5,7 @@ only marshals torch tensors (device memory and the current stream) into the
 C ABI declared in include/bimamba.h. It has no compute path of its own and
 raises if the library is not built.
 """
+import array
 import ctypes
 import functools
 import math
@@ -58,8 +59,12 @@ def _within_32_bits(vals, name):
 
 def _int32s(vals, name):
     """A C array of integers for the library."""
-    _within_32_bits(vals, name)
-    return (ctypes.c_int32 * len(vals))(*vals)
+    try:
+        a = array.array("i", vals)   # checks the range as it converts
+    except OverflowError:
+        _within_32_bits(vals, name)
+        raise
+    return (ctypes.c_int32 * len(a)).from_buffer(a)
 
 
 def _int32(v, name):
