@@ -4,6 +4,13 @@ Every step of the computation runs in libbimamba's HIP kernels; this module
 only marshals torch tensors (device memory and the current stream) into the
 C ABI declared in include/bimamba.h. It has no compute path of its own and
 raises if the library is not built.
+
+Every call is enqueued on the current stream of its tensors' device, or on
+``stream``, which it then makes current while it runs: the results and
+workspaces that it allocates belong to that stream, and the results may be
+used on the stream that was current before, too. As with any torch call on a
+side stream, the caller orders that stream against the ones its inputs come
+from and its results go to.
 """
 import array
 import ctypes
@@ -26,6 +33,52 @@ def _stream(stream=None):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+# Small calls are short next to their own overhead, so they take the current
+# stream's handle and device without the objects that torch.cuda makes of them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _elsewhere(dev, stream):
+    """Whether a call has to go through _run_on()."""
+    return stream is not None or dev.index != _current_device()
+
+
+def _on(dev, stream):
+    """The context of a call on another stream than the current one, or on
+    tensors of another device than the current one: both are made current, so
+    that what the call allocates belongs to the stream it is used on."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _run_on(dev, stream, call, *args):
+    """call(*args) under _on(). Its results go back to the stream that was
+    current, so their memory, which is the other stream's, is not given away
+    before that stream has done with them, either."""
+    outer = torch.cuda.current_stream(dev) if stream is not None else None
+    with _on(dev, stream):
+        res = call(*args)
+    if outer is not None and outer != stream:
+        for t in _tensors(res):
+            t.record_stream(outer)
+    return res
+
+
+def _tensors(res):
+    if isinstance(res, torch.Tensor):
+        return [res]
+    if isinstance(res, Act8):
+        return [res.q, res.scale]
+    if isinstance(res, dict):
+        res = res.values()
+    return [t for r in res for t in _tensors(r)] if res is not None else []
 
 
 def _ptr(t):
@@ -149,9 +202,12 @@ def ssd_fwd(fwd, bwd=None, chunk=256, cu_seqlens=None, init_state=None,
     x = fwd["x"]
     dims = _dims(fwd)
     batch, L, H, P, G, N = dims
-    shape = make_shape(x, fwd["B"], chunk, dt_softplus=dt_softplus)
     dtype = x.dtype
     dev = _cuda_device(x)
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, ssd_fwd, fwd, bwd, chunk, cu_seqlens, init_state, final_state, y, workspace,
+                       None, dt_softplus)
+    shape = make_shape(x, fwd["B"], chunk, dt_softplus=dt_softplus)
     fd = _dir(fwd, dtype, dims, dev, "fwd")
     bd = _dir(bwd, dtype, dims, dev, "bwd") if bwd is not None else None
     cu_arr, nseq = _offsets(cu_seqlens)
@@ -172,7 +228,7 @@ def ssd_fwd(fwd, bwd=None, chunk=256, cu_seqlens=None, init_state=None,
     _abi.check(lib().bimamba_ssd_fwd(
         ctypes.byref(shape), ctypes.byref(fd), ctypes.byref(bd) if bd is not None else None,
         cu_arr, nseq, _ptr(init_state), _ptr(final_state), _ptr(y),
-        _ptr(workspace), ws_bytes, _stream(stream)))
+        _ptr(workspace), ws_bytes, _stream()))
     return y
 
 
@@ -206,8 +262,10 @@ def ssd_bwd(fwd, bwd, dy, grads=None, workspace=None, stream=None):
     x = fwd["x"]
     dims = _dims(fwd)
     batch, L, H, P, G, N = dims
-    shape = make_shape(x, fwd["B"], 64)
     dev = _cuda_device(x)
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, ssd_bwd, fwd, bwd, dy, grads, workspace)
+    shape = make_shape(x, fwd["B"], 64)
     fd = _dir(fwd, x.dtype, dims, dev, "fwd")
     bd = _dir(bwd, x.dtype, dims, dev, "bwd") if bwd is not None else None
     _check(dy, "dy", (batch, L, H, P), torch.float32, dev)
@@ -223,7 +281,7 @@ def ssd_bwd(fwd, bwd, dy, grads=None, workspace=None, stream=None):
     _abi.check(lib().bimamba_ssd_bwd(
         ctypes.byref(shape), ctypes.byref(fd), ctypes.byref(bd) if bd is not None else None,
         _ptr(dy), ctypes.byref(gfs), ctypes.byref(gbs) if gbs is not None else None,
-        _ptr(workspace), ws_bytes, _stream(stream)))
+        _ptr(workspace), ws_bytes, _stream()))
     return gf, gb
 
 
@@ -235,8 +293,11 @@ def ssd_fwd_noalloc(fwd, bwd, y, chunk=256, cu_seqlens=None, init_state=None,
     x = fwd["x"]
     dims = _dims(fwd)
     batch, L, H, P, G, N = dims
-    shape = make_shape(x, fwd["B"], chunk, dt_softplus=dt_softplus)
     dev = _cuda_device(x)
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, ssd_fwd_noalloc, fwd, bwd, y, chunk, cu_seqlens, init_state, final_state, None,
+                       dt_softplus)
+    shape = make_shape(x, fwd["B"], chunk, dt_softplus=dt_softplus)
     fd = _dir(fwd, x.dtype, dims, dev, "fwd")
     bd = _dir(bwd, x.dtype, dims, dev, "bwd") if bwd is not None else None
     cu_arr, nseq = _offsets(cu_seqlens)
@@ -247,7 +308,7 @@ def ssd_fwd_noalloc(fwd, bwd, y, chunk=256, cu_seqlens=None, init_state=None,
     _check(y, "y", (batch, L, H, P), torch.float32, dev)
     _abi.check(lib().bimamba_ssd_fwd_noalloc(
         ctypes.byref(shape), ctypes.byref(fd), ctypes.byref(bd) if bd is not None else None,
-        cu_arr, nseq, _ptr(init_state), _ptr(final_state), _ptr(y), _stream(stream)))
+        cu_arr, nseq, _ptr(init_state), _ptr(final_state), _ptr(y), _stream()))
     return y
 
 
@@ -258,8 +319,11 @@ def ssd_fwd_streams(fwd, bwd, chunk=256, cu_seqlens=None, init_state=None,
     x = fwd["x"]
     dims = _dims(fwd)
     batch, L, H, P, G, N = dims
-    shape = make_shape(x, fwd["B"], chunk)
     dev = _cuda_device(x)
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, ssd_fwd_streams, fwd, bwd, chunk, cu_seqlens, init_state, final_state, y_fwd,
+                       y_bwd, workspace)
+    shape = make_shape(x, fwd["B"], chunk)
     fd = _dir(fwd, x.dtype, dims, dev, "fwd")
     bd = _dir(bwd, x.dtype, dims, dev, "bwd")
     cu_arr, nseq = _offsets(cu_seqlens)
@@ -280,7 +344,7 @@ def ssd_fwd_streams(fwd, bwd, chunk=256, cu_seqlens=None, init_state=None,
     _abi.check(lib().bimamba_ssd_fwd_streams(
         ctypes.byref(shape), ctypes.byref(fd), ctypes.byref(bd), cu_arr, nseq,
         _ptr(init_state), _ptr(final_state), _ptr(outs[0]), _ptr(outs[1]),
-        _ptr(workspace), ws_bytes, _stream(stream)))
+        _ptr(workspace), ws_bytes, _stream()))
     return outs[0], outs[1]
 
 
@@ -289,6 +353,8 @@ def merge_linear(y_fwd, y_bwd, weight, bias=None, out=None, stream=None):
     y_bwd float32 [..., cin]; weight bf16 [cout, 2 cin]; bias float32 [cout]
     or None. Returns float32 [..., cout]."""
     dev = _cuda_device(y_fwd)
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, merge_linear, y_fwd, y_bwd, weight, bias, out)
     cin = y_fwd.shape[-1]
     rows = y_fwd.numel() // cin if cin else 0
     cout = weight.shape[0]
@@ -303,7 +369,7 @@ def merge_linear(y_fwd, y_bwd, weight, bias=None, out=None, stream=None):
     _check(out, "out", oshape, torch.float32, dev)
     _within_32_bits((cin, cout), "the merge's channels")
     _abi.check(lib().bimamba_merge_linear(rows, cin, cout, _ptr(y_fwd), _ptr(y_bwd), _ptr(weight),
-                                          _ptr(bias), _ptr(out), _stream(stream)))
+                                          _ptr(bias), _ptr(out), _stream()))
     return out
 
 
@@ -389,8 +455,10 @@ def block_step(state, fwd, bwd, commit=False, chunk=64, y=None, stream=None, dt_
     """One cached block-diffusion step (bimamba_block_step)."""
     x = fwd["x"]
     dims = _dims(fwd)
-    shape = make_shape(x, fwd["B"], chunk, dt_softplus=dt_softplus)
     dev = _cuda_device(x)
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, block_step, state, fwd, bwd, commit, chunk, y, None, dt_softplus)
+    shape = make_shape(x, fwd["B"], chunk, dt_softplus=dt_softplus)
     fd = _dir(fwd, x.dtype, dims, dev, "fwd")
     bd = _dir(bwd, x.dtype, dims, dev, "bwd")
     if y is None:
@@ -398,7 +466,7 @@ def block_step(state, fwd, bwd, commit=False, chunk=64, y=None, stream=None, dt_
     _check(y, "y", tuple(x.shape), torch.float32, x.device)
     _abi.check(lib().bimamba_block_step(state.handle, ctypes.byref(shape), ctypes.byref(fd),
                                         ctypes.byref(bd), int(bool(commit)), _ptr(y),
-                                        _stream(stream)))
+                                        _stream()))
     return y
 
 
@@ -419,6 +487,9 @@ def block_step_conv(state, fwd, bwd, conv_fwd, conv_bwd, commit=False, chunk=64,
     ngroups, W, cdtype, ch = state.conv
     xbc = conv_fwd["xbc"]
     dev = _cuda_device(xbc)
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, block_step_conv, state, fwd, bwd, conv_fwd, conv_bwd, commit, chunk, y,
+                       activation, conv_out, None, dt_softplus)
     if xbc.dim() != 3:
         raise ValueError("xbc must be [batch, L, channels]")
     batch, L, chx = xbc.shape
@@ -446,7 +517,7 @@ def block_step_conv(state, fwd, bwd, conv_fwd, conv_bwd, commit=False, chunk=64,
     _abi.check(lib().bimamba_block_step_conv(
         state.handle, ctypes.byref(cshape), ctypes.byref(cfd), ctypes.byref(cbd),
         ctypes.byref(shape), ctypes.byref(fd), ctypes.byref(bd), int(bool(commit)), _ptr(y),
-        _stream(stream)))
+        _stream()))
     return y
 
 
@@ -467,14 +538,15 @@ class BlockStepPlan:
         self._fd = _dir(fwd, x.dtype, dims, dev, "fwd")
         self._bd = _dir(bwd, x.dtype, dims, dev, "bwd")
         if y is None:
-            y = torch.empty(x.shape, dtype=torch.float32, device=x.device)
+            y = _run_on(dev, stream, functools.partial(torch.empty, x.shape, dtype=torch.float32, device=dev))
         _check(y, "y", tuple(x.shape), torch.float32, x.device)
         self.y = y
         self._state = state
         self._keep = (fwd, bwd)
         self._fn = lib().bimamba_block_step
-        self._args = (ctypes.byref(self._shape), ctypes.byref(self._fd), ctypes.byref(self._bd),
-                      int(bool(commit)), _ptr(y), _stream(stream))
+        with _on(dev, stream):
+            self._args = (ctypes.byref(self._shape), ctypes.byref(self._fd), ctypes.byref(self._bd),
+                          int(bool(commit)), _ptr(y), _stream())
 
     def run(self):
         # the cache's handle is read per call: a freed cache is rejected by
@@ -536,6 +608,9 @@ def conv1d(fwd, bwd, nheads, headdim, ngroups, d_state, activation="silu",
     if dtype is not None and dtype != xbc.dtype:
         raise TypeError(f"dtype {dtype} is not xbc's {xbc.dtype}")
     dev = _cuda_device(xbc)
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, conv1d, fwd, bwd, nheads, headdim, ngroups, d_state, activation, cu_seqlens,
+                       init_ctx, final_ctx, out)
     if xbc.dim() != 3 or fwd["weight"].dim() != 2:
         raise ValueError("xbc must be [batch, L, channels] and weight [channels, width]")
     batch, L, ch = xbc.shape
@@ -565,7 +640,7 @@ def conv1d(fwd, bwd, nheads, headdim, ngroups, d_state, activation="silu",
     ws = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
     _abi.check(lib().bimamba_conv1d(
         ctypes.byref(shape), ctypes.byref(fd), ctypes.byref(bd) if bd is not None else None,
-        cu_arr, nseq, _ptr(init_ctx), _ptr(final_ctx), _ptr(ws), n.value, _stream(stream)))
+        cu_arr, nseq, _ptr(init_ctx), _ptr(final_ctx), _ptr(ws), n.value, _stream()))
     return fo, bo
 
 
@@ -574,6 +649,8 @@ def gated_norm(y, z, weight, group_size=None, eps=1e-5, out=None, stream=None):
     [..., C], z [..., C] (bf16 or fp32, also the output dtype), weight
     float32 [C]. group_size defaults to C (one group)."""
     dev = _cuda_device(y)
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, gated_norm, y, z, weight, group_size, eps, out)
     C = y.shape[-1]
     rows = y.numel() // C if C else 0
     if z.dtype not in DTYPES:
@@ -586,32 +663,8 @@ def gated_norm(y, z, weight, group_size=None, eps=1e-5, out=None, stream=None):
     _check(out, "out", tuple(y.shape), z.dtype, dev)
     gs = _int32(C if group_size is None else group_size, "group_size")
     _abi.check(lib().bimamba_gated_norm(rows, _int32(C, "channels"), gs, DTYPES[z.dtype], _ptr(y), _ptr(z), _ptr(weight), float(eps),
-                                        _ptr(out), _stream(stream)))
+                                        _ptr(out), _stream()))
     return out
-
-
-# The calls of the training steps are short next to their own overhead, so
-# they take the current stream's handle and device without the objects that
-# torch.cuda makes of them, and pass addresses as plain integers.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-
-
-def _elsewhere(dev, stream):
-    """Whether a call has to run under _on() first."""
-    return stream is not None or dev.index != _current_device()
-
-
-def _on(dev, stream):
-    """The context of a call on another stream than the current one, or on
-    tensors of another device than the current one: both are made current, so
-    that what the call allocates belongs to the stream it is used on."""
-    if stream is None:
-        return torch.cuda.device(dev)
-    if stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    return torch.cuda.stream(stream)
 
 
 def _adr(t):
@@ -715,8 +768,7 @@ def act8_pack(x, out=None, stream=None):
     out: an Act8 to write. Returns the Act8."""
     dev = _cuda_device(x)
     if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return act8_pack(x, out)
+        return _run_on(dev, stream, act8_pack, x, out)
     code, shape = _dtype_code(x.dtype), tuple(x.shape)
     _check(x, "x", shape, x.dtype, dev)
     rows, C = _rows(shape)
@@ -735,8 +787,7 @@ def act8_unpack(a, dtype=torch.bfloat16, out=None, stream=None):
     """The values an Act8 stands for, as bf16 or fp32 (bimamba_act8_unpack)."""
     dev = _cuda_device(a)
     if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return act8_unpack(a, dtype, out)
+        return _run_on(dev, stream, act8_unpack, a, dtype, out)
     code, shape = _dtype_code(dtype), tuple(a.shape)
     rows, C = _rows(shape)
     p = a._ptrs("a", shape, dev)
@@ -761,8 +812,7 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, checkpoint=Fa
     or None)."""
     dev = _cuda_device(x)
     if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return layer_norm(x, weight, bias, residual, eps, checkpoint, out, sum_out)
+        return _run_on(dev, stream, layer_norm, x, weight, bias, residual, eps, checkpoint, out, sum_out)
     dt, shape = x.dtype, tuple(x.shape)
     code = _dtype_code(dt)
     _check(x, "x", shape, dt, dev)
@@ -806,8 +856,7 @@ def layer_norm_bwd(dout, x, mean, rstd, weight=None, dsum=None, wgrad=True, dx=N
     float32 [C], None with wgrad=False."""
     dev = _cuda_device(dout)
     if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return layer_norm_bwd(dout, x, mean, rstd, weight, dsum, wgrad, dx)
+        return _run_on(dev, stream, layer_norm_bwd, dout, x, mean, rstd, weight, dsum, wgrad, dx)
     dt, shape = dout.dtype, tuple(dout.shape)
     code = _dtype_code(dt)
     _check(dout, "dout", shape, dt, dev)
@@ -845,8 +894,7 @@ def gated_norm_bwd(dout, y, z, weight, group_size=None, eps=1e-5, wgrad=True, dy
     dweight float32 [C] or None)."""
     dev = _cuda_device(dout)
     if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return gated_norm_bwd(dout, y, z, weight, group_size, eps, wgrad, dy, dz)
+        return _run_on(dev, stream, gated_norm_bwd, dout, y, z, weight, group_size, eps, wgrad, dy, dz)
     dt, shape = dout.dtype, tuple(dout.shape)
     code = _dtype_code(dt)
     _check(dout, "dout", shape, dt, dev)
@@ -892,8 +940,7 @@ def _conv1d_act8(fwd, bwd, dims, activation, cu_seqlens, out, dtype, stream):
     xbc = fwd["xbc"]
     dev = _cuda_device(xbc)
     if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return _conv1d_act8(fwd, bwd, dims, activation, cu_seqlens, out, dtype, None)
+        return _run_on(dev, stream, _conv1d_act8, fwd, bwd, dims, activation, cu_seqlens, out, dtype, None)
     sizes, ch = _conv_plan(xbc, fwd["weight"], dims, activation, dtype)
     batch, L, W = sizes[0], sizes[1], sizes[6]
     H, P, G, N = dims
@@ -947,9 +994,8 @@ def conv1d_bwd(fwd, bwd, gfwd, gbwd, nheads, headdim, ngroups, d_state, activati
     xbc = fwd["xbc"]
     dev = _cuda_device(xbc)
     if _elsewhere(dev, stream):
-        with _on(dev, stream):
-            return conv1d_bwd(fwd, bwd, gfwd, gbwd, nheads, headdim, ngroups, d_state, activation, cu_seqlens, out,
-                              None, dtype)
+        return _run_on(dev, stream, conv1d_bwd, fwd, bwd, gfwd, gbwd, nheads, headdim, ngroups, d_state, activation,
+                       cu_seqlens, out, None, dtype)
     q8 = isinstance(xbc, Act8)
     if dtype is None:
         dtype = torch.bfloat16 if q8 else xbc.dtype
@@ -999,8 +1045,13 @@ def seq_index(cu_seqlens, device="cuda", stream=None):
     total = arr[nseq]
     if torch.device(device).type != "cuda":
         raise ValueError(f"device must be a CUDA device, not {device}")
-    out = torch.empty(max(total, 1), dtype=torch.int32, device=device)
-    _abi.check(lib().bimamba_seq_index(arr, nseq, total, _ptr(out), _stream(stream)))
+    dev = torch.device(device)
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, seq_index, cu_seqlens, dev)
+    out = torch.empty(max(total, 1), dtype=torch.int32, device=dev)
+    _abi.check(lib().bimamba_seq_index(arr, nseq, total, _ptr(out), _stream()))
     return out[:total]
 
 
