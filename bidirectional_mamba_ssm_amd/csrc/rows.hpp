@@ -6,9 +6,11 @@
 // one power of two. With E the largest fp32 exponent field among them, an
 // element v is kept as the integer q = clamp(round(v 2^(133-E)), -127, 127)
 // (nearest, ties to even) and stands for q 2^(E-133). Scaling by a power of
-// two is exact, so the one rounding is the integer's: half a unit, 2^(E-134),
-// at most 2^-7 of the block's largest magnitude (one unit, as much, where the
-// clamp takes effect). q has 7 bits, so a decoded value is exact in bf16.
+// two is exact, so the one rounding is the integer's: half a unit, 2^(E-134).
+// For E >= 1 that is at most 2^-7 of the block's largest magnitude (one unit,
+// as much, where the clamp takes effect); for E = 0, a largest magnitude of
+// zero or an fp32 subnormal, the unit is 2^-133 whatever that magnitude is. q
+// has 7 bits, so a decoded value is exact in bf16.
 // A block that holds an infinity or a NaN has E = 255 and decodes as NaN.
 #pragma once
 #include <hip/hip_runtime.h>

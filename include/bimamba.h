@@ -387,9 +387,11 @@ int bimamba_block_step_conv(bimamba_state *st, const bimamba_conv_shape *cs,
  * shorter) share a power of two. With E the largest fp32 exponent field among
  * a block's elements, an element v is kept as the signed integer
  * q = clamp(round(v * 2^(133-E)), -127, 127) (to nearest, ties to even) and
- * stands for q * 2^(E-133): within 2^-7 of the block's largest magnitude.
- * E = 0 (zeros and fp32 subnormals) is kept as such; a block that holds an
- * infinity or a NaN has E = 255 and stands for NaNs. Values read back are
+ * stands for q * 2^(E-133): within 2^-7 of the block's largest magnitude, or,
+ * where that is smaller, within 2^-134. (E = 0, where the largest magnitude is
+ * zero or an fp32 subnormal, has the unit 2^-133 whatever that magnitude is: a
+ * block of 2^-140 and 2^-135 is kept as zeros.) A block that holds an infinity
+ * or a NaN has E = 255 and stands for NaNs. Values read back are
  * exact in either dtype. bimamba_conv1d_act8, bimamba_conv1d_bwd,
  * bimamba_gated_norm_bwd and bimamba_layer_norm_bwd read a checkpoint where
  * they would read the array, without a full-size copy in between. */
