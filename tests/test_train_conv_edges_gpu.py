@@ -5,6 +5,8 @@ import pytest
 import torch
 
 import bidirectional_mamba_ssm_amd as bm
+from metrics import bf16_rne
+from oracle import train as otrain
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +61,41 @@ def test_one_infinity_a_channel(W, dtype, cu):
         meets = ~np.isnan(want)
         assert np.array_equal(w[meets], want[meets])
         assert np.isfinite(w[~meets]).all()
+
+
+def _close(name, got, ref, S, rel, dtype):
+    """As in the parity tests: within rel * S, bf16 between the roundings of
+    that interval's ends."""
+    got, delta = got.double().cpu().numpy().reshape(ref.shape), rel * S
+    lo, hi = ref - delta, ref + delta
+    if dtype == "bf16":
+        lo, hi = bf16_rne(lo), bf16_rne(hi)
+    bad = ~((got >= lo) & (got <= hi))
+    assert not bad.any(), (name, np.argwhere(bad)[:3].tolist())
+
+
+@pytest.mark.parametrize("batch,L", [(1000, 1), (400, 2), (300, 5), (257, 8), (130, 33), (96, 64), (40, 129)])
+@pytest.mark.parametrize("W", [2, 4])
+@pytest.mark.parametrize("kept", [False, True], ids=["array", "ckpt"])
+def test_rows_shorter_than_a_workgroups_runs(batch, L, W, kept):
+    """A workgroup never crosses a row, so in short ones some of its waves (or
+    of a wave's positions) have nothing to do. Bars as for one long row: 2^-18
+    S, 2^-17 S for the weights' gradient (a run's 32 serial terms and 4 joins,
+    the rest in 64 bits)."""
+    dtype = "bf16" if W == 4 else "f32"
+    print(f"{batch} x {L}, W {W} {dtype} {kept}", flush=True)
+    g = torch.Generator(device=DEV).manual_seed(batch + L)
+    pairs = [_direction(g, batch, L, W, dtype) for _ in range(2)]
+    dirs = [dict(d, xbc=bm.act8_pack(d["xbc"])) if kept else d for d, _ in pairs]
+    res = bm.conv1d_bwd(dirs[0], dirs[1], pairs[0][1], pairs[1][1], H, P, G, N, dtype=DT[dtype])
+    plain = [dict(d, xbc=bm.act8_unpack(d["xbc"], dtype=DT[dtype])) if kept else d for d in dirs]
+    for d, (_, gr), o, rev in zip(plain, pairs, res, (False, True)):
+        dout = torch.cat([gr[k].reshape(batch, L, -1) for k in ("x", "B", "C")], dim=2)
+        rx, rw, rb = otrain.conv1d_bwd(d["xbc"], d["weight"], d["bias"], dout, rev, None, "silu")
+        _close("dxbc", o["xbc"], *rx, 2.0 ** -18, dtype)
+        _close("dweight", o["weight"], *rw, 2.0 ** -17, "f32")
+        _close("dbias", o["bias"], *rb, 2.0 ** -17, "f32")
+    if kept:
+        for o, p in zip(bm.conv1d(dirs[0], dirs[1], H, P, G, N, dtype=DT[dtype]),
+                        bm.conv1d(plain[0], plain[1], H, P, G, N)):
+            assert all(torch.equal(o[k], p[k]) for k in ("x", "B", "C"))
