@@ -10,14 +10,16 @@
 // kBatch positions ahead, and a run starts W-1 positions early.
 //
 // At 8 x 1024 tokens of 4352 channels, width 4, bf16, SiLU, both directions:
-// 43 us, 216 MB at 5.0 TB/s (the convolution from bf16 input: 54 us, 285 MB).
+// 44 us, 216 MB at 4.9 TB/s, where launches follow one another for long, 49
+// where the clock has just risen from idle (the convolution from bf16 input: 54
+// us, 285 MB); 8192 packed tokens, 32 sequences, 49 us.
 // Its arithmetic alone takes some 35 us (212 vector instructions for 16
 // elements a lane, 32 of them exp and rcp at a quarter of the rate), so what
 // it spends elsewhere shows: pointers that walk with the rows instead of a
 // product each, no test of the activation, a window that is not moved, 62 ->
 // 43 us together with the walk itself (the bf16 kernel's form, with a decoding
-// load, took 62), and 50 where the clock has just risen from idle. 8 channels
-// a lane need 180 registers and ran 66 us; runs of 16 or 64 positions 50.
+// load, took 62). 8 channels a lane need 180 registers and ran 66 us; runs of
+// 16 or 64 positions 50.
 #include <type_traits>
 
 #include "conv_seqs.hpp"

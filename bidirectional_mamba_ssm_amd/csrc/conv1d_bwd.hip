@@ -19,8 +19,10 @@
 // workgroup through LDS and over workgroups by col_sum.hip.
 //
 // Measured (8 x 1024 tokens, 4352 channels, width 4, bf16, SiLU, both
-// directions): 119 us, 571 MB at 4.8 TB/s, and 5 us for the sums; 2500 packed
-// tokens of 96 channels in fp32 9.5 us. Tests in every batch 131; the inner
+// directions): 119 us, 571 MB at 4.8 TB/s, and 5 us for the sums; from the
+// checkpoint 107 us, 502 MB at 4.7; packed, 32 sequences, 124; 128 rows of 64
+// tokens, where half of a workgroup's waves have no run, 127 and 7; 2500 packed
+// tokens of 96 channels in fp32 10 us. Tests in every batch 131; the inner
 // batches' code shared with a store under a branch, which made each batch wait
 // for the stores of the one before, 138. The arithmetic (432 vector
 // instructions for 16 elements a lane) would take 60.

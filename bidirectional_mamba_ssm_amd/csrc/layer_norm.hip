@@ -124,7 +124,9 @@ __global__ __launch_bounds__(G == 0 ? 64 * kMaxWaves : 64 * kRows) void k_layer_
             if constexpr (RES) nr[k] = L::load((const T *)a.res + r * C + at.c[k]);
         }
     };
-    constexpr bool kAhead = NV * V <= 16;   // wider lanes have no registers for it
+    // wider lanes have no registers for it (4096 x 16 384 fp32 with checkpoint
+    // 225 us, 316 with the next row ahead and its spills; bf16 132 and 135)
+    constexpr bool kAhead = NV * V <= 16;
     if (kAhead && row < a.rows) fetch(row);
     for (int flip = 0; row < a.rows; row += step, flip ^= 1) {
         if (!kAhead) fetch(row);
@@ -298,7 +300,10 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
     // last one and uses nothing of it
     const long long step = (long long)gridDim.x * R, last = a.rows - 1;
     long long base = (long long)blockIdx.x * R;
-    constexpr bool kAhead = E <= 16;   // wider lanes have no registers for it
+    // wider lanes have no registers for it (4096 x 16 384 bf16 from a checkpoint
+    // 100 us, 166 with the next row ahead and its spills; from the array 113 and
+    // 116; what would gain is the array without dsum at 12 000, 68 and 61)
+    constexpr bool kAhead = E <= 16;
     Row next;
     if (kAhead) fetch(next, min(base + slot, last));
     for (int flip = 0; base < a.rows; base += step, flip ^= 1) {
@@ -443,10 +448,11 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
 }
 
 // How a row is held: G lanes of one wave or (G = 0) `waves` waves, nv vectors
-// a lane. Rows of up to 256 channels take the fewest lanes, 8 elements each (a
-// wave a row instead: 60 000 x 64 bf16 25 us for 10, their gradient 21 for 12);
-// wider ones `lane` elements a lane, or the fewest that kMaxWaves waves can do
-// with.
+// a lane. Rows of up to 256 channels take the fewest lanes, 8 elements each
+// (kernel times, bf16: 60 000 x 64 5.6 us, with residual and checkpoint 8.9,
+// their gradient 12.4; a wave a row 16.8, 26.9 and 21.8; 60 000 x 128 13.3 and
+// 16.0 for 27.2 and 23.4); wider ones `lane` elements a lane, or the fewest
+// that kMaxWaves waves can do with.
 struct Form {
     int nv, waves, G;
 };
