@@ -889,8 +889,8 @@ def layer_norm_bwd(dout, x, mean, rstd, weight=None, dsum=None, wgrad=True, dx=N
 def gated_norm_bwd(dout, y, z, weight, group_size=None, eps=1e-5, wgrad=True, dy=None, dz=None, stream=None):
     """Gradient of gated_norm (bimamba_gated_norm_bwd): dout [..., C] in z's
     dtype, y float32 and z [..., C] (each the tensor or its Act8 checkpoint).
-    dy (where to write it) may be the tensor y, dz may be dout or the tensor
-    z; other overlaps are refused. Returns (dy float32, dz in dout's dtype,
+    dy and dz (where to write them) may each be one of the tensors y, z and
+    dout of its dtype; other overlaps are refused. Returns (dy float32, dz in dout's dtype,
     dweight float32 [C] or None)."""
     dev = _cuda_device(dout)
     if _elsewhere(dev, stream):

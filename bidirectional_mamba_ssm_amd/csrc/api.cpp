@@ -1128,14 +1128,17 @@ int bimamba_gated_norm_bwd(long long rows, int channels, int group_size, int dty
     if ((uintptr_t)dweight & 3u) return fail(BIMAMBA_EINVAL, "dweight must be 4-byte aligned");
     const size_t need = dweight ? (size_t)gated_norm_bwd_wgs(rows, channels) * channels * 4 : 0;
     if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
-    // dy may be y itself, dz dout or z (as arrays, not checkpoints): a lane
-    // writes the elements that it has read
+    // dy and dz may each be y, z or dout itself where the elements are as long
+    // (arrays, not checkpoints): a lane writes the elements that it has read
     const size_t C = channels, n = rows * C, el = elem_size(dtype), nb = rows * act8_blocks(channels);
+    auto apart = [&](const void *in, size_t size) {
+        return (in == dy && size == 4) || (in == dz && size == el) ? nullptr : in;
+    };
     if ((rc = check_apart({{"dy", dy, n * 4}, {"dz", dz, n * el}, {"dweight", dweight, C * 4},
                            {"the workspace", workspace, need}},
-                          {{"y", y == dy && !y_scale ? nullptr : y, y_scale ? n : n * 4}, {"y_scale", y_scale, nb},
-                           {"z", z == dz && !z_scale ? nullptr : z, z_scale ? n : n * el}, {"z_scale", z_scale, nb},
-                           {"weight", weight, C * 4}, {"dout", dout == dz ? nullptr : dout, n * el}})))
+                          {{"y", y_scale ? y : apart(y, 4), y_scale ? n : n * 4}, {"y_scale", y_scale, nb},
+                           {"z", z_scale ? z : apart(z, el), z_scale ? n : n * el}, {"z_scale", z_scale, nb},
+                           {"weight", weight, C * 4}, {"dout", apart(dout, el), n * el}})))
         return rc;
     EpiBwdArgs a;
     memset(&a, 0, sizeof a);

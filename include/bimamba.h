@@ -462,10 +462,10 @@ int bimamba_conv1d_bwd(const bimamba_conv_shape *s, const bimamba_conv_grad *fwd
  *  dz        out dtype [rows][channels]
  *  dweight   out float [channels], or NULL if not wanted
  * The workspace is needed with dweight only. Pointers 16-byte aligned (scales
- * to one byte, dweight to 4), workspace 256-byte aligned. dy may be y itself
- * and dz may be dout or z (arrays, not checkpoints); calls whose outputs or
- * workspace overlap each other, or an input in any other way, are refused.
- * With no row dweight is 0. */
+ * to one byte, dweight to 4), workspace 256-byte aligned. dy and dz may each be
+ * y, z or dout itself where the elements are as long (arrays, not checkpoints);
+ * calls whose outputs or workspace overlap each other, or an input in any
+ * other way, are refused. With no row dweight is 0. */
 int bimamba_gated_norm_bwd_workspace_size(long long rows, int channels, int group_size, int dtype, size_t *bytes);
 int bimamba_gated_norm_bwd(long long rows, int channels, int group_size, int dtype, const void *y,
                            const uint8_t *y_scale, const void *z, const uint8_t *z_scale, const float *weight,
