@@ -110,6 +110,15 @@ def _within_32_bits(vals, name):
         raise ValueError(f"{name} goes beyond 32 bits ({min(vals)} .. {max(vals)})")
 
 
+def _sizes(struct, name, *vals):
+    """A structure of C ints."""
+    try:
+        return struct.from_buffer_copy(array.array("i", vals))   # checks the range as it converts
+    except OverflowError:
+        _within_32_bits(vals, name)
+        raise
+
+
 def _int32s(vals, name):
     """A C array of integers for the library."""
     try:
@@ -174,14 +183,12 @@ def make_shape(x, B, chunk, seqlen=None, dt_softplus=False):
     G, N = B.shape[2], B.shape[3]
     if x.dtype not in DTYPES:
         raise TypeError(f"unsupported dtype {x.dtype}")
-    sizes = (batch, L if seqlen is None else seqlen, H, P, N, G, chunk)
-    _within_32_bits(sizes, "the problem's shape")
-    return _abi.Shape(*sizes, DTYPES[x.dtype], _abi.DT_SOFTPLUS if dt_softplus else 0)
+    return _sizes(_abi.Shape, "the problem's shape", batch, L if seqlen is None else seqlen, H, P, N, G, chunk,
+                  DTYPES[x.dtype], _abi.DT_SOFTPLUS if dt_softplus else 0)
 
 
 def _conv_shape(*sizes):
-    _within_32_bits(sizes, "the convolution's shape")
-    return _abi.ConvShape(*sizes)
+    return _sizes(_abi.ConvShape, "the convolution's shape", *sizes)
 
 
 def workspace_size(shape, nseq=0):
@@ -228,7 +235,7 @@ def ssd_fwd(fwd, bwd=None, chunk=256, cu_seqlens=None, init_state=None,
     _abi.check(lib().bimamba_ssd_fwd(
         ctypes.byref(shape), ctypes.byref(fd), ctypes.byref(bd) if bd is not None else None,
         cu_arr, nseq, _ptr(init_state), _ptr(final_state), _ptr(y),
-        _ptr(workspace), ws_bytes, _stream()))
+        _ptr(workspace), ws_bytes, _raw_stream(dev.index)))
     return y
 
 
@@ -281,7 +288,7 @@ def ssd_bwd(fwd, bwd, dy, grads=None, workspace=None, stream=None):
     _abi.check(lib().bimamba_ssd_bwd(
         ctypes.byref(shape), ctypes.byref(fd), ctypes.byref(bd) if bd is not None else None,
         _ptr(dy), ctypes.byref(gfs), ctypes.byref(gbs) if gbs is not None else None,
-        _ptr(workspace), ws_bytes, _stream()))
+        _ptr(workspace), ws_bytes, _raw_stream(dev.index)))
     return gf, gb
 
 
@@ -308,7 +315,7 @@ def ssd_fwd_noalloc(fwd, bwd, y, chunk=256, cu_seqlens=None, init_state=None,
     _check(y, "y", (batch, L, H, P), torch.float32, dev)
     _abi.check(lib().bimamba_ssd_fwd_noalloc(
         ctypes.byref(shape), ctypes.byref(fd), ctypes.byref(bd) if bd is not None else None,
-        cu_arr, nseq, _ptr(init_state), _ptr(final_state), _ptr(y), _stream()))
+        cu_arr, nseq, _ptr(init_state), _ptr(final_state), _ptr(y), _raw_stream(dev.index)))
     return y
 
 
@@ -344,7 +351,7 @@ def ssd_fwd_streams(fwd, bwd, chunk=256, cu_seqlens=None, init_state=None,
     _abi.check(lib().bimamba_ssd_fwd_streams(
         ctypes.byref(shape), ctypes.byref(fd), ctypes.byref(bd), cu_arr, nseq,
         _ptr(init_state), _ptr(final_state), _ptr(outs[0]), _ptr(outs[1]),
-        _ptr(workspace), ws_bytes, _stream()))
+        _ptr(workspace), ws_bytes, _raw_stream(dev.index)))
     return outs[0], outs[1]
 
 
@@ -369,7 +376,7 @@ def merge_linear(y_fwd, y_bwd, weight, bias=None, out=None, stream=None):
     _check(out, "out", oshape, torch.float32, dev)
     _within_32_bits((cin, cout), "the merge's channels")
     _abi.check(lib().bimamba_merge_linear(rows, cin, cout, _ptr(y_fwd), _ptr(y_bwd), _ptr(weight),
-                                          _ptr(bias), _ptr(out), _stream()))
+                                          _ptr(bias), _ptr(out), _raw_stream(dev.index)))
     return out
 
 
@@ -466,7 +473,7 @@ def block_step(state, fwd, bwd, commit=False, chunk=64, y=None, stream=None, dt_
     _check(y, "y", tuple(x.shape), torch.float32, x.device)
     _abi.check(lib().bimamba_block_step(state.handle, ctypes.byref(shape), ctypes.byref(fd),
                                         ctypes.byref(bd), int(bool(commit)), _ptr(y),
-                                        _stream()))
+                                        _raw_stream(dev.index)))
     return y
 
 
@@ -517,7 +524,7 @@ def block_step_conv(state, fwd, bwd, conv_fwd, conv_bwd, commit=False, chunk=64,
     _abi.check(lib().bimamba_block_step_conv(
         state.handle, ctypes.byref(cshape), ctypes.byref(cfd), ctypes.byref(cbd),
         ctypes.byref(shape), ctypes.byref(fd), ctypes.byref(bd), int(bool(commit)), _ptr(y),
-        _stream()))
+        _raw_stream(dev.index)))
     return y
 
 
@@ -546,7 +553,7 @@ class BlockStepPlan:
         self._fn = lib().bimamba_block_step
         with _on(dev, stream):
             self._args = (ctypes.byref(self._shape), ctypes.byref(self._fd), ctypes.byref(self._bd),
-                          int(bool(commit)), _ptr(y), _stream())
+                          int(bool(commit)), _ptr(y), _raw_stream(dev.index))
 
     def run(self):
         # the cache's handle is read per call: a freed cache is rejected by
@@ -640,7 +647,7 @@ def conv1d(fwd, bwd, nheads, headdim, ngroups, d_state, activation="silu",
     ws = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
     _abi.check(lib().bimamba_conv1d(
         ctypes.byref(shape), ctypes.byref(fd), ctypes.byref(bd) if bd is not None else None,
-        cu_arr, nseq, _ptr(init_ctx), _ptr(final_ctx), _ptr(ws), n.value, _stream()))
+        cu_arr, nseq, _ptr(init_ctx), _ptr(final_ctx), _ptr(ws), n.value, _raw_stream(dev.index)))
     return fo, bo
 
 
@@ -663,7 +670,7 @@ def gated_norm(y, z, weight, group_size=None, eps=1e-5, out=None, stream=None):
     _check(out, "out", tuple(y.shape), z.dtype, dev)
     gs = _int32(C if group_size is None else group_size, "group_size")
     _abi.check(lib().bimamba_gated_norm(rows, _int32(C, "channels"), gs, DTYPES[z.dtype], _ptr(y), _ptr(z), _ptr(weight), float(eps),
-                                        _ptr(out), _stream()))
+                                        _ptr(out), _raw_stream(dev.index)))
     return out
 
 
@@ -1051,7 +1058,7 @@ def seq_index(cu_seqlens, device="cuda", stream=None):
     if _elsewhere(dev, stream):
         return _run_on(dev, stream, seq_index, cu_seqlens, dev)
     out = torch.empty(max(total, 1), dtype=torch.int32, device=dev)
-    _abi.check(lib().bimamba_seq_index(arr, nseq, total, _ptr(out), _stream()))
+    _abi.check(lib().bimamba_seq_index(arr, nseq, total, _ptr(out), _raw_stream(dev.index)))
     return out[:total]
 
 
