@@ -2,10 +2,13 @@
 documentation allows gives the bits of separate arrays, and what it does not
 allow is refused. Widths at which a row's last vector overlaps a vector of
 another wave are among them."""
+import ctypes
+
 import pytest
 import torch
 
 import bidirectional_mamba_ssm_amd as bm
+from bidirectional_mamba_ssm_amd import _abi
 
 pytestmark = pytest.mark.gpu
 
@@ -144,3 +147,23 @@ def test_conv1d_refusals():
     # the same input, weights or gradients for both directions are no overlap
     want = bm.conv1d_bwd(dirs[0], dict(dirs[0]), g, g, H, P, G, N, out=(t, torch.zeros_like(t)))
     assert want[0]["xbc"] is t
+
+
+@pytest.mark.parametrize("C", [100, 513, 1025, 2049, 8193])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_layer_norm_onto_x_through_the_library(C, dtype):
+    """Without a residual the library takes out = x (the binding, which returns
+    x as the sum, does not)."""
+    rows = 700
+    print(f"rows {rows} C {C} {dtype}", flush=True)
+    x, = _arrays(rows, C, dtype, C, 1)
+    want = bm.layer_norm(x, checkpoint=True)
+    mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    ck = bm.Act8.empty((rows, C), torch.device(DEV))
+    p = _abi.Act8Ptrs(ck.q.data_ptr(), ck.scale.data_ptr())
+    rc = bm.lib().bimamba_layer_norm(rows, C, bm.DTYPES[x.dtype], x.data_ptr(), None, None, None, 1e-5, x.data_ptr(),
+                                     None, mean.data_ptr(), rstd.data_ptr(), ctypes.byref(p),
+                                     torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    assert _same([x, mean, rstd, ck.q, ck.scale],
+                 [want["out"], want["mean"], want["rstd"], want["ckpt"].q, want["ckpt"].scale])
