@@ -74,7 +74,7 @@ def _run_on(dev, stream, call, *args):
 def _tensors(res):
     if isinstance(res, torch.Tensor):
         return [res]
-    if isinstance(res, Act8):
+    if isinstance(res, (Act8, Rows8)):
         return [res.q, res.scale]
     if isinstance(res, dict):
         res = res.values()
@@ -1090,3 +1090,166 @@ class profile:
             name = raw[i * nl:(i + 1) * nl].split(b"\0", 1)[0].decode()
             self.kernels[name] = (counts[i], ms[i])
         return False
+
+
+class Rows8:
+    """Rows of 8-bit integers with a scale each (include/bimamba.h,
+    bimamba_rows8): q int8 [..., C] and scale float32 [...]; a row stands for
+    q * scale. Made by rows8_pack (activations, or a weight [cout, cin] by output
+    channel) or rms_norm; read by linear8."""
+
+    __slots__ = ("q", "scale")
+
+    def __init__(self, q, scale):
+        self.q, self.scale = q, scale
+
+    @property
+    def shape(self):
+        return self.q.shape
+
+    @property
+    def device(self):
+        return self.q.device
+
+    @staticmethod
+    def empty(shape, device):
+        shape = tuple(shape)
+        return Rows8(torch.empty(shape, dtype=torch.int8, device=device),
+                     torch.empty(shape[:-1], dtype=torch.float32, device=device))
+
+    def _ptrs(self, name, shape, dev):
+        _check(self.q, name + ".q", shape, torch.int8, dev)
+        _check(self.scale, name + ".scale", shape[:-1], torch.float32, dev)
+        return _abi.Rows8Ptrs(self.q.data_ptr(), self.scale.data_ptr())
+
+
+def _rows8(r, name):
+    if not isinstance(r, Rows8):
+        raise TypeError(f"{name} must be a Rows8, not {type(r).__name__}")
+    return r
+
+
+def rows8_pack(x, out=None, stream=None):
+    """x [..., C] (bf16 or fp32, C in 8..16384) as 8-bit rows
+    (bimamba_rows8_pack). out: a Rows8 to write. Returns the Rows8."""
+    dev = _cuda_device(x)
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, rows8_pack, x, out)
+    code, shape = _dtype_code(x.dtype), tuple(x.shape)
+    _check(x, "x", shape, x.dtype, dev)
+    rows, C = _rows(shape)
+    out = Rows8.empty(shape, dev) if out is None else _rows8(out, "out")
+    p = out._ptrs("out", shape, dev)
+    rc = lib().bimamba_rows8_pack(rows, C, code, x.data_ptr(), ctypes.byref(p), _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
+    return out
+
+
+def rms_norm(x, weight=None, residual=None, eps=1e-5, rows8=False, dense=None, out=None, sum_out=None, stream=None):
+    """RMS norm over the last dimension (bimamba_rms_norm) of h = x, or of
+    h = x + residual rounded to x's dtype. x, residual [..., C] bf16 or fp32,
+    C in 8..16384; weight float32 [C] or None.
+
+    rows8: write the result as 8-bit rows for linear8 (True, or a Rows8 to
+    write). dense: write it in x's dtype; unless said, where rows8 is not
+    asked for or out is given. sum_out: where to write h with a residual. out
+    and sum_out may be residual or x itself with a residual (without one x is
+    what sum returns); other overlaps are refused. Returns a dict: out (or
+    None), sum (h; x itself without a residual), rstd (float32 [...], for
+    rms_norm_bwd), rows8 (Rows8 or None)."""
+    dev = _cuda_device(x)
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, rms_norm, x, weight, residual, eps, rows8, dense, out, sum_out)
+    dt, shape = x.dtype, tuple(x.shape)
+    code = _dtype_code(dt)
+    _check(x, "x", shape, dt, dev)
+    rows, C = _rows(shape)
+    if residual is not None:
+        _check(residual, "residual", shape, dt, dev)
+        sum_out = _out(sum_out, "sum_out", shape, dt, dev, x)
+    elif sum_out is not None:
+        raise ValueError("sum_out goes with a residual")
+    if weight is not None:
+        _check(weight, "weight", (C,), torch.float32, dev)
+    if dense is None:
+        dense = not rows8 or out is not None
+    if not dense and (out is not None or not rows8):
+        raise ValueError("dense=False goes with rows8 and without out")
+    if dense:
+        if out is not None and residual is None and rows and out.data_ptr() == x.data_ptr():
+            raise ValueError("out overlaps x, which is returned as sum without a residual")
+        out = _out(out, "out", shape, dt, dev, x)
+    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    r8 = p = None
+    if rows8:
+        r8 = rows8 if isinstance(rows8, Rows8) else Rows8.empty(shape, dev)
+        p = ctypes.byref(r8._ptrs("rows8", shape, dev))
+    rc = lib().bimamba_rms_norm(rows, C, code, x.data_ptr(), _adr(residual), _adr(weight), float(eps), _adr(out),
+                                _adr(sum_out), rstd.data_ptr(), p, _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
+    return dict(out=out, sum=x if residual is None else sum_out, rstd=rstd, rows8=r8)
+
+
+def rms_norm_bwd(dout, x, rstd, weight=None, dsum=None, wgrad=True, dx=None, stream=None):
+    """Gradient of rms_norm's out (bimamba_rms_norm_bwd). dout [..., C]; x:
+    what rms_norm returned as sum (dout's dtype) or its Act8 checkpoint; rstd
+    float32 [...]; dsum: the gradient reaching sum along the residual stream,
+    added to dx. dx (where to write it) may be dout, dsum or the tensor x
+    itself; other overlaps are refused. Returns (dx, dweight): dx in dout's
+    dtype (the gradient of x and of residual), dweight float32 [C], None with
+    wgrad=False."""
+    dev = _cuda_device(dout)
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, rms_norm_bwd, dout, x, rstd, weight, dsum, wgrad, dx)
+    dt, shape = dout.dtype, tuple(dout.shape)
+    code = _dtype_code(dt)
+    _check(dout, "dout", shape, dt, dev)
+    rows, C = _rows(shape)
+    xp, xs = _kept(x, "x", shape, dt, dev)
+    _check(rstd, "rstd", shape[:-1], torch.float32, dev)
+    if weight is not None:
+        _check(weight, "weight", (C,), torch.float32, dev)
+    if dsum is not None:
+        _check(dsum, "dsum", shape, dt, dev)
+    dx = _out(dx, "dx", shape, dt, dev, dout)
+    dw = ws = None
+    nbytes = 0
+    if wgrad:
+        dw = torch.empty(C, dtype=torch.float32, device=dev)
+        nbytes = _size("bimamba_rms_norm_bwd_workspace_size", rows, C, code)
+        ws = _workspace(nbytes, dev)
+    rc = lib().bimamba_rms_norm_bwd(
+        rows, C, code, xp, xs, rstd.data_ptr(), _adr(weight), dout.data_ptr(), _adr(dsum), dx.data_ptr(), _adr(dw),
+        _adr(ws), nbytes, _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
+    return dx, dw
+
+
+def linear8(x, weight, bias=None, dtype=torch.bfloat16, out=None, stream=None):
+    """Product of 8-bit rows (bimamba_linear8): x Rows8 [..., cin], weight
+    Rows8 [cout, cin], bias float32 [cout] or None. Returns [..., cout] in
+    dtype (bf16 or fp32; out's, if out is given), which may not overlap an
+    input."""
+    dev = _cuda_device(_rows8(x, "x"))
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, linear8, x, weight, bias, dtype, out)
+    if out is not None:
+        dtype = out.dtype
+    code, shape = _dtype_code(dtype), tuple(x.shape)
+    rows, cin = _rows(shape)
+    if len(_rows8(weight, "weight").shape) != 2:
+        raise ValueError(f"weight has shape {tuple(weight.shape)}, expected [cout, cin]")
+    cout = _int32(weight.shape[0], "cout")
+    xp = x._ptrs("x", shape, dev)
+    wp = weight._ptrs("weight", (cout, cin), dev)
+    if bias is not None:
+        _check(bias, "bias", (cout,), torch.float32, dev)
+    out = _out(out, "out", shape[:-1] + (cout,), dtype, dev)
+    rc = lib().bimamba_linear8(rows, cin, cout, code, ctypes.byref(xp), ctypes.byref(wp), _adr(bias), out.data_ptr(),
+                               _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
+    return out

@@ -28,6 +28,8 @@ EXPORTS = (
     "bimamba_conv1d_bwd_workspace_size", "bimamba_conv1d_bwd",
     "bimamba_gated_norm_bwd_workspace_size", "bimamba_gated_norm_bwd", "bimamba_layer_norm",
     "bimamba_layer_norm_bwd_workspace_size", "bimamba_layer_norm_bwd",
+    "bimamba_rows8_pack", "bimamba_rms_norm", "bimamba_rms_norm_bwd_workspace_size", "bimamba_rms_norm_bwd",
+    "bimamba_linear8",
 )
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -71,6 +73,10 @@ class ConvDir(ctypes.Structure):
 
 
 class Act8Ptrs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class Rows8Ptrs(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
@@ -151,6 +157,12 @@ def load():
     lib.bimamba_layer_norm.argtypes = [ll, ci, ci, vp, vp, vp, vp, cf, vp, vp, vp, vp, ap, vp]
     lib.bimamba_layer_norm_bwd_workspace_size.argtypes = [ll, ci, ci, np_]
     lib.bimamba_layer_norm_bwd.argtypes = [ll, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, size, vp]
+    rp = ctypes.POINTER(Rows8Ptrs)
+    lib.bimamba_rows8_pack.argtypes = [ll, ci, ci, vp, rp, vp]
+    lib.bimamba_rms_norm.argtypes = [ll, ci, ci, vp, vp, vp, cf, vp, vp, vp, rp, vp]
+    lib.bimamba_rms_norm_bwd_workspace_size.argtypes = [ll, ci, ci, np_]
+    lib.bimamba_rms_norm_bwd.argtypes = [ll, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, size, vp]
+    lib.bimamba_linear8.argtypes = [ll, ci, ci, ci, rp, rp, vp, vp, vp]
     for name in EXPORTS:
         getattr(lib, name).restype = getattr(lib, name).restype or ctypes.c_int
     _LIB = lib

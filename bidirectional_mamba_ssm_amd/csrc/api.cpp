@@ -1290,4 +1290,167 @@ int bimamba_act8_unpack(long long rows, long long channels, int dtype, const bim
     return act8_call(rows, channels, dtype, x, in, false, stream);
 }
 
+
+// ---- RMS norm, 8-bit rows and their product ------------------------------------
+
+int bimamba_rms_norm(long long rows, int channels, int dtype, const void *x, const void *residual,
+                     const float *weight, float eps, void *out, void *sum, float *rstd, const bimamba_rows8 *out8,
+                     bimamba_stream stream) {
+    int rc = check_layer_norm(rows, channels, dtype);
+    if (rc) return rc;
+    if (!(eps >= 0.f) || eps > 3.0e38f) return fail(BIMAMBA_EINVAL, "eps must be finite and >= 0");
+    if (!!residual != !!sum && rows > 0) return fail(BIMAMBA_EINVAL, "residual and sum go together");
+    if (rows == 0) return BIMAMBA_OK;
+    if (!x) return fail(BIMAMBA_EINVAL, "x is required");
+    if (!out && !out8) return fail(BIMAMBA_EINVAL, "out, out8 or both are required");
+    if (out8 && (!out8->q || !out8->scale)) return fail(BIMAMBA_EINVAL, "out8's q and scale are required");
+    if (!aligned_to(x, dtype) || !aligned_to(residual, dtype) || !aligned_to(out, dtype) || !aligned_to(sum, dtype))
+        return fail(BIMAMBA_EINVAL, "x, residual, out and sum must be aligned to their elements");
+    if (((uintptr_t)weight | (uintptr_t)rstd | (out8 ? (uintptr_t)out8->scale : 0)) & 3u)
+        return fail(BIMAMBA_EINVAL, "weight, rstd and the rows' scales must be 4-byte aligned");
+    const size_t n = (size_t)rows * channels * elem_size(dtype), r4 = (size_t)rows * 4;
+    const Array in[3] = {{"x", x, n}, {"residual", residual, n}, {"weight", weight, (size_t)channels * 4}};
+    const Array o[5] = {{"out", out, n}, {"sum", sum, n}, {"rstd", rstd, r4},
+                        {"out8's q", out8 ? out8->q : nullptr, (size_t)rows * channels},
+                        {"out8's scale", out8 ? out8->scale : nullptr, r4}};
+    for (int i = 0; i < 5; ++i) {
+        for (int j = i + 1; j < 5; ++j)
+            if (overlap(o[i], o[j])) return fail(BIMAMBA_EINVAL, "%s overlaps %s", o[i].name, o[j].name);
+        for (int j = 0; j < 3; ++j)
+            if (overlap(o[i], in[j]) && !(i < 2 && j < 2 && o[i].p == in[j].p))
+                return fail(BIMAMBA_EINVAL, "%s overlaps %s", o[i].name, in[j].name);
+    }
+    RmsArgs a;
+    memset(&a, 0, sizeof a);
+    a.rows = rows;
+    a.C = channels;
+    a.eps = eps;
+    a.norm = true;
+    a.x = x;
+    a.res = residual;
+    a.w = weight;
+    a.out = out;
+    a.sum = sum;
+    a.rstd = rstd;
+    a.q = out8 ? (int8_t *)out8->q : nullptr;
+    a.scale = out8 ? out8->scale : nullptr;
+    hipError_t e = launch_rms_norm(a, dtype == BIMAMBA_BF16, (hipStream_t)stream);
+    return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the RMS norm");
+}
+
+int bimamba_rms_norm_bwd_workspace_size(long long rows, int channels, int dtype, size_t *bytes) {
+    int rc = check_layer_norm(rows, channels, dtype);
+    if (rc) return rc;
+    if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
+    *bytes = align256((size_t)layer_norm_bwd_wgs(rows, channels, dtype == BIMAMBA_BF16) * channels * 4);
+    return BIMAMBA_OK;
+}
+
+int bimamba_rms_norm_bwd(long long rows, int channels, int dtype, const void *x, const uint8_t *x_scale,
+                         const float *rstd, const float *weight, const void *dout, const void *dsum, void *dx,
+                         float *dweight, void *workspace, size_t workspace_bytes, bimamba_stream stream) {
+    int rc = check_layer_norm(rows, channels, dtype);
+    if (rc) return rc;
+    if (rows > 0) {
+        if (!x || !rstd || !dout || !dx) return fail(BIMAMBA_EINVAL, "x, rstd, dout and dx are required");
+        if ((!x_scale && !aligned_to(x, dtype)) || !aligned_to(dout, dtype) || !aligned_to(dsum, dtype) ||
+            !aligned_to(dx, dtype))
+            return fail(BIMAMBA_EINVAL, "x, dout, dsum and dx must be aligned to their elements");
+    }
+    if (((uintptr_t)rstd | (uintptr_t)weight | (uintptr_t)dweight) & 3u)
+        return fail(BIMAMBA_EINVAL, "rstd, weight and its gradient must be 4-byte aligned");
+    size_t need = 0;
+    if (dweight) {
+        if ((rc = bimamba_rms_norm_bwd_workspace_size(rows, channels, dtype, &need))) return rc;
+        if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+    }
+    const size_t n = (size_t)rows * channels, e = elem_size(dtype), c4 = (size_t)channels * 4;
+    const Array in[6] = {{"x", x, x_scale ? n : n * e}, {"x's scale", x_scale, rows * act8_blocks(channels)},
+                         {"rstd", rstd, (size_t)rows * 4}, {"weight", weight, c4},
+                         {"dout", dout, n * e}, {"dsum", dsum, n * e}};
+    const Array o[3] = {{"dx", dx, n * e}, {"dweight", dweight, c4}, {"the workspace", workspace, need}};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = i + 1; j < 3; ++j)
+            if (overlap(o[i], o[j])) return fail(BIMAMBA_EINVAL, "%s overlaps %s", o[i].name, o[j].name);
+        for (int j = 0; j < 6; ++j) {
+            const bool same = i == 0 && o[i].p == in[j].p && (j == 4 || j == 5 || (j == 0 && !x_scale));
+            if (overlap(o[i], in[j]) && !same) return fail(BIMAMBA_EINVAL, "%s overlaps %s", o[i].name, in[j].name);
+        }
+    }
+    LnBwdArgs a;
+    memset(&a, 0, sizeof a);
+    a.rows = rows;
+    a.C = channels;
+    a.x = x;
+    a.xscale = x_scale;
+    a.rstd = rstd;
+    a.w = weight;
+    a.dout = dout;
+    a.dsum = dsum;
+    a.dx = dx;
+    a.dw = dweight;
+    a.part = dweight ? (float *)workspace : nullptr;
+    hipError_t err = launch_rms_norm_bwd(a, dtype == BIMAMBA_BF16, (hipStream_t)stream);
+    return err == hipSuccess ? BIMAMBA_OK : hip_fail(err, "launching the RMS norm's gradient");
+}
+
+int bimamba_rows8_pack(long long rows, int channels, int dtype, const void *x, const bimamba_rows8 *out,
+                       bimamba_stream stream) {
+    int rc = check_layer_norm(rows, channels, dtype);
+    if (rc) return rc;
+    if (!out) return fail(BIMAMBA_EINVAL, "out is NULL");
+    if (rows == 0) return BIMAMBA_OK;
+    if (!x || !out->q || !out->scale) return fail(BIMAMBA_EINVAL, "x, q and scale are required");
+    if (!aligned_to(x, dtype)) return fail(BIMAMBA_EINVAL, "x must be aligned to its elements");
+    if ((uintptr_t)out->scale & 3u) return fail(BIMAMBA_EINVAL, "the rows' scales must be 4-byte aligned");
+    if ((rc = check_apart({{"q", out->q, (size_t)rows * channels}, {"scale", out->scale, (size_t)rows * 4}},
+                          {{"x", x, (size_t)rows * channels * elem_size(dtype)}})))
+        return rc;
+    RmsArgs a;
+    memset(&a, 0, sizeof a);
+    a.rows = rows;
+    a.C = channels;
+    a.x = x;
+    a.q = (int8_t *)out->q;
+    a.scale = out->scale;
+    hipError_t e = launch_rms_norm(a, dtype == BIMAMBA_BF16, (hipStream_t)stream);
+    return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the rows' quantization");
+}
+
+int bimamba_linear8(long long rows, int cin, int cout, int dtype, const bimamba_rows8 *x, const bimamba_rows8 *weight,
+                    const float *bias, void *out, bimamba_stream stream) {
+    int rc = check_rows(rows, dtype);
+    if (rc) return rc;
+    // sums of cin products of magnitude 2^14 at most stay inside int32
+    if (cin < 1 || cin > 131071) return fail(BIMAMBA_EUNSUPPORTED, "cin %d not in [1, 131071]", cin);
+    if (cout < 1 || cout > (1 << 24)) return fail(BIMAMBA_EUNSUPPORTED, "cout %d not in [1, 2^24]", cout);
+    // the most workgroups of the smallest tile, 64 x 64
+    if (((rows + 63) / 64) * ((cout + 63) / 64) > (1LL << 24) - 16)
+        return fail(BIMAMBA_EUNSUPPORTED, "%lld rows of %d channels are too many for one launch", rows, cout);
+    if (!x || !weight) return fail(BIMAMBA_EINVAL, "x and weight are required");
+    if (rows == 0) return BIMAMBA_OK;
+    if (!x->q || !x->scale || !weight->q || !weight->scale || !out)
+        return fail(BIMAMBA_EINVAL, "x's and weight's q and scale, and out are required");
+    if (((uintptr_t)x->scale | (uintptr_t)weight->scale | (uintptr_t)bias) & 3u)
+        return fail(BIMAMBA_EINVAL, "the scales and bias must be 4-byte aligned");
+    if (!aligned_to(out, dtype)) return fail(BIMAMBA_EINVAL, "out must be aligned to its elements");
+    if ((rc = check_apart({{"out", out, (size_t)rows * cout * elem_size(dtype)}},
+                          {{"x's q", x->q, (size_t)rows * cin}, {"x's scale", x->scale, (size_t)rows * 4},
+                           {"weight's q", weight->q, (size_t)cout * cin},
+                           {"weight's scale", weight->scale, (size_t)cout * 4}, {"bias", bias, (size_t)cout * 4}})))
+        return rc;
+    Linear8Args a;
+    a.rows = rows;
+    a.cin = cin;
+    a.cout = cout;
+    a.x = (const int8_t *)x->q;
+    a.w = (const int8_t *)weight->q;
+    a.xs = x->scale;
+    a.ws = weight->scale;
+    a.bias = bias;
+    a.out = out;
+    hipError_t e = launch_linear8(a, dtype == BIMAMBA_BF16, (hipStream_t)stream);
+    return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the 8-bit product");
+}
+
 }  // extern "C"

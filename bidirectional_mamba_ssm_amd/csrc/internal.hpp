@@ -173,6 +173,34 @@ struct LnBwdArgs {
 };
 int layer_norm_bwd_wgs(long long rows, int C, bool bf16);
 hipError_t launch_layer_norm_bwd(const LnBwdArgs &a, bool bf16, hipStream_t s);
+// mean and db not used
+hipError_t launch_rms_norm_bwd(const LnBwdArgs &a, bool bf16, hipStream_t s);
+
+// rms_norm.hip: RMS norm to the dtype, to 8-bit rows, or to both; rows alone
+struct RmsArgs {
+    long long rows;
+    int C;                     // 8 .. 16384
+    float eps;
+    bool norm;                 // false: x itself, to 8 bits (no residual, weight, out)
+    const void *x, *res;       // [rows][C]; res may be nullptr
+    const float *w;            // [C] or nullptr
+    void *out, *sum;           // [rows][C]; out may be nullptr with q, sum only with res
+    float *rstd;               // [rows] or nullptr
+    int8_t *q;                 // [rows][C] or nullptr
+    float *scale;              // [rows], with q
+};
+hipError_t launch_rms_norm(const RmsArgs &a, bool bf16, hipStream_t s);
+
+// linear8.hip: product of 8-bit rows
+struct Linear8Args {
+    long long rows;
+    int cin, cout;
+    const int8_t *x, *w;       // [rows][cin], [cout][cin]
+    const float *xs, *ws;      // [rows], [cout]
+    const float *bias;         // [cout] or nullptr
+    void *out;                 // [rows][cout]
+};
+hipError_t launch_linear8(const Linear8Args &a, bool bf16, hipStream_t s);
 
 // gated_norm_bwd.hip
 struct EpiBwdArgs {

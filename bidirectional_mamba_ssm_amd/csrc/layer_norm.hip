@@ -29,71 +29,18 @@
 // 521); in the gradient 8 waves a workgroup and two workgroups a CU (four
 // waves: 35 us; 1024 workgroups: 28 us and 10 us of sums; more workgroups than
 // are resident cost a second round).
+// Rows are laid over the lanes as row_form.hpp says.
 //
-// The last vector of a row whose length is no multiple of it starts at C - V
-// instead: it overlaps its neighbour, its first `skip` elements count in no
-// sum, and its stores repeat the neighbour's values. No load leaves the row.
-#include "internal.hpp"
-#include "rows.hpp"
+// The RMS norm's gradient (rms_norm.hip holds its forward) is the same kernel
+// without the mean: mu = 0, no mean g, no db.
+#include "row_form.hpp"
 
 namespace bm {
 namespace {
 
-constexpr int kMaxWaves = 8;   // of a row
-
-// Where a lane's vectors lie in a row of C channels shared by `waves` waves:
-// vector k starts at channel c[k]. has[k] is false for a lane past the end (it
-// reads the row's last vector again). In vector kt (-1: none) some lane's
-// first `skip` elements belong to the vector before.
-template <int V, int NV>
-struct Place {
-    int c[NV];
-    bool has[NV];
-    int kt, skip;
-    float count;   // elements of this wave
-    __device__ __forceinline__ Place(int C, int t, int lanes) {
-        kt = C % V ? C / (V * lanes) : -1;
-        skip = 0;
-        int n = 0;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int at = (k * lanes + t) * V;
-            c[k] = min(at, C - V);
-            has[k] = at < C;
-            if (at < C && at != c[k]) skip = at - c[k];
-            const int first = (k * lanes + (t & ~63)) * V;
-            n += max(0, min(64 * V, C - first));
-        }
-        count = (float)n;
-    }
-    // v's element j of vector k counts: all do but the overlapped ones
-    __device__ __forceinline__ float own(int k, int j, float v) const { return k == kt && j < skip ? 0.f : v; }
-};
-
-template <int V>
-__device__ __forceinline__ void load_w(const float *p, int c, float none, float *v) {
-    if (p) {
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-            const rvec r = *(const u4_a4 *)(p + c + 4 * i);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[4 * i + j] = __uint_as_float(r[j]);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = none;
-    }
-}
-
 // Lanes of a row: G of a wave, or (G = 0) several waves.
 // The forward pass has workgroups of kRows waves, or (G = 0) one row each.
 constexpr int kRows = 4;
-
-template <int G>
-__device__ __forceinline__ float lanes_total(float v) {
-    if constexpr (G == 0 || G == 64) return wave_total(v);
-    else return group_total<G>(v);
-}
 
 template <typename T, int NV, int G, bool RES, bool CK>
 __global__ __launch_bounds__(G == 0 ? 64 * kMaxWaves : 64 * kRows) void k_layer_norm(LnArgs a) {
@@ -250,15 +197,16 @@ __global__ __launch_bounds__(G == 0 ? 64 * kMaxWaves : 64 * kRows) void k_layer_
 // each, MULTI if W > 1.
 constexpr int kBwdWaves = 8;
 
-template <typename T, int NV, int G, bool Q8, bool DSUM>
+template <typename T, int NV, int G, bool Q8, bool DSUM, bool RMS>
 __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, int W, int R) {
     using L = Lane<T>;
     constexpr int V = L::V, E = V * NV;
     constexpr bool MULTI = G == 0;
     constexpr int kShare = MULTI ? 1 : 64 / G;   // rows of a wave
+    constexpr int kSums = RMS ? 1 : 2;           // dw, and db
     __shared__ float2 part[MULTI ? 2 : 1][MULTI ? kBwdWaves : 1];
     // sums to join: W E 64 of dw and of db, where R > 1 (then W <= 4)
-    __shared__ float sum[E > 16 ? 1 : MULTI ? 2 * E * 256 : 2 * E * 64];
+    __shared__ float sum[E > 16 ? 1 : MULTI ? kSums * E * 256 : kSums * E * 64];
     const int C = a.C;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int sub = MULTI ? wave / W : wave, lanes = MULTI ? 64 * W : G;
@@ -281,7 +229,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
         float mean, rstd;
     };
     auto fetch = [&](Row &o, long long r) {
-        o.mean = a.mean[r];
+        o.mean = RMS ? 0.f : a.mean[r];
         o.rstd = a.rstd[r];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -327,9 +275,9 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float d = L::get(r.g[k], j);
-                xh[k][j] = (xh[k][j] - r.mean) * r.rstd;
+                xh[k][j] = (RMS ? xh[k][j] : xh[k][j] - r.mean) * r.rstd;
                 if (!MULTI || live) {
-                    db[k][j] += d;
+                    if (!RMS) db[k][j] += d;
                     dw[k][j] = fmaf(d, xh[k][j], dw[k][j]);
                 }
                 const float gw = d * w[k][j];
@@ -361,7 +309,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
             }
             if (!live) continue;
         }
-        const float m1 = t1 * inv, m2 = t2 * inv;
+        const float m1 = RMS ? 0.f : t1 * inv, m2 = t2 * inv;
         T *dx = (T *)a.dx + row * C;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -390,7 +338,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
     }
     if (!a.part) return;
     // this workgroup's share of dw | db: the sums of the R rows at a time added in order
-    float *out = a.part + (size_t)blockIdx.x * 2 * C;
+    float *out = a.part + (size_t)blockIdx.x * kSums * C;
     if constexpr (kShare > 1) {
         // the rows that share a wave first
 #pragma unroll
@@ -400,7 +348,7 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     dw[k][j] += __shfl_xor(dw[k][j], off);
-                    db[k][j] += __shfl_xor(db[k][j], off);
+                    if (!RMS) db[k][j] += __shfl_xor(db[k][j], off);
                 }
     }
     if constexpr (E <= 16) {
@@ -414,11 +362,11 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
                         float *p = sum + (k * V + j) * lanes + t, *q = p + E * lanes;
                         if (s > 0) {
                             dw[k][j] += *p;
-                            db[k][j] += *q;
+                            if (!RMS) db[k][j] += *q;
                         }
                         if (s < n - 1) {
                             *p = dw[k][j];
-                            *q = db[k][j];
+                            if (!RMS) *q = db[k][j];
                         }
                     }
             }
@@ -434,47 +382,19 @@ __global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(LnBwdArgs a, 
 #pragma unroll
             for (int i = 0; i < V / 4; ++i) {
                 Lane<float>::store(out + at.c[k] + 4 * i, Lane<float>::pack(dw[k] + 4 * i));
-                Lane<float>::store(out + C + at.c[k] + 4 * i, Lane<float>::pack(db[k] + 4 * i));
+                if (!RMS) Lane<float>::store(out + C + at.c[k] + 4 * i, Lane<float>::pack(db[k] + 4 * i));
             }
         } else {
 #pragma unroll
             for (int j = 0; j < V; ++j)
                 if (j >= skip) {
                     out[at.c[k] + j] = dw[k][j];
-                    out[C + at.c[k] + j] = db[k][j];
+                    if (!RMS) out[C + at.c[k] + j] = db[k][j];
                 }
         }
     }
 }
 
-// How a row is held: G lanes of one wave or (G = 0) `waves` waves, nv vectors
-// a lane. Rows of up to 256 channels take the fewest lanes, 8 elements each
-// (kernel times, bf16: 60 000 x 64 5.6 us, with residual and checkpoint 8.9,
-// their gradient 12.4; a wave a row 16.8, 26.9 and 21.8; 60 000 x 128 13.3 and
-// 16.0 for 27.2 and 23.4); wider ones `lane` elements a lane, or the fewest
-// that kMaxWaves waves can do with.
-struct Form {
-    int nv, waves, G;
-};
-template <typename T>
-Form row_form(int C, int lane) {
-    const int V = 16 / (int)sizeof(T);
-    Form f;
-    f.nv = 1;
-    f.waves = 1;
-    f.G = 64;
-    if (C <= 256) {
-        f.nv = 8 / V;
-        f.G = C <= 64 ? 8 : C <= 128 ? 16 : 32;
-        return f;
-    }
-    const int units = (C + 64 * V - 1) / (64 * V);          // vectors of a row, in waves
-    while (f.nv * V < lane && f.nv < units) f.nv *= 2;
-    while (f.nv * kMaxWaves < units) f.nv *= 2;
-    f.waves = (units + f.nv - 1) / f.nv;
-    if (f.waves > 1) f.G = 0;
-    return f;
-}
 template <typename T>
 Form bwd_form(int C) { return row_form<T>(C, 8); }
 // rows that a workgroup of the gradient takes at a time
@@ -511,15 +431,15 @@ hipError_t launch_fwd(const LnArgs &a, hipStream_t s) {
     return hipErrorInvalidValue;
 }
 
-template <typename T, bool Q8, bool DSUM>
+template <typename T, bool Q8, bool DSUM, bool RMS>
 hipError_t launch_b(const LnBwdArgs &a, hipStream_t s) {
     const Form f = bwd_form<T>(a.C);
     const int R = bwd_rows(f);
     const dim3 grid((unsigned)bwd_wgs<T>(a.rows, a.C)), block(64 * (f.G ? kBwdWaves : f.waves * R));
 #define GO(NV, G_)                                                                                       \
     if (f.nv == NV && f.G == G_) {                                                                       \
-        BM_LAUNCH("layer_norm_bwd", (k_layer_norm_bwd<T, NV, G_, Q8, DSUM>), grid, block, 0, s, a,         \
-                  f.waves, R);                                                                           \
+        BM_LAUNCH(RMS ? "rms_norm_bwd" : "layer_norm_bwd", (k_layer_norm_bwd<T, NV, G_, Q8, DSUM, RMS>), grid, \
+                  block, 0, s, a, f.waves, R);                                                           \
         return hipGetLastError();                                                                        \
     }
     constexpr int N8 = 8 * sizeof(T) / 16;   // vectors that make 8 elements
@@ -533,10 +453,20 @@ hipError_t launch_fwd_t(const LnArgs &a, hipStream_t s) {
     if (a.res) return a.q ? launch_fwd<T, true, true>(a, s) : launch_fwd<T, true, false>(a, s);
     return a.q ? launch_fwd<T, false, true>(a, s) : launch_fwd<T, false, false>(a, s);
 }
-template <typename T>
+template <typename T, bool RMS>
 hipError_t launch_b_t(const LnBwdArgs &a, hipStream_t s) {
-    if (a.xscale) return a.dsum ? launch_b<T, true, true>(a, s) : launch_b<T, true, false>(a, s);
-    return a.dsum ? launch_b<T, false, true>(a, s) : launch_b<T, false, false>(a, s);
+    if (a.xscale) return a.dsum ? launch_b<T, true, true, RMS>(a, s) : launch_b<T, true, false, RMS>(a, s);
+    return a.dsum ? launch_b<T, false, true, RMS>(a, s) : launch_b<T, false, false, RMS>(a, s);
+}
+template <bool RMS>
+hipError_t launch_bwd(const LnBwdArgs &a, bool bf16, hipStream_t s) {
+    if (a.rows > 0) {
+        hipError_t e = bf16 ? launch_b_t<uint16_t, RMS>(a, s) : launch_b_t<float, RMS>(a, s);
+        if (e != hipSuccess) return e;
+    }
+    if (!a.dw && !a.db) return hipSuccess;
+    const ColSum c{a.part, layer_norm_bwd_wgs(a.rows, a.C, bf16), a.C, 1, RMS ? 0 : 1, a.dw, a.db};
+    return launch_col_sum(&c, 1, s);
 }
 
 }  // namespace
@@ -546,19 +476,13 @@ hipError_t launch_layer_norm(const LnArgs &a, bool bf16, hipStream_t s) {
     return bf16 ? launch_fwd_t<uint16_t>(a, s) : launch_fwd_t<float>(a, s);
 }
 
-// workgroups of the gradient: each leaves one row of 2 C partial sums
+// workgroups of the gradient: each leaves one row of 2 C partial sums (C of
+// the RMS norm's)
 int layer_norm_bwd_wgs(long long rows, int C, bool bf16) {
     return bf16 ? bwd_wgs<uint16_t>(rows, C) : bwd_wgs<float>(rows, C);
 }
 
-hipError_t launch_layer_norm_bwd(const LnBwdArgs &a, bool bf16, hipStream_t s) {
-    if (a.rows > 0) {
-        hipError_t e = bf16 ? launch_b_t<uint16_t>(a, s) : launch_b_t<float>(a, s);
-        if (e != hipSuccess) return e;
-    }
-    if (!a.dw && !a.db) return hipSuccess;
-    const ColSum c{a.part, layer_norm_bwd_wgs(a.rows, a.C, bf16), a.C, 1, 1, a.dw, a.db};
-    return launch_col_sum(&c, 1, s);
-}
+hipError_t launch_layer_norm_bwd(const LnBwdArgs &a, bool bf16, hipStream_t s) { return launch_bwd<false>(a, bf16, s); }
+hipError_t launch_rms_norm_bwd(const LnBwdArgs &a, bool bf16, hipStream_t s) { return launch_bwd<true>(a, bf16, s); }
 
 }  // namespace bm

@@ -509,6 +509,69 @@ int bimamba_layer_norm_bwd(long long rows, int channels, int dtype, const void *
                            const void *dsum, void *dx, float *dweight, float *dbias, void *workspace,
                            size_t workspace_bytes, bimamba_stream stream);
 
+/* ---- 8-bit rows, the norm that writes them and the product that reads them ---
+ *
+ * For serving a mixer's projections in 8 bits: each row (a token's activations,
+ * or an output channel's weights) is kept as signed integers and one scale,
+ *
+ *   top = max |v|,  scale = top / 127,  q = round(v * (127 / top))
+ *
+ * the division and the product rounded to fp32, round() to the nearest
+ * integer, ties to even; the row stands for q * scale. A row with
+ * top < 2^-100 stands for zeros (scale 0); a row that holds an infinity or a NaN
+ * has a NaN for its scale and zeros for q. */
+typedef struct {
+    void *q;       /* int8 [rows][channels]                                    */
+    float *scale;  /* [rows]                                                   */
+} bimamba_rows8;
+/* x: dtype [rows][channels], channels 8..16384. Arrays are aligned to their
+ * elements; calls whose outputs overlap each other or x are refused. */
+int bimamba_rows8_pack(long long rows, int channels, int dtype, const void *x, const bimamba_rows8 *out,
+                       bimamba_stream stream);
+
+/* RMS norm of each row, optionally after a residual add:
+ *
+ *   h = x + residual,  out = h * rstd * weight,  rstd = 1 / sqrt(mean h^2 + eps)
+ *
+ *  channels  8..16384
+ *  x         dtype [rows][channels]
+ *  residual  dtype [rows][channels], or NULL (h = x)
+ *  weight    float [channels], or NULL (1)
+ *  out       dtype [rows][channels], or NULL with out8
+ *  sum       dtype [rows][channels]: h rounded to the dtype, which is what the
+ *            norm then sees; with residual only (NULL without)
+ *  rstd      float [rows] for the gradient, or NULL
+ *  out8      NULL, or where to write out (before its rounding to the dtype) as
+ *            8-bit rows, in the same pass
+ * out and sum may each be x or residual itself; calls whose outputs overlap
+ * each other, or an input in any other way, are refused. Arrays are aligned
+ * to their elements. Computed in fp32. */
+int bimamba_rms_norm(long long rows, int channels, int dtype, const void *x, const void *residual,
+                     const float *weight, float eps, void *out, void *sum, float *rstd, const bimamba_rows8 *out8,
+                     bimamba_stream stream);
+/* Its gradient, with rstd from the forward pass; x, x_scale, dout, dsum and
+ * dx as in bimamba_layer_norm_bwd (x: h, or its 8-bit checkpoint). dweight:
+ * out float [channels], or NULL if not wanted (the workspace is needed with it
+ * only). The same overlaps are allowed. With no row dweight is 0. */
+int bimamba_rms_norm_bwd_workspace_size(long long rows, int channels, int dtype, size_t *bytes);
+int bimamba_rms_norm_bwd(long long rows, int channels, int dtype, const void *x, const uint8_t *x_scale,
+                         const float *rstd, const float *weight, const void *dout, const void *dsum, void *dx,
+                         float *dweight, void *workspace, size_t workspace_bytes, bimamba_stream stream);
+
+/* Product of 8-bit rows, on the integer matrix cores:
+ *
+ *   out[r][n] = x.scale[r] * weight.scale[n] * sum_c x.q[r][c] * weight.q[n][c] + bias[n]
+ *
+ *  rows, cin, cout  >= 0, 1..131071, 1..2^24 (and at most 2^24 - 16 tiles of 64 x 64)
+ *  x         8-bit rows [rows][cin];  weight  8-bit rows [cout][cin]
+ *  bias      float [cout], or NULL
+ *  out       dtype [rows][cout], which may not overlap an input
+ * The sums are exact (int32), whatever the order; scaled and rounded in fp32,
+ * bf16 to nearest even. Arrays are aligned to their elements (16-byte
+ * aligned rows, cin a multiple of 16, are read faster). */
+int bimamba_linear8(long long rows, int cin, int cout, int dtype, const bimamba_rows8 *x,
+                    const bimamba_rows8 *weight, const float *bias, void *out, bimamba_stream stream);
+
 /* Per-kernel timing for benchmarks and profilers, per calling thread.
  * Between bimamba_profile_begin() and bimamba_profile_end(), every kernel the
  * library launches from this thread is bracketed by two hipEvents recorded on
