@@ -1253,3 +1253,160 @@ def linear8(x, weight, bias=None, dtype=torch.bfloat16, out=None, stream=None):
     if rc:
         _abi.check(rc)
     return out
+
+
+DELTA = ("q", "k", "v", "g", "beta")
+
+
+def _delta_dims(d):
+    q, v = d["q"], d["v"]
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("v must be [batch, L, H, P] and q [batch, L, G, N]")
+    return tuple(v.shape) + tuple(q.shape[2:])
+
+
+def _delta_dir(d, dims, dtype, dev, name):
+    batch, L, H, P, G, N = dims
+    for k, shape, dt in (("q", (batch, L, G, N), dtype), ("k", (batch, L, G, N), dtype),
+                         ("v", (batch, L, H, P), dtype), ("g", (batch, L, H), torch.float32),
+                         ("beta", (batch, L, H), torch.float32)):
+        _check(d[k], f"{name}.{k}", shape, dt, dev)
+    return ctypes.byref(_abi.DeltaDir(*(d[k].data_ptr() for k in DELTA)))
+
+
+@functools.lru_cache(maxsize=4096)
+def _delta_size(query, dims, dtype, nseq):
+    """(the workspace, the bimamba_shape to pass, which the library only reads)."""
+    batch, L, H, P, G, N = dims
+    n = ctypes.c_size_t(0)
+    shape = ctypes.byref(_sizes(_abi.Shape, "the problem's shape", batch, L, H, P, N, G, 64, _dtype_code(dtype), 0))
+    _abi.check(getattr(lib(), query)(shape, nseq, ctypes.byref(n)))
+    return n.value, shape
+
+
+def _delta_scale(scale, N):
+    return N ** -0.5 if scale is None else float(scale)
+
+
+def _delta_workspace(workspace, nbytes, dev):
+    if workspace is None:
+        return _workspace(nbytes, dev), nbytes
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def delta_workspace_size(fwd, nseq=0):
+    """Bytes of workspace of delta_fwd and delta_step for such a direction."""
+    return _delta_size("bimamba_delta_workspace_size", _delta_dims(fwd), fwd["v"].dtype, nseq)[0]
+
+
+def delta_bwd_workspace_size(fwd, nseq=0):
+    """Bytes of workspace of delta_bwd for such a direction."""
+    return _delta_size("bimamba_delta_bwd_workspace_size", _delta_dims(fwd), fwd["v"].dtype, nseq)[0]
+
+
+def delta_fwd(fwd, bwd=None, scale=None, cu_seqlens=None, init_state=None, final_state=None, y=None,
+              workspace=None, stream=None):
+    """The gated delta rule over whole sequences (bimamba_delta_fwd).
+
+    fwd/bwd: dicts of device tensors q, k [b,L,G,N], v [b,L,H,P] (bf16 or
+    fp32), g (the decay's logarithm) and beta [b,L,H] float32; bwd, in forward
+    time order, runs over the reversed sequence, and both outputs are summed.
+    scale: of the output, N^-1/2 unless given. cu_seqlens: host list/tensor of
+    nseq+1 offsets. init_state, final_state: float32 [sequences,H,P,N] of the
+    forward direction (final_state is written and may be init_state). Returns
+    y (float32 [b,L,H,P])."""
+    dev = _cuda_device(fwd["v"])
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, delta_fwd, fwd, bwd, scale, cu_seqlens, init_state, final_state, y, workspace)
+    dims, dtype = _delta_dims(fwd), fwd["v"].dtype
+    batch, L, H, P, G, N = dims
+    cu_arr, nseq = _offsets(cu_seqlens)
+    nbytes, shape = _delta_size("bimamba_delta_workspace_size", dims, dtype, max(nseq, 0))
+    fd = _delta_dir(fwd, dims, dtype, dev, "fwd")
+    bd = _delta_dir(bwd, dims, dtype, dev, "bwd") if bwd is not None else None
+    units = nseq if cu_seqlens is not None else batch
+    for t, name in ((init_state, "init_state"), (final_state, "final_state")):
+        if t is not None:
+            _check(t, name, (units, H, P, N), torch.float32, dev)
+    y = _out(y, "y", (batch, L, H, P), torch.float32, dev)
+    ws, nbytes = _delta_workspace(workspace, nbytes, dev)
+    rc = lib().bimamba_delta_fwd(shape, fd, bd, _delta_scale(scale, N), cu_arr, nseq, _adr(init_state),
+                                 _adr(final_state), y.data_ptr(), _adr(ws), nbytes, _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
+    return y
+
+
+def delta_step(state, fwd, bwd=None, commit=True, scale=None, y=None, workspace=None, stream=None):
+    """One cached step of the gated delta rule (bimamba_delta_step): a block
+    of 1..256 tokens (one, when decoding) for each row of fwd, which continues
+    the state of its number. state: a State of the shape (slots, H, P, N), or a
+    float32 tensor [slots,H,P,N]; with commit the rows' last states replace
+    theirs. bwd sees the block alone. Returns y (float32 [b,L,H,P])."""
+    dev = _cuda_device(fwd["v"])
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, delta_step, state, fwd, bwd, commit, scale, y, workspace)
+    dims, dtype = _delta_dims(fwd), fwd["v"].dtype
+    batch, L, H, P, G, N = dims
+    nbytes, shape = _delta_size("bimamba_delta_workspace_size", dims, dtype, 0)
+    fd = _delta_dir(fwd, dims, dtype, dev, "fwd")
+    bd = _delta_dir(bwd, dims, dtype, dev, "bwd") if bwd is not None else None
+    slots = state.shape[0]
+    if isinstance(state, State):
+        if tuple(state.shape) != (slots, H, P, N):
+            raise ValueError(f"state has shape {tuple(state.shape)}, expected (slots, {H}, {P}, {N})")
+        at = state.data_ptr()
+    else:
+        _check(state, "state", (slots, H, P, N), torch.float32, dev)
+        at = state.data_ptr()
+    if batch > slots:
+        raise ValueError(f"batch {batch} exceeds the state's {slots} slots")
+    y = _out(y, "y", (batch, L, H, P), torch.float32, dev)
+    ws, nbytes = _delta_workspace(workspace, nbytes, dev)
+    rc = lib().bimamba_delta_step(shape, at, fd, bd, _delta_scale(scale, N), int(bool(commit)), y.data_ptr(),
+                                  _adr(ws), nbytes, _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
+    return y
+
+
+def _delta_grads(g, dims, dev, name):
+    batch, L, H, P, G, N = dims
+    shapes = dict(q=(batch, L, G, N), k=(batch, L, G, N), v=(batch, L, H, P), g=(batch, L, H), beta=(batch, L, H))
+    g = {k: _out(None if g is None else g[k], f"{name}_grad.{k}", v, torch.float32, dev) for k, v in shapes.items()}
+    return g, ctypes.byref(_abi.DeltaGrad(*(g[k].data_ptr() for k in DELTA)))
+
+
+def delta_bwd(fwd, bwd, dy, scale=None, cu_seqlens=None, init_state=None, dfinal=None, dinit=None, grads=None,
+              workspace=None, stream=None):
+    """Gradient of delta_fwd (bimamba_delta_bwd) for dy (float32 [b,L,H,P],
+    which both streams get) and dfinal (float32 like final_state, or None).
+    init_state: the forward's. dinit: where to write init_state's gradient, or
+    None. Returns (gfwd, gbwd), dicts of float32 tensors keyed q, k, v, g, beta
+    (gbwd None without bwd); grads: optional such dicts to write into."""
+    dev = _cuda_device(fwd["v"])
+    if _elsewhere(dev, stream):
+        return _run_on(dev, stream, delta_bwd, fwd, bwd, dy, scale, cu_seqlens, init_state, dfinal, dinit, grads,
+                       workspace)
+    dims, dtype = _delta_dims(fwd), fwd["v"].dtype
+    batch, L, H, P, G, N = dims
+    cu_arr, nseq = _offsets(cu_seqlens)
+    nbytes, shape = _delta_size("bimamba_delta_bwd_workspace_size", dims, dtype, max(nseq, 0))
+    fd = _delta_dir(fwd, dims, dtype, dev, "fwd")
+    bd = _delta_dir(bwd, dims, dtype, dev, "bwd") if bwd is not None else None
+    _check(dy, "dy", (batch, L, H, P), torch.float32, dev)
+    units = nseq if cu_seqlens is not None else batch
+    for t, name in ((init_state, "init_state"), (dfinal, "dfinal"), (dinit, "dinit")):
+        if t is not None:
+            _check(t, name, (units, H, P, N), torch.float32, dev)
+    gl = tuple(grads) if grads is not None else (None, None)
+    gf, gfp = _delta_grads(gl[0], dims, dev, "fwd")
+    gb, gbp = _delta_grads(gl[1], dims, dev, "bwd") if bwd is not None else (None, None)
+    ws, nbytes = _delta_workspace(workspace, nbytes, dev)
+    rc = lib().bimamba_delta_bwd(shape, fd, bd, _delta_scale(scale, N), cu_arr, nseq, _adr(init_state), _adr(dfinal),
+                                 dy.data_ptr(), gfp, gbp, _adr(dinit), _adr(ws), nbytes, _raw_stream(dev.index))
+    if rc:
+        _abi.check(rc)
+    return gf, gb

@@ -29,7 +29,8 @@ EXPORTS = (
     "bimamba_gated_norm_bwd_workspace_size", "bimamba_gated_norm_bwd", "bimamba_layer_norm",
     "bimamba_layer_norm_bwd_workspace_size", "bimamba_layer_norm_bwd",
     "bimamba_rows8_pack", "bimamba_rms_norm", "bimamba_rms_norm_bwd_workspace_size", "bimamba_rms_norm_bwd",
-    "bimamba_linear8",
+    "bimamba_linear8", "bimamba_delta_workspace_size", "bimamba_delta_fwd", "bimamba_delta_step",
+    "bimamba_delta_bwd_workspace_size", "bimamba_delta_bwd",
 )
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -78,6 +79,16 @@ class Act8Ptrs(ctypes.Structure):
 
 class Rows8Ptrs(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class DeltaDir(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("g", ctypes.c_void_p), ("beta", ctypes.c_void_p)]
+
+
+class DeltaGrad(ctypes.Structure):
+    _fields_ = [("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p),
+                ("dg", ctypes.c_void_p), ("dbeta", ctypes.c_void_p)]
 
 
 class ConvGrad(ctypes.Structure):
@@ -162,6 +173,12 @@ def load():
     lib.bimamba_rms_norm.argtypes = [ll, ci, ci, vp, vp, vp, cf, vp, vp, vp, rp, vp]
     lib.bimamba_rms_norm_bwd_workspace_size.argtypes = [ll, ci, ci, np_]
     lib.bimamba_rms_norm_bwd.argtypes = [ll, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, size, vp]
+    ddp, dgp = ctypes.POINTER(DeltaDir), ctypes.POINTER(DeltaGrad)
+    lib.bimamba_delta_workspace_size.argtypes = [sp, ci, np_]
+    lib.bimamba_delta_fwd.argtypes = [sp, ddp, ddp, cf, i32p, ci, vp, vp, vp, vp, size, vp]
+    lib.bimamba_delta_step.argtypes = [sp, vp, ddp, ddp, cf, ci, vp, vp, size, vp]
+    lib.bimamba_delta_bwd_workspace_size.argtypes = [sp, ci, np_]
+    lib.bimamba_delta_bwd.argtypes = [sp, ddp, ddp, cf, i32p, ci, vp, vp, vp, dgp, dgp, vp, vp, size, vp]
     lib.bimamba_linear8.argtypes = [ll, ci, ci, ci, rp, rp, vp, vp, vp]
     for name in EXPORTS:
         getattr(lib, name).restype = getattr(lib, name).restype or ctypes.c_int

@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "../../include/bimamba.h"
+#include "delta.hpp"
 #include "internal.hpp"
 
 using namespace bm;
@@ -1451,6 +1452,279 @@ int bimamba_linear8(long long rows, int cin, int cout, int dtype, const bimamba_
     a.out = out;
     hipError_t e = launch_linear8(a, dtype == BIMAMBA_BF16, (hipStream_t)stream);
     return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the 8-bit product");
+}
+
+// ---- the gated delta rule --------------------------------------------------------
+
+namespace {
+
+int check_delta_shape(const bimamba_shape *s, int nseq, bool step) {
+    int rc = check_shape(s, step);
+    if (rc) return rc;
+    if (s->flags) return fail(BIMAMBA_EINVAL, "flags 0x%x: none is defined for the delta rule", s->flags);
+    if (s->chunk != kDeltaChunk) return fail(BIMAMBA_EUNSUPPORTED, "chunk %d is not %d", s->chunk, kDeltaChunk);
+    if (nseq < 0) return fail(BIMAMBA_EINVAL, "nseq %d < 0", nseq);
+    // a launch has fewer than 2^32 threads: 64 for 16 columns of a head of a
+    // unit, 512 for a chunk and group
+    const long long units = nseq ? nseq : s->batch, cols = (s->headdim + 15) / 16;
+    if (units * s->nheads > (1LL << 25) / cols)
+        return fail(BIMAMBA_EUNSUPPORTED, "%lld sequences of %d heads are too many for one launch", units, s->nheads);
+    if (delta_slots((int)units, s->seqlen, nseq > 0) * s->ngroups > (1LL << 23) - 8)
+        return fail(BIMAMBA_EUNSUPPORTED, "%lld x %d tokens are too many for one launch", units, s->seqlen);
+    return BIMAMBA_OK;
+}
+int check_delta_dir(const bimamba_delta_dir *d, const char *name, bool empty) {
+    if (!d) return fail(BIMAMBA_EINVAL, "%s direction is NULL", name);
+    if (empty) return BIMAMBA_OK;
+    if (!d->q || !d->k || !d->v || !d->g || !d->beta)
+        return fail(BIMAMBA_EINVAL, "%s: q, k, v, g and beta are required", name);
+    if (!aligned16(d->q) || !aligned16(d->k) || !aligned16(d->v))
+        return fail(BIMAMBA_EINVAL, "%s: q, k and v must be 16-byte aligned", name);
+    if (((uintptr_t)d->g | (uintptr_t)d->beta) & 3u)
+        return fail(BIMAMBA_EINVAL, "%s: g and beta must be 4-byte aligned", name);
+    return BIMAMBA_OK;
+}
+int check_packed(const bimamba_shape *s, const int32_t *cu, int nseq) {
+    if (!cu) return nseq ? fail(BIMAMBA_EINVAL, "nseq %d given without cu_seqlens", nseq) : BIMAMBA_OK;
+    if (s->batch != 1) return fail(BIMAMBA_EINVAL, "cu_seqlens requires batch == 1");
+    return check_offsets(cu, nseq, s->seqlen);
+}
+int check_scale(float scale) {
+    // not a NaN, not infinite
+    return scale - scale == 0.f ? BIMAMBA_OK : fail(BIMAMBA_EINVAL, "scale must be finite");
+}
+struct DeltaSizes {
+    size_t qk, v, gates, y, state;   // bytes of q or k, v, g or beta, y, a state of every unit
+};
+DeltaSizes delta_sizes(const bimamba_shape *s, int nseq) {
+    const size_t tok = (size_t)s->batch * s->seqlen, e = elem_size(s->dtype), hp = (size_t)s->nheads * s->headdim;
+    DeltaSizes z;
+    z.qk = tok * s->ngroups * s->d_state * e;
+    z.v = tok * hp * e;
+    z.gates = tok * s->nheads * 4;
+    z.y = tok * hp * 4;
+    z.state = (size_t)(nseq ? nseq : s->batch) * hp * s->d_state * 4;
+    return z;
+}
+DeltaArgs delta_args(const bimamba_shape *s, const bimamba_delta_dir *d, float scale, const int32_t *cu, int nseq,
+                     bool reverse) {
+    DeltaArgs a;
+    memset(&a, 0, sizeof a);
+    a.q = d->q;
+    a.k = d->k;
+    a.v = d->v;
+    a.g = d->g;
+    a.beta = d->beta;
+    a.scale = scale;
+    a.units = cu ? nseq : s->batch;
+    a.L = s->seqlen;
+    a.H = s->nheads;
+    a.P = s->headdim;
+    a.N = s->d_state;
+    a.G = s->ngroups;
+    a.reverse = reverse;
+    a.cu = cu;
+    return a;
+}
+size_t delta_table(int nseq) { return nseq > 0 ? align256((size_t)(nseq + 1) * 4) : 0; }
+
+// The arrays of one or both directions, by name.
+struct DeltaNames {
+    Array in[10];
+    int n = 0;
+    void add(const bimamba_delta_dir *d, const DeltaSizes &z, bool reverse) {
+        if (!d) return;
+        const Array five[5] = {{reverse ? "the reverse q" : "the forward q", d->q, z.qk},
+                               {reverse ? "the reverse k" : "the forward k", d->k, z.qk},
+                               {reverse ? "the reverse v" : "the forward v", d->v, z.v},
+                               {reverse ? "the reverse g" : "the forward g", d->g, z.gates},
+                               {reverse ? "the reverse beta" : "the forward beta", d->beta, z.gates}};
+        for (const Array &a : five) in[n++] = a;
+    }
+};
+int check_delta_apart(const Array *written, int nw, const Array *read, int nr) {
+    for (int i = 0; i < nw; ++i) {
+        for (int j = i + 1; j < nw; ++j)
+            if (overlap(written[i], written[j]))
+                return fail(BIMAMBA_EINVAL, "%s overlaps %s", written[i].name, written[j].name);
+        for (int j = 0; j < nr; ++j)
+            if (overlap(written[i], read[j]))
+                return fail(BIMAMBA_EINVAL, "%s overlaps %s", written[i].name, read[j].name);
+    }
+    return BIMAMBA_OK;
+}
+
+}  // namespace
+
+int bimamba_delta_workspace_size(const bimamba_shape *s, int nseq, size_t *bytes) {
+    int rc = check_delta_shape(s, nseq, false);
+    if (rc) return rc;
+    if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
+    *bytes = delta_table(nseq);
+    return BIMAMBA_OK;
+}
+
+int bimamba_delta_fwd(const bimamba_shape *s, const bimamba_delta_dir *fwd, const bimamba_delta_dir *bwd, float scale,
+                      const int32_t *cu_seqlens, int nseq, const float *init_state, float *final_state, float *y,
+                      void *workspace, size_t workspace_bytes, bimamba_stream stream) {
+    int rc = check_delta_shape(s, cu_seqlens ? nseq : 0, false);
+    if (rc) return rc;
+    const bool empty = s->seqlen == 0;
+    if ((rc = check_delta_dir(fwd, "forward", empty))) return rc;
+    if (bwd && (rc = check_delta_dir(bwd, "reverse", empty))) return rc;
+    if ((rc = check_packed(s, cu_seqlens, nseq))) return rc;
+    if ((rc = check_scale(scale))) return rc;
+    if (!empty && !y) return fail(BIMAMBA_EINVAL, "y is NULL");
+    if (!aligned16(y) || !aligned16(init_state) || !aligned16(final_state))
+        return fail(BIMAMBA_EINVAL, "y, init_state and final_state must be 16-byte aligned");
+    size_t need = 0;
+    if ((rc = bimamba_delta_workspace_size(s, cu_seqlens ? nseq : 0, &need))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+    const DeltaSizes z = delta_sizes(s, cu_seqlens ? nseq : 0);
+    DeltaNames in;
+    in.add(fwd, z, false);
+    in.add(bwd, z, true);
+    const Array out[3] = {{"y", y, z.y}, {"final_state", final_state, z.state}, {"the workspace", workspace, need}};
+    if ((rc = check_delta_apart(out, 3, in.in, in.n))) return rc;
+    const Array init = {"init_state", init_state, z.state};
+    for (const Array &o : out)
+        if (overlap(o, init) && !(o.p == init.p && o.p == final_state))
+            return fail(BIMAMBA_EINVAL, "%s overlaps init_state", o.name);
+    hipStream_t st = (hipStream_t)stream;
+    const bool bf16 = s->dtype == BIMAMBA_BF16;
+    hipError_t e;
+    const int32_t *cu = nullptr;
+    if (cu_seqlens) {
+        if ((e = launch_store_offsets(cu_seqlens, nseq, (int32_t *)workspace, st)) != hipSuccess)
+            return hip_fail(e, "storing the offsets");
+        cu = (const int32_t *)workspace;
+    }
+    if (bwd && !empty) {
+        DeltaArgs a = delta_args(s, bwd, scale, cu, nseq, true);
+        a.y = y;
+        if ((e = launch_delta_seq(a, bf16, st)) != hipSuccess) return hip_fail(e, "launching the delta rule");
+    }
+    if (empty && !final_state) return BIMAMBA_OK;
+    DeltaArgs a = delta_args(s, fwd, scale, cu, nseq, false);
+    a.add = bwd != nullptr;
+    a.init = init_state;
+    a.last = final_state;
+    a.y = y;
+    if ((e = launch_delta_seq(a, bf16, st)) != hipSuccess) return hip_fail(e, "launching the delta rule");
+    return BIMAMBA_OK;
+}
+
+int bimamba_delta_step(const bimamba_shape *s, float *state, const bimamba_delta_dir *fwd,
+                       const bimamba_delta_dir *bwd, float scale, int commit, float *y, void *workspace,
+                       size_t workspace_bytes, bimamba_stream stream) {
+    int rc = check_delta_shape(s, 0, true);
+    if (rc) return rc;
+    if (!state) return fail(BIMAMBA_EINVAL, "state is NULL");
+    return bimamba_delta_fwd(s, fwd, bwd, scale, nullptr, 0, state, commit ? state : nullptr, y, workspace,
+                             workspace_bytes, stream);
+}
+
+int bimamba_delta_bwd_workspace_size(const bimamba_shape *s, int nseq, size_t *bytes) {
+    int rc = check_delta_shape(s, nseq, false);
+    if (rc) return rc;
+    if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
+    const DeltaSizes z = delta_sizes(s, 0);
+    const size_t slots = (size_t)delta_slots(nseq ? nseq : s->batch, s->seqlen, nseq > 0);
+    *bytes = delta_table(nseq) + 2 * align256(z.y) +
+             2 * align256(slots * s->nheads * s->headdim * s->d_state * 4);
+    return BIMAMBA_OK;
+}
+
+int bimamba_delta_bwd(const bimamba_shape *s, const bimamba_delta_dir *fwd, const bimamba_delta_dir *bwd, float scale,
+                      const int32_t *cu_seqlens, int nseq, const float *init_state, const float *dfinal,
+                      const float *dy, const bimamba_delta_grad *gfwd, const bimamba_delta_grad *gbwd, float *dinit,
+                      void *workspace, size_t workspace_bytes, bimamba_stream stream) {
+    int rc = check_delta_shape(s, cu_seqlens ? nseq : 0, false);
+    if (rc) return rc;
+    const bool empty = s->seqlen == 0;
+    const bimamba_delta_dir *dirs[2] = {fwd, bwd};
+    const bimamba_delta_grad *grads[2] = {gfwd, gbwd};
+    for (int i = 0; i < (bwd ? 2 : 1); ++i) {
+        const char *name = i ? "reverse" : "forward";
+        if ((rc = check_delta_dir(dirs[i], name, empty))) return rc;
+        const bimamba_delta_grad *g = grads[i];
+        if (!g) return fail(BIMAMBA_EINVAL, "%s gradients are NULL", name);
+        if (empty) continue;
+        if (!g->dq || !g->dk || !g->dv || !g->dg || !g->dbeta)
+            return fail(BIMAMBA_EINVAL, "%s: dq, dk, dv, dg and dbeta are required", name);
+        if (((uintptr_t)g->dq | (uintptr_t)g->dk | (uintptr_t)g->dv | (uintptr_t)g->dg | (uintptr_t)g->dbeta) & 3u)
+            return fail(BIMAMBA_EINVAL, "%s: gradient arrays must be 4-byte aligned", name);
+    }
+    if (!bwd && gbwd) return fail(BIMAMBA_EINVAL, "reverse gradients are given without the reverse direction");
+    if ((rc = check_packed(s, cu_seqlens, nseq))) return rc;
+    if ((rc = check_scale(scale))) return rc;
+    if (!empty && !dy) return fail(BIMAMBA_EINVAL, "dy is NULL");
+    if (!aligned16(dy) || !aligned16(init_state) || !aligned16(dfinal) || !aligned16(dinit))
+        return fail(BIMAMBA_EINVAL, "dy, init_state, dfinal and dinit must be 16-byte aligned");
+    size_t need = 0;
+    const int packed = cu_seqlens ? nseq : 0;
+    if ((rc = bimamba_delta_bwd_workspace_size(s, packed, &need))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+    const DeltaSizes z = delta_sizes(s, packed);
+    const size_t tok = (size_t)s->batch * s->seqlen, qk4 = tok * s->ngroups * s->d_state * 4;
+    DeltaNames in;
+    in.add(fwd, z, false);
+    in.add(bwd, z, true);
+    Array read[13];
+    for (int i = 0; i < in.n; ++i) read[i] = in.in[i];
+    read[in.n] = {"dy", dy, z.y};
+    read[in.n + 1] = {"init_state", init_state, z.state};
+    read[in.n + 2] = {"dfinal", dfinal, z.state};
+    Array out[12];
+    int n = 0;
+    for (int i = 0; i < (bwd ? 2 : 1); ++i) {
+        const bimamba_delta_grad *g = grads[i];
+        const Array five[5] = {{i ? "the reverse dq" : "the forward dq", g->dq, qk4},
+                               {i ? "the reverse dk" : "the forward dk", g->dk, qk4},
+                               {i ? "the reverse dv" : "the forward dv", g->dv, z.y},
+                               {i ? "the reverse dg" : "the forward dg", g->dg, z.gates},
+                               {i ? "the reverse dbeta" : "the forward dbeta", g->dbeta, z.gates}};
+        for (const Array &a : five) out[n++] = a;
+    }
+    out[n++] = {"dinit", dinit, z.state};
+    out[n++] = {"the workspace", workspace, need};
+    if ((rc = check_delta_apart(out, n, read, in.n + 3))) return rc;
+    hipStream_t st = (hipStream_t)stream;
+    const bool bf16 = s->dtype == BIMAMBA_BF16;
+    hipError_t e;
+    char *ws = (char *)workspace;
+    const int32_t *cu = nullptr;
+    if (cu_seqlens) {
+        if ((e = launch_store_offsets(cu_seqlens, nseq, (int32_t *)ws, st)) != hipSuccess)
+            return hip_fail(e, "storing the offsets");
+        cu = (const int32_t *)ws;
+    }
+    ws += delta_table(packed);
+    float *errors = (float *)ws, *zs = (float *)(ws + align256(z.y));
+    ws += 2 * align256(z.y);
+    const size_t kept = align256((size_t)delta_slots(packed ? nseq : s->batch, s->seqlen, packed > 0) * s->nheads *
+                                 s->headdim * s->d_state * 4);
+    float *enter = (float *)ws, *leave = (float *)(ws + kept);
+    for (int i = 0; i < (bwd ? 2 : 1); ++i) {
+        DeltaArgs a = delta_args(s, dirs[i], scale, cu, nseq, i == 1);
+        a.init = i ? nullptr : init_state;
+        a.y = errors;
+        a.states = enter;
+        if (!empty && (e = launch_delta_keep(a, bf16, st)) != hipSuccess) return hip_fail(e, "launching the delta rule");
+        a.v = dy;
+        a.init = i ? nullptr : dfinal;
+        a.last = i ? nullptr : dinit;
+        a.y = zs;
+        a.states = leave;
+        if ((!empty || a.last) && (e = launch_delta_back(a, bf16, st)) != hipSuccess)
+            return hip_fail(e, "launching the delta rule's walk back");
+        if (empty) continue;
+        const bimamba_delta_grad *g = grads[i];
+        const DeltaGradArgs o = {dy, errors, zs, enter, leave, g->dq, g->dk, g->dv, g->dg, g->dbeta};
+        if ((e = launch_delta_grad(a, o, bf16, st)) != hipSuccess)
+            return hip_fail(e, "launching the delta rule's gradient");
+    }
+    return BIMAMBA_OK;
 }
 
 }  // extern "C"

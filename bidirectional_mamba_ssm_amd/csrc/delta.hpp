@@ -1,0 +1,91 @@
+// The gated delta rule, as its kernels see it. Per head (query and key group
+// g = h / (H / G)), with the state S [N][P]:
+//   a_t = e^{g_t},  e_t = v_t - a_t S_{t-1}^T k_t,
+//   S_t = a_t S_{t-1} + beta_t k_t e_t^T,  y_t = scale S_t^T q_t
+// States are kept [P][N] in memory, as the scan's are.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "common.hpp"
+
+namespace bm {
+
+constexpr int kDeltaChunk = 64;   // tokens between kept states
+
+// One direction of a problem (validated). Units are rows of the batch or
+// packed sequences; a reversed direction takes a unit's tokens from its end.
+struct DeltaArgs {
+    const void *q, *k;         // [tok][G][N]
+    const void *v;             // [tok][H][P]; the gradient's walk back: float, the gradient of y
+    const float *g, *beta;     // [tok][H]
+    float scale;
+    int units, L, H, P, N, G;  // L: tokens of a row (packed: of all)
+    bool reverse, add;         // add: y += instead of y =
+    const int32_t *cu;         // device offsets [units + 1] of packed sequences, or nullptr
+    const float *init;         // [units][H][P][N] or nullptr (zeros); walk back: of the last state's gradient
+    float *last;               // the same, written at the end, or nullptr
+    float *y;                  // [tok][H][P]: y; for the gradient e, walk back z = d loss / d (beta e)
+    float *states;             // [slot][H][P][N]: chunks' incoming states; walk back: gradients of what they leave
+};
+
+// What the gradient reads beside a direction's inputs, and writes.
+struct DeltaGradArgs {
+    const float *dy, *e, *z;         // [tok][H][P]
+    const float *enter, *leave;      // [slot][H][P][N]: incoming states, gradients of the outgoing
+    float *dq, *dk, *dv, *dg, *dbeta;
+};
+
+// A unit's chunk c is kept in slot first_slot + c. Packed units' slots are
+// given out without a table: floor(x) + ceil(y) <= floor(x + y) + 1.
+__host__ __device__ inline long long delta_slots(int units, int L, bool packed) {
+    return packed ? (long long)L / kDeltaChunk + units
+                  : (long long)units * ((L + kDeltaChunk - 1) / kDeltaChunk);
+}
+struct DeltaUnit {
+    long long start, slot;
+    int len;
+};
+__device__ __forceinline__ DeltaUnit delta_unit(const DeltaArgs &a, int u) {
+    DeltaUnit d;
+    if (a.cu) {
+        d.start = a.cu[u];
+        d.len = a.cu[u + 1] - a.cu[u];
+        d.slot = d.start / kDeltaChunk + u;
+    } else {
+        d.start = (long long)u * a.L;
+        d.len = a.L;
+        d.slot = (long long)u * ((a.L + kDeltaChunk - 1) / kDeltaChunk);
+    }
+    return d;
+}
+// the unit whose chunk a slot keeps, and the chunk (past its end if the slot is
+// not used)
+__device__ __forceinline__ DeltaUnit delta_slot(const DeltaArgs &a, long long slot, int &chunk) {
+    int u;
+    if (a.cu) {
+        int lo = 0, hi = a.units;   // slot of unit lo <= slot < slot of unit hi
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if ((long long)a.cu[mid] / kDeltaChunk + mid <= slot) lo = mid;
+            else hi = mid;
+        }
+        u = lo;
+    } else {
+        u = (int)(slot / ((a.L + kDeltaChunk - 1) / kDeltaChunk));
+    }
+    const DeltaUnit d = delta_unit(a, u);
+    chunk = (int)(slot - d.slot);
+    return d;
+}
+__device__ __forceinline__ long long delta_token(const DeltaUnit &d, bool reverse, int i) {
+    return d.start + (reverse ? d.len - 1 - i : i);
+}
+
+// delta_seq.hip: y and the last state; e and the chunks' states; z and their gradients
+hipError_t launch_delta_seq(const DeltaArgs &a, bool bf16, hipStream_t s);
+hipError_t launch_delta_keep(const DeltaArgs &a, bool bf16, hipStream_t s);
+hipError_t launch_delta_back(const DeltaArgs &a, bool bf16, hipStream_t s);
+// delta_grad.hip
+hipError_t launch_delta_grad(const DeltaArgs &a, const DeltaGradArgs &o, bool bf16, hipStream_t s);
+
+}  // namespace bm

@@ -572,6 +572,71 @@ int bimamba_rms_norm_bwd(long long rows, int channels, int dtype, const void *x,
 int bimamba_linear8(long long rows, int cin, int cout, int dtype, const bimamba_rows8 *x,
                     const bimamba_rows8 *weight, const float *bias, void *out, bimamba_stream stream);
 
+/* ---- The gated delta rule ----------------------------------------------------
+ *
+ * A mixer's recurrence whose writes correct what the state already answers.
+ * Per head h (query and key group h / (nheads / ngroups)), with the state
+ * S [d_state][headdim]:
+ *
+ *   S' = e^{g_t} S,  e_t = v_t - S'^T k_t,  S = S' + beta_t k_t e_t^T,
+ *   y_t = scale S^T q_t
+ *
+ * q and k are used as given (a model normalizes them to length one; beta |k|^2
+ * in [0, 2] keeps the state bounded). g is the decay's logarithm, <= 0 as a rule
+ * (-INFINITY resets the state); a token with g = beta = 0 leaves it as it is.
+ * The shape is the scan's (bimamba_shape: x is v, B is k, C is q; headdim up
+ * to 128, d_state 16, 32, 64 or 128) with chunk 64 and flags 0. States are
+ * float [sequences][nheads][headdim][d_state], a bimamba_state's data among
+ * them. As in the scan, both directions' outputs are summed, the reverse
+ * direction is given in forward time order, and init_state and final_state
+ * are the forward direction's.
+ *
+ * Accuracy: fp32 inputs are computed in fp32 throughout; with bf16 inputs the
+ * operands that the kernels compute enter the matrix cores as two bf16 each (16
+ * significant bits, of fp32's range), sums and states are fp32. */
+typedef struct {
+    const void *q, *k;         /* dtype [batch][seqlen][ngroups][d_state]      */
+    const void *v;             /* dtype [batch][seqlen][nheads][headdim]       */
+    const float *g, *beta;     /* [batch][seqlen][nheads]                      */
+} bimamba_delta_dir;
+int bimamba_delta_workspace_size(const bimamba_shape *s, int nseq, size_t *bytes);
+/* fwd, bwd (or NULL), cu_seqlens, nseq, init_state and final_state as in
+ * bimamba_ssd_fwd; y float [batch][seqlen][nheads][headdim]. final_state may be
+ * init_state; calls whose outputs or workspace overlap each other or an input
+ * in any other way are refused. q, k, v, y and states 16-byte aligned, g and
+ * beta 4-byte, the workspace 256-byte. */
+int bimamba_delta_fwd(const bimamba_shape *s, const bimamba_delta_dir *fwd, const bimamba_delta_dir *bwd,
+                      float scale, const int32_t *cu_seqlens, int nseq, const float *init_state,
+                      float *final_state, float *y, void *workspace, size_t workspace_bytes,
+                      bimamba_stream stream);
+/* The cached step: a block of 1..256 tokens for each of s->batch states (row i
+ * continues state i; a token a call for decoding). The forward direction
+ * starts from the state and, with commit != 0, leaves its last state there;
+ * the reverse direction (or NULL) sees the block alone. The workspace is
+ * bimamba_delta_workspace_size(s, 0). */
+int bimamba_delta_step(const bimamba_shape *s, float *state, const bimamba_delta_dir *fwd,
+                       const bimamba_delta_dir *bwd, float scale, int commit, float *y, void *workspace,
+                       size_t workspace_bytes, bimamba_stream stream);
+/* Gradients of bimamba_delta_fwd's y and final_state, as floats. dk and dq are
+ * summed over the heads of each group, in their order; the same inputs give
+ * the same bits.
+ *  init_state  as in the forward pass, or NULL (zeros)
+ *  dy          float [batch][seqlen][nheads][headdim]
+ *  dfinal      float, the gradient that reaches final_state, or NULL (zeros)
+ *  dinit       out float, init_state's gradient, or NULL if not wanted
+ * Calls whose outputs or workspace overlap each other or an input are refused. */
+typedef struct {
+    float *dq, *dk;            /* [batch][seqlen][ngroups][d_state]            */
+    float *dv;                 /* [batch][seqlen][nheads][headdim]             */
+    float *dg, *dbeta;         /* [batch][seqlen][nheads]                      */
+} bimamba_delta_grad;
+int bimamba_delta_bwd_workspace_size(const bimamba_shape *s, int nseq, size_t *bytes);
+int bimamba_delta_bwd(const bimamba_shape *s, const bimamba_delta_dir *fwd, const bimamba_delta_dir *bwd,
+                      float scale, const int32_t *cu_seqlens, int nseq, const float *init_state,
+                      const float *dfinal, const float *dy, const bimamba_delta_grad *gfwd,
+                      const bimamba_delta_grad *gbwd, float *dinit, void *workspace, size_t workspace_bytes,
+                      bimamba_stream stream);
+
 /* Per-kernel timing for benchmarks and profilers, per calling thread.
  * Between bimamba_profile_begin() and bimamba_profile_end(), every kernel the
  * library launches from this thread is bracketed by two hipEvents recorded on
