@@ -1275,12 +1275,12 @@ def _delta_dir(d, dims, dtype, dev, name):
 
 
 @functools.lru_cache(maxsize=4096)
-def _delta_size(query, dims, dtype, nseq):
+def _delta_size(query, dims, dtype, *rest):
     """(the workspace, the bimamba_shape to pass, which the library only reads)."""
     batch, L, H, P, G, N = dims
     n = ctypes.c_size_t(0)
     shape = ctypes.byref(_sizes(_abi.Shape, "the problem's shape", batch, L, H, P, N, G, 64, _dtype_code(dtype), 0))
-    _abi.check(getattr(lib(), query)(shape, nseq, ctypes.byref(n)))
+    _abi.check(getattr(lib(), query)(shape, *rest, ctypes.byref(n)))
     return n.value, shape
 
 
@@ -1296,9 +1296,10 @@ def _delta_workspace(workspace, nbytes, dev):
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def delta_workspace_size(fwd, nseq=0):
-    """Bytes of workspace of delta_fwd and delta_step for such a direction."""
-    return _delta_size("bimamba_delta_workspace_size", _delta_dims(fwd), fwd["v"].dtype, nseq)[0]
+def delta_workspace_size(fwd, has_bwd=True, nseq=0):
+    """Bytes of workspace of delta_fwd and delta_step for such a direction, or
+    for two."""
+    return _delta_size("bimamba_delta_workspace_size", _delta_dims(fwd), fwd["v"].dtype, int(bool(has_bwd)), nseq)[0]
 
 
 def delta_bwd_workspace_size(fwd, nseq=0):
@@ -1323,7 +1324,7 @@ def delta_fwd(fwd, bwd=None, scale=None, cu_seqlens=None, init_state=None, final
     dims, dtype = _delta_dims(fwd), fwd["v"].dtype
     batch, L, H, P, G, N = dims
     cu_arr, nseq = _offsets(cu_seqlens)
-    nbytes, shape = _delta_size("bimamba_delta_workspace_size", dims, dtype, max(nseq, 0))
+    nbytes, shape = _delta_size("bimamba_delta_workspace_size", dims, dtype, int(bwd is not None), max(nseq, 0))
     fd = _delta_dir(fwd, dims, dtype, dev, "fwd")
     bd = _delta_dir(bwd, dims, dtype, dev, "bwd") if bwd is not None else None
     units = nseq if cu_seqlens is not None else batch
@@ -1350,7 +1351,7 @@ def delta_step(state, fwd, bwd=None, commit=True, scale=None, y=None, workspace=
         return _run_on(dev, stream, delta_step, state, fwd, bwd, commit, scale, y, workspace)
     dims, dtype = _delta_dims(fwd), fwd["v"].dtype
     batch, L, H, P, G, N = dims
-    nbytes, shape = _delta_size("bimamba_delta_workspace_size", dims, dtype, 0)
+    nbytes, shape = _delta_size("bimamba_delta_workspace_size", dims, dtype, int(bwd is not None), 0)
     fd = _delta_dir(fwd, dims, dtype, dev, "fwd")
     bd = _delta_dir(bwd, dims, dtype, dev, "bwd") if bwd is not None else None
     slots = state.shape[0]

@@ -174,7 +174,7 @@ def load():
     lib.bimamba_rms_norm_bwd_workspace_size.argtypes = [ll, ci, ci, np_]
     lib.bimamba_rms_norm_bwd.argtypes = [ll, ci, ci, vp, vp, vp, vp, vp, vp, vp, vp, vp, size, vp]
     ddp, dgp = ctypes.POINTER(DeltaDir), ctypes.POINTER(DeltaGrad)
-    lib.bimamba_delta_workspace_size.argtypes = [sp, ci, np_]
+    lib.bimamba_delta_workspace_size.argtypes = [sp, ci, ci, np_]
     lib.bimamba_delta_fwd.argtypes = [sp, ddp, ddp, cf, i32p, ci, vp, vp, vp, vp, size, vp]
     lib.bimamba_delta_step.argtypes = [sp, vp, ddp, ddp, cf, ci, vp, vp, size, vp]
     lib.bimamba_delta_bwd_workspace_size.argtypes = [sp, ci, np_]

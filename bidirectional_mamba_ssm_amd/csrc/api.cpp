@@ -1556,18 +1556,34 @@ int check_delta_apart(const Array *written, int nw, const Array *read, int nr) {
 
 }  // namespace
 
-int bimamba_delta_workspace_size(const bimamba_shape *s, int nseq, size_t *bytes) {
+namespace {
+
+// By chunks, or token by token: short sequences do not fill a chunk
+bool delta_chunked(const bimamba_shape *s, int nseq) {
+    return s->seqlen > 16LL * (nseq ? nseq : 1);
+}
+size_t delta_dir_workspace(const bimamba_shape *s, int nseq, bool grad) {
+    const bimamba_delta_dir none = {};
+    // only whether there are offsets counts
+    const DeltaArgs a = delta_args(s, &none, 1.f, nseq ? (const int32_t *)16 : nullptr, nseq, false);
+    return delta_chunk_workspace(a, s->dtype == BIMAMBA_BF16, grad);
+}
+
+}  // namespace
+
+int bimamba_delta_workspace_size(const bimamba_shape *s, int has_bwd, int nseq, size_t *bytes) {
     int rc = check_delta_shape(s, nseq, false);
     if (rc) return rc;
     if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
-    *bytes = delta_table(nseq);
+    *bytes = delta_table(nseq) + (delta_chunked(s, nseq) ? (has_bwd ? 2 : 1) * delta_dir_workspace(s, nseq, false) : 0);
     return BIMAMBA_OK;
 }
 
 int bimamba_delta_fwd(const bimamba_shape *s, const bimamba_delta_dir *fwd, const bimamba_delta_dir *bwd, float scale,
                       const int32_t *cu_seqlens, int nseq, const float *init_state, float *final_state, float *y,
                       void *workspace, size_t workspace_bytes, bimamba_stream stream) {
-    int rc = check_delta_shape(s, cu_seqlens ? nseq : 0, false);
+    const int packed = cu_seqlens ? nseq : 0;
+    int rc = check_delta_shape(s, packed, false);
     if (rc) return rc;
     const bool empty = s->seqlen == 0;
     if ((rc = check_delta_dir(fwd, "forward", empty))) return rc;
@@ -1578,9 +1594,9 @@ int bimamba_delta_fwd(const bimamba_shape *s, const bimamba_delta_dir *fwd, cons
     if (!aligned16(y) || !aligned16(init_state) || !aligned16(final_state))
         return fail(BIMAMBA_EINVAL, "y, init_state and final_state must be 16-byte aligned");
     size_t need = 0;
-    if ((rc = bimamba_delta_workspace_size(s, cu_seqlens ? nseq : 0, &need))) return rc;
+    if ((rc = bimamba_delta_workspace_size(s, bwd != nullptr, packed, &need))) return rc;
     if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
-    const DeltaSizes z = delta_sizes(s, cu_seqlens ? nseq : 0);
+    const DeltaSizes z = delta_sizes(s, packed);
     DeltaNames in;
     in.add(fwd, z, false);
     in.add(bwd, z, true);
@@ -1590,28 +1606,37 @@ int bimamba_delta_fwd(const bimamba_shape *s, const bimamba_delta_dir *fwd, cons
     for (const Array &o : out)
         if (overlap(o, init) && !(o.p == init.p && o.p == final_state))
             return fail(BIMAMBA_EINVAL, "%s overlaps init_state", o.name);
+    if (empty && !final_state) return BIMAMBA_OK;
     hipStream_t st = (hipStream_t)stream;
     const bool bf16 = s->dtype == BIMAMBA_BF16;
     hipError_t e;
+    char *ws = (char *)workspace;
     const int32_t *cu = nullptr;
     if (cu_seqlens) {
-        if ((e = launch_store_offsets(cu_seqlens, nseq, (int32_t *)workspace, st)) != hipSuccess)
+        if ((e = launch_store_offsets(cu_seqlens, nseq, (int32_t *)ws, st)) != hipSuccess)
             return hip_fail(e, "storing the offsets");
-        cu = (const int32_t *)workspace;
+        cu = (const int32_t *)ws;
+        ws += delta_table(nseq);
     }
-    if (bwd && !empty) {
-        DeltaArgs a = delta_args(s, bwd, scale, cu, nseq, true);
-        a.y = y;
-        if ((e = launch_delta_seq(a, bf16, st)) != hipSuccess) return hip_fail(e, "launching the delta rule");
+    const int ndir = bwd && !empty ? 2 : 1;
+    DeltaArgs a[2];
+    void *parts[2];
+    const size_t part = delta_chunked(s, packed) ? delta_dir_workspace(s, packed, false) : 0;
+    for (int i = 0; i < ndir; ++i) {
+        a[i] = delta_args(s, i ? bwd : fwd, scale, cu, nseq, i == 1);
+        a[i].add = i == 0 && ndir == 2;
+        a[i].init = i ? nullptr : init_state;
+        a[i].last = i ? nullptr : final_state;
+        a[i].y = y;
+        parts[i] = ws + i * part;
     }
-    if (empty && !final_state) return BIMAMBA_OK;
-    DeltaArgs a = delta_args(s, fwd, scale, cu, nseq, false);
-    a.add = bwd != nullptr;
-    a.init = init_state;
-    a.last = final_state;
-    a.y = y;
-    if ((e = launch_delta_seq(a, bf16, st)) != hipSuccess) return hip_fail(e, "launching the delta rule");
-    return BIMAMBA_OK;
+    if (delta_chunked(s, packed)) {
+        e = launch_delta_chunked(a, ndir, bf16, parts, st);
+    } else {
+        e = ndir == 2 ? launch_delta_seq(a[1], bf16, st) : hipSuccess;
+        if (e == hipSuccess) e = launch_delta_seq(a[0], bf16, st);
+    }
+    return e == hipSuccess ? BIMAMBA_OK : hip_fail(e, "launching the delta rule");
 }
 
 int bimamba_delta_step(const bimamba_shape *s, float *state, const bimamba_delta_dir *fwd,
@@ -1624,14 +1649,28 @@ int bimamba_delta_step(const bimamba_shape *s, float *state, const bimamba_delta
                              workspace_bytes, stream);
 }
 
+namespace {
+
+// The gradient's workspace, one direction at a time: offsets, images and gates,
+// e and z, the chunks' states and their gradients.
+struct DeltaBwdLayout {
+    size_t chunked, row, states;
+    explicit DeltaBwdLayout(const bimamba_shape *s, int nseq) {
+        chunked = delta_dir_workspace(s, nseq, true);
+        row = align256(delta_sizes(s, nseq).y);
+        states = align256((size_t)delta_slots(nseq ? nseq : s->batch, s->seqlen, nseq > 0) * s->nheads * s->headdim *
+                          s->d_state * 4);
+    }
+    size_t total(int nseq) const { return delta_table(nseq) + chunked + 2 * row + 2 * states; }
+};
+
+}  // namespace
+
 int bimamba_delta_bwd_workspace_size(const bimamba_shape *s, int nseq, size_t *bytes) {
     int rc = check_delta_shape(s, nseq, false);
     if (rc) return rc;
     if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
-    const DeltaSizes z = delta_sizes(s, 0);
-    const size_t slots = (size_t)delta_slots(nseq ? nseq : s->batch, s->seqlen, nseq > 0);
-    *bytes = delta_table(nseq) + 2 * align256(z.y) +
-             2 * align256(slots * s->nheads * s->headdim * s->d_state * 4);
+    *bytes = DeltaBwdLayout(s, nseq).total(nseq);
     return BIMAMBA_OK;
 }
 
@@ -1700,23 +1739,23 @@ int bimamba_delta_bwd(const bimamba_shape *s, const bimamba_delta_dir *fwd, cons
         cu = (const int32_t *)ws;
     }
     ws += delta_table(packed);
-    float *errors = (float *)ws, *zs = (float *)(ws + align256(z.y));
-    ws += 2 * align256(z.y);
-    const size_t kept = align256((size_t)delta_slots(packed ? nseq : s->batch, s->seqlen, packed > 0) * s->nheads *
-                                 s->headdim * s->d_state * 4);
-    float *enter = (float *)ws, *leave = (float *)(ws + kept);
+    const DeltaBwdLayout lay(s, packed);
+    void *chunked = ws;
+    float *errors = (float *)(ws + lay.chunked), *zs = (float *)((char *)errors + lay.row);
+    float *enter = (float *)((char *)zs + lay.row), *leave = (float *)((char *)enter + lay.states);
     for (int i = 0; i < (bwd ? 2 : 1); ++i) {
         DeltaArgs a = delta_args(s, dirs[i], scale, cu, nseq, i == 1);
         a.init = i ? nullptr : init_state;
         a.y = errors;
         a.states = enter;
-        if (!empty && (e = launch_delta_keep(a, bf16, st)) != hipSuccess) return hip_fail(e, "launching the delta rule");
+        if (!empty && (e = launch_delta_keep(a, bf16, chunked, st)) != hipSuccess)
+            return hip_fail(e, "launching the delta rule");
         a.v = dy;
         a.init = i ? nullptr : dfinal;
         a.last = i ? nullptr : dinit;
         a.y = zs;
         a.states = leave;
-        if ((!empty || a.last) && (e = launch_delta_back(a, bf16, st)) != hipSuccess)
+        if ((!empty || a.last) && (e = launch_delta_back(a, bf16, chunked, st)) != hipSuccess)
             return hip_fail(e, "launching the delta rule's walk back");
         if (empty) continue;
         const bimamba_delta_grad *g = grads[i];

@@ -16,16 +16,16 @@ constexpr int kDeltaChunk = 64;   // tokens between kept states
 // packed sequences; a reversed direction takes a unit's tokens from its end.
 struct DeltaArgs {
     const void *q, *k;         // [tok][G][N]
-    const void *v;             // [tok][H][P]; the gradient's walk back: float, the gradient of y
+    const void *v;             // [tok][H][P]; walking back: float, the gradient of y
     const float *g, *beta;     // [tok][H]
     float scale;
     int units, L, H, P, N, G;  // L: tokens of a row (packed: of all)
     bool reverse, add;         // add: y += instead of y =
     const int32_t *cu;         // device offsets [units + 1] of packed sequences, or nullptr
-    const float *init;         // [units][H][P][N] or nullptr (zeros); walk back: of the last state's gradient
+    const float *init;         // [units][H][P][N] or nullptr (zeros); walking back: its gradient
     float *last;               // the same, written at the end, or nullptr
-    float *y;                  // [tok][H][P]: y; for the gradient e, walk back z = d loss / d (beta e)
-    float *states;             // [slot][H][P][N]: chunks' incoming states; walk back: gradients of what they leave
+    float *y;                  // [tok][H][P]: y; for the gradient e, walking back z = d loss / d (beta e)
+    float *states;             // [slot][H][P][N]: chunks' incoming states; walking back: gradients of what they leave
 };
 
 // What the gradient reads beside a direction's inputs, and writes.
@@ -81,10 +81,15 @@ __device__ __forceinline__ long long delta_token(const DeltaUnit &d, bool revers
     return d.start + (reverse ? d.len - 1 - i : i);
 }
 
-// delta_seq.hip: y and the last state; e and the chunks' states; z and their gradients
+// delta_seq.hip: y and the last state, token by token
 hipError_t launch_delta_seq(const DeltaArgs &a, bool bf16, hipStream_t s);
-hipError_t launch_delta_keep(const DeltaArgs &a, bool bf16, hipStream_t s);
-hipError_t launch_delta_back(const DeltaArgs &a, bool bf16, hipStream_t s);
+// delta_chunk.hip: the same by chunks, of one or both directions (a[0] forward,
+// a[1] reverse, each with its workspace); e and the chunks' incoming states; z and
+// the gradients of the outgoing (with the workspace that the call before filled)
+size_t delta_chunk_workspace(const DeltaArgs &a, bool bf16, bool grad);
+hipError_t launch_delta_chunked(const DeltaArgs *a, int ndir, bool bf16, void *const *ws, hipStream_t s);
+hipError_t launch_delta_keep(const DeltaArgs &a, bool bf16, void *ws, hipStream_t s);
+hipError_t launch_delta_back(const DeltaArgs &a, bool bf16, void *ws, hipStream_t s);
 // delta_grad.hip
 hipError_t launch_delta_grad(const DeltaArgs &a, const DeltaGradArgs &o, bool bf16, hipStream_t s);
 

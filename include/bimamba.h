@@ -599,7 +599,8 @@ typedef struct {
     const void *v;             /* dtype [batch][seqlen][nheads][headdim]       */
     const float *g, *beta;     /* [batch][seqlen][nheads]                      */
 } bimamba_delta_dir;
-int bimamba_delta_workspace_size(const bimamba_shape *s, int nseq, size_t *bytes);
+/* Bytes of device workspace bimamba_delta_fwd needs (has_bwd: both directions). */
+int bimamba_delta_workspace_size(const bimamba_shape *s, int has_bwd, int nseq, size_t *bytes);
 /* fwd, bwd (or NULL), cu_seqlens, nseq, init_state and final_state as in
  * bimamba_ssd_fwd; y float [batch][seqlen][nheads][headdim]. final_state may be
  * init_state; calls whose outputs or workspace overlap each other or an input
@@ -613,7 +614,7 @@ int bimamba_delta_fwd(const bimamba_shape *s, const bimamba_delta_dir *fwd, cons
  * continues state i; a token a call for decoding). The forward direction
  * starts from the state and, with commit != 0, leaves its last state there;
  * the reverse direction (or NULL) sees the block alone. The workspace is
- * bimamba_delta_workspace_size(s, 0). */
+ * bimamba_delta_workspace_size(s, bwd != NULL, 0). */
 int bimamba_delta_step(const bimamba_shape *s, float *state, const bimamba_delta_dir *fwd,
                        const bimamba_delta_dir *bwd, float scale, int commit, float *y, void *workspace,
                        size_t workspace_bytes, bimamba_stream stream);

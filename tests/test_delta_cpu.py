@@ -160,18 +160,19 @@ def test_shapes(lib, kw, code):
     _code(lib, _fwd(lib, at, _shape(**kw)), code)
     _code(lib, _bwd(lib, at, _shape(**kw)), code)
     n = ctypes.c_size_t(0)
-    for query in (lib.bimamba_delta_workspace_size, lib.bimamba_delta_bwd_workspace_size):
-        _code(lib, query(_shape(**kw), 0, ctypes.byref(n)), code)
+    for query, both in ((lib.bimamba_delta_workspace_size, (1,)), (lib.bimamba_delta_bwd_workspace_size, ())):
+        _code(lib, query(_shape(**kw), *both, 0, ctypes.byref(n)), code)
     rc = lib.bimamba_delta_step(_shape(**kw), STEP * 40, _dir(at, "f"), None, 1.0, 1, at["y"], None, 0, None)
     _code(lib, rc, code if kw.get("seqlen", 0) <= 256 else _abi.EINVAL)
 
 
 def test_queries(lib):
     n = ctypes.c_size_t(0)
-    for query in (lib.bimamba_delta_workspace_size, lib.bimamba_delta_bwd_workspace_size):
-        assert query(_shape(), 0, ctypes.byref(n)) == 0
-        assert query(_shape(), 0, None) == _abi.EINVAL and query(_shape(), -1, ctypes.byref(n)) == _abi.EINVAL
-        assert query(None, 0, ctypes.byref(n)) == _abi.EINVAL
+    for query, both in ((lib.bimamba_delta_workspace_size, (1,)), (lib.bimamba_delta_bwd_workspace_size, ())):
+        assert query(_shape(), *both, 0, ctypes.byref(n)) == 0
+        assert query(_shape(), *both, 0, None) == _abi.EINVAL
+        assert query(_shape(), *both, -1, ctypes.byref(n)) == _abi.EINVAL
+        assert query(None, *both, 0, ctypes.byref(n)) == _abi.EINVAL
 
 
 @pytest.mark.parametrize("name", ["fq", "fk", "fv", "fg", "fb", "rq", "rv", "rb", "y"])
