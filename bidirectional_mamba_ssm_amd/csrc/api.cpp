@@ -1464,12 +1464,15 @@ int check_delta_shape(const bimamba_shape *s, int nseq, bool step) {
     if (s->flags) return fail(BIMAMBA_EINVAL, "flags 0x%x: none is defined for the delta rule", s->flags);
     if (s->chunk != kDeltaChunk) return fail(BIMAMBA_EUNSUPPORTED, "chunk %d is not %d", s->chunk, kDeltaChunk);
     if (nseq < 0) return fail(BIMAMBA_EINVAL, "nseq %d < 0", nseq);
-    // a launch has fewer than 2^32 threads: 64 for 16 columns of a head of a
-    // unit, 512 for a chunk and group
-    const long long units = nseq ? nseq : s->batch, cols = (s->headdim + 15) / 16;
-    if (units * s->nheads > (1LL << 25) / cols)
+    // the rows of a chunk of 64 tokens are reached by offsets under 2^30 bytes
+    if (s->nheads > 32768) return fail(BIMAMBA_EUNSUPPORTED, "nheads %d exceeds 32768", s->nheads);
+    // a launch has fewer than 2^32 threads: 256 for 64 columns of a head of a
+    // unit (64 for 16), and for a chunk and head; 512 for a chunk and group
+    const long long units = nseq ? nseq : s->batch, most = (1LL << 24) - 8;
+    if (units * s->nheads * ((s->headdim + 63) / 64) > most)
         return fail(BIMAMBA_EUNSUPPORTED, "%lld sequences of %d heads are too many for one launch", units, s->nheads);
-    if (delta_slots((int)units, s->seqlen, nseq > 0) * s->ngroups > (1LL << 23) - 8)
+    const long long slots = delta_slots((int)units, s->seqlen, nseq > 0);
+    if (slots * s->nheads > most || slots * s->ngroups > most / 2)
         return fail(BIMAMBA_EUNSUPPORTED, "%lld x %d tokens are too many for one launch", units, s->seqlen);
     return BIMAMBA_OK;
 }
@@ -1562,11 +1565,13 @@ namespace {
 bool delta_chunked(const bimamba_shape *s, int nseq) {
     return s->seqlen > 16LL * (nseq ? nseq : 1);
 }
-size_t delta_dir_workspace(const bimamba_shape *s, int nseq, bool grad) {
+// for the sizes of workspaces: only whether there are offsets counts
+DeltaArgs delta_sized(const bimamba_shape *s, int nseq) {
     const bimamba_delta_dir none = {};
-    // only whether there are offsets counts
-    const DeltaArgs a = delta_args(s, &none, 1.f, nseq ? (const int32_t *)16 : nullptr, nseq, false);
-    return delta_chunk_workspace(a, s->dtype == BIMAMBA_BF16, grad);
+    return delta_args(s, &none, 1.f, nseq ? (const int32_t *)256 : nullptr, nseq, false);
+}
+size_t delta_dir_workspace(const bimamba_shape *s, int nseq, bool grad) {
+    return delta_chunk_workspace(delta_sized(s, nseq), grad);
 }
 
 }  // namespace
@@ -1657,9 +1662,8 @@ struct DeltaBwdLayout {
     size_t chunked, row, states;
     explicit DeltaBwdLayout(const bimamba_shape *s, int nseq) {
         chunked = delta_dir_workspace(s, nseq, true);
-        row = align256(delta_sizes(s, nseq).y);
-        states = align256((size_t)delta_slots(nseq ? nseq : s->batch, s->seqlen, nseq > 0) * s->nheads * s->headdim *
-                          s->d_state * 4);
+        row = align256(delta_rows_bytes(delta_sized(s, nseq)));
+        states = align256(delta_states_bytes(delta_sized(s, nseq)));
     }
     size_t total(int nseq) const { return delta_table(nseq) + chunked + 2 * row + 2 * states; }
 };

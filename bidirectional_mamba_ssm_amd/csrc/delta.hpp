@@ -24,14 +24,17 @@ struct DeltaArgs {
     const int32_t *cu;         // device offsets [units + 1] of packed sequences, or nullptr
     const float *init;         // [units][H][P][N] or nullptr (zeros); walking back: its gradient
     float *last;               // the same, written at the end, or nullptr
-    float *y;                  // [tok][H][P]: y; for the gradient e, walking back z = d loss / d (beta e)
-    float *states;             // [slot][H][P][N]: chunks' incoming states; walking back: gradients of what they leave
+    float *y;                  // [tok][H][P]: y; for the gradient [tok][H][P rounded up]: e, walking back
+                               // z = d loss / d (beta e)
+    float *states;             // [slot][H][N][P rounded up]: chunks' incoming states; walking back: gradients
+                               // of what they leave
 };
 
 // What the gradient reads beside a direction's inputs, and writes.
 struct DeltaGradArgs {
-    const float *dy, *e, *z;         // [tok][H][P]
-    const float *enter, *leave;      // [slot][H][P][N]: incoming states, gradients of the outgoing
+    const float *dy;                 // [tok][H][P]
+    const float *e, *z;              // [tok][H][P rounded up]
+    const float *enter, *leave;      // [slot][H][N][P rounded up]: incoming states, gradients of the outgoing
     float *dq, *dk, *dv, *dg, *dbeta;
 };
 
@@ -86,11 +89,13 @@ hipError_t launch_delta_seq(const DeltaArgs &a, bool bf16, hipStream_t s);
 // delta_chunk.hip: the same by chunks, of one or both directions (a[0] forward,
 // a[1] reverse, each with its workspace); e and the chunks' incoming states; z and
 // the gradients of the outgoing (with the workspace that the call before filled)
-size_t delta_chunk_workspace(const DeltaArgs &a, bool bf16, bool grad);
+size_t delta_chunk_workspace(const DeltaArgs &a, bool grad);
 hipError_t launch_delta_chunked(const DeltaArgs *a, int ndir, bool bf16, void *const *ws, hipStream_t s);
 hipError_t launch_delta_keep(const DeltaArgs &a, bool bf16, void *ws, hipStream_t s);
 hipError_t launch_delta_back(const DeltaArgs &a, bool bf16, void *ws, hipStream_t s);
-// delta_grad.hip
+// delta_grad.hip, and the bytes of e or z, and of the kept states or their gradients
+size_t delta_rows_bytes(const DeltaArgs &a);
+size_t delta_states_bytes(const DeltaArgs &a);
 hipError_t launch_delta_grad(const DeltaArgs &a, const DeltaGradArgs &o, bool bf16, hipStream_t s);
 
 }  // namespace bm

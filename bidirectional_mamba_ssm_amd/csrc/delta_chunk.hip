@@ -13,8 +13,7 @@
 // k_delta_prep, a chunk and head to a workgroup, makes what does not wait for
 // the state: the triangles, inverted in fp32 (16 x 16 blocks by substitution, a
 // column a lane; the blocks below by products on v_mfma_f32_16x16x4_f32), as
-// operand images. G is summed in 64 bits, so that a reset in the middle of a
-// chunk takes nothing from the decays behind it.
+// operand images.
 //
 // k_delta_walk takes a head's chunks in order. A wave owns 16 NC columns of the
 // state for all N rows; columns never meet. The matrix cores' result order (rows
@@ -41,10 +40,6 @@ __device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-// eight consecutive elements of a row
-__device__ __forceinline__ Operand<1> row8(const uint16_t *p) { return {*(const u32x4 *)p}; }
-__device__ __forceinline__ Operand<3> row8(const float *p) { return split8<3>(*(const f32x4 *)p, *(const f32x4 *)(p + 4)); }
-
 struct PrepDir {
     DeltaArgs a;
     uint8_t *images;   // [slot][H]
@@ -57,7 +52,7 @@ struct PrepArgs {
 template <typename T, int N, bool GRAD>
 __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs args) {
     constexpr int IN = Terms<T>::IN, OWN = Terms<T>::OWN, KS = (N + 31) / 32, NM = GRAD ? 2 : 1;
-    __shared__ __attribute__((aligned(16))) float ms[NM][C * kLd], xs[NM][C * kLd], ps[C * kLd];
+    __shared__ __attribute__((aligned(16))) float ms[NM][C * kLd], xs[NM][C * kLd];
     __shared__ double sums[C];
     __shared__ float beta[C];
     const PrepDir &pd = args.dir[blockIdx.y];
@@ -70,82 +65,119 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs args) {
     const DeltaUnit at = delta_slot(a, slot, chunk);
     const int first = chunk * C, live = min(C, at.len - first);
     if (live <= 0) return;
-    auto token = [&](int i) { return (size_t)delta_token(at, a.reverse, first + min(i, live - 1)); };
-    if (tid < C) {
-        const size_t i = token(tid) * a.H + h;
-        // nothing is told from a reset below e^-1000, and infinities would cancel
-        const float gl = tid < live ? a.g[i] : 0.f;
-        sums[tid] = gl < -1000.f ? -1000.0 : (double)gl;
-        beta[tid] = tid < live ? a.beta[i] : 0.f;
+    const uint32_t row = (uint32_t)(a.G * N * sizeof(T)), off = (uint32_t)(grp * N * sizeof(T));
+    const ChunkRows kr(a.k, at, a.reverse, first, live, row, off, N * sizeof(T));
+    const ChunkRows qr(a.q, at, a.reverse, first, live, row, off, N * sizeof(T));
+    // all of K and this wave's 16 rows of Q, k in the rows' order
+    constexpr int V = 16 / sizeof(T), kRegs = 8 / V;
+    u32x4 kv[4][KS][kRegs], qv[KS][kRegs];
+#pragma unroll
+    for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int e = 0; e < kRegs; ++e) {
+            const int n = 32 * s + 8 * g + V * e;
+            const uint32_t col = n < N ? n * sizeof(T) : kFar;
+            qv[s][e] = buf16(qr.rsrc, qr.offset(16 * wave + l16) + col);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) kv[c][s][e] = buf16(kr.rsrc, kr.offset(16 * c + l16) + col);
+        }
+    if (wave == 0) {
+        const size_t i = (size_t)delta_token(at, a.reverse, first + min(lane, live - 1)) * a.H + h;
+        const double sum = decay_sums(lane < live ? a.g[i] : 0.f, lane);
+        const float b = lane < live ? a.beta[i] : 0.f;
+        sums[lane] = sum;
+        beta[lane] = b;
+        float *to = pd.gates + ((size_t)slot * a.H + h) * kGates;
+        to[lane] = expf((float)sum);
+        to[C + lane] = expf((float)(__shfl(sum, 63) - sum));
+        to[2 * C + lane] = b;
     }
-    // this wave's 16 rows of K K^T and Q K^T, columns up to them
+    auto operand = [&](const u32x4 *r) {
+        if constexpr (IN == 1) return Operand<1>{r[0]};
+        else return split8<3>(__builtin_bit_cast(f32x4, r[0]), __builtin_bit_cast(f32x4, r[1]));
+    };
+    // column c of the wave's rows of K K^T; of the other triangle the tile that is
+    // an image's lane as it comes (rows j for q_i k_j, rows i for its transpose)
     f32x4 kk[4], qk[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) kk[c] = qk[c] = zero4();
-    const size_t mine = (token(16 * wave + l16) * a.G + grp) * N;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
-        const int n = 32 * s + 8 * g;
-        const bool in = n < N;
-        Operand<IN> zero;
+        const Operand<IN> q = operand(qv[s]);
+        Operand<IN> k[4];
 #pragma unroll
-        for (int i = 0; i < IN; ++i) zero.t[i] = u32x4{0u, 0u, 0u, 0u};
-        const Operand<IN> k = in ? row8((const T *)a.k + mine + n) : zero;
-        const Operand<IN> q = in ? row8((const T *)a.q + mine + n) : zero;
+        for (int c = 0; c < 4; ++c) k[c] = operand(kv[c][s]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            if (c > wave) break;
-            const size_t other = (token(16 * c + l16) * a.G + grp) * N;
-            const Operand<IN> o = in ? row8((const T *)a.k + other + n) : zero;
-            kk[c] = mm(k, o, kk[c]);
-            qk[c] = mm(q, o, qk[c]);
-        }
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+                if (c <= w && w == wave) {
+                    kk[c] = mm(k[w], k[c], kk[c]);
+                    qk[c] = GRAD ? mm(q, k[c], qk[c]) : mm(k[c], q, qk[c]);
+                }
     }
     __syncthreads();
-    double sum = 0.0;
-    if (tid < C)
-        for (int i = 0; i <= tid; ++i) sum += sums[i];
-    __syncthreads();
-    if (tid < C) sums[tid] = sum;
-    __syncthreads();
-    if (tid < C) {
-        float *to = pd.gates + ((size_t)slot * a.H + h) * kGates;
-        to[tid] = expf((float)sum);
-        to[C + tid] = expf((float)(sums[C - 1] - sum));
-        to[2 * C + tid] = beta[tid];
-    }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         if (c > wave) break;
-        const int j = 16 * c + l16;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int i = 16 * wave + 4 * g + r;
-            const float w = j <= i ? expf((float)(sums[i] - sums[j])) : 0.f;
-            // places past the last token hold its rows again, with beta 0
-            const float m = j < i ? w * kk[c][r] : 0.f;
-            ms[0][i * kLd + j] = m * beta[j];
-            if constexpr (GRAD) ms[1][i * kLd + j] = m * beta[i];
-            ps[i * kLd + j] = j <= i && i < live ? a.scale * w * qk[c][r] * (GRAD ? 1.f : beta[j]) : 0.f;
+            {
+                const int i = 16 * wave + 4 * g + r, j = 16 * c + l16;
+                const float w = j < i ? expf((float)(sums[i] - sums[j])) * kk[c][r] : 0.f;
+                ms[0][i * kLd + j] = w * beta[j];
+                if constexpr (GRAD) ms[1][i * kLd + j] = w * beta[i];
+            }
+            // FWD: lane's row i = l16, columns j; GRAD: rows i, lane's column j
+            const int i = 16 * wave + (GRAD ? 4 * g + r : l16), j = 16 * c + (GRAD ? l16 : 4 * g + r);
+            const float w = j <= i && i < live ? a.scale * expf((float)(sums[i] - sums[j])) : 0.f;
+            qk[c][r] *= GRAD ? w : w * beta[j];
+        }
+    }
+    uint8_t *img = pd.images + ((size_t)slot * a.H + h) * images(GRAD) * kImage<OWN>;
+    auto put = [&](uint8_t *image, int b, f32x4 lo, f32x4 hi) {
+        const Operand<OWN> o = split8<OWN>(lo, hi);
+#pragma unroll
+        for (int t = 0; t < OWN; ++t) *(u32x4 *)(image + (b * OWN + t) * 1024 + 16 * lane) = o.t[t];
+    };
+    if constexpr (!GRAD) {
+        // tiles above the diagonal are zeros as they were
+        put(img + kImage<OWN>, wave < 2 ? wave : 2 * wave - 2, qk[0], qk[1]);
+        if (wave >= 2) put(img + kImage<OWN>, 2 * wave - 1, qk[2], qk[3]);
+    } else {
+        // the transposed triangle's rows 16 c .. take k from 16 wave ..: half a
+        // block is one wave's, four slots of eight
+        uint8_t *to = img + 2 * kImage<OWN>;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint32_t lo[OWN], hi[OWN];
+            split2<OWN>(qk[c][0], qk[c][1], lo);
+            split2<OWN>(qk[c][2], qk[c][3], hi);
+            if (c < 2 || wave >= 2) {
+#pragma unroll
+                for (int t = 0; t < OWN; ++t)
+                    *(u32x2 *)(to + (upper_block(c, wave >> 1) * OWN + t) * 1024 + 16 * lane + 8 * (wave & 1)) =
+                        u32x2{lo[t], hi[t]};
+            }
         }
     }
     __syncthreads();
     {   // this wave's diagonal block: lane's column l16 of the inverse
         const int which = GRAD ? g >> 1 : 0, o = 16 * wave;
-        const float *m = ms[which];
+        const float *m = ms[which] + o * kLd + o;
+        f32x4 rows[16][4];
+#pragma unroll
+        for (int i = 1; i < 16; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (4 * k < i) rows[i][k] = *(const f32x4 *)(m + i * kLd + 4 * k);
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float v = i == l16 ? 1.f : 0.f;
+            float v[4] = {i == l16 ? 1.f : 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-                if (k >= i) break;
-                const f32x4 row = *(const f32x4 *)(m + (o + i) * kLd + o + k);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (k + e < i) v = fmaf(-row[e], x[k + e], v);
-            }
-            x[i] = v;
+            for (int k = 0; k < i; ++k) v[k & 3] = fmaf(-rows[i][k >> 2][k & 3], x[k], v[k & 3]);
+            x[i] = (v[0] + v[1]) + (v[2] + v[3]);
         }
         if (GRAD ? (g & 1) == 0 : g == 0) {
 #pragma unroll
@@ -160,41 +192,41 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs args) {
             const int which = job / (4 - d), j = job % (4 - d), i = j + d;
             const float *m = ms[which];
             float *x = xs[which];
-            f32x4 t = zero4();
-            for (int k = 16 * j; k < 16 * i; k += 4)
-                t = mfma4(m[(16 * i + l16) * kLd + k + g], x[(k + g) * kLd + 16 * j + l16], t);
             const f32x4 own = *(const f32x4 *)(x + (16 * i + l16) * kLd + 16 * i + 4 * g);
+            f32x4 t[2] = {zero4(), zero4()};
+#pragma unroll
+            for (int k = 0; k < 16 * d; k += 4) {
+                const int n = 16 * j + k + g;
+                t[(k >> 2) & 1] = mfma4(m[(16 * i + l16) * kLd + n], x[n * kLd + 16 * j + l16], t[(k >> 2) & 1]);
+            }
+            t[0] += t[1];
             f32x4 v = zero4();
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v = mfma4(own[r], t[r], v);
+            for (int r = 0; r < 4; ++r) v = mfma4(own[r], t[0][r], v);
 #pragma unroll
             for (int r = 0; r < 4; ++r) x[(16 * i + 4 * g + r) * kLd + 16 * j + l16] = -v[r];
         }
         __syncthreads();
     }
-    uint8_t *img = pd.images + ((size_t)slot * a.H + h) * images(GRAD) * kImage<OWN>;
-    for (int job = wave; job < images(GRAD) * kBlocks; job += 4) {
+    for (int job = wave; job < NM * kBlocks; job += 4) {
         const int which = job / kBlocks, b = job % kBlocks;
-        const bool upper = GRAD && which > 0;   // transposed
+        const bool upper = which > 0;   // transposed
         const int rt = upper ? (b < 4 ? b >> 1 : b - 2) : (b < 2 ? b : (b + 2) >> 1);
         const int s = upper ? (b < 4 ? b & 1 : 1) : (b < 2 ? 0 : b & 1);
-        const float *src = which == 0 ? xs[0] : which == 1 && GRAD ? xs[NM - 1] : ps;
+        const float *src = xs[which];
         f32x4 v[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int ct = 2 * s + e, col = 16 * ct + 4 * g, row = 16 * rt + l16;
+            const int ct = 2 * s + e, col = 16 * ct + 4 * g, at16 = 16 * rt + l16;
             v[e] = zero4();
             if (!upper) {
-                if (ct <= rt) v[e] = *(const f32x4 *)(src + row * kLd + col);
+                if (ct <= rt) v[e] = *(const f32x4 *)(src + at16 * kLd + col);
             } else if (ct >= rt) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[e][r] = src[(col + r) * kLd + row];
+                for (int r = 0; r < 4; ++r) v[e][r] = src[(col + r) * kLd + at16];
             }
         }
-        const Operand<OWN> o = split8<OWN>(v[0], v[1]);
-#pragma unroll
-        for (int t = 0; t < OWN; ++t)
-            *(u32x4 *)(img + which * kImage<OWN> + (b * OWN + t) * 1024 + 16 * lane) = o.t[t];
+        put(img + which * kImage<OWN>, b, v[0], v[1]);
     }
 }
 
@@ -212,78 +244,81 @@ __global__ __launch_bounds__(256, 1) void k_delta_walk(WalkArgs args) {
     using X = typename std::conditional<MODE == BACK, float, T>::type;   // the third input's type
     constexpr int IN = Terms<T>::IN, OWN = Terms<T>::OWN;
     constexpr bool GRAD = MODE != FWD;
-    constexpr int NP = N < 32 ? 32 : N, KS = NP / 32, NT = NP / 16;
+    constexpr int NP = N < 32 ? 32 : N, KS = NP / 32, NT = N / 16;
     constexpr int RS = NP + 16;                         // row stride of K and Q in LDS, in elements
     constexpr int kRows = C * RS * 2 * IN;              // bytes of K or Q
-    constexpr bool kQ = MODE != KEEP, kTwo = MODE != KEEP;   // Q read; a second image
-    constexpr int kImg = kImage<OWN>;
-    constexpr int kBuf = kRows * (kQ ? 2 : 1) + kImg * (kTwo ? 2 : 1) + kGates * 4;
+    constexpr bool kQ = MODE != KEEP;                   // Q read, and a second image
+    constexpr int kImages = kQ ? 2 : 1, kImg = kImage<OWN>;
+    constexpr int kBuf = kRows * (kQ ? 2 : 1) + kImg * kImages + kGates * 4;
     constexpr int kBufs = 2 * kBuf <= 160 * 1024 ? 2 : 1;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kBufs][kBuf];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l16 = lane & 15;
     const int block = blockIdx.x % args.blocks, h = blockIdx.x / args.blocks % args.dir[0].a.H;
     const int u = blockIdx.x / args.blocks / args.dir[0].a.H;
     const int p0 = (block * 4 + wave) * 16 * NC;
+    // the wave has columns, those of the walks' own arrays past the head's width among them
+    const bool works = p0 < (GRAD ? padded(args.dir[0].a.P) : args.dir[0].a.P);
     for (int di = args.ndir - 1; di >= 0; --di) {
         const PrepDir &pd = args.dir[di];
         const DeltaArgs &a = pd.a;
-        const int grp = h / (a.H / a.G);
+        const int grp = h / (a.H / a.G), PP = padded(a.P);
         const DeltaUnit at = delta_unit(a, u);
         const int chunks = (at.len + C - 1) / C;
-        int p[NC];
-        bool own[NC];
+        // a lane's columns, in the caller's arrays and in the walks' own
+        uint32_t pc[NC], pw[NC];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            own[c] = p0 + 16 * c + l16 < a.P;
-            p[c] = min(p0 + 16 * c + l16, a.P - 1);
+            const int p = p0 + 16 * c + l16;
+            pc[c] = p < a.P ? p : kFar;
+            pw[c] = p < PP ? 4 * p : kFar;
         }
         f32x4 S[NT][NC];
+        const size_t state = ((size_t)u * a.H + h) * a.P * N + 4 * g;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 S[t][c] = zero4();
-                if (a.init && own[c] && 16 * t < N)
-                    S[t][c] = *(const f32x4 *)(a.init + (((size_t)u * a.H + h) * a.P + p[c]) * N + 16 * t + 4 * g);
+                if (a.init && pc[c] != kFar) S[t][c] = *(const f32x4 *)(a.init + state + (size_t)pc[c] * N + 16 * t);
             }
-        // the next chunk on its way: rows of K and Q, images, gates, the third input
-        constexpr int V = 16 / sizeof(T), kVecs = C * NP / V / 256, kIv = kImg / 16 / 256 + (kImg / 16 % 256 ? 1 : 0);
-        rvec nk[kVecs], nq[kQ ? kVecs : 1];
-        u32x4 ni[kTwo ? 2 * kIv : kIv];
+        // the next chunk on its way: rows of K and Q, gates, the third input (the
+        // images go straight to LDS)
+        constexpr int V = 16 / sizeof(T), kVecs = C * NP / V / 256;
+        u32x4 nk[kVecs], nq[kQ ? kVecs : 1];
         float ngate = 0.f;
         X nx[4][NC][4];
         auto order = [&](int i) { return MODE == BACK ? chunks - 1 - i : i; };
-        auto fetch = [&](int chunk) {
+        auto fetch = [&](int chunk, uint8_t *to) {
             const int first = chunk * C, live = min(C, at.len - first);
             const size_t sh = (size_t)(at.slot + chunk) * a.H + h;
+            const uint32_t row = (uint32_t)(a.G * N * sizeof(T)), off = (uint32_t)(grp * N * sizeof(T));
+            const ChunkRows kr(a.k, at, a.reverse, first, live, row, off, N * sizeof(T));
+            const ChunkRows qr(a.q, at, a.reverse, first, live, row, off, N * sizeof(T));
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const int e = tid + 256 * i, row = e / (NP / V), col = e % (NP / V) * V;
-                nk[i] = rvec{0u, 0u, 0u, 0u};
-                if (kQ) nq[i] = nk[i];
-                if (row < live && col < N) {
-                    const size_t m = ((size_t)delta_token(at, a.reverse, first + row) * a.G + grp) * N + col;
-                    nk[i] = *(const rvec *)((const T *)a.k + m);
-                    if (kQ) nq[i] = *(const rvec *)((const T *)a.q + m);
-                }
+                const int e = tid + 256 * i, col = e % (NP / V) * V;
+                const uint32_t o = kr.offset(e / (NP / V)) + (col < N ? (uint32_t)(col * sizeof(T)) : kFar);
+                nk[i] = buf16(kr.rsrc, o);
+                if (kQ) nq[i] = buf16(qr.rsrc, o);
             }
-            const uint8_t *img = pd.images + sh * images(GRAD) * kImg + (MODE == BACK ? kImg : 0);
-#pragma unroll
-            for (int i = 0; i < (kTwo ? 2 * kIv : kIv); ++i) {
-                const int e = tid + 256 * (i % kIv);
-                if (kImg / 16 % 256 == 0 || e < kImg / 16) ni[i] = *(const u32x4 *)(img + i / kIv * kImg + 16 * e);
-            }
+            const uint8_t *img = pd.images + sh * images(GRAD) * kImg + (MODE == BACK ? kImg : 0) + 16 * lane;
+            for (int i = wave; i < kImages * kImg / 1024; i += 4)
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(img + i * 1024),
+                                                 (__attribute__((address_space(3))) void *)(to + (kQ ? 2 : 1) * kRows + i * 1024),
+                                                 16, 0, 0);
             if (tid < kGates) ngate = pd.gates[sh * kGates + tid];
+            if (!works) return;
+            const uint32_t xrow = (uint32_t)(a.H * a.P * sizeof(X));
+            const ChunkRows xr(a.v, at, a.reverse, first, live, xrow, (uint32_t)(h * a.P * sizeof(X)), a.P * sizeof(X));
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int c = 0; c < NC; ++c) {
+                const uint32_t col = xr.offset(4 * g) + (pc[c] == kFar ? kFar : pc[c] * (uint32_t)sizeof(X));
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = 16 * t + 4 * g + r;
-                    const size_t tok = (size_t)delta_token(at, a.reverse, first + min(i, live - 1));
+                for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) nx[t][c][r] = ((const X *)a.v)[(tok * a.H + h) * a.P + p[c]];
-                }
+                    for (int r = 0; r < 4; ++r) nx[t][c][r] = buf_value(xr.rsrc, col + (16 * t + r) * xr.step, X());
+            }
         };
         auto stash = [&](uint8_t *to) {
 #pragma unroll
@@ -292,9 +327,9 @@ __global__ __launch_bounds__(256, 1) void k_delta_walk(WalkArgs args) {
                 for (int i = 0; i < kVecs; ++i) {
                     const int e = tid + 256 * i, row = e / (NP / V), col = e % (NP / V) * V;
                     uint16_t *at16 = (uint16_t *)(to + w * kRows) + row * RS + col;
-                    const rvec r = w ? nq[i] : nk[i];
+                    const u32x4 r = w ? nq[i] : nk[i];
                     if constexpr (IN == 1) {
-                        *(rvec *)at16 = r;
+                        *(u32x4 *)at16 = r;
                     } else {
                         uint32_t lo[IN], hi[IN];
                         split2<IN>(__uint_as_float(r[0]), __uint_as_float(r[1]), lo);
@@ -303,22 +338,19 @@ __global__ __launch_bounds__(256, 1) void k_delta_walk(WalkArgs args) {
                         for (int t = 0; t < IN; ++t) *(u32x2 *)(at16 + t * C * RS) = u32x2{lo[t], hi[t]};
                     }
                 }
-            uint8_t *img = to + (kQ ? 2 : 1) * kRows;
-#pragma unroll
-            for (int i = 0; i < (kTwo ? 2 * kIv : kIv); ++i) {
-                const int e = tid + 256 * (i % kIv);
-                if (kImg / 16 % 256 == 0 || e < kImg / 16) *(u32x4 *)(img + i / kIv * kImg + 16 * e) = ni[i];
-            }
-            if (tid < kGates) *(float *)(img + (kTwo ? 2 : 1) * kImg + 4 * tid) = ngate;
+            if (tid < kGates) *(float *)(to + (kQ ? 2 : 1) * kRows + kImages * kImg + 4 * tid) = ngate;
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the images are in LDS
         };
         if (di != args.ndir - 1) __syncthreads();   // the direction before has read its last chunk
         if (chunks > 0) {
-            fetch(order(0));
+            fetch(order(0), lds[0]);
             stash(lds[0]);
         }
         for (int step = 0; step < chunks; ++step) {
             const int chunk = order(step), first = chunk * C, live = min(C, at.len - first);
             const uint8_t *buf = lds[kBufs == 2 ? step & 1 : 0];
+            uint8_t *nextbuf = lds[kBufs == 2 ? (step + 1) & 1 : 0];
+            const bool more = step + 1 < chunks;
             __syncthreads();
             f32x4 x[4][NC];
 #pragma unroll
@@ -327,15 +359,13 @@ __global__ __launch_bounds__(256, 1) void k_delta_walk(WalkArgs args) {
                 for (int c = 0; c < NC; ++c)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        float v;
-                        if constexpr (sizeof(X) == 2) v = bf2f(nx[t][c][r]);
-                        else v = nx[t][c][r];
-                        x[t][c][r] = 16 * t + 4 * g + r < live ? v : 0.f;
+                        if constexpr (sizeof(X) == 2) x[t][c][r] = bf2f(nx[t][c][r]);
+                        else x[t][c][r] = nx[t][c][r];
                     }
-            if (step + 1 < chunks) fetch(order(step + 1));
+            if (kBufs == 2 && more) fetch(order(step + 1), nextbuf);
             const uint16_t *kl = (const uint16_t *)buf, *ql = (const uint16_t *)(buf + kRows);
             const uint8_t *one = buf + (kQ ? 2 : 1) * kRows, *two = one + kImg;
-            const float *gate = (const float *)(one + (kTwo ? 2 : 1) * kImg);
+            const float *gate = (const float *)(one + kImages * kImg);
             // rows 16 rt .. of K or Q, k = n in the order of S's tiles
             auto rows = [&](const uint16_t *m, int rt, int s) {
                 Operand<IN> o;
@@ -368,177 +398,183 @@ __global__ __launch_bounds__(256, 1) void k_delta_walk(WalkArgs args) {
                 return o;
             };
             auto gates = [&](int which, int rt) { return *(const f32x4 *)(gate + which * C + 16 * rt + 4 * g); };
-            if constexpr (GRAD) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        if (own[c] && 16 * t < N)
-                            *(f32x4 *)(a.states + (((size_t)(at.slot + chunk) * a.H + h) * a.P + p[c]) * N + 16 * t + 4 * g) =
-                                S[t][c];
-            }
-            Operand<OWN> sb[KS][NC];
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int c = 0; c < NC; ++c) sb[s][c] = split8<OWN>(S[2 * s][c], S[2 * s + 1][c]);
-            // K S
-            f32x4 ks[4][NC];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-#pragma unroll
-                for (int c = 0; c < NC; ++c) ks[t][c] = zero4();
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const Operand<IN> k = rows(kl, t, s);
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) ks[t][c] = mm(k, sb[s][c], ks[t][c]);
-                }
-            }
             f32x4 out[4][NC];
-            Operand<OWN> kb[2][NC], qb[MODE == BACK ? 2 : 1][NC];   // what K^T and, walking back, Q^T multiply
-            if constexpr (MODE != BACK) {
-                Operand<OWN> b[2][NC];
+            if (works) {
+                if constexpr (GRAD) {
+                    const __amdgpu_buffer_rsrc_t sr = __builtin_amdgcn_make_buffer_rsrc(
+                        a.states + ((size_t)(at.slot + chunk) * a.H + h) * N * PP, 0, N * PP * 4, 0x00027000);
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
+                    for (int c = 0; c < NC; ++c) {
+                        const uint32_t o = pw[c] + 4 * g * PP * 4;
 #pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        b[s][c] = split8<OWN>(x[2 * s][c] - gates(0, 2 * s) * ks[2 * s][c],
-                                              x[2 * s + 1][c] - gates(0, 2 * s + 1) * ks[2 * s + 1][c]);
-                f32x4 e[4][NC];
+                        for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) e[t][c] = zero4();
-#pragma unroll
-                    for (int s = 0; s < (t < 2 ? 1 : 2); ++s) {
-                        const Operand<OWN> m = image(one, lower_block(t, s));
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) e[t][c] = mm(m, b[s][c], e[t][c]);
+                            for (int r = 0; r < 4; ++r) buf_store(sr, o + (16 * t + r) * PP * 4, S[t][c][r]);
                     }
                 }
-                if constexpr (MODE == FWD) {
-                    Operand<OWN> eb[2][NC];
+                // K S and Q S
+                f32x4 ks[4][NC];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) ks[t][c] = out[t][c] = zero4();
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    Operand<OWN> sb[NC];
+#pragma unroll
+                    for (int c = 0; c < NC; ++c)
+                        sb[c] = split8<OWN>(S[2 * s][c], 2 * s + 1 < NT ? S[min(2 * s + 1, NT - 1)][c] : zero4());
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const Operand<IN> k = rows(kl, t, s);
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) ks[t][c] = mm(k, sb[c], ks[t][c]);
+                        if constexpr (MODE == FWD) {
+                            const Operand<IN> q = rows(ql, t, s);
+#pragma unroll
+                            for (int c = 0; c < NC; ++c) out[t][c] = mm(q, sb[c], out[t][c]);
+                        }
+                    }
+                }
+                Operand<OWN> b[2][NC], kb[2][NC];   // kb: what K^T multiplies
+                if constexpr (MODE != BACK) {
 #pragma unroll
                     for (int s = 0; s < 2; ++s)
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) eb[s][c] = split8<OWN>(e[2 * s][c], e[2 * s + 1][c]);
+                        for (int c = 0; c < NC; ++c)
+                            b[s][c] = split8<OWN>(x[2 * s][c] - gates(0, 2 * s) * ks[2 * s][c],
+                                                  x[2 * s + 1][c] - gates(0, 2 * s + 1) * ks[2 * s + 1][c]);
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) out[t][c] = zero4();
+                        for (int c = 0; c < NC; ++c) ks[t][c] = zero4();
 #pragma unroll
-                        for (int s = 0; s < KS; ++s) {
-                            const Operand<IN> q = rows(ql, t, s);
+                        for (int s = 0; s < (t < 2 ? 1 : 2); ++s) {
+                            const Operand<OWN> m = image(one, lower_block(t, s));
 #pragma unroll
-                            for (int c = 0; c < NC; ++c) out[t][c] = mm(q, sb[s][c], out[t][c]);
+                            for (int c = 0; c < NC; ++c) ks[t][c] = mm(m, b[s][c], ks[t][c]);
                         }
+                    }
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int c = 0; c < NC; ++c)
+                            kb[s][c] = split8<OWN>(gates(1, 2 * s) * gates(2, 2 * s) * ks[2 * s][c],
+                                                   gates(1, 2 * s + 1) * gates(2, 2 * s + 1) * ks[2 * s + 1][c]);
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) b[s][c] = split8<OWN>(x[2 * s][c], x[2 * s + 1][c]);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) ks[t][c] *= gates(1, t);
+#pragma unroll
+                        for (int s = t < 2 ? 0 : 1; s < 2; ++s) {
+                            const Operand<OWN> m = image(two, upper_block(t, s));
+#pragma unroll
+                            for (int c = 0; c < NC; ++c) ks[t][c] = mm(m, b[s][c], ks[t][c]);
+                        }
+                    }
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) b[s][c] = split8<OWN>(ks[2 * s][c], ks[2 * s + 1][c]);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int s = t < 2 ? 0 : 1; s < 2; ++s) {
+                            const Operand<OWN> m = image(one, upper_block(t, s));
+#pragma unroll
+                            for (int c = 0; c < NC; ++c) out[t][c] = mm(m, b[s][c], out[t][c]);
+                        }
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) {
+                            kb[s][c] = split8<OWN>(-gates(0, 2 * s) * gates(2, 2 * s) * out[2 * s][c],
+                                                   -gates(0, 2 * s + 1) * gates(2, 2 * s + 1) * out[2 * s + 1][c]);
+                            b[s][c] = split8<OWN>(a.scale * gates(0, 2 * s) * x[2 * s][c],
+                                                  a.scale * gates(0, 2 * s + 1) * x[2 * s + 1][c]);   // Q^T's
+                        }
+                }
+                const float last = gate[C - 1];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) S[t][c] *= last;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const Operand<IN> k = cols(kl, t, s);
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) S[t][c] = mm(k, kb[s][c], S[t][c]);
+                        if constexpr (MODE == BACK) {
+                            const Operand<IN> q = cols(ql, t, s);
+#pragma unroll
+                            for (int c = 0; c < NC; ++c) S[t][c] = mm(q, b[s][c], S[t][c]);
+                        }
+                    }
+                }
+                if constexpr (MODE == FWD) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) b[s][c] = split8<OWN>(ks[2 * s][c], ks[2 * s + 1][c]);
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
 #pragma unroll
                         for (int c = 0; c < NC; ++c) out[t][c] *= a.scale * gates(0, t);
 #pragma unroll
                         for (int s = 0; s < (t < 2 ? 1 : 2); ++s) {
                             const Operand<OWN> m = image(two, lower_block(t, s));
 #pragma unroll
-                            for (int c = 0; c < NC; ++c) out[t][c] = mm(m, eb[s][c], out[t][c]);
+                            for (int c = 0; c < NC; ++c) out[t][c] = mm(m, b[s][c], out[t][c]);
                         }
                     }
-                } else {
+                } else if constexpr (MODE == KEEP) {
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) out[t][c] = e[t][c];
-                }
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        kb[s][c] = split8<OWN>(gates(1, 2 * s) * gates(2, 2 * s) * e[2 * s][c],
-                                               gates(1, 2 * s + 1) * gates(2, 2 * s + 1) * e[2 * s + 1][c]);
-            } else {
-                Operand<OWN> b[2][NC];
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        b[s][c] = split8<OWN>(x[2 * s][c], x[2 * s + 1][c]);
-                        qb[s][c] = split8<OWN>(a.scale * gates(0, 2 * s) * x[2 * s][c],
-                                               a.scale * gates(0, 2 * s + 1) * x[2 * s + 1][c]);
-                    }
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) ks[t][c] *= gates(1, t);
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int s = t < 2 ? 0 : 1; s < 2; ++s) {
-                        const Operand<OWN> m = image(two, upper_block(t, s));
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) ks[t][c] = mm(m, b[s][c], ks[t][c]);
-                    }
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) b[s][c] = split8<OWN>(ks[2 * s][c], ks[2 * s + 1][c]);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) out[t][c] = zero4();
-#pragma unroll
-                    for (int s = t < 2 ? 0 : 1; s < 2; ++s) {
-                        const Operand<OWN> m = image(one, upper_block(t, s));
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) out[t][c] = mm(m, b[s][c], out[t][c]);
-                    }
-                }
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        kb[s][c] = split8<OWN>(-gates(0, 2 * s) * gates(2, 2 * s) * out[2 * s][c],
-                                               -gates(0, 2 * s + 1) * gates(2, 2 * s + 1) * out[2 * s + 1][c]);
-            }
-            const float last = gate[C - 1];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                for (int c = 0; c < NC; ++c) S[t][c] *= last;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const Operand<IN> k = cols(kl, t, s);
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) S[t][c] = mm(k, kb[s][c], S[t][c]);
-                    if constexpr (MODE == BACK) {
-                        const Operand<IN> q = cols(ql, t, s);
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) S[t][c] = mm(q, qb[s][c], S[t][c]);
-                    }
+                        for (int c = 0; c < NC; ++c) out[t][c] = ks[t][c];
                 }
             }
+            // what the next chunk brought goes to LDS before this one's results go
+            // out, so that nothing waits for stores
+            if (kBufs == 1) {
+                __syncthreads();
+                if (more) fetch(order(step + 1), nextbuf);
+            }
+            if (more) stash(nextbuf);
+            if (works) {
+                const int P = GRAD ? PP : a.P;
+                const ChunkRows yr(a.y, at, a.reverse, first, live, (uint32_t)(a.H * P * 4), (uint32_t)(h * P * 4), P * 4);
+                uint32_t o[NC];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = 16 * t + 4 * g + r;
-                    if (i >= live) continue;
-                    float *y = a.y + ((size_t)delta_token(at, a.reverse, first + i) * a.H + h) * a.P;
+                for (int c = 0; c < NC; ++c) o[c] = yr.offset(4 * g) + (GRAD ? pw[c] : pc[c] == kFar ? kFar : 4 * pc[c]);
+                if (MODE == FWD && a.add) {
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
-                        if (own[c]) {
-                            if (MODE == FWD && a.add) y[p[c]] += out[t][c][r];
-                            else y[p[c]] = out[t][c][r];
-                        }
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                out[t][c][r] += buf_value(yr.rsrc, o[c] + (16 * t + r) * yr.step, 0.f);
                 }
-            if (kBufs == 1) __syncthreads();
-            if (step + 1 < chunks) stash(lds[kBufs == 2 ? (step + 1) & 1 : 0]);
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) buf_store(yr.rsrc, o[c] + (16 * t + r) * yr.step, out[t][c][r]);
+            }
         }
         if (a.last) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
-                    if (own[c] && 16 * t < N)
-                        *(f32x4 *)(a.last + (((size_t)u * a.H + h) * a.P + p[c]) * N + 16 * t + 4 * g) = S[t][c];
+                    if (pc[c] != kFar) *(f32x4 *)(a.last + state + (size_t)pc[c] * N + 16 * t) = S[t][c];
         }
     }
 }
@@ -579,14 +615,14 @@ struct Chunked {
 };
 
 // the workspace of a direction: images, then gates
-size_t prep_images(const DeltaArgs &a, bool bf16, bool grad) {
-    return (size_t)delta_slots(a.units, a.L, a.cu != nullptr) * a.H * images(grad) * (bf16 ? kImage<2> : kImage<3>);
+size_t prep_images(const DeltaArgs &a, bool grad) {
+    return (size_t)delta_slots(a.units, a.L, a.cu != nullptr) * a.H * images(grad) * kImage<3>;
 }
-PrepDir prep_dir(const DeltaArgs &a, void *ws, bool bf16, bool grad) {
+PrepDir prep_dir(const DeltaArgs &a, void *ws, bool grad) {
     PrepDir d;
     d.a = a;
     d.images = (uint8_t *)ws;
-    d.gates = (float *)((uint8_t *)ws + prep_images(a, bf16, grad));
+    d.gates = (float *)((uint8_t *)ws + prep_images(a, grad));
     return d;
 }
 
@@ -602,14 +638,14 @@ hipError_t with_shape(const DeltaArgs &a, bool bf16, F f) {
 }  // namespace
 
 // bytes, a multiple of 256; L and units of a, and whether it is packed (cu)
-size_t delta_chunk_workspace(const DeltaArgs &a, bool bf16, bool grad) {
+size_t delta_chunk_workspace(const DeltaArgs &a, bool grad) {
     const size_t slots = (size_t)delta_slots(a.units, a.L, a.cu != nullptr) * a.H;
-    return prep_images(a, bf16, grad) + ((slots * kGates * 4 + 255) & ~(size_t)255);
+    return prep_images(a, grad) + ((slots * kGates * 4 + 255) & ~(size_t)255);
 }
 
 hipError_t launch_delta_chunked(const DeltaArgs *a, int ndir, bool bf16, void *const *ws, hipStream_t s) {
     PrepDir d[2];
-    for (int i = 0; i < ndir; ++i) d[i] = prep_dir(a[i], ws[i], bf16, false);
+    for (int i = 0; i < ndir; ++i) d[i] = prep_dir(a[i], ws[i], false);
     return with_shape(a[0], bf16, [&](auto k) {
         hipError_t e = hipSuccess;
         if (a[0].L > 0) e = k.prep(d, ndir, false, s);
@@ -618,7 +654,7 @@ hipError_t launch_delta_chunked(const DeltaArgs *a, int ndir, bool bf16, void *c
 }
 
 hipError_t launch_delta_keep(const DeltaArgs &a, bool bf16, void *ws, hipStream_t s) {
-    const PrepDir d = prep_dir(a, ws, bf16, true);
+    const PrepDir d = prep_dir(a, ws, true);
     return with_shape(a, bf16, [&](auto k) {
         hipError_t e = k.prep(&d, 1, true, s);
         return e != hipSuccess ? e : k.template walk<KEEP>(&d, 1, s);
@@ -626,7 +662,7 @@ hipError_t launch_delta_keep(const DeltaArgs &a, bool bf16, void *ws, hipStream_
 }
 
 hipError_t launch_delta_back(const DeltaArgs &a, bool bf16, void *ws, hipStream_t s) {
-    const PrepDir d = prep_dir(a, ws, bf16, true);
+    const PrepDir d = prep_dir(a, ws, true);
     return with_shape(a, bf16, [&](auto k) { return k.template walk<BACK>(&d, 1, s); });
 }
 

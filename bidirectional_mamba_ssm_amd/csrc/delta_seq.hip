@@ -27,6 +27,32 @@ __device__ __forceinline__ void widen(float *to, rvec r, float) {
 __device__ __forceinline__ float as_float(uint16_t v) { return bf2f(v); }
 __device__ __forceinline__ float as_float(float v) { return v; }
 
+// R consecutive entries of a column, 16 bytes at a time
+template <int R>
+__device__ __forceinline__ void load_state(bool given, const float *p, float *s) {
+    constexpr int V = R < 4 ? R : 4;
+    typedef float vec __attribute__((ext_vector_type(V)));
+#pragma unroll
+    for (int j = 0; j < R; j += V) {
+        vec v = 0.f;
+        if (given) v = *(const vec *)(p + j);
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[j + e] = v[e];
+    }
+}
+template <int R>
+__device__ __forceinline__ void store_state(bool wanted, float *p, const float *s) {
+    constexpr int V = R < 4 ? R : 4;
+    typedef float vec __attribute__((ext_vector_type(V)));
+#pragma unroll
+    for (int j = 0; j < R; j += V) {
+        vec v;
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = s[j + e];
+        if (wanted) *(vec *)(p + j) = v;
+    }
+}
+
 template <typename T, int N, int W>
 __global__ __launch_bounds__(64 * W) void k_delta_seq(DeltaArgs a, int blocks) {
     constexpr int kThreads = 64 * W, V = 16 / sizeof(T), R = N / 8, kCols = 16 * W;
@@ -42,11 +68,8 @@ __global__ __launch_bounds__(64 * W) void k_delta_seq(DeltaArgs a, int blocks) {
     const bool own0 = p < a.P, own1 = p + 1 < a.P;
     float s0[R], s1[R];
     const size_t state = (((size_t)u * a.H + h) * a.P + p) * N + part * R;
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-        s0[j] = a.init && own0 ? a.init[state + j] : 0.f;
-        s1[j] = a.init && own1 ? a.init[state + N + j] : 0.f;
-    }
+    load_state<R>(a.init && own0, a.init + state, s0);
+    load_state<R>(a.init && own1, a.init + state + N, s1);
     rvec nqk[kPer];
     T nv[4];
     float ngate = 0.f;
@@ -134,12 +157,8 @@ __global__ __launch_bounds__(64 * W) void k_delta_seq(DeltaArgs a, int blocks) {
         }
         if (t + kTile < at.len) stash(buf ^ 1);
     }
-    if (!a.last) return;
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-        if (own0) a.last[state + j] = s0[j];
-        if (own1) a.last[state + N + j] = s1[j];
-    }
+    store_state<R>(a.last && own0, a.last + state, s0);
+    store_state<R>(a.last && own1, a.last + state + N, s1);
 }
 
 template <typename T, int N>

@@ -1,12 +1,17 @@
 // Operands of the delta rule's chunk kernels: numbers as sums of bf16 terms.
 //
-// bf16 inputs are one term, exactly. What the kernels compute (states, errors,
-// the chunk's inverse) is kept as two terms, hi = bf16(v) and bf16(v - hi): 16
-// significant bits over fp32's range. fp32 inputs and what is computed
-// from them are three terms, all 24 bits. A product of operands keeps the pairs
-// of terms that reach its last one: 2 for one by two, 3 for two by two, 6
-// for three by three, each a v_mfma_f32_16x16x32_bf16 summed in fp32, the
-// smallest first.
+// bf16 inputs are one term, exactly; fp32 inputs and everything the kernels
+// compute (states, errors, the chunk's inverse) are three terms, bf16(v), bf16 of
+// what is left and bf16 of what is left then: all 24 bits over fp32's range. A
+// product of operands keeps the pairs of terms that reach its last one: 3 for one
+// by three, 6 for three by three, each a v_mfma_f32_16x16x32_bf16 summed in
+// fp32, the smallest first. (Two terms, 2 and 3 products, are off by 5e-6 of a
+// result's norm, three by 1e-7; six bf16 products take 96 cycles where the fp32
+// matrix instructions take 256.)
+//
+// Rows of tokens are read and written through buffer descriptors that end
+// with the chunk's last token: reads past it give zeros, writes past it are
+// dropped, and so are those of lanes whose column is put far outside.
 #pragma once
 #include "delta.hpp"
 #include "mfma.hpp"
@@ -17,7 +22,7 @@ namespace {
 
 template <typename T> struct Terms;
 template <> struct Terms<uint16_t> {
-    static constexpr int IN = 1, OWN = 2;
+    static constexpr int IN = 1, OWN = 3;
 };
 template <> struct Terms<float> {
     static constexpr int IN = 3, OWN = 3;
@@ -68,6 +73,50 @@ __device__ __forceinline__ f32x4 mm(const Operand<A> &a, const Operand<B> &b, f3
     return c;
 }
 
+constexpr uint32_t kFar = 0x80000000u;   // an offset past every descriptor's end (chunks are under 2^30 bytes)
+
+// The rows of one chunk of an array [tok][row bytes], `len` bytes of each from
+// `off` on. Row i of the walk is at offset(i).
+struct ChunkRows {
+    __amdgpu_buffer_rsrc_t rsrc;
+    uint32_t base;    // of row 0
+    int32_t step;     // to the next row
+    __device__ __forceinline__ ChunkRows(const void *p, const DeltaUnit &d, bool reverse, int first, int live,
+                                         uint32_t row, uint32_t off, uint32_t len) {
+        const long long low = d.start + (reverse ? d.len - first - live : first);
+        rsrc = __builtin_amdgcn_make_buffer_rsrc((uint8_t *)const_cast<void *>(p) + low * row + off, 0,
+                                                 (int)((live - 1) * row + len), 0x00027000);
+        base = reverse ? (uint32_t)(live - 1) * row : 0u;
+        step = reverse ? -(int32_t)row : (int32_t)row;
+    }
+    __device__ __forceinline__ uint32_t offset(int i) const { return base + (uint32_t)(i * step); }
+};
+__device__ __forceinline__ u32x4 buf16(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+}
+__device__ __forceinline__ float buf_value(__amdgpu_buffer_rsrc_t r, uint32_t at, float) {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
+}
+__device__ __forceinline__ uint16_t buf_value(__amdgpu_buffer_rsrc_t r, uint32_t at, uint16_t) {
+    return __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
+}
+__device__ __forceinline__ void buf_store(__amdgpu_buffer_rsrc_t r, uint32_t at, float v) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, at, 0, 0);
+}
+
+// the sum of a chunk's logarithms of decays up to each token, a token a lane, in
+// 64 bits: nothing is told from a reset below e^-1000, infinities would cancel,
+// and a reset in the middle takes nothing from the decays behind it
+__device__ __forceinline__ double decay_sums(float g, int lane) {
+    double s = g < -1000.f ? -1000.0 : (double)g;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const double o = __shfl_up(s, d);
+        if (lane >= d) s += o;
+    }
+    return s;
+}
+
 // Workspace of a chunk and head: images of 64 x 64 triangles and the gates. An
 // image holds the 6 blocks of 16 rows by 32 that are not zero, each as the
 // operand's registers, a kilobyte a term: lane l's row l % 16, k slots 0..3 at
@@ -77,6 +126,8 @@ __device__ __forceinline__ constexpr int lower_block(int rt, int s) { return rt 
 __device__ __forceinline__ constexpr int upper_block(int rt, int s) { return rt < 2 ? 2 * rt + s : rt + 2; }
 template <int OWN> constexpr int kImage = kBlocks * OWN * 1024;   // bytes
 constexpr int kGates = 3 * kDeltaChunk;                           // e^{G_i}, e^{G_C - G_i}, beta
+// columns of the walks' own arrays: e and z [tok][H][padded], states [slot][H][N][padded]
+__host__ __device__ constexpr int padded(int P) { return (P + 31) & ~31; }
 
 }  // namespace
 }  // namespace bm

@@ -150,6 +150,7 @@ BAD_SHAPES = [
     (dict(headdim=129), _abi.EUNSUPPORTED), (dict(d_state=48), _abi.EUNSUPPORTED), (dict(d_state=256), _abi.EUNSUPPORTED),
     (dict(chunk=128), _abi.EUNSUPPORTED), (dict(chunk=1), _abi.EUNSUPPORTED), (dict(flags=1), _abi.EINVAL),
     (dict(dtype=5), _abi.EINVAL), (dict(batch=1 << 20, nheads=64, headdim=16, seqlen=1), _abi.EUNSUPPORTED),
+    (dict(batch=1, nheads=32770, headdim=16, seqlen=1), _abi.EUNSUPPORTED),
     (dict(batch=1 << 22, nheads=2, seqlen=4, headdim=16, ngroups=2), _abi.EUNSUPPORTED),
     (dict(batch=1 << 16, seqlen=1 << 16), _abi.EUNSUPPORTED)]
 
