@@ -10,20 +10,24 @@
 //   D <- e^{G_C} D + Q^T (scale e^G do) - K^T (e^G beta Z)
 // (both inverses, since a beta may be 0 and (I + L)^-1 diag(beta) = diag(beta) (I + M)^-1).
 //
-// k_delta_prep, a chunk and head to a workgroup, makes what does not wait for
-// the state: the triangles, inverted in fp32 (16 x 16 blocks by substitution, a
-// column a lane; the blocks below by products on v_mfma_f32_16x16x4_f32), as
-// operand images.
+// k_delta_prep, a chunk and head to a wave, makes what does not wait for the
+// state: the triangles, inverted in fp32, as operand images. Everything but the
+// diagonal 16 x 16 blocks stays in registers: a result's lanes (rows 4 g + r of a
+// tile, column l % 16) are the transpose's first operand, or the second one's, as
+// they come, for v_mfma_f32_16x16x4_f32 taken with k = 4 g + r in its r-th step. The
+// diagonal blocks are inverted by substitution, a column a lane, all four at
+// once. A tile's decays are products of a row's and a column's factor (and the
+// tiles' between), both at most 1 where g <= 0; the diagonal tiles' are taken
+// one by one.
 //
-// k_delta_walk takes a head's chunks in order. A wave owns 16 NC columns of the
-// state for all N rows; columns never meet. The matrix cores' result order (rows
-// 4 g + r of a tile, column l % 16) serves as the next product's second operand as
-// it is, if the first one's k order follows it: so S, V, E and Y never leave the
-// wave's registers, and no product waits for another wave. K and Q come
-// to LDS row by row (read as rows for K S and Q S, transposed by
-// ds_read_b64_tr_b16 for K^T E), the images as they are; the next chunk's
-// loads are under way meanwhile, one barrier a chunk (two where one buffer
-// is all that fits).
+// k_delta_walk takes a head's chunks in order. A wave owns 16 columns of the
+// state for all N rows; columns never meet. The matrix cores' result order serves
+// as the next product's second operand as it is, if the first one's k order
+// follows it: so S, V, E and Y never leave the wave's registers, and no product
+// waits for another wave. K and Q come to LDS row by row (read as rows for
+// K S and Q S, transposed by ds_read_b64_tr_b16 for K^T E), the images as they
+// are; the next chunk's loads are under way meanwhile, in registers: one buffer,
+// so that two workgroups share a CU and hide each other's waits.
 #include "delta_split.hpp"
 #include "internal.hpp"
 
@@ -31,7 +35,6 @@ namespace bm {
 namespace {
 
 constexpr int C = kDeltaChunk;
-constexpr int kLd = C + 4;   // rows of the fp32 triangles in LDS
 enum { FWD, KEEP, BACK };
 // images of a chunk and head: FWD (I + M)^-1, A; for the gradient (I + M)^-1, (I + L)^-T, B^T
 constexpr int images(bool grad) { return grad ? 3 : 2; }
@@ -49,18 +52,56 @@ struct PrepArgs {
     PrepDir dir[2];
 };
 
+constexpr int kPrepWaves = 4;
+constexpr int kDiag = 16 * 20;   // a diagonal block in LDS: rows of 20 words
+
+// one wave's exchange through LDS
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+__device__ __forceinline__ constexpr int lower(int i, int j) { return i * (i + 1) / 2 + j; }
+
+// the inverse of I + m for four strictly lower 16 x 16 blocks, a column a lane
+__device__ __forceinline__ void invert_diagonal(const float *m, float *x, int g, int l16) {
+    const float *from = m + g * kDiag;
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float s[2] = {i == l16 ? 1.f : 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < i; k += 4) {
+            const f32x4 row = *(const f32x4 *)(from + i * 20 + k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (k + e < i) s[e & 1] = fmaf(-row[e], v[k + e], s[e & 1]);
+        }
+        v[i] = s[0] + s[1];
+    }
+    float *to = x + g * kDiag + l16;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) to[i * 20] = v[i];
+}
+
 template <typename T, int N, bool GRAD>
-__global__ __launch_bounds__(256) void k_delta_prep(PrepArgs args) {
+__global__ __launch_bounds__(64 * kPrepWaves, 2) void k_delta_prep(PrepArgs args, long long items) {
     constexpr int IN = Terms<T>::IN, OWN = Terms<T>::OWN, KS = (N + 31) / 32, NM = GRAD ? 2 : 1;
-    __shared__ __attribute__((aligned(16))) float ms[NM][C * kLd], xs[NM][C * kLd];
-    __shared__ double sums[C];
-    __shared__ float beta[C];
+    struct Wave {
+        // diagonal blocks of M, (L,) and of M's inverse; L's takes M's place
+        float d[NM + 1][4 * kDiag];
+        double sums[C];
+        float rows[C], cols[C], beta[C];
+    };
+    __shared__ __attribute__((aligned(16))) Wave waves[kPrepWaves];
     const PrepDir &pd = args.dir[blockIdx.y];
     const DeltaArgs &a = pd.a;
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, l16 = lane & 15;
-    const int h = blockIdx.x % a.H, grp = h / (a.H / a.G);
-    const long long slot = blockIdx.x / a.H;
+    Wave &w = waves[wave];
+    const long long item = (long long)blockIdx.x * kPrepWaves + wave;
+    if (item >= items) return;
+    const int h = (int)(item % a.H), grp = h / (a.H / a.G);
+    const long long slot = item / a.H;
     int chunk;
     const DeltaUnit at = delta_slot(a, slot, chunk);
     const int first = chunk * C, live = min(C, at.len - first);
@@ -68,70 +109,87 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs args) {
     const uint32_t row = (uint32_t)(a.G * N * sizeof(T)), off = (uint32_t)(grp * N * sizeof(T));
     const ChunkRows kr(a.k, at, a.reverse, first, live, row, off, N * sizeof(T));
     const ChunkRows qr(a.q, at, a.reverse, first, live, row, off, N * sizeof(T));
-    // all of K and this wave's 16 rows of Q, k in the rows' order
-    constexpr int V = 16 / sizeof(T), kRegs = 8 / V;
-    u32x4 kv[4][KS][kRegs], qv[KS][kRegs];
+    auto operand = [&](const ChunkRows &r, int tile, int s) {
+        constexpr int V = 16 / sizeof(T);
+        const uint32_t from = r.offset(16 * tile + l16);
+        const int n = 32 * s + 8 * g;
+        const uint32_t col = n < N ? (uint32_t)(n * sizeof(T)) : kFar;
+        if constexpr (IN == 1)
+            return Operand<1>{buf16(r.rsrc, from + col)};
+        else
+            return split8<3>(__builtin_bit_cast(f32x4, buf16(r.rsrc, from + col)),
+                             __builtin_bit_cast(f32x4, buf16(r.rsrc, from + col + 4 * V)));
+    };
+    const size_t gate = (size_t)delta_token(at, a.reverse, first + min(lane, live - 1)) * a.H + h;
+    const float glog = lane < live ? a.g[gate] : 0.f, gbeta = lane < live ? a.beta[gate] : 0.f;
+    // kk: rows i = 4 g + r, column j = l16 of tile (i, j); kt: its transpose; qk: FWD
+    // rows j, column i, GRAD rows i, column j
+    f32x4 kk[10], kt[GRAD ? 10 : 1], qk[10];
 #pragma unroll
-    for (int s = 0; s < KS; ++s)
+    for (int l = 0; l < 10; ++l) kk[l] = qk[l] = kt[GRAD ? l : 0] = zero4();
 #pragma unroll
-        for (int e = 0; e < kRegs; ++e) {
-            const int n = 32 * s + 8 * g + V * e;
-            const uint32_t col = n < N ? n * sizeof(T) : kFar;
-            qv[s][e] = buf16(qr.rsrc, qr.offset(16 * wave + l16) + col);
+    for (int s = 0; s < KS; ++s) {
+        Operand<IN> k[4], q[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) kv[c][s][e] = buf16(kr.rsrc, kr.offset(16 * c + l16) + col);
+        for (int t = 0; t < 4; ++t) {
+            k[t] = operand(kr, t, s);
+            q[t] = operand(qr, t, s);
         }
-    if (wave == 0) {
-        const size_t i = (size_t)delta_token(at, a.reverse, first + min(lane, live - 1)) * a.H + h;
-        const double sum = decay_sums(lane < live ? a.g[i] : 0.f, lane);
-        const float b = lane < live ? a.beta[i] : 0.f;
-        sums[lane] = sum;
-        beta[lane] = b;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j <= i; ++j) {
+                const int l = lower(i, j);
+                kk[l] = mm(k[i], k[j], kk[l]);
+                if (GRAD && i != j) kt[GRAD ? l : 0] = mm(k[j], k[i], kt[GRAD ? l : 0]);
+                qk[l] = GRAD ? mm(q[i], k[j], qk[l]) : mm(k[j], q[i], qk[l]);
+            }
+    }
+    {
+        const double sum = decay_sums(glog, lane);
+        const double before = __shfl(sum, max((lane & 48) - 1, 0)), end = __shfl(sum, lane | 15);
+        w.sums[lane] = sum;
+        w.rows[lane] = expf((float)(lane < 16 ? sum : sum - before));
+        w.cols[lane] = expf((float)(end - sum));
+        w.beta[lane] = gbeta;
         float *to = pd.gates + ((size_t)slot * a.H + h) * kGates;
         to[lane] = expf((float)sum);
         to[C + lane] = expf((float)(__shfl(sum, 63) - sum));
-        to[2 * C + lane] = b;
+        to[2 * C + lane] = gbeta;
     }
-    auto operand = [&](const u32x4 *r) {
-        if constexpr (IN == 1) return Operand<1>{r[0]};
-        else return split8<3>(__builtin_bit_cast(f32x4, r[0]), __builtin_bit_cast(f32x4, r[1]));
-    };
-    // column c of the wave's rows of K K^T; of the other triangle the tile that is
-    // an image's lane as it comes (rows j for q_i k_j, rows i for its transpose)
-    f32x4 kk[4], qk[4];
+    wave_sync();
 #pragma unroll
-    for (int c = 0; c < 4; ++c) kk[c] = qk[c] = zero4();
+    for (int i = 0; i < 4; ++i) {
+        const float ri = w.rows[16 * i + l16], bi = w.beta[16 * i + l16];
+        const f32x4 r4 = *(const f32x4 *)&w.rows[16 * i + 4 * g], b4 = *(const f32x4 *)&w.beta[16 * i + 4 * g];
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-        const Operand<IN> q = operand(qv[s]);
-        Operand<IN> k[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) k[c] = operand(kv[c][s]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-                if (c <= w && w == wave) {
-                    kk[c] = mm(k[w], k[c], kk[c]);
-                    qk[c] = GRAD ? mm(q, k[c], qk[c]) : mm(k[c], q, qk[c]);
-                }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if (c > wave) break;
+        for (int j = 0; j < i; ++j) {
+            const int l = lower(i, j);
+            // between the tiles: from column tile's end to row tile's start
+            const float t = i - j > 1 ? expf((float)(w.sums[16 * i - 1] - w.sums[16 * j + 15])) : 1.f;
+            const float cj = t * w.cols[16 * j + l16], bj = w.beta[16 * j + l16];
+            const f32x4 c4 = t * *(const f32x4 *)&w.cols[16 * j + 4 * g], d4 = *(const f32x4 *)&w.beta[16 * j + 4 * g];
+            kk[l] *= r4 * (cj * bj);                              // M
+            if constexpr (GRAD) kt[l] *= c4 * (ri * bi);          // L^T
+            qk[l] *= GRAD ? r4 * (cj * a.scale) : c4 * d4 * (ri * a.scale);
+        }
+        // diagonal tile: the rows' sums beside this lane's column's
+        const int l = lower(i, i);
+        const double own = w.sums[16 * i + l16];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            {
-                const int i = 16 * wave + 4 * g + r, j = 16 * c + l16;
-                const float w = j < i ? expf((float)(sums[i] - sums[j])) * kk[c][r] : 0.f;
-                ms[0][i * kLd + j] = w * beta[j];
-                if constexpr (GRAD) ms[1][i * kLd + j] = w * beta[i];
+            const int n = 4 * g + r;
+            const double other = w.sums[16 * i + n];
+            const float up = n >= l16 ? expf((float)(other - own)) : 0.f;   // rows i = n
+            const float m = n > l16 ? up * kk[l][r] : 0.f;
+            w.d[0][i * kDiag + n * 20 + l16] = m * bi;
+            if constexpr (GRAD) {
+                w.d[1][i * kDiag + n * 20 + l16] = m * b4[r];
+                qk[l][r] *= a.scale * up;
+            } else {
+                const float dn = n <= l16 ? expf((float)(own - other)) : 0.f;   // rows j = n
+                qk[l][r] *= a.scale * dn * b4[r];
             }
-            // FWD: lane's row i = l16, columns j; GRAD: rows i, lane's column j
-            const int i = 16 * wave + (GRAD ? 4 * g + r : l16), j = 16 * c + (GRAD ? l16 : 4 * g + r);
-            const float w = j <= i && i < live ? a.scale * expf((float)(sums[i] - sums[j])) : 0.f;
-            qk[c][r] *= GRAD ? w : w * beta[j];
         }
     }
     uint8_t *img = pd.images + ((size_t)slot * a.H + h) * images(GRAD) * kImage<OWN>;
@@ -140,93 +198,83 @@ __global__ __launch_bounds__(256) void k_delta_prep(PrepArgs args) {
 #pragma unroll
         for (int t = 0; t < OWN; ++t) *(u32x4 *)(image + (b * OWN + t) * 1024 + 16 * lane) = o.t[t];
     };
-    if constexpr (!GRAD) {
-        // tiles above the diagonal are zeros as they were
-        put(img + kImage<OWN>, wave < 2 ? wave : 2 * wave - 2, qk[0], qk[1]);
-        if (wave >= 2) put(img + kImage<OWN>, 2 * wave - 1, qk[2], qk[3]);
-    } else {
-        // the transposed triangle's rows 16 c .. take k from 16 wave ..: half a
-        // block is one wave's, four slots of eight
-        uint8_t *to = img + 2 * kImage<OWN>;
+    // tiles (i, j) whose lanes are rows i with k = j; or rows j with k = i
+    auto put_lower = [&](uint8_t *image, const f32x4 *v) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t lo[OWN], hi[OWN];
-            split2<OWN>(qk[c][0], qk[c][1], lo);
-            split2<OWN>(qk[c][2], qk[c][3], hi);
-            if (c < 2 || wave >= 2) {
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int t = 0; t < OWN; ++t)
-                    *(u32x2 *)(to + (upper_block(c, wave >> 1) * OWN + t) * 1024 + 16 * lane + 8 * (wave & 1)) =
-                        u32x2{lo[t], hi[t]};
-            }
-        }
+            for (int s = 0; s < (i < 2 ? 1 : 2); ++s)
+                put(image, lower_block(i, s), v[lower(i, 2 * s)], 2 * s + 1 <= i ? v[lower(i, min(2 * s + 1, i))] : zero4());
+    };
+    auto put_upper = [&](uint8_t *image, const f32x4 *v) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int s = j < 2 ? 0 : 1; s < 2; ++s)
+                put(image, upper_block(j, s), 2 * s >= j ? v[lower(max(2 * s, j), j)] : zero4(), v[lower(2 * s + 1, j)]);
+    };
+    if constexpr (GRAD) put_upper(img + 2 * kImage<OWN>, qk);
+    else put_lower(img + kImage<OWN>, qk);
+    wave_sync();
+    invert_diagonal(w.d[0], w.d[NM], g, l16);
+    wave_sync();
+    if constexpr (GRAD) {
+        invert_diagonal(w.d[1], w.d[0], g, l16);
+        wave_sync();
     }
-    __syncthreads();
-    {   // this wave's diagonal block: lane's column l16 of the inverse
-        const int which = GRAD ? g >> 1 : 0, o = 16 * wave;
-        const float *m = ms[which] + o * kLd + o;
-        f32x4 rows[16][4];
+    // a diagonal block as a result of its own lanes (rows 4 g + r, column l16) and transposed
+    auto plain = [&](int which, int i) {
+        f32x4 v;
 #pragma unroll
-        for (int i = 1; i < 16; ++i)
+        for (int r = 0; r < 4; ++r) v[r] = w.d[which][i * kDiag + (4 * g + r) * 20 + l16];
+        return v;
+    };
+    auto turned = [&](int which, int i) { return *(const f32x4 *)&w.d[which][i * kDiag + l16 * 20 + 4 * g]; };
+    {
+        // X = (I + M)^-1 by its transpose: X^T_ji = -X^T_jj sum_{j < m <= i} M^T_jm X^T_mi
+        f32x4 x[10];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (4 * k < i) rows[i][k] = *(const f32x4 *)(m + i * kLd + 4 * k);
-        float x[16];
+        for (int i = 0; i < 4; ++i) x[lower(i, i)] = turned(NM, i);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float v[4] = {i == l16 ? 1.f : 0.f, 0.f, 0.f, 0.f};
+        for (int d = 1; d < 4; ++d)
 #pragma unroll
-            for (int k = 0; k < i; ++k) v[k & 3] = fmaf(-rows[i][k >> 2][k & 3], x[k], v[k & 3]);
-            x[i] = (v[0] + v[1]) + (v[2] + v[3]);
-        }
-        if (GRAD ? (g & 1) == 0 : g == 0) {
+            for (int j = 0; j < 4 - d; ++j) {
+                const int i = j + d;
+                f32x4 t = zero4();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) xs[which][(o + i) * kLd + o + l16] = x[i];
-        }
-    }
-    __syncthreads();
-    // X_ij = -X_ii sum_m M_im X_mj, a subdiagonal of blocks at a time
+                for (int m = j + 1; m <= i; ++m)
 #pragma unroll
-    for (int d = 1; d < 4; ++d) {
-        for (int job = wave; job < NM * (4 - d); job += 4) {
-            const int which = job / (4 - d), j = job % (4 - d), i = j + d;
-            const float *m = ms[which];
-            float *x = xs[which];
-            const f32x4 own = *(const f32x4 *)(x + (16 * i + l16) * kLd + 16 * i + 4 * g);
-            f32x4 t[2] = {zero4(), zero4()};
+                    for (int r = 0; r < 4; ++r) t = mfma4(kk[lower(m, j)][r], x[lower(i, m)][r], t);
+                const f32x4 own = plain(NM, j);
+                f32x4 v = zero4();
 #pragma unroll
-            for (int k = 0; k < 16 * d; k += 4) {
-                const int n = 16 * j + k + g;
-                t[(k >> 2) & 1] = mfma4(m[(16 * i + l16) * kLd + n], x[n * kLd + 16 * j + l16], t[(k >> 2) & 1]);
+                for (int r = 0; r < 4; ++r) v = mfma4(own[r], t[r], v);
+                x[lower(i, j)] = -v;
             }
-            t[0] += t[1];
-            f32x4 v = zero4();
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v = mfma4(own[r], t[0][r], v);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[(16 * i + 4 * g + r) * kLd + 16 * j + l16] = -v[r];
-        }
-        __syncthreads();
+        put_lower(img, x);
     }
-    for (int job = wave; job < NM * kBlocks; job += 4) {
-        const int which = job / kBlocks, b = job % kBlocks;
-        const bool upper = which > 0;   // transposed
-        const int rt = upper ? (b < 4 ? b >> 1 : b - 2) : (b < 2 ? b : (b + 2) >> 1);
-        const int s = upper ? (b < 4 ? b & 1 : 1) : (b < 2 ? 0 : b & 1);
-        const float *src = xs[which];
-        f32x4 v[2];
+    if constexpr (GRAD) {
+        // Y = (I + L)^-1: Y_ij = -Y_ii sum_{j <= m < i} L_im Y_mj
+        f32x4 y[10];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int ct = 2 * s + e, col = 16 * ct + 4 * g, at16 = 16 * rt + l16;
-            v[e] = zero4();
-            if (!upper) {
-                if (ct <= rt) v[e] = *(const f32x4 *)(src + at16 * kLd + col);
-            } else if (ct >= rt) {
+        for (int i = 0; i < 4; ++i) y[lower(i, i)] = plain(0, i);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[e][r] = src[(col + r) * kLd + at16];
+        for (int d = 1; d < 4; ++d)
+#pragma unroll
+            for (int j = 0; j < 4 - d; ++j) {
+                const int i = j + d;
+                f32x4 t = zero4();
+#pragma unroll
+                for (int m = j; m < i; ++m)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) t = mfma4(kt[lower(i, m)][r], y[lower(m, j)][r], t);
+                const f32x4 own = turned(0, i);
+                f32x4 v = zero4();
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v = mfma4(own[r], t[r], v);
+                y[lower(i, j)] = -v;
             }
-        }
-        put(img + which * kImage<OWN>, b, v[0], v[1]);
+        put_upper(img + kImage<OWN>, y);
     }
 }
 
@@ -239,8 +287,8 @@ struct WalkArgs {
     int blocks;        // workgroups of a head
 };
 
-template <typename T, int N, int NC, int MODE>
-__global__ __launch_bounds__(256, 1) void k_delta_walk(WalkArgs args) {
+template <typename T, int N, int MODE>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(WalkArgs args) {
     using X = typename std::conditional<MODE == BACK, float, T>::type;   // the third input's type
     constexpr int IN = Terms<T>::IN, OWN = Terms<T>::OWN;
     constexpr bool GRAD = MODE != FWD;
@@ -250,13 +298,12 @@ __global__ __launch_bounds__(256, 1) void k_delta_walk(WalkArgs args) {
     constexpr bool kQ = MODE != KEEP;                   // Q read, and a second image
     constexpr int kImages = kQ ? 2 : 1, kImg = kImage<OWN>;
     constexpr int kBuf = kRows * (kQ ? 2 : 1) + kImg * kImages + kGates * 4;
-    constexpr int kBufs = 2 * kBuf <= 160 * 1024 ? 2 : 1;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kBufs][kBuf];
+    __shared__ __attribute__((aligned(16))) uint8_t buf[kBuf];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l16 = lane & 15;
     const int block = blockIdx.x % args.blocks, h = blockIdx.x / args.blocks % args.dir[0].a.H;
     const int u = blockIdx.x / args.blocks / args.dir[0].a.H;
-    const int p0 = (block * 4 + wave) * 16 * NC;
+    const int p0 = (block * 4 + wave) * 16;
     // the wave has columns, those of the walks' own arrays past the head's width among them
     const bool works = p0 < (GRAD ? padded(args.dir[0].a.P) : args.dir[0].a.P);
     for (int di = args.ndir - 1; di >= 0; --di) {
@@ -265,31 +312,24 @@ __global__ __launch_bounds__(256, 1) void k_delta_walk(WalkArgs args) {
         const int grp = h / (a.H / a.G), PP = padded(a.P);
         const DeltaUnit at = delta_unit(a, u);
         const int chunks = (at.len + C - 1) / C;
-        // a lane's columns, in the caller's arrays and in the walks' own
-        uint32_t pc[NC], pw[NC];
+        // the lane's column, in the caller's arrays and in the walks' own
+        const int p = p0 + l16;
+        const bool own = p < a.P;
+        const uint32_t pw = p < PP ? 4 * p : kFar;
+        f32x4 S[NT];
+        const size_t state = (((size_t)u * a.H + h) * a.P + p) * N + 4 * g;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int p = p0 + 16 * c + l16;
-            pc[c] = p < a.P ? p : kFar;
-            pw[c] = p < PP ? 4 * p : kFar;
+        for (int t = 0; t < NT; ++t) {
+            S[t] = zero4();
+            if (a.init && own) S[t] = *(const f32x4 *)(a.init + state + 16 * t);
         }
-        f32x4 S[NT][NC];
-        const size_t state = ((size_t)u * a.H + h) * a.P * N + 4 * g;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                S[t][c] = zero4();
-                if (a.init && pc[c] != kFar) S[t][c] = *(const f32x4 *)(a.init + state + (size_t)pc[c] * N + 16 * t);
-            }
-        // the next chunk on its way: rows of K and Q, gates, the third input (the
-        // images go straight to LDS)
-        constexpr int V = 16 / sizeof(T), kVecs = C * NP / V / 256;
-        u32x4 nk[kVecs], nq[kQ ? kVecs : 1];
+        // the next chunk on its way: rows of K and Q, images, gates, the third input
+        constexpr int V = 16 / sizeof(T), kVecs = C * NP / V / 256, kVi = (kImages * kImg / 16 + 255) / 256;
+        u32x4 nk[kVecs], nq[kQ ? kVecs : 1], ni[kVi];
         float ngate = 0.f;
-        X nx[4][NC][4];
+        X nx[4][4];
         auto order = [&](int i) { return MODE == BACK ? chunks - 1 - i : i; };
-        auto fetch = [&](int chunk, uint8_t *to) {
+        auto fetch = [&](int chunk) {
             const int first = chunk * C, live = min(C, at.len - first);
             const size_t sh = (size_t)(at.slot + chunk) * a.H + h;
             const uint32_t row = (uint32_t)(a.G * N * sizeof(T)), off = (uint32_t)(grp * N * sizeof(T));
@@ -302,67 +342,60 @@ __global__ __launch_bounds__(256, 1) void k_delta_walk(WalkArgs args) {
                 nk[i] = buf16(kr.rsrc, o);
                 if (kQ) nq[i] = buf16(qr.rsrc, o);
             }
-            const uint8_t *img = pd.images + sh * images(GRAD) * kImg + (MODE == BACK ? kImg : 0) + 16 * lane;
-            for (int i = wave; i < kImages * kImg / 1024; i += 4)
-                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(img + i * 1024),
-                                                 (__attribute__((address_space(3))) void *)(to + (kQ ? 2 : 1) * kRows + i * 1024),
-                                                 16, 0, 0);
+            const __amdgpu_buffer_rsrc_t ir = __builtin_amdgcn_make_buffer_rsrc(
+                pd.images + sh * images(GRAD) * kImg + (MODE == BACK ? kImg : 0), 0, kImages * kImg, 0x00027000);
+#pragma unroll
+            for (int i = 0; i < kVi; ++i) ni[i] = buf16(ir, 16 * tid + 4096 * i);
             if (tid < kGates) ngate = pd.gates[sh * kGates + tid];
-            if (!works) return;
             const uint32_t xrow = (uint32_t)(a.H * a.P * sizeof(X));
             const ChunkRows xr(a.v, at, a.reverse, first, live, xrow, (uint32_t)(h * a.P * sizeof(X)), a.P * sizeof(X));
+            const uint32_t to = xr.offset(4 * g) + (own ? (uint32_t)(p * sizeof(X)) : kFar);
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const uint32_t col = xr.offset(4 * g) + (pc[c] == kFar ? kFar : pc[c] * (uint32_t)sizeof(X));
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) nx[t][c][r] = buf_value(xr.rsrc, col + (16 * t + r) * xr.step, X());
-            }
+                for (int r = 0; r < 4; ++r) nx[t][r] = buf_value(xr.rsrc, to + (16 * t + r) * xr.step, X());
         };
-        auto stash = [&](uint8_t *to) {
+        auto stash = [&]() {
 #pragma unroll
             for (int w = 0; w < (kQ ? 2 : 1); ++w)
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
                     const int e = tid + 256 * i, row = e / (NP / V), col = e % (NP / V) * V;
-                    uint16_t *at16 = (uint16_t *)(to + w * kRows) + row * RS + col;
+                    uint16_t *to = (uint16_t *)(buf + w * kRows) + row * RS + col;
                     const u32x4 r = w ? nq[i] : nk[i];
                     if constexpr (IN == 1) {
-                        *(u32x4 *)at16 = r;
+                        *(u32x4 *)to = r;
                     } else {
                         uint32_t lo[IN], hi[IN];
                         split2<IN>(__uint_as_float(r[0]), __uint_as_float(r[1]), lo);
                         split2<IN>(__uint_as_float(r[2]), __uint_as_float(r[3]), hi);
 #pragma unroll
-                        for (int t = 0; t < IN; ++t) *(u32x2 *)(at16 + t * C * RS) = u32x2{lo[t], hi[t]};
+                        for (int t = 0; t < IN; ++t) *(u32x2 *)(to + t * C * RS) = u32x2{lo[t], hi[t]};
                     }
                 }
-            if (tid < kGates) *(float *)(to + (kQ ? 2 : 1) * kRows + kImages * kImg + 4 * tid) = ngate;
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the images are in LDS
+#pragma unroll
+            for (int i = 0; i < kVi; ++i)
+                if (kImages * kImg % 4096 == 0 || 16 * tid + 4096 * i < kImages * kImg)
+                    *(u32x4 *)(buf + (kQ ? 2 : 1) * kRows + 16 * tid + 4096 * i) = ni[i];
+            if (tid < kGates) *(float *)(buf + (kQ ? 2 : 1) * kRows + kImages * kImg + 4 * tid) = ngate;
         };
         if (di != args.ndir - 1) __syncthreads();   // the direction before has read its last chunk
         if (chunks > 0) {
-            fetch(order(0), lds[0]);
-            stash(lds[0]);
+            fetch(order(0));
+            stash();
         }
         for (int step = 0; step < chunks; ++step) {
             const int chunk = order(step), first = chunk * C, live = min(C, at.len - first);
-            const uint8_t *buf = lds[kBufs == 2 ? step & 1 : 0];
-            uint8_t *nextbuf = lds[kBufs == 2 ? (step + 1) & 1 : 0];
-            const bool more = step + 1 < chunks;
             __syncthreads();
-            f32x4 x[4][NC];
+            f32x4 x[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int c = 0; c < NC; ++c)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        if constexpr (sizeof(X) == 2) x[t][c][r] = bf2f(nx[t][c][r]);
-                        else x[t][c][r] = nx[t][c][r];
-                    }
-            if (kBufs == 2 && more) fetch(order(step + 1), nextbuf);
+                for (int r = 0; r < 4; ++r) {
+                    if constexpr (sizeof(X) == 2) x[t][r] = bf2f(nx[t][r]);
+                    else x[t][r] = nx[t][r];
+                }
+            if (step + 1 < chunks) fetch(order(step + 1));
             const uint16_t *kl = (const uint16_t *)buf, *ql = (const uint16_t *)(buf + kRows);
             const uint8_t *one = buf + (kQ ? 2 : 1) * kRows, *two = one + kImg;
             const float *gate = (const float *)(one + kImages * kImg);
@@ -398,183 +431,116 @@ __global__ __launch_bounds__(256, 1) void k_delta_walk(WalkArgs args) {
                 return o;
             };
             auto gates = [&](int which, int rt) { return *(const f32x4 *)(gate + which * C + 16 * rt + 4 * g); };
-            f32x4 out[4][NC];
+            f32x4 out[4];
             if (works) {
                 if constexpr (GRAD) {
                     const __amdgpu_buffer_rsrc_t sr = __builtin_amdgcn_make_buffer_rsrc(
                         a.states + ((size_t)(at.slot + chunk) * a.H + h) * N * PP, 0, N * PP * 4, 0x00027000);
+                    const uint32_t to = pw + 4 * g * PP * 4;
 #pragma unroll
-                    for (int c = 0; c < NC; ++c) {
-                        const uint32_t o = pw[c] + 4 * g * PP * 4;
+                    for (int t = 0; t < NT; ++t)
 #pragma unroll
-                        for (int t = 0; t < NT; ++t)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) buf_store(sr, o + (16 * t + r) * PP * 4, S[t][c][r]);
-                    }
+                        for (int r = 0; r < 4; ++r) buf_store(sr, to + (16 * t + r) * PP * 4, S[t][r]);
                 }
                 // K S and Q S
-                f32x4 ks[4][NC];
+                f32x4 ks[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) ks[t][c] = out[t][c] = zero4();
+                for (int t = 0; t < 4; ++t) ks[t] = out[t] = zero4();
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
-                    Operand<OWN> sb[NC];
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-                        sb[c] = split8<OWN>(S[2 * s][c], 2 * s + 1 < NT ? S[min(2 * s + 1, NT - 1)][c] : zero4());
+                    const Operand<OWN> sb = split8<OWN>(S[2 * s], 2 * s + 1 < NT ? S[min(2 * s + 1, NT - 1)] : zero4());
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
-                        const Operand<IN> k = rows(kl, t, s);
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) ks[t][c] = mm(k, sb[c], ks[t][c]);
-                        if constexpr (MODE == FWD) {
-                            const Operand<IN> q = rows(ql, t, s);
-#pragma unroll
-                            for (int c = 0; c < NC; ++c) out[t][c] = mm(q, sb[c], out[t][c]);
-                        }
+                        ks[t] = mm(rows(kl, t, s), sb, ks[t]);
+                        if constexpr (MODE == FWD) out[t] = mm(rows(ql, t, s), sb, out[t]);
                     }
                 }
-                Operand<OWN> b[2][NC], kb[2][NC];   // kb: what K^T multiplies
+                Operand<OWN> b[2], kb[2];   // kb: what K^T multiplies
                 if constexpr (MODE != BACK) {
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
+                    for (int t = 0; t < 4; ++t) x[t] -= gates(0, t) * ks[t];
 #pragma unroll
-                        for (int c = 0; c < NC; ++c)
-                            b[s][c] = split8<OWN>(x[2 * s][c] - gates(0, 2 * s) * ks[2 * s][c],
-                                                  x[2 * s + 1][c] - gates(0, 2 * s + 1) * ks[2 * s + 1][c]);
+                    for (int s = 0; s < 2; ++s) b[s] = split8<OWN>(x[2 * s], x[2 * s + 1]);
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
+                        ks[t] = zero4();
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) ks[t][c] = zero4();
-#pragma unroll
-                        for (int s = 0; s < (t < 2 ? 1 : 2); ++s) {
-                            const Operand<OWN> m = image(one, lower_block(t, s));
-#pragma unroll
-                            for (int c = 0; c < NC; ++c) ks[t][c] = mm(m, b[s][c], ks[t][c]);
-                        }
+                        for (int s = 0; s < (t < 2 ? 1 : 2); ++s) ks[t] = mm(image(one, lower_block(t, s)), b[s], ks[t]);
+                        x[t] = gates(1, t) * gates(2, t) * ks[t];
                     }
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
-#pragma unroll
-                        for (int c = 0; c < NC; ++c)
-                            kb[s][c] = split8<OWN>(gates(1, 2 * s) * gates(2, 2 * s) * ks[2 * s][c],
-                                                   gates(1, 2 * s + 1) * gates(2, 2 * s + 1) * ks[2 * s + 1][c]);
+                    for (int s = 0; s < 2; ++s) kb[s] = split8<OWN>(x[2 * s], x[2 * s + 1]);
                 } else {
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
+                    for (int s = 0; s < 2; ++s) b[s] = split8<OWN>(x[2 * s], x[2 * s + 1]);
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) b[s][c] = split8<OWN>(x[2 * s][c], x[2 * s + 1][c]);
+                    for (int t = 0; t < 4; ++t) {
+                        ks[t] *= gates(1, t);
+                        x[t] *= a.scale * gates(0, t);
+#pragma unroll
+                        for (int s = t < 2 ? 0 : 1; s < 2; ++s) ks[t] = mm(image(two, upper_block(t, s)), b[s], ks[t]);
+                    }
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) b[s] = split8<OWN>(ks[2 * s], ks[2 * s + 1]);
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) ks[t][c] *= gates(1, t);
-#pragma unroll
-                        for (int s = t < 2 ? 0 : 1; s < 2; ++s) {
-                            const Operand<OWN> m = image(two, upper_block(t, s));
-#pragma unroll
-                            for (int c = 0; c < NC; ++c) ks[t][c] = mm(m, b[s][c], ks[t][c]);
-                        }
+                        for (int s = t < 2 ? 0 : 1; s < 2; ++s) out[t] = mm(image(one, upper_block(t, s)), b[s], out[t]);
+                        ks[t] = -gates(0, t) * gates(2, t) * out[t];
                     }
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) b[s][c] = split8<OWN>(ks[2 * s][c], ks[2 * s + 1][c]);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int s = t < 2 ? 0 : 1; s < 2; ++s) {
-                            const Operand<OWN> m = image(one, upper_block(t, s));
-#pragma unroll
-                            for (int c = 0; c < NC; ++c) out[t][c] = mm(m, b[s][c], out[t][c]);
-                        }
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) {
-                            kb[s][c] = split8<OWN>(-gates(0, 2 * s) * gates(2, 2 * s) * out[2 * s][c],
-                                                   -gates(0, 2 * s + 1) * gates(2, 2 * s + 1) * out[2 * s + 1][c]);
-                            b[s][c] = split8<OWN>(a.scale * gates(0, 2 * s) * x[2 * s][c],
-                                                  a.scale * gates(0, 2 * s + 1) * x[2 * s + 1][c]);   // Q^T's
-                        }
+                    for (int s = 0; s < 2; ++s) {
+                        kb[s] = split8<OWN>(ks[2 * s], ks[2 * s + 1]);
+                        b[s] = split8<OWN>(x[2 * s], x[2 * s + 1]);   // Q^T's
+                    }
                 }
                 const float last = gate[C - 1];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) S[t][c] *= last;
+                    S[t] *= last;
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        const Operand<IN> k = cols(kl, t, s);
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) S[t][c] = mm(k, kb[s][c], S[t][c]);
-                        if constexpr (MODE == BACK) {
-                            const Operand<IN> q = cols(ql, t, s);
-#pragma unroll
-                            for (int c = 0; c < NC; ++c) S[t][c] = mm(q, b[s][c], S[t][c]);
-                        }
+                        S[t] = mm(cols(kl, t, s), kb[s], S[t]);
+                        if constexpr (MODE == BACK) S[t] = mm(cols(ql, t, s), b[s], S[t]);
                     }
                 }
                 if constexpr (MODE == FWD) {
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) b[s][c] = split8<OWN>(ks[2 * s][c], ks[2 * s + 1][c]);
+                    for (int s = 0; s < 2; ++s) b[s] = split8<OWN>(ks[2 * s], ks[2 * s + 1]);
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
+                        out[t] *= a.scale * gates(0, t);
 #pragma unroll
-                        for (int c = 0; c < NC; ++c) out[t][c] *= a.scale * gates(0, t);
-#pragma unroll
-                        for (int s = 0; s < (t < 2 ? 1 : 2); ++s) {
-                            const Operand<OWN> m = image(two, lower_block(t, s));
-#pragma unroll
-                            for (int c = 0; c < NC; ++c) out[t][c] = mm(m, b[s][c], out[t][c]);
-                        }
+                        for (int s = 0; s < (t < 2 ? 1 : 2); ++s) out[t] = mm(image(two, lower_block(t, s)), b[s], out[t]);
                     }
                 } else if constexpr (MODE == KEEP) {
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-#pragma unroll
-                        for (int c = 0; c < NC; ++c) out[t][c] = ks[t][c];
+                    for (int t = 0; t < 4; ++t) out[t] = ks[t];
                 }
             }
-            // what the next chunk brought goes to LDS before this one's results go
-            // out, so that nothing waits for stores
-            if (kBufs == 1) {
-                __syncthreads();
-                if (more) fetch(order(step + 1), nextbuf);
-            }
-            if (more) stash(nextbuf);
+            __syncthreads();
+            // the next chunk goes to LDS before this one's results go out, so that
+            // nothing waits for stores
+            if (step + 1 < chunks) stash();
             if (works) {
                 const int P = GRAD ? PP : a.P;
                 const ChunkRows yr(a.y, at, a.reverse, first, live, (uint32_t)(a.H * P * 4), (uint32_t)(h * P * 4), P * 4);
-                uint32_t o[NC];
-#pragma unroll
-                for (int c = 0; c < NC; ++c) o[c] = yr.offset(4 * g) + (GRAD ? pw[c] : pc[c] == kFar ? kFar : 4 * pc[c]);
+                const uint32_t to = yr.offset(4 * g) + (GRAD ? pw : own ? (uint32_t)(4 * p) : kFar);
                 if (MODE == FWD && a.add) {
-#pragma unroll
-                    for (int c = 0; c < NC; ++c)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                out[t][c][r] += buf_value(yr.rsrc, o[c] + (16 * t + r) * yr.step, 0.f);
-                }
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) buf_store(yr.rsrc, o[c] + (16 * t + r) * yr.step, out[t][c][r]);
+                        for (int r = 0; r < 4; ++r) out[t][r] += buf_value(yr.rsrc, to + (16 * t + r) * yr.step, 0.f);
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) buf_store(yr.rsrc, to + (16 * t + r) * yr.step, out[t][r]);
             }
         }
-        if (a.last) {
+        if (a.last && own) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    if (pc[c] != kFar) *(f32x4 *)(a.last + state + (size_t)pc[c] * N + 16 * t) = S[t][c];
+            for (int t = 0; t < NT; ++t) *(f32x4 *)(a.last + state + 16 * t) = S[t];
         }
     }
 }
@@ -586,9 +552,10 @@ struct Chunked {
         p.dir[0] = d[0];
         p.dir[1] = d[ndir - 1];
         const DeltaArgs &a = d[0].a;
-        const dim3 grid((unsigned)(delta_slots(a.units, a.L, a.cu != nullptr) * a.H), ndir);
-        if (grad) BM_LAUNCH("delta_prep", (k_delta_prep<T, N, true>), grid, dim3(256), 0, s, p);
-        else BM_LAUNCH("delta_prep", (k_delta_prep<T, N, false>), grid, dim3(256), 0, s, p);
+        const long long items = delta_slots(a.units, a.L, a.cu != nullptr) * a.H;
+        const dim3 grid((unsigned)((items + kPrepWaves - 1) / kPrepWaves), ndir), block(64 * kPrepWaves);
+        if (grad) BM_LAUNCH("delta_prep", (k_delta_prep<T, N, true>), grid, block, 0, s, p, items);
+        else BM_LAUNCH("delta_prep", (k_delta_prep<T, N, false>), grid, block, 0, s, p, items);
         return hipGetLastError();
     }
     template <int MODE>
@@ -599,17 +566,9 @@ struct Chunked {
         w.dir[1] = d[ndir - 1];
         w.ndir = ndir;
         const DeltaArgs &a = d[0].a;
-        const long long heads = (long long)a.units * a.H;
-        const int wide = (a.P + 127) / 128, narrow = (a.P + 63) / 64;
-        if constexpr (sizeof(T) == 2) {
-            if (a.P > 64 && heads * wide >= 256) {
-                w.blocks = wide;
-                BM_LAUNCH(names[MODE], (k_delta_walk<T, N, 2, MODE>), dim3((unsigned)(heads * wide)), dim3(256), 0, s, w);
-                return hipGetLastError();
-            }
-        }
-        w.blocks = narrow;
-        BM_LAUNCH(names[MODE], (k_delta_walk<T, N, 1, MODE>), dim3((unsigned)(heads * narrow)), dim3(256), 0, s, w);
+        w.blocks = (a.P + 63) / 64;
+        const dim3 grid((unsigned)((long long)a.units * a.H * w.blocks));
+        BM_LAUNCH(names[MODE], (k_delta_walk<T, N, MODE>), grid, dim3(256), 0, s, w);
         return hipGetLastError();
     }
 };
