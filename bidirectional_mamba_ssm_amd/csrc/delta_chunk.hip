@@ -36,8 +36,16 @@ namespace {
 
 constexpr int C = kDeltaChunk;
 enum { FWD, KEEP, BACK };
-// images of a chunk and head: FWD (I + M)^-1, A; for the gradient (I + M)^-1, (I + L)^-T, B^T
-constexpr int images(bool grad) { return grad ? 3 : 2; }
+// triangles of a chunk and head: FWD (I + M)^-1, A; for the gradient (I + M)^-1, (I + L)^-T, B^T
+constexpr int triangles(bool grad) { return grad ? 3 : 2; }
+
+// Workgroup ids go round the 8 XCDs: each takes a run of the work, so that what
+// neighbours share (a group's K and Q, a head's triangles) meets in one L2.
+__device__ __forceinline__ long long xcd_order(long long n) {
+    const long long per = (n + 7) / 8, w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    return (long long)(blockIdx.x >> 3) < per ? w : n;
+}
+inline long long xcd_grid(long long n) { return (n + 7) / 8 * 8; }
 
 __device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
@@ -45,7 +53,7 @@ __device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c) {
 
 struct PrepDir {
     DeltaArgs a;
-    uint8_t *images;   // [slot][H]
+    uint8_t *tri;      // [slot][H]
     float *gates;      // [slot][H][kGates]
 };
 struct PrepArgs {
@@ -60,7 +68,6 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 }
-__device__ __forceinline__ constexpr int lower(int i, int j) { return i * (i + 1) / 2 + j; }
 
 // the inverse of I + m for four strictly lower 16 x 16 blocks, a column a lane
 __device__ __forceinline__ void invert_diagonal(const float *m, float *x, int g, int l16) {
@@ -85,7 +92,7 @@ __device__ __forceinline__ void invert_diagonal(const float *m, float *x, int g,
 
 template <typename T, int N, bool GRAD>
 __global__ __launch_bounds__(64 * kPrepWaves, 2) void k_delta_prep(PrepArgs args, long long items) {
-    constexpr int IN = Terms<T>::IN, OWN = Terms<T>::OWN, KS = (N + 31) / 32, NM = GRAD ? 2 : 1;
+    constexpr int IN = Terms<T>::IN, KS = (N + 31) / 32, NM = GRAD ? 2 : 1;
     struct Wave {
         // diagonal blocks of M, (L,) and of M's inverse; L's takes M's place
         float d[NM + 1][4 * kDiag];
@@ -98,7 +105,7 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void k_delta_prep(PrepArgs args
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, l16 = lane & 15;
     Wave &w = waves[wave];
-    const long long item = (long long)blockIdx.x * kPrepWaves + wave;
+    const long long item = xcd_order((items + kPrepWaves - 1) / kPrepWaves) * kPrepWaves + wave;
     if (item >= items) return;
     const int h = (int)(item % a.H), grp = h / (a.H / a.G);
     const long long slot = item / a.H;
@@ -192,29 +199,12 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void k_delta_prep(PrepArgs args
             }
         }
     }
-    uint8_t *img = pd.images + ((size_t)slot * a.H + h) * images(GRAD) * kImage<OWN>;
-    auto put = [&](uint8_t *image, int b, f32x4 lo, f32x4 hi) {
-        const Operand<OWN> o = split8<OWN>(lo, hi);
+    uint8_t *tri = pd.tri + ((size_t)slot * a.H + h) * triangles(GRAD) * kTriangle + 16 * lane;
+    auto put = [&](int which, const f32x4 *v) {
 #pragma unroll
-        for (int t = 0; t < OWN; ++t) *(u32x4 *)(image + (b * OWN + t) * 1024 + 16 * lane) = o.t[t];
+        for (int l = 0; l < kTiles; ++l) *(f32x4 *)(tri + which * kTriangle + l * 1024) = v[l];
     };
-    // tiles (i, j) whose lanes are rows i with k = j; or rows j with k = i
-    auto put_lower = [&](uint8_t *image, const f32x4 *v) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int s = 0; s < (i < 2 ? 1 : 2); ++s)
-                put(image, lower_block(i, s), v[lower(i, 2 * s)], 2 * s + 1 <= i ? v[lower(i, min(2 * s + 1, i))] : zero4());
-    };
-    auto put_upper = [&](uint8_t *image, const f32x4 *v) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int s = j < 2 ? 0 : 1; s < 2; ++s)
-                put(image, upper_block(j, s), 2 * s >= j ? v[lower(max(2 * s, j), j)] : zero4(), v[lower(2 * s + 1, j)]);
-    };
-    if constexpr (GRAD) put_upper(img + 2 * kImage<OWN>, qk);
-    else put_lower(img + kImage<OWN>, qk);
+    put(GRAD ? 2 : 1, qk);
     wave_sync();
     invert_diagonal(w.d[0], w.d[NM], g, l16);
     wave_sync();
@@ -236,22 +226,28 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void k_delta_prep(PrepArgs args
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[lower(i, i)] = turned(NM, i);
 #pragma unroll
-        for (int d = 1; d < 4; ++d)
+        for (int d = 1; d < 4; ++d) {
+            f32x4 t[3], v[3];
 #pragma unroll
-            for (int j = 0; j < 4 - d; ++j) {
-                const int i = j + d;
-                f32x4 t = zero4();
+            for (int j = 0; j < 4 - d; ++j) t[j] = v[j] = zero4();
 #pragma unroll
-                for (int m = j + 1; m <= i; ++m)
+            for (int m = 1; m <= d; ++m)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) t = mfma4(kk[lower(m, j)][r], x[lower(i, m)][r], t);
-                const f32x4 own = plain(NM, j);
-                f32x4 v = zero4();
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v = mfma4(own[r], t[r], v);
-                x[lower(i, j)] = -v;
-            }
-        put_lower(img, x);
+                    for (int j = 0; j < 4 - d; ++j)
+                        t[j] = mfma4(kk[lower(j + m, j)][r], x[lower(j + d, j + m)][r], t[j]);
+            f32x4 own[3];
+#pragma unroll
+            for (int j = 0; j < 4 - d; ++j) own[j] = plain(NM, j);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < 4 - d; ++j) v[j] = mfma4(own[j][r], t[j][r], v[j]);
+#pragma unroll
+            for (int j = 0; j < 4 - d; ++j) x[lower(j + d, j)] = -v[j];
+        }
+        put(0, x);
     }
     if constexpr (GRAD) {
         // Y = (I + L)^-1: Y_ij = -Y_ii sum_{j <= m < i} L_im Y_mj
@@ -259,22 +255,28 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void k_delta_prep(PrepArgs args
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[lower(i, i)] = plain(0, i);
 #pragma unroll
-        for (int d = 1; d < 4; ++d)
+        for (int d = 1; d < 4; ++d) {
+            f32x4 t[3], v[3];
 #pragma unroll
-            for (int j = 0; j < 4 - d; ++j) {
-                const int i = j + d;
-                f32x4 t = zero4();
+            for (int j = 0; j < 4 - d; ++j) t[j] = v[j] = zero4();
 #pragma unroll
-                for (int m = j; m < i; ++m)
+            for (int m = 0; m < d; ++m)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) t = mfma4(kt[lower(i, m)][r], y[lower(m, j)][r], t);
-                const f32x4 own = turned(0, i);
-                f32x4 v = zero4();
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v = mfma4(own[r], t[r], v);
-                y[lower(i, j)] = -v;
-            }
-        put_upper(img + kImage<OWN>, y);
+                    for (int j = 0; j < 4 - d; ++j)
+                        t[j] = mfma4(kt[lower(j + d, j + m)][r], y[lower(j + m, j)][r], t[j]);
+            f32x4 own[3];
+#pragma unroll
+            for (int j = 0; j < 4 - d; ++j) own[j] = turned(0, j + d);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < 4 - d; ++j) v[j] = mfma4(own[j][r], t[j][r], v[j]);
+#pragma unroll
+            for (int j = 0; j < 4 - d; ++j) y[lower(j + d, j)] = -v[j];
+        }
+        put(1, y);
     }
 }
 
@@ -301,11 +303,21 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
     __shared__ __attribute__((aligned(16))) uint8_t buf[kBuf];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l16 = lane & 15;
-    const int block = blockIdx.x % args.blocks, h = blockIdx.x / args.blocks % args.dir[0].a.H;
-    const int u = blockIdx.x / args.blocks / args.dir[0].a.H;
+    const long long work = (long long)args.dir[0].a.units * args.dir[0].a.H * args.blocks, mine = xcd_order(work);
+    if (mine >= work) return;
+    const int block = (int)(mine % args.blocks), h = (int)(mine / args.blocks % args.dir[0].a.H);
+    const int u = (int)(mine / args.blocks / args.dir[0].a.H);
     const int p0 = (block * 4 + wave) * 16;
     // the wave has columns, those of the walks' own arrays past the head's width among them
     const bool works = p0 < (GRAD ? padded(args.dir[0].a.P) : args.dir[0].a.P);
+    // the halves of blocks that lie beyond the diagonal stay zeros
+    for (int i = tid; i < kImages * 2 * OWN * 64; i += 256) {
+        const int which = i / (2 * OWN * 64), e = i / 64 % (2 * OWN), term = e % OWN, second = e / OWN;
+        const int half = MODE == BACK ? 2 * (second ? upper_block(3, 1) : upper_block(1, 0))
+                                      : 2 * (second ? lower_block(2, 1) : lower_block(0, 0)) + 1;
+        *(u32x2 *)(buf + (kQ ? 2 : 1) * kRows + which * kImg + ((half >> 1) * OWN + term) * 1024 + 16 * lane +
+                   8 * (half & 1)) = u32x2{0u, 0u};
+    }
     for (int di = args.ndir - 1; di >= 0; --di) {
         const PrepDir &pd = args.dir[di];
         const DeltaArgs &a = pd.a;
@@ -324,7 +336,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
             if (a.init && own) S[t] = *(const f32x4 *)(a.init + state + 16 * t);
         }
         // the next chunk on its way: rows of K and Q, images, gates, the third input
-        constexpr int V = 16 / sizeof(T), kVecs = C * NP / V / 256, kVi = (kImages * kImg / 16 + 255) / 256;
+        constexpr int V = 16 / sizeof(T), kVecs = C * NP / V / 256, kVi = (kImages * kTriangle / 16 + 255) / 256;
         u32x4 nk[kVecs], nq[kQ ? kVecs : 1], ni[kVi];
         float ngate = 0.f;
         X nx[4][4];
@@ -343,7 +355,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
                 if (kQ) nq[i] = buf16(qr.rsrc, o);
             }
             const __amdgpu_buffer_rsrc_t ir = __builtin_amdgcn_make_buffer_rsrc(
-                pd.images + sh * images(GRAD) * kImg + (MODE == BACK ? kImg : 0), 0, kImages * kImg, 0x00027000);
+                pd.tri + (sh * triangles(GRAD) + (MODE == BACK ? 1 : 0)) * kTriangle, 0, kImages * kTriangle, 0x00027000);
 #pragma unroll
             for (int i = 0; i < kVi; ++i) ni[i] = buf16(ir, 16 * tid + 4096 * i);
             if (tid < kGates) ngate = pd.gates[sh * kGates + tid];
@@ -374,9 +386,18 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
                     }
                 }
 #pragma unroll
-            for (int i = 0; i < kVi; ++i)
-                if (kImages * kImg % 4096 == 0 || 16 * tid + 4096 * i < kImages * kImg)
-                    *(u32x4 *)(buf + (kQ ? 2 : 1) * kRows + 16 * tid + 4096 * i) = ni[i];
+            for (int i = 0; i < kVi; ++i) {
+                const int tile = wave + 4 * i, which = tile / kTiles, l = tile % kTiles;
+                if (kImages * kTiles % 4 && tile >= kImages * kTiles) break;
+                const int half = MODE == BACK ? upper_half(l) : lower_half(l);
+                uint8_t *to = buf + (kQ ? 2 : 1) * kRows + which * kImg + (half >> 1) * OWN * 1024 + 16 * lane + 8 * (half & 1);
+                const f32x4 v = __builtin_bit_cast(f32x4, ni[i]);
+                uint32_t lo[OWN], hi[OWN];
+                split2<OWN>(v[0], v[1], lo);
+                split2<OWN>(v[2], v[3], hi);
+#pragma unroll
+                for (int t = 0; t < OWN; ++t) *(u32x2 *)(to + t * 1024) = u32x2{lo[t], hi[t]};
+            }
             if (tid < kGates) *(float *)(buf + (kQ ? 2 : 1) * kRows + kImages * kImg + 4 * tid) = ngate;
         };
         if (di != args.ndir - 1) __syncthreads();   // the direction before has read its last chunk
@@ -430,6 +451,27 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
                 for (int t = 0; t < OWN; ++t) o.t[t] = *(const u32x4 *)(m + (b * OWN + t) * 1024 + 16 * lane);
                 return o;
             };
+            // c += the triangle times what b holds, two tiles at a time
+            auto times_lower = [&](const uint8_t *m, const Operand<OWN> *b, f32x4 *c) {
+                {
+                    const Operand<OWN> i[2] = {image(m, lower_block(0, 0)), image(m, lower_block(1, 0))};
+                    mm_tiles(i, b[0], c);
+                }
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const Operand<OWN> i[2] = {image(m, lower_block(2, s)), image(m, lower_block(3, s))};
+                    mm_tiles(i, b[s], c + 2);
+                }
+            };
+            auto times_upper = [&](const uint8_t *m, const Operand<OWN> *b, f32x4 *c) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const Operand<OWN> i[2] = {image(m, upper_block(0, s)), image(m, upper_block(1, s))};
+                    mm_tiles(i, b[s], c);
+                }
+                const Operand<OWN> i[2] = {image(m, upper_block(2, 1)), image(m, upper_block(3, 1))};
+                mm_tiles(i, b[1], c + 2);
+            };
             auto gates = [&](int which, int rt) { return *(const f32x4 *)(gate + which * C + 16 * rt + 4 * g); };
             f32x4 out[4];
             if (works) {
@@ -449,10 +491,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
                     const Operand<OWN> sb = split8<OWN>(S[2 * s], 2 * s + 1 < NT ? S[min(2 * s + 1, NT - 1)] : zero4());
+                    Operand<IN> r[4];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        ks[t] = mm(rows(kl, t, s), sb, ks[t]);
-                        if constexpr (MODE == FWD) out[t] = mm(rows(ql, t, s), sb, out[t]);
+                    for (int t = 0; t < 4; ++t) r[t] = rows(kl, t, s);
+                    mm_tiles(r, sb, ks);
+                    if constexpr (MODE == FWD) {
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) r[t] = rows(ql, t, s);
+                        mm_tiles(r, sb, out);
                     }
                 }
                 Operand<OWN> b[2], kb[2];   // kb: what K^T multiplies
@@ -462,12 +508,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
 #pragma unroll
                     for (int s = 0; s < 2; ++s) b[s] = split8<OWN>(x[2 * s], x[2 * s + 1]);
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        ks[t] = zero4();
+                    for (int t = 0; t < 4; ++t) ks[t] = zero4();
+                    times_lower(one, b, ks);
 #pragma unroll
-                        for (int s = 0; s < (t < 2 ? 1 : 2); ++s) ks[t] = mm(image(one, lower_block(t, s)), b[s], ks[t]);
-                        x[t] = gates(1, t) * gates(2, t) * ks[t];
-                    }
+                    for (int t = 0; t < 4; ++t) x[t] = gates(1, t) * gates(2, t) * ks[t];
 #pragma unroll
                     for (int s = 0; s < 2; ++s) kb[s] = split8<OWN>(x[2 * s], x[2 * s + 1]);
                 } else {
@@ -477,17 +521,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
                     for (int t = 0; t < 4; ++t) {
                         ks[t] *= gates(1, t);
                         x[t] *= a.scale * gates(0, t);
-#pragma unroll
-                        for (int s = t < 2 ? 0 : 1; s < 2; ++s) ks[t] = mm(image(two, upper_block(t, s)), b[s], ks[t]);
                     }
+                    times_upper(two, b, ks);
 #pragma unroll
                     for (int s = 0; s < 2; ++s) b[s] = split8<OWN>(ks[2 * s], ks[2 * s + 1]);
+                    times_upper(one, b, out);
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-                        for (int s = t < 2 ? 0 : 1; s < 2; ++s) out[t] = mm(image(one, upper_block(t, s)), b[s], out[t]);
-                        ks[t] = -gates(0, t) * gates(2, t) * out[t];
-                    }
+                    for (int t = 0; t < 4; ++t) ks[t] = -gates(0, t) * gates(2, t) * out[t];
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
                         kb[s] = split8<OWN>(ks[2 * s], ks[2 * s + 1]);
@@ -496,23 +536,28 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
                 }
                 const float last = gate[C - 1];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    S[t] *= last;
+                for (int t = 0; t < NT; ++t) S[t] *= last;
+                constexpr int kGroup = NT < 4 ? NT : 4;
+#pragma unroll
+                for (int t = 0; t < NT; t += kGroup)
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        S[t] = mm(cols(kl, t, s), kb[s], S[t]);
-                        if constexpr (MODE == BACK) S[t] = mm(cols(ql, t, s), b[s], S[t]);
+                        Operand<IN> m[kGroup];
+#pragma unroll
+                        for (int e = 0; e < kGroup; ++e) m[e] = cols(kl, t + e, s);
+                        mm_tiles(m, kb[s], S + t);
+                        if constexpr (MODE == BACK) {
+#pragma unroll
+                            for (int e = 0; e < kGroup; ++e) m[e] = cols(ql, t + e, s);
+                            mm_tiles(m, b[s], S + t);
+                        }
                     }
-                }
                 if constexpr (MODE == FWD) {
 #pragma unroll
                     for (int s = 0; s < 2; ++s) b[s] = split8<OWN>(ks[2 * s], ks[2 * s + 1]);
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        out[t] *= a.scale * gates(0, t);
-#pragma unroll
-                        for (int s = 0; s < (t < 2 ? 1 : 2); ++s) out[t] = mm(image(two, lower_block(t, s)), b[s], out[t]);
-                    }
+                    for (int t = 0; t < 4; ++t) out[t] *= a.scale * gates(0, t);
+                    times_lower(two, b, out);
                 } else if constexpr (MODE == KEEP) {
 #pragma unroll
                     for (int t = 0; t < 4; ++t) out[t] = ks[t];
@@ -553,7 +598,7 @@ struct Chunked {
         p.dir[1] = d[ndir - 1];
         const DeltaArgs &a = d[0].a;
         const long long items = delta_slots(a.units, a.L, a.cu != nullptr) * a.H;
-        const dim3 grid((unsigned)((items + kPrepWaves - 1) / kPrepWaves), ndir), block(64 * kPrepWaves);
+        const dim3 grid((unsigned)xcd_grid((items + kPrepWaves - 1) / kPrepWaves), ndir), block(64 * kPrepWaves);
         if (grad) BM_LAUNCH("delta_prep", (k_delta_prep<T, N, true>), grid, block, 0, s, p, items);
         else BM_LAUNCH("delta_prep", (k_delta_prep<T, N, false>), grid, block, 0, s, p, items);
         return hipGetLastError();
@@ -567,21 +612,21 @@ struct Chunked {
         w.ndir = ndir;
         const DeltaArgs &a = d[0].a;
         w.blocks = (a.P + 63) / 64;
-        const dim3 grid((unsigned)((long long)a.units * a.H * w.blocks));
+        const dim3 grid((unsigned)xcd_grid((long long)a.units * a.H * w.blocks));
         BM_LAUNCH(names[MODE], (k_delta_walk<T, N, MODE>), grid, dim3(256), 0, s, w);
         return hipGetLastError();
     }
 };
 
-// the workspace of a direction: images, then gates
-size_t prep_images(const DeltaArgs &a, bool grad) {
-    return (size_t)delta_slots(a.units, a.L, a.cu != nullptr) * a.H * images(grad) * kImage<3>;
+// the workspace of a direction: triangles, then gates
+size_t prep_triangles(const DeltaArgs &a, bool grad) {
+    return (size_t)delta_slots(a.units, a.L, a.cu != nullptr) * a.H * triangles(grad) * kTriangle;
 }
 PrepDir prep_dir(const DeltaArgs &a, void *ws, bool grad) {
     PrepDir d;
     d.a = a;
-    d.images = (uint8_t *)ws;
-    d.gates = (float *)((uint8_t *)ws + prep_images(a, grad));
+    d.tri = (uint8_t *)ws;
+    d.gates = (float *)((uint8_t *)ws + prep_triangles(a, grad));
     return d;
 }
 
@@ -599,7 +644,7 @@ hipError_t with_shape(const DeltaArgs &a, bool bf16, F f) {
 // bytes, a multiple of 256; L and units of a, and whether it is packed (cu)
 size_t delta_chunk_workspace(const DeltaArgs &a, bool grad) {
     const size_t slots = (size_t)delta_slots(a.units, a.L, a.cu != nullptr) * a.H;
-    return prep_images(a, grad) + ((slots * kGates * 4 + 255) & ~(size_t)255);
+    return prep_triangles(a, grad) + ((slots * kGates * 4 + 255) & ~(size_t)255);
 }
 
 hipError_t launch_delta_chunked(const DeltaArgs *a, int ndir, bool bf16, void *const *ws, hipStream_t s) {

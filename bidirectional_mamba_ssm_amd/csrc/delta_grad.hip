@@ -28,13 +28,6 @@ namespace {
 
 constexpr int C = kDeltaChunk;
 
-// row and column tile of the l-th lower tile
-__device__ __forceinline__ constexpr int lower_row(int l) { return l < 1 ? 0 : l < 3 ? 1 : l < 6 ? 2 : 3; }
-__device__ __forceinline__ constexpr int lower_col(int l) {
-    const int r = lower_row(l);
-    return l - r * (r + 1) / 2;
-}
-
 template <typename T, int N>
 __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a, DeltaGradArgs o) {
     constexpr int IN = Terms<T>::IN, OWN = 3, W = N == 128 ? 8 : 4, SL = W / 4;   // waves; k steps of a slice

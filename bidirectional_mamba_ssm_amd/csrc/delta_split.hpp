@@ -117,14 +117,47 @@ __device__ __forceinline__ double decay_sums(float g, int lane) {
     return s;
 }
 
-// Workspace of a chunk and head: images of 64 x 64 triangles and the gates. An
-// image holds the 6 blocks of 16 rows by 32 that are not zero, each as the
-// operand's registers, a kilobyte a term: lane l's row l % 16, k slots 0..3 at
-// 4 (l / 16) and 4..7 at 16 more.
-constexpr int kBlocks = 6;
+// all pairs of terms for M tiles at a time, so that products on one result
+// are apart
+template <int A, int B, int M>
+__device__ __forceinline__ void mm_tiles(const Operand<A> (&a)[M], const Operand<B> &b, f32x4 *c) {
+    constexpr int most = A > B ? A : B;
+#pragma unroll
+    for (int s = most - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < A; ++i) {
+            const int j = s - i;
+            if (j >= 0 && j < B) {
+#pragma unroll
+                for (int m = 0; m < M; ++m) c[m] = mfma16x16x32(a[m].t[i], b.t[j], c[m]);
+            }
+        }
+}
+
+// Workspace of a chunk and head: 64 x 64 triangles and the gates. A triangle is
+// kept as its 10 tiles of 16 x 16, fp32, a kilobyte each, a lane's four
+// entries as an operand wants them: row l % 16, k = 4 (l / 16) ... In LDS it is
+// an image: 6 blocks of 16 rows by 32 that are not zero, each as the operand's
+// registers, a kilobyte a term: k slots 0..3 from one tile, 4..7 from the next.
+constexpr int kBlocks = 6, kTiles = 10;
+__device__ __forceinline__ constexpr int lower(int i, int j) { return i * (i + 1) / 2 + j; }
 __device__ __forceinline__ constexpr int lower_block(int rt, int s) { return rt < 2 ? rt : 2 * rt - 2 + s; }
 __device__ __forceinline__ constexpr int upper_block(int rt, int s) { return rt < 2 ? 2 * rt + s : rt + 2; }
-template <int OWN> constexpr int kImage = kBlocks * OWN * 1024;   // bytes
+// row and column tile of the l-th lower tile
+__device__ __forceinline__ constexpr int lower_row(int l) { return l < 1 ? 0 : l < 3 ? 1 : l < 6 ? 2 : 3; }
+__device__ __forceinline__ constexpr int lower_col(int l) { return l - lower_row(l) * (lower_row(l) + 1) / 2; }
+template <int OWN> constexpr int kImage = kBlocks * OWN * 1024;   // bytes, in LDS
+constexpr int kTriangle = kTiles * 1024;                          // bytes, in memory
+// where a tile's half of a block is, in kilobytes of one term and its half of the
+// 16 bytes of a lane: as rows i with k = j, or as rows j with k = i
+__device__ __forceinline__ int lower_half(int l) {
+    const int i = lower_row(l), j = lower_col(l);
+    return 2 * lower_block(i, j >> 1) + (j & 1);
+}
+__device__ __forceinline__ int upper_half(int l) {
+    const int i = lower_row(l), j = lower_col(l);
+    return 2 * upper_block(j, i >> 1) + (i & 1);
+}
 constexpr int kGates = 3 * kDeltaChunk;                           // e^{G_i}, e^{G_C - G_i}, beta
 // columns of the walks' own arrays: e and z [tok][H][padded], states [slot][H][N][padded]
 __host__ __device__ constexpr int padded(int P) { return (P + 31) & ~31; }
