@@ -289,17 +289,32 @@ struct WalkArgs {
     int blocks;        // workgroups of a head
 };
 
+// Where element (row, col) of K or Q is in LDS, col a multiple of 4: four
+// columns and the four 16 beyond lie side by side, which is a lane's 16 bytes of a
+// row operand; the 16-byte places of a row are permuted by its number, so that
+// the 16 rows that a read touches lie in different banks. A row and the 16th
+// after it are permuted alike. (64-bit reads of rows 72 words apart took 25
+// cycles where these take 12.)
+template <int NP>
+__device__ __forceinline__ int row_place(int row, int col) {
+    constexpr int kPlaces = NP / 8;
+    const int place = col / 32 * 4 + col % 16 / 4;
+    const int turn = row / (16 / kPlaces) % kPlaces;
+    return row * NP * 2 + 16 * (place ^ turn) + col % 32 / 16 * 8;
+}
+
 template <typename T, int N, int MODE>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(WalkArgs args) {
     using X = typename std::conditional<MODE == BACK, float, T>::type;   // the third input's type
     constexpr int IN = Terms<T>::IN, OWN = Terms<T>::OWN;
     constexpr bool GRAD = MODE != FWD;
     constexpr int NP = N < 32 ? 32 : N, KS = NP / 32, NT = N / 16;
-    constexpr int RS = NP + 16;                         // row stride of K and Q in LDS, in elements
-    constexpr int kRows = C * RS * 2 * IN;              // bytes of K or Q
+    constexpr int kRows = C * NP * 2 * IN;              // bytes of K or Q in LDS
+    constexpr bool kStaged = sizeof(X) == 2;            // the third input comes through LDS
+    constexpr int VS = 80;                              // its row stride, elements
     constexpr bool kQ = MODE != KEEP;                   // Q read, and a second image
     constexpr int kImages = kQ ? 2 : 1, kImg = kImage<OWN>;
-    constexpr int kBuf = kRows * (kQ ? 2 : 1) + kImg * kImages + kGates * 4;
+    constexpr int kBuf = kRows * (kQ ? 2 : 1) + kImg * kImages + kGates * 4 + (kStaged ? C * VS * 2 : 0);
     __shared__ __attribute__((aligned(16))) uint8_t buf[kBuf];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l16 = lane & 15;
@@ -337,13 +352,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
         }
         // the next chunk on its way: rows of K and Q, images, gates, the third input
         constexpr int V = 16 / sizeof(T), kVecs = C * NP / V / 256, kVi = (kImages * kTriangle / 16 + 255) / 256;
-        u32x4 nk[kVecs], nq[kQ ? kVecs : 1], ni[kVi];
+        u32x4 nk[kVecs], nq[kQ ? kVecs : 1], ni[kVi], nv[2];
         float ngate = 0.f;
         X nx[4][4];
+        const bool whole = a.P % 8 == 0;   // rows of V are 16-byte vectors
         auto order = [&](int i) { return MODE == BACK ? chunks - 1 - i : i; };
-        auto fetch = [&](int chunk) {
+        auto fetch_rows = [&](int chunk) {
             const int first = chunk * C, live = min(C, at.len - first);
-            const size_t sh = (size_t)(at.slot + chunk) * a.H + h;
             const uint32_t row = (uint32_t)(a.G * N * sizeof(T)), off = (uint32_t)(grp * N * sizeof(T));
             const ChunkRows kr(a.k, at, a.reverse, first, live, row, off, N * sizeof(T));
             const ChunkRows qr(a.q, at, a.reverse, first, live, row, off, N * sizeof(T));
@@ -354,6 +369,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
                 nk[i] = buf16(kr.rsrc, o);
                 if (kQ) nq[i] = buf16(qr.rsrc, o);
             }
+        };
+        auto fetch = [&](int chunk) {
+            const int first = chunk * C, live = min(C, at.len - first);
+            const size_t sh = (size_t)(at.slot + chunk) * a.H + h;
             const __amdgpu_buffer_rsrc_t ir = __builtin_amdgcn_make_buffer_rsrc(
                 pd.tri + (sh * triangles(GRAD) + (MODE == BACK ? 1 : 0)) * kTriangle, 0, kImages * kTriangle, 0x00027000);
 #pragma unroll
@@ -361,11 +380,29 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
             if (tid < kGates) ngate = pd.gates[sh * kGates + tid];
             const uint32_t xrow = (uint32_t)(a.H * a.P * sizeof(X));
             const ChunkRows xr(a.v, at, a.reverse, first, live, xrow, (uint32_t)(h * a.P * sizeof(X)), a.P * sizeof(X));
-            const uint32_t to = xr.offset(4 * g) + (own ? (uint32_t)(p * sizeof(X)) : kFar);
+            if constexpr (kStaged) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+                for (int i = 0; i < 2; ++i) {
+                    // eight columns of the workgroup's 64
+                    const int e = tid + 256 * i, c = 64 * block + e % 8 * 8;
+                    const uint32_t from = xr.offset(e / 8);
+                    if (whole) {
+                        nv[i] = buf16(xr.rsrc, from + (c < a.P ? 2 * c : kFar));
+                    } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) nx[t][r] = buf_value(xr.rsrc, to + (16 * t + r) * xr.step, X());
+                        for (int j = 0; j < 4; ++j)
+                            nv[i][j] = (uint32_t)buf_value(xr.rsrc, from + (c + 2 * j < a.P ? 2 * (c + 2 * j) : kFar), X()) |
+                                       (uint32_t)buf_value(xr.rsrc, from + (c + 2 * j + 1 < a.P ? 2 * (c + 2 * j + 1) : kFar), X())
+                                           << 16;
+                    }
+                }
+            } else {
+                const uint32_t to = xr.offset(4 * g) + (own ? (uint32_t)(p * sizeof(X)) : kFar);
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) nx[t][r] = buf_value(xr.rsrc, to + (16 * t + r) * xr.step, X());
+            }
         };
         auto stash = [&]() {
 #pragma unroll
@@ -373,16 +410,18 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
                     const int e = tid + 256 * i, row = e / (NP / V), col = e % (NP / V) * V;
-                    uint16_t *to = (uint16_t *)(buf + w * kRows) + row * RS + col;
+                    uint8_t *to = buf + w * kRows;
                     const u32x4 r = w ? nq[i] : nk[i];
                     if constexpr (IN == 1) {
-                        *(u32x4 *)to = r;
+                        *(u32x2 *)(to + row_place<NP>(row, col)) = u32x2{r[0], r[1]};
+                        *(u32x2 *)(to + row_place<NP>(row, col + 4)) = u32x2{r[2], r[3]};
                     } else {
                         uint32_t lo[IN], hi[IN];
                         split2<IN>(__uint_as_float(r[0]), __uint_as_float(r[1]), lo);
                         split2<IN>(__uint_as_float(r[2]), __uint_as_float(r[3]), hi);
 #pragma unroll
-                        for (int t = 0; t < IN; ++t) *(u32x2 *)(to + t * C * RS) = u32x2{lo[t], hi[t]};
+                        for (int t = 0; t < IN; ++t)
+                            *(u32x2 *)(to + t * C * NP * 2 + row_place<NP>(row, col)) = u32x2{lo[t], hi[t]};
                     }
                 }
 #pragma unroll
@@ -399,48 +438,62 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
                 for (int t = 0; t < OWN; ++t) *(u32x2 *)(to + t * 1024) = u32x2{lo[t], hi[t]};
             }
             if (tid < kGates) *(float *)(buf + (kQ ? 2 : 1) * kRows + kImages * kImg + 4 * tid) = ngate;
+            if constexpr (kStaged) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int e = tid + 256 * i;
+                    *(u32x4 *)(buf + kBuf - C * VS * 2 + 2 * (e / 8 * VS + e % 8 * 8)) = nv[i];
+                }
+            }
         };
         if (di != args.ndir - 1) __syncthreads();   // the direction before has read its last chunk
         if (chunks > 0) {
             fetch(order(0));
+            fetch_rows(order(0));
             stash();
         }
         for (int step = 0; step < chunks; ++step) {
             const int chunk = order(step), first = chunk * C, live = min(C, at.len - first);
             __syncthreads();
             f32x4 x[4];
+            if constexpr (kStaged) {
+                // a tile's columns as lanes, four rows a lane: a result's order
+                const uint16_t *v = (const uint16_t *)(buf + kBuf - C * VS * 2) + (4 * g + (l16 >> 2)) * VS + 16 * wave + 4 * (l16 & 3);
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    if constexpr (sizeof(X) == 2) x[t][r] = bf2f(nx[t][r]);
-                    else x[t][r] = nx[t][r];
+                for (int t = 0; t < 4; ++t) {
+                    const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_d *)(v + 16 * t * VS)));
+                    x[t] = f32x4{__uint_as_float(r[0] << 16), __uint_as_float(r[0] & 0xffff0000u),
+                                 __uint_as_float(r[1] << 16), __uint_as_float(r[1] & 0xffff0000u)};
                 }
-            if (step + 1 < chunks) fetch(order(step + 1));
-            const uint16_t *kl = (const uint16_t *)buf, *ql = (const uint16_t *)(buf + kRows);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) x[t][r] = nx[t][r];
+            }
+            const bool more = step + 1 < chunks;
+            if (more) fetch(order(step + 1));
+            const uint8_t *kl = buf, *ql = buf + kRows;
             const uint8_t *one = buf + (kQ ? 2 : 1) * kRows, *two = one + kImg;
             const float *gate = (const float *)(one + kImages * kImg);
             // rows 16 rt .. of K or Q, k = n in the order of S's tiles
-            auto rows = [&](const uint16_t *m, int rt, int s) {
+            auto rows = [&](const uint8_t *m, int rt, int s) {
                 Operand<IN> o;
 #pragma unroll
-                for (int t = 0; t < IN; ++t) {
-                    const uint16_t *q = m + t * C * RS + (16 * rt + l16) * RS + 32 * s + 4 * g;
-                    const u32x2 lo = *(const u32x2 *)q, hi = *(const u32x2 *)(q + 16);
-                    o.t[t] = u32x4{lo[0], lo[1], hi[0], hi[1]};
-                }
+                for (int t = 0; t < IN; ++t)
+                    o.t[t] = *(const u32x4 *)(m + t * C * NP * 2 + row_place<NP>(16 * rt + l16, 32 * s + 4 * g));
                 return o;
             };
             // columns 16 nt .. as rows, k = tokens 32 s .. in the order of a result's tiles
-            auto cols = [&](const uint16_t *m, int nt, int s) {
+            auto cols = [&](const uint8_t *m, int nt, int s) {
                 Operand<IN> o;
 #pragma unroll
                 for (int t = 0; t < IN; ++t) {
-                    const uint16_t *q =
-                        m + t * C * RS + (32 * s + 4 * g + (l16 >> 2)) * RS + 16 * nt + 4 * (l16 & 3);
+                    const int row = 32 * s + 4 * g + (l16 >> 2), col = 16 * nt + 4 * (l16 & 3);
+                    const uint8_t *q = m + t * C * NP * 2 + row_place<NP>(row, col);
                     const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_d *)q));
-                    const u32x2 hi =
-                        __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_d *)(q + 16 * RS)));
+                    const u32x2 hi = __builtin_bit_cast(
+                        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_d *)(q + 16 * NP * 2)));
                     o.t[t] = u32x4{lo[0], lo[1], hi[0], hi[1]};
                 }
                 return o;
@@ -501,6 +554,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
                         mm_tiles(r, sb, out);
                     }
                 }
+                if (more) fetch_rows(order(step + 1));
                 Operand<OWN> b[2], kb[2];   // kb: what K^T multiplies
                 if constexpr (MODE != BACK) {
 #pragma unroll
@@ -563,10 +617,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
                     for (int t = 0; t < 4; ++t) out[t] = ks[t];
                 }
             }
+            else if (more) {
+                fetch_rows(order(step + 1));
+            }
             __syncthreads();
             // the next chunk goes to LDS before this one's results go out, so that
             // nothing waits for stores
-            if (step + 1 < chunks) stash();
+            if (more) stash();
             if (works) {
                 const int P = GRAD ? PP : a.P;
                 const ChunkRows yr(a.y, at, a.reverse, first, live, (uint32_t)(a.H * P * 4), (uint32_t)(h * P * 4), P * 4);
