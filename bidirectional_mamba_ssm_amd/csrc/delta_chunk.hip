@@ -303,15 +303,16 @@ __device__ __forceinline__ int row_place(int row, int col) {
     return row * NP * 2 + 16 * (place ^ turn) + col % 32 / 16 * 8;
 }
 
-template <typename T, int N, int MODE>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(WalkArgs args) {
+// W waves: 64 columns, two workgroups a CU (bf16), or 128, one
+template <typename T, int N, int MODE, int W>
+__global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_delta_walk(WalkArgs args) {
     using X = typename std::conditional<MODE == BACK, float, T>::type;   // the third input's type
     constexpr int IN = Terms<T>::IN, OWN = Terms<T>::OWN;
     constexpr bool GRAD = MODE != FWD;
     constexpr int NP = N < 32 ? 32 : N, KS = NP / 32, NT = N / 16;
     constexpr int kRows = C * NP * 2 * IN;              // bytes of K or Q in LDS
     constexpr bool kStaged = sizeof(X) == 2;            // the third input comes through LDS
-    constexpr int VS = 80;                              // its row stride, elements
+    constexpr int kThreads = 64 * W, VS = 16 * W + 16;  // row stride of the third input in LDS, elements
     constexpr bool kQ = MODE != KEEP;                   // Q read, and a second image
     constexpr int kImages = kQ ? 2 : 1, kImg = kImage<OWN>;
     constexpr int kBuf = kRows * (kQ ? 2 : 1) + kImg * kImages + kGates * 4 + (kStaged ? C * VS * 2 : 0);
@@ -322,11 +323,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
     if (mine >= work) return;
     const int block = (int)(mine % args.blocks), h = (int)(mine / args.blocks % args.dir[0].a.H);
     const int u = (int)(mine / args.blocks / args.dir[0].a.H);
-    const int p0 = (block * 4 + wave) * 16;
+    const int p0 = (block * W + wave) * 16;
     // the wave has columns, those of the walks' own arrays past the head's width among them
     const bool works = p0 < (GRAD ? padded(args.dir[0].a.P) : args.dir[0].a.P);
     // the halves of blocks that lie beyond the diagonal stay zeros
-    for (int i = tid; i < kImages * 2 * OWN * 64; i += 256) {
+    for (int i = tid; i < kImages * 2 * OWN * 64; i += kThreads) {
         const int which = i / (2 * OWN * 64), e = i / 64 % (2 * OWN), term = e % OWN, second = e / OWN;
         const int half = MODE == BACK ? 2 * (second ? upper_block(3, 1) : upper_block(1, 0))
                                       : 2 * (second ? lower_block(2, 1) : lower_block(0, 0)) + 1;
@@ -351,7 +352,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
             if (a.init && own) S[t] = *(const f32x4 *)(a.init + state + 16 * t);
         }
         // the next chunk on its way: rows of K and Q, images, gates, the third input
-        constexpr int V = 16 / sizeof(T), kVecs = C * NP / V / 256, kVi = (kImages * kTriangle / 16 + 255) / 256;
+        constexpr int V = 16 / sizeof(T), kAll = C * NP / V, kVecs = (kAll + kThreads - 1) / kThreads;
+        constexpr int kVi = (kImages * kTiles + W - 1) / W;
         u32x4 nk[kVecs], nq[kQ ? kVecs : 1], ni[kVi], nv[2];
         float ngate = 0.f;
         X nx[4][4];
@@ -364,8 +366,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
             const ChunkRows qr(a.q, at, a.reverse, first, live, row, off, N * sizeof(T));
 #pragma unroll
             for (int i = 0; i < kVecs; ++i) {
-                const int e = tid + 256 * i, col = e % (NP / V) * V;
-                const uint32_t o = kr.offset(e / (NP / V)) + (col < N ? (uint32_t)(col * sizeof(T)) : kFar);
+                const int e = tid + kThreads * i, col = e % (NP / V) * V;
+                const uint32_t o = kr.offset(e / (NP / V)) + (col < N && e < kAll ? (uint32_t)(col * sizeof(T)) : kFar);
                 nk[i] = buf16(kr.rsrc, o);
                 if (kQ) nq[i] = buf16(qr.rsrc, o);
             }
@@ -376,16 +378,16 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
             const __amdgpu_buffer_rsrc_t ir = __builtin_amdgcn_make_buffer_rsrc(
                 pd.tri + (sh * triangles(GRAD) + (MODE == BACK ? 1 : 0)) * kTriangle, 0, kImages * kTriangle, 0x00027000);
 #pragma unroll
-            for (int i = 0; i < kVi; ++i) ni[i] = buf16(ir, 16 * tid + 4096 * i);
+            for (int i = 0; i < kVi; ++i) ni[i] = buf16(ir, 16 * (tid + kThreads * i));
             if (tid < kGates) ngate = pd.gates[sh * kGates + tid];
             const uint32_t xrow = (uint32_t)(a.H * a.P * sizeof(X));
             const ChunkRows xr(a.v, at, a.reverse, first, live, xrow, (uint32_t)(h * a.P * sizeof(X)), a.P * sizeof(X));
             if constexpr (kStaged) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    // eight columns of the workgroup's 64
-                    const int e = tid + 256 * i, c = 64 * block + e % 8 * 8;
-                    const uint32_t from = xr.offset(e / 8);
+                    // eight columns of the workgroup's
+                    const int e = tid + kThreads * i, c = 16 * W * block + e % (2 * W) * 8;
+                    const uint32_t from = xr.offset(e / (2 * W));
                     if (whole) {
                         nv[i] = buf16(xr.rsrc, from + (c < a.P ? 2 * c : kFar));
                     } else {
@@ -409,7 +411,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
             for (int w = 0; w < (kQ ? 2 : 1); ++w)
 #pragma unroll
                 for (int i = 0; i < kVecs; ++i) {
-                    const int e = tid + 256 * i, row = e / (NP / V), col = e % (NP / V) * V;
+                    const int e = tid + kThreads * i, row = e / (NP / V), col = e % (NP / V) * V;
+                    if (kAll % kThreads && e >= kAll) break;
                     uint8_t *to = buf + w * kRows;
                     const u32x4 r = w ? nq[i] : nk[i];
                     if constexpr (IN == 1) {
@@ -426,8 +429,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
                 }
 #pragma unroll
             for (int i = 0; i < kVi; ++i) {
-                const int tile = wave + 4 * i, which = tile / kTiles, l = tile % kTiles;
-                if (kImages * kTiles % 4 && tile >= kImages * kTiles) break;
+                const int tile = wave + W * i, which = tile / kTiles, l = tile % kTiles;
+                if (kImages * kTiles % W && tile >= kImages * kTiles) break;
                 const int half = MODE == BACK ? upper_half(l) : lower_half(l);
                 uint8_t *to = buf + (kQ ? 2 : 1) * kRows + which * kImg + (half >> 1) * OWN * 1024 + 16 * lane + 8 * (half & 1);
                 const f32x4 v = __builtin_bit_cast(f32x4, ni[i]);
@@ -441,8 +444,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_delta_walk(Walk
             if constexpr (kStaged) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int e = tid + 256 * i;
-                    *(u32x4 *)(buf + kBuf - C * VS * 2 + 2 * (e / 8 * VS + e % 8 * 8)) = nv[i];
+                    const int e = tid + kThreads * i;
+                    *(u32x4 *)(buf + kBuf - C * VS * 2 + 2 * (e / (2 * W) * VS + e % (2 * W) * 8)) = nv[i];
                 }
             }
         };
@@ -668,9 +671,10 @@ struct Chunked {
         w.dir[1] = d[ndir - 1];
         w.ndir = ndir;
         const DeltaArgs &a = d[0].a;
-        w.blocks = (a.P + 63) / 64;
-        const dim3 grid((unsigned)xcd_grid((long long)a.units * a.H * w.blocks));
-        BM_LAUNCH(names[MODE], (k_delta_walk<T, N, MODE>), grid, dim3(256), 0, s, w);
+        w.blocks = 1;
+        const dim3 grid((unsigned)xcd_grid((long long)a.units * a.H));
+        if (a.P > 64) BM_LAUNCH(names[MODE], (k_delta_walk<T, N, MODE, 8>), grid, dim3(512), 0, s, w);
+        else BM_LAUNCH(names[MODE], (k_delta_walk<T, N, MODE, 4>), grid, dim3(256), 0, s, w);
         return hipGetLastError();
     }
 };
