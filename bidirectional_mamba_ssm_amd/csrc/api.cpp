@@ -1763,7 +1763,7 @@ int bimamba_delta_bwd(const bimamba_shape *s, const bimamba_delta_dir *fwd, cons
             return hip_fail(e, "launching the delta rule's walk back");
         if (empty) continue;
         const bimamba_delta_grad *g = grads[i];
-        const DeltaGradArgs o = {dy, errors, zs, enter, leave, g->dq, g->dk, g->dv, g->dg, g->dbeta};
+        const DeltaGradArgs o = {dy, errors, zs, enter, leave, delta_gates(a, chunked), g->dq, g->dk, g->dv, g->dg, g->dbeta};
         if ((e = launch_delta_grad(a, o, bf16, st)) != hipSuccess)
             return hip_fail(e, "launching the delta rule's gradient");
     }

@@ -35,6 +35,7 @@ struct DeltaGradArgs {
     const float *dy;                 // [tok][H][P]
     const float *e, *z;              // [tok][H][P rounded up]
     const float *enter, *leave;      // [slot][H][N][P rounded up]: incoming states, gradients of the outgoing
+    const float *gates;              // the preparing kernel's (delta_gates)
     float *dq, *dk, *dv, *dg, *dbeta;
 };
 
@@ -93,6 +94,7 @@ size_t delta_chunk_workspace(const DeltaArgs &a, bool grad);
 hipError_t launch_delta_chunked(const DeltaArgs *a, int ndir, bool bf16, void *const *ws, hipStream_t s);
 hipError_t launch_delta_keep(const DeltaArgs &a, bool bf16, void *ws, hipStream_t s);
 hipError_t launch_delta_back(const DeltaArgs &a, bool bf16, void *ws, hipStream_t s);
+const float *delta_gates(const DeltaArgs &a, void *ws);
 // delta_grad.hip, and the bytes of e or z, and of the kept states or their gradients
 size_t delta_rows_bytes(const DeltaArgs &a);
 size_t delta_states_bytes(const DeltaArgs &a);

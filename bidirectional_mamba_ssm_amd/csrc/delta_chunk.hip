@@ -54,7 +54,7 @@ __device__ __forceinline__ f32x4 mfma4(float a, float b, f32x4 c) {
 struct PrepDir {
     DeltaArgs a;
     uint8_t *tri;      // [slot][H]
-    float *gates;      // [slot][H][kGates]
+    float *gates;      // [slot][H][kGateFloats]
 };
 struct PrepArgs {
     PrepDir dir[2];
@@ -159,7 +159,8 @@ __global__ __launch_bounds__(64 * kPrepWaves, 2) void k_delta_prep(PrepArgs args
         w.rows[lane] = expf((float)(lane < 16 ? sum : sum - before));
         w.cols[lane] = expf((float)(end - sum));
         w.beta[lane] = gbeta;
-        float *to = pd.gates + ((size_t)slot * a.H + h) * kGates;
+        float *to = pd.gates + ((size_t)slot * a.H + h) * kGateFloats;
+        ((double *)(to + kGates))[lane] = sum;
         to[lane] = expf((float)sum);
         to[C + lane] = expf((float)(__shfl(sum, 63) - sum));
         to[2 * C + lane] = gbeta;
@@ -379,7 +380,7 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
                 pd.tri + (sh * triangles(GRAD) + (MODE == BACK ? 1 : 0)) * kTriangle, 0, kImages * kTriangle, 0x00027000);
 #pragma unroll
             for (int i = 0; i < kVi; ++i) ni[i] = buf16(ir, 16 * (tid + kThreads * i));
-            if (tid < kGates) ngate = pd.gates[sh * kGates + tid];
+            if (tid < kGates) ngate = pd.gates[sh * kGateFloats + tid];
             const uint32_t xrow = (uint32_t)(a.H * a.P * sizeof(X));
             const ChunkRows xr(a.v, at, a.reverse, first, live, xrow, (uint32_t)(h * a.P * sizeof(X)), a.P * sizeof(X));
             if constexpr (kStaged) {
@@ -705,7 +706,7 @@ hipError_t with_shape(const DeltaArgs &a, bool bf16, F f) {
 // bytes, a multiple of 256; L and units of a, and whether it is packed (cu)
 size_t delta_chunk_workspace(const DeltaArgs &a, bool grad) {
     const size_t slots = (size_t)delta_slots(a.units, a.L, a.cu != nullptr) * a.H;
-    return prep_triangles(a, grad) + ((slots * kGates * 4 + 255) & ~(size_t)255);
+    return prep_triangles(a, grad) + ((slots * kGateFloats * 4 + 255) & ~(size_t)255);
 }
 
 hipError_t launch_delta_chunked(const DeltaArgs *a, int ndir, bool bf16, void *const *ws, hipStream_t s) {
@@ -725,6 +726,8 @@ hipError_t launch_delta_keep(const DeltaArgs &a, bool bf16, void *ws, hipStream_
         return e != hipSuccess ? e : k.template walk<KEEP>(&d, 1, s);
     });
 }
+
+const float *delta_gates(const DeltaArgs &a, void *ws) { return prep_dir(a, ws, true).gates; }
 
 hipError_t launch_delta_back(const DeltaArgs &a, bool bf16, void *ws, hipStream_t s) {
     const PrepDir d = prep_dir(a, ws, true);

@@ -89,120 +89,132 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
     const uint32_t row4 = (uint32_t)(a.G * N * 4), off4 = (uint32_t)(grp * N * 4);
     const ChunkRows dqr(o.dq, at, a.reverse, first, live, row4, off4, N * 4);
     const ChunkRows dkr(o.dk, at, a.reverse, first, live, row4, off4, N * 4);
-    const int rep = a.H / a.G;
-    for (int h = grp * rep; h < (grp + 1) * rep; ++h) {
-        if (wave == 0) {
-            const size_t i = (size_t)delta_token(at, a.reverse, first + min(lane, live - 1)) * a.H + h;
-            const double sum = decay_sums(lane < live ? a.g[i] : 0.f, lane);
-            sums[lane] = sum;
-            gate[0][lane] = expf((float)sum);
-            gate[1][lane] = expf((float)(__shfl(sum, 63) - sum));
-            gate[2][lane] = lane < live ? a.beta[i] : 0.f;
+    const int h0 = grp * (a.H / a.G), h1 = h0 + a.H / a.G;
+    // a thread brings eight columns of a token of do, e and z, a wave's lanes their
+    // row of S and of D, the first wave's the gates
+    const int mytok = 16 * (wave & 3) + l16, mycol = 32 * (wave >> 2) + 8 * g;
+    const bool whole = a.P % 8 == 0;
+    u32x4 nd[2], ne[2], nz[2], ns[SL][2], nl[SL][2];
+    float ng[3];
+    double nsum;
+    auto fetch = [&](int h, int p0) {
+        const ChunkRows dr(o.dy, at, a.reverse, first, live, (uint32_t)a.H * a.P * 4, (uint32_t)h * a.P * 4, a.P * 4);
+        const ChunkRows er(o.e, at, a.reverse, first, live, (uint32_t)a.H * PP * 4, (uint32_t)h * PP * 4, PP * 4);
+        const ChunkRows zr(o.z, at, a.reverse, first, live, (uint32_t)a.H * PP * 4, (uint32_t)h * PP * 4, PP * 4);
+        const int p = p0 + mycol;
+        const uint32_t in = er.offset(mytok) + (p < PP ? 4 * p : kFar);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            ne[e] = buf16(er.rsrc, in + 16 * e);
+            nz[e] = buf16(zr.rsrc, in + 16 * e);
         }
-        // a thread brings eight columns of a token of do, e and z
-        const uint32_t off = (uint32_t)h * a.P * 4, row = (uint32_t)a.H * a.P * 4;
-        const uint32_t offp = (uint32_t)h * PP * 4, rowp = (uint32_t)a.H * PP * 4;
-        const ChunkRows dr(o.dy, at, a.reverse, first, live, row, off, a.P * 4);
-        const ChunkRows vr(o.dv, at, a.reverse, first, live, row, off, a.P * 4);
-        const ChunkRows er(o.e, at, a.reverse, first, live, rowp, offp, PP * 4);
-        const ChunkRows zr(o.z, at, a.reverse, first, live, rowp, offp, PP * 4);
-        const int mytok = 16 * (wave & 3) + l16, mycol = 32 * (wave >> 2) + 8 * g;
-        const bool whole = a.P % 8 == 0;
-        u32x4 nd[2], ne[2], nz[2];
-        u32x4 ns[SL][2], nl[SL][2];
-        const float *S = o.enter + (((size_t)slot * a.H + h) * N + n0 + l16) * PP;
-        const float *D = o.leave + (((size_t)slot * a.H + h) * N + n0 + l16) * PP;
-        auto fetch = [&](int p0) {
-            const int p = p0 + mycol;
-            const uint32_t in = p < PP ? 4 * p : kFar;
+        if (whole) {
+            const uint32_t from = dr.offset(mytok) + (p < a.P ? 4 * p : kFar);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                ne[e] = buf16(er.rsrc, er.offset(mytok) + in + 16 * e);
-                nz[e] = buf16(zr.rsrc, zr.offset(mytok) + in + 16 * e);
-                if (whole) {
-                    nd[e] = buf16(dr.rsrc, dr.offset(mytok) + (p < a.P ? 4 * p : kFar) + 16 * e);
-                } else {
+            for (int e = 0; e < 2; ++e) nd[e] = buf16(dr.rsrc, from + 16 * e);
+        } else {
+            const uint32_t from = dr.offset(mytok) + 4 * p;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int q = p + 4 * e + j;
-                        nd[e][j] = __float_as_uint(buf_value(dr.rsrc, dr.offset(mytok) + (q < a.P ? 4 * q : kFar), 0.f));
-                    }
-                }
-            }
-        };
-        auto fetch_states = [&](int s, int p0) {
-            if (!mine || p0 + 32 * s >= PP) return;
+            for (int j = 0; j < 8; ++j)
+                nd[j >> 2][j & 3] = __float_as_uint(buf_value(dr.rsrc, p + j < a.P ? from + 4 * j : kFar, 0.f));
+        }
+        if (p0 == 0 && wave == 0) {
+            const float *from = o.gates + ((size_t)slot * a.H + h) * kGateFloats;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                ns[s][e] = *(const u32x4 *)(S + p0 + 32 * s + 8 * g + 4 * e);
-                nl[s][e] = *(const u32x4 *)(D + p0 + 32 * s + 8 * g + 4 * e);
-            }
-        };
-        f32x4 aq[4], af[4], ae[4], x[kJobs];
+            for (int e = 0; e < 3; ++e) ng[e] = from[e * C + lane];
+            nsum = ((const double *)(from + kGates))[lane];
+        }
+    };
+    auto fetch_states = [&](int h, int p0, int s) {
+        const size_t from = (((size_t)slot * a.H + h) * N + n0 + l16) * PP + p0 + 32 * s + 8 * g;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) aq[i] = af[i] = ae[i] = zero4();
+        for (int e = 0; e < 2; ++e) {
+            ns[s][e] = *(const u32x4 *)(o.enter + from + 4 * e);
+            nl[s][e] = *(const u32x4 *)(o.leave + from + 4 * e);
+        }
+    };
+    fetch(h0, 0);
+#pragma unroll
+    for (int s = 0; s < SL; ++s)
+        if (mine && 32 * s < PP) fetch_states(h0, 0, s);
+    for (int h = h0; h < h1; ++h) {
+        if (wave == 0) {
+#pragma unroll
+            for (int e = 0; e < 3; ++e) gate[e][lane] = ng[e];
+            sums[lane] = nsum;
+        }
+        const ChunkRows vr(o.dv, at, a.reverse, first, live, (uint32_t)a.H * a.P * 4, (uint32_t)h * a.P * 4, a.P * 4);
+        f32x4 acc[4][3], x[kJobs];   // acc: do S, e D, z S
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = zero4();
 #pragma unroll
         for (int i = 0; i < kJobs; ++i) x[i] = zero4();
         float along = 0.f, db = 0.f;   // <S, D> and e . z of this lane
-        fetch(0);
-#pragma unroll
-        for (int s = 0; s < SL; ++s) fetch_states(s, 0);
         for (int p0 = 0; p0 < a.P; p0 += 32 * SL) {
             __syncthreads();
-            const f32x4 e0 = __builtin_bit_cast(f32x4, ne[0]), e1 = __builtin_bit_cast(f32x4, ne[1]);
-            const f32x4 z0 = __builtin_bit_cast(f32x4, nz[0]), z1 = __builtin_bit_cast(f32x4, nz[1]);
             {
-                const Operand<OWN> d = split8<OWN>(__builtin_bit_cast(f32x4, nd[0]), __builtin_bit_cast(f32x4, nd[1]));
-                const Operand<OWN> e = split8<OWN>(e0, e1), z = split8<OWN>(z0, z1);
+                const f32x4 e0 = __builtin_bit_cast(f32x4, ne[0]), e1 = __builtin_bit_cast(f32x4, ne[1]);
+                const f32x4 z0 = __builtin_bit_cast(f32x4, nz[0]), z1 = __builtin_bit_cast(f32x4, nz[1]);
                 uint8_t *to = lds + (wave >> 2) * 3 * kRow + (wave & 3) * OWN * 1024 + 16 * lane;
+                auto put = [&](int which, f32x4 lo, f32x4 hi) {
+                    const Operand<OWN> v = split8<OWN>(lo, hi);
 #pragma unroll
-                for (int t = 0; t < OWN; ++t) {
-                    *(u32x4 *)(to + t * 1024) = d.t[t];
-                    *(u32x4 *)(to + kRow + t * 1024) = e.t[t];
-                    *(u32x4 *)(to + 2 * kRow + t * 1024) = z.t[t];
-                }
-            }
-            const float beta = gate[2][mytok];
+                    for (int t = 0; t < OWN; ++t) *(u32x4 *)(to + which * kRow + t * 1024) = v.t[t];
+                };
+                put(0, __builtin_bit_cast(f32x4, nd[0]), __builtin_bit_cast(f32x4, nd[1]));
+                put(1, e0, e1);
+                put(2, z0, z1);
+                const float beta = gate[2][mytok];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) db = fmaf(e0[j], z0[j], fmaf(e1[j], z1[j], db));
-            {
+                for (int j = 0; j < 4; ++j) db = fmaf(e0[j], z0[j], fmaf(e1[j], z1[j], db));
                 const int p = p0 + mycol;
                 const f32x4 f[2] = {beta * z0, beta * z1};
                 if (whole) {
-                    const uint32_t to = vr.offset(mytok) + (p < a.P ? 4 * p : kFar);
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f[0]), vr.rsrc, to, 0, 0);
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f[1]), vr.rsrc, to + 16, 0, 0);
+                    const uint32_t out = vr.offset(mytok) + (p < a.P ? 4 * p : kFar);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f[0]), vr.rsrc, out, 0, 0);
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f[1]), vr.rsrc, out + 16, 0, 0);
                 } else {
+                    const uint32_t out = vr.offset(mytok) + 4 * p;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        buf_store(vr.rsrc, vr.offset(mytok) + (p + j < a.P ? 4 * (p + j) : kFar), f[j >> 2][j & 3]);
+                    for (int j = 0; j < 8; ++j) buf_store(vr.rsrc, p + j < a.P ? out + 4 * j : kFar, f[j >> 2][j & 3]);
                 }
             }
             __syncthreads();
-            if (p0 + 32 * SL < a.P) fetch(p0 + 32 * SL);
+            // the next slice, this head's or the next one's
+            const bool ends_head = p0 + 32 * SL >= a.P;
+            const int hn = ends_head ? h + 1 : h, pn = ends_head ? 0 : p0 + 32 * SL;
+            if (hn < h1) fetch(hn, pn);
 #pragma unroll
             for (int s = 0; s < SL; ++s) {
                 const int im = s * 3 * kRow;
-#pragma unroll
-                for (int t = 0; t < kJobs; ++t) {
-                    const int job = wave + W * t;
-                    if (job >= 20) break;
-                    const int l = job < 10 ? job : job - 10;
-                    x[t] = mm(image(im + (job < 10 ? 0 : 2) * kRow, lower_row(l)), image(im + kRow, lower_col(l)), x[t]);
-                }
                 if (mine && p0 + 32 * s < PP) {
                     const f32x4 s0 = __builtin_bit_cast(f32x4, ns[s][0]), s1 = __builtin_bit_cast(f32x4, ns[s][1]);
                     const f32x4 l0 = __builtin_bit_cast(f32x4, nl[s][0]), l1 = __builtin_bit_cast(f32x4, nl[s][1]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) along = fmaf(s0[j], l0[j], fmaf(s1[j], l1[j], along));
                     const Operand<OWN> sb = split8<OWN>(s0, s1), lb = split8<OWN>(l0, l1);
-                    fetch_states(s, p0 + 32 * SL);
+                    if (hn < h1 && pn + 32 * s < PP) fetch_states(hn, pn, s);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        aq[i] = mm(image(im, i), sb, aq[i]);
-                        ae[i] = mm(image(im + kRow, i), lb, ae[i]);
-                        af[i] = mm(image(im + 2 * kRow, i), sb, af[i]);
+                        Operand<OWN> m[3];
+#pragma unroll
+                        for (int e = 0; e < 3; ++e) m[e] = image(im + e * kRow, i);
+#pragma unroll
+                        for (int q = OWN - 1; q >= 0; --q)
+#pragma unroll
+                            for (int t = 0; t <= q; ++t) {
+                                acc[i][0] = mfma16x16x32(m[0].t[t], sb.t[q - t], acc[i][0]);
+                                acc[i][1] = mfma16x16x32(m[1].t[t], lb.t[q - t], acc[i][1]);
+                                acc[i][2] = mfma16x16x32(m[2].t[t], sb.t[q - t], acc[i][2]);
+                            }
                     }
+                }
+#pragma unroll
+                for (int t = 0; t < kJobs; ++t) {
+                    const int job = wave + W * t;
+                    if (job >= 20) break;
+                    const int l = job < 10 ? job : job - 10;
+                    x[t] = mm(image(im + (job < 10 ? 0 : 2) * kRow, lower_row(l)), image(im + kRow, lower_col(l)), x[t]);
                 }
             }
         }
@@ -223,12 +235,16 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
             if (job >= 20) break;
             const bool second = job >= 10;
             const int l = second ? job - 10 : job, it = lower_row(l), jt = lower_col(l), j = 16 * jt + l16;
+            const double from = sums[j];
+            const float bj = gate[2][j];
+            const f32x4 bi = *(const f32x4 *)&gate[2][16 * it + 4 * g];
             float v[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = 16 * it + 4 * g + r;
-                const float w = j <= i ? gate[2][j] * expf((float)(sums[i] - sums[j])) : 0.f;
-                v[r] = !second ? a.scale * w * x[t][r] : j < i ? -w * gate[2][i] * x[t][r] : 0.f;
+                const float decay = expf((float)(sums[i] - from));
+                const float w = x[t][r] * bj * (second ? -bi[r] : a.scale);
+                v[r] = j < i || (j == i && !second) ? w * decay : 0.f;
             }
             uint32_t lo[OWN], hi[OWN];
             split2<OWN>(v[0], v[1], lo);
@@ -249,27 +265,33 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
         }
         __syncthreads();
         if (mine) {
+            uint32_t to = dqr.offset(4 * g) + 4 * (n0 + l16);
+            asm("" : "+v"(to));   // sixteen addresses kept over the heads would crowd out what is worked on
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f32x4 up = *(const f32x4 *)&gate[0][16 * i + 4 * g], down = *(const f32x4 *)&gate[1][16 * i + 4 * g];
                 const f32x4 beta = *(const f32x4 *)&gate[2][16 * i + 4 * g];
-                f32x4 rowk = -up * beta * af[i], colk = down * beta * ae[i];
+                f32x4 q4 = acc[i][0] * (a.scale * up), rowk = -up * beta * acc[i][2], colk = down * beta * acc[i][1];
                 const f32x4 fall = colk;
-                aq[i] *= a.scale * up;
 #pragma unroll
                 for (int s = 0; s < (i < 2 ? 1 : 2); ++s) {
-                    aq[i] = mm(image(0, lower_block(i, s)), kb[s], aq[i]);
-                    rowk = mm(image(kImage<OWN>, lower_block(i, s)), kb[s], rowk);
+                    const Operand<OWN> m[2] = {image(0, lower_block(i, s)), image(kImage<OWN>, lower_block(i, s))};
+                    f32x4 two[2] = {q4, rowk};
+                    mm_tiles(m, kb[s], two);
+                    q4 = two[0];
+                    rowk = two[1];
                 }
+                f32x4 more = zero4();
 #pragma unroll
                 for (int s = i < 2 ? 0 : 1; s < 2; ++s) {
                     colk = mm(image(2 * kImage<OWN>, upper_block(i, s)), qb[s], colk);
-                    colk = mm(image(3 * kImage<OWN>, upper_block(i, s)), kb[s], colk);
+                    more = mm(image(3 * kImage<OWN>, upper_block(i, s)), kb[s], more);
                 }
+                colk += more;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float q = value(qb, i, r), k = value(kb, i, r);
-                    const float l = group_total<16>(fmaf(q, aq[i][r], k * (rowk[r] - colk[r])));
+                    const float l = group_total<16>(fmaf(q, q4[r], k * (rowk[r] - colk[r])));
                     const float f = group_total<16>(k * fall[r]);
                     if (l16 == 0) {
                         logs[0][wave][16 * i + 4 * g + r] = l;
@@ -278,17 +300,16 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
                 }
                 // this lane's sums over the heads so far
                 rowk += colk;
-                const uint32_t to = dqr.offset(4 * g) + 4 * (n0 + l16);
-                if (h > grp * rep) {
+                if (h > h0) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        aq[i][r] += buf_value(dqr.rsrc, to + (16 * i + r) * dqr.step, 0.f);
+                        q4[r] += buf_value(dqr.rsrc, to + (16 * i + r) * dqr.step, 0.f);
                         rowk[r] += buf_value(dkr.rsrc, to + (16 * i + r) * dqr.step, 0.f);
                     }
                 }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    buf_store(dqr.rsrc, to + (16 * i + r) * dqr.step, aq[i][r]);
+                    buf_store(dqr.rsrc, to + (16 * i + r) * dqr.step, q4[r]);
                     buf_store(dkr.rsrc, to + (16 * i + r) * dqr.step, rowk[r]);
                 }
             }
@@ -302,30 +323,30 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
         if (wave == 0) {
             // dG of this lane's token; the chunk's end is its last token's, which
             // every token reaches back from (places past it hold zeros)
-            double d = 0.0, f = 0.0, dot = 0.0;
-            float b = 0.f;
+            float d = 0.f, f = 0.f, dot = 0.f, b = 0.f;
 #pragma unroll
             for (int w = 0; w < N / 16; ++w) {
-                d += (double)logs[0][w][lane];
-                f += (double)logs[1][w][lane];
-                dot += (double)ends[w];
+                d += logs[0][w][lane];
+                f += logs[1][w][lane];
+                dot += ends[w];
             }
 #pragma unroll
             for (int w = 0; w < SL; ++w) b += dbs[w][lane];
-#pragma unroll
-            for (int m = 1; m < 64; m *= 2) {
-                const double from = __shfl_down(d, m);
-                if (lane + m < 64) d += from;
-                f += __shfl_xor(f, m);
-            }
-            d += f + dot * (double)gate[0][C - 1];
+            // sums from this lane on: within 16 lanes, then the groups behind
+            d += __uint_as_float(dpp<0x101>(__float_as_uint(d)));
+            d += __uint_as_float(dpp<0x102>(__float_as_uint(d)));
+            d += __uint_as_float(dpp<0x104>(__float_as_uint(d)));
+            d += __uint_as_float(dpp<0x108>(__float_as_uint(d)));
+            auto total = [&](int l) { return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(d), l)); };
+            const float t3 = total(48), t2 = total(32) + t3, t1 = total(16) + t2;
+            d += g == 0 ? t1 : g == 1 ? t2 : g == 2 ? t3 : 0.f;
+            d += wave_total(f) + dot * gate[0][C - 1];
             if (lane < live) {
                 const size_t i = (size_t)delta_token(at, a.reverse, first + lane) * a.H + h;
-                o.dg[i] = (float)d;
+                o.dg[i] = d;
                 o.dbeta[i] = b;
             }
         }
-        __syncthreads();   // the next head's gates and slices
     }
 }
 

@@ -158,7 +158,8 @@ __device__ __forceinline__ int upper_half(int l) {
     const int i = lower_row(l), j = lower_col(l);
     return 2 * upper_block(j, i >> 1) + (i & 1);
 }
-constexpr int kGates = 3 * kDeltaChunk;                           // e^{G_i}, e^{G_C - G_i}, beta
+// the gates: e^{G_i}, e^{G_C - G_i}, beta, and G_i in 64 bits
+constexpr int kGates = 3 * kDeltaChunk, kGateFloats = 5 * kDeltaChunk;
 // columns of the walks' own arrays: e and z [tok][H][padded], states [slot][H][N][padded]
 __host__ __device__ constexpr int padded(int P) { return (P + 31) & ~31; }
 
