@@ -360,7 +360,16 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
         X nx[4][4];
         const bool whole = a.P % 8 == 0;   // rows of V are 16-byte vectors
         auto order = [&](int i) { return MODE == BACK ? chunks - 1 - i : i; };
+        // A lane's own numbers, as a stage of a chunk has them: the compiler would
+        // keep what all stages make of them through the whole walk, more than the
+        // registers hold.
+        constexpr bool kCrowded = N == 128 && (MODE == BACK || (MODE == FWD && (W == 4 || IN == 3)));
+        auto fresh = [&](int v) {
+            if constexpr (kCrowded) asm volatile("" : "+v"(v));
+            return v;
+        };
         auto fetch_rows = [&](int chunk) {
+            const int tid = fresh(threadIdx.x);
             const int first = chunk * C, live = min(C, at.len - first);
             const uint32_t row = (uint32_t)(a.G * N * sizeof(T)), off = (uint32_t)(grp * N * sizeof(T));
             const ChunkRows kr(a.k, at, a.reverse, first, live, row, off, N * sizeof(T));
@@ -374,6 +383,7 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
             }
         };
         auto fetch = [&](int chunk) {
+            const int tid = fresh(threadIdx.x), g = (tid & 63) >> 4;
             const int first = chunk * C, live = min(C, at.len - first);
             const size_t sh = (size_t)(at.slot + chunk) * a.H + h;
             const __amdgpu_buffer_rsrc_t ir = __builtin_amdgcn_make_buffer_rsrc(
@@ -408,6 +418,7 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
             }
         };
         auto stash = [&]() {
+            const int tid = fresh(threadIdx.x), lane = tid & 63;
 #pragma unroll
             for (int w = 0; w < (kQ ? 2 : 1); ++w)
 #pragma unroll
@@ -459,6 +470,7 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
         for (int step = 0; step < chunks; ++step) {
             const int chunk = order(step), first = chunk * C, live = min(C, at.len - first);
             __syncthreads();
+            const int lane = fresh(threadIdx.x & 63), g = lane >> 4, l16 = lane & 15;
             f32x4 x[4];
             if constexpr (kStaged) {
                 // a tile's columns as lanes, four rows a lane: a result's order

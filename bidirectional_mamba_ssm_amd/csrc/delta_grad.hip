@@ -45,10 +45,18 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
     const DeltaUnit at = delta_slot(a, slot, chunk);
     const int first = chunk * C, live = min(C, at.len - first);
     if (live <= 0) return;
-    auto image = [&](int off, int b) {
+    // A lane's own number, as a stage of a head's work has it: the compiler would
+    // keep what all stages make of it through the whole walk, far more than the
+    // registers hold (58 of them went to memory, 590 us at the layer's shape).
+    auto fresh = [&]() {
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        return l;
+    };
+    auto image = [&](int off, int b, int l) {
         Operand<OWN> v;
 #pragma unroll
-        for (int t = 0; t < OWN; ++t) v.t[t] = *(const u32x4 *)(lds + off + (b * OWN + t) * 1024 + 16 * lane);
+        for (int t = 0; t < OWN; ++t) v.t[t] = *(const u32x4 *)(lds + off + (b * OWN + t) * 1024 + 16 * l);
         return v;
     };
     const int n0 = 16 * wave;              // this wave's columns of dq and dk
@@ -92,12 +100,12 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
     const int h0 = grp * (a.H / a.G), h1 = h0 + a.H / a.G;
     // a thread brings eight columns of a token of do, e and z, a wave's lanes their
     // row of S and of D, the first wave's the gates
-    const int mytok = 16 * (wave & 3) + l16, mycol = 32 * (wave >> 2) + 8 * g;
     const bool whole = a.P % 8 == 0;
     u32x4 nd[2], ne[2], nz[2], ns[SL][2], nl[SL][2];
     float ng[3];
     double nsum;
     auto fetch = [&](int h, int p0) {
+        const int lane = fresh(), mytok = 16 * (wave & 3) + (lane & 15), mycol = 32 * (wave >> 2) + 8 * (lane >> 4);
         const ChunkRows dr(o.dy, at, a.reverse, first, live, (uint32_t)a.H * a.P * 4, (uint32_t)h * a.P * 4, a.P * 4);
         const ChunkRows er(o.e, at, a.reverse, first, live, (uint32_t)a.H * PP * 4, (uint32_t)h * PP * 4, PP * 4);
         const ChunkRows zr(o.z, at, a.reverse, first, live, (uint32_t)a.H * PP * 4, (uint32_t)h * PP * 4, PP * 4);
@@ -126,7 +134,8 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
         }
     };
     auto fetch_states = [&](int h, int p0, int s) {
-        const size_t from = (((size_t)slot * a.H + h) * N + n0 + l16) * PP + p0 + 32 * s + 8 * g;
+        const int lane = fresh();
+        const size_t from = (((size_t)slot * a.H + h) * N + n0 + (lane & 15)) * PP + p0 + 32 * s + 8 * (lane >> 4);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             ns[s][e] = *(const u32x4 *)(o.enter + from + 4 * e);
@@ -152,6 +161,7 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
         float along = 0.f, db = 0.f;   // <S, D> and e . z of this lane
         for (int p0 = 0; p0 < a.P; p0 += 32 * SL) {
             __syncthreads();
+            const int lane = fresh(), mytok = 16 * (wave & 3) + (lane & 15), mycol = 32 * (wave >> 2) + 8 * (lane >> 4);
             {
                 const f32x4 e0 = __builtin_bit_cast(f32x4, ne[0]), e1 = __builtin_bit_cast(f32x4, ne[1]);
                 const f32x4 z0 = __builtin_bit_cast(f32x4, nz[0]), z1 = __builtin_bit_cast(f32x4, nz[1]);
@@ -198,7 +208,7 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
                     for (int i = 0; i < 4; ++i) {
                         Operand<OWN> m[3];
 #pragma unroll
-                        for (int e = 0; e < 3; ++e) m[e] = image(im + e * kRow, i);
+                        for (int e = 0; e < 3; ++e) m[e] = image(im + e * kRow, i, lane);
 #pragma unroll
                         for (int q = OWN - 1; q >= 0; --q)
 #pragma unroll
@@ -214,11 +224,13 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
                     const int job = wave + W * t;
                     if (job >= 20) break;
                     const int l = job < 10 ? job : job - 10;
-                    x[t] = mm(image(im + (job < 10 ? 0 : 2) * kRow, lower_row(l)), image(im + kRow, lower_col(l)), x[t]);
+                    x[t] = mm(image(im + (job < 10 ? 0 : 2) * kRow, lower_row(l), lane), image(im + kRow, lower_col(l), lane), x[t]);
                 }
             }
         }
         __syncthreads();   // slices read: dP, dM and their transposes take their place
+        {
+        const int lane = fresh(), g = lane >> 4, l16 = lane & 15;
         if (wave < 4) {
             // tiles beyond the diagonal that share a block with one that is not
             const int b = wave == 0 ? lower_block(0, 0) : wave == 1 ? lower_block(2, 1) : wave == 2 ? upper_block(1, 0) : upper_block(3, 1);
@@ -263,29 +275,46 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
                 *(uint16_t *)(low + e * 1024 + 48) = (uint16_t)(hi[e] >> 16);
             }
         }
+        }
         __syncthreads();
         if (mine) {
-            uint32_t to = dqr.offset(4 * g) + 4 * (n0 + l16);
-            asm("" : "+v"(to));   // sixteen addresses kept over the heads would crowd out what is worked on
+            const int lane = fresh(), g = lane >> 4, l16 = lane & 15;
+            const uint32_t to = dqr.offset(4 * g) + 4 * (n0 + l16);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const f32x4 up = *(const f32x4 *)&gate[0][16 * i + 4 * g], down = *(const f32x4 *)&gate[1][16 * i + 4 * g];
                 const f32x4 beta = *(const f32x4 *)&gate[2][16 * i + 4 * g];
                 f32x4 q4 = acc[i][0] * (a.scale * up), rowk = -up * beta * acc[i][2], colk = down * beta * acc[i][1];
                 const f32x4 fall = colk;
-#pragma unroll
-                for (int s = 0; s < (i < 2 ? 1 : 2); ++s) {
-                    const Operand<OWN> m[2] = {image(0, lower_block(i, s)), image(kImage<OWN>, lower_block(i, s))};
-                    f32x4 two[2] = {q4, rowk};
-                    mm_tiles(m, kb[s], two);
-                    q4 = two[0];
-                    rowk = two[1];
-                }
+                // row i's blocks of dP and dM, and column i's, four results at a time
                 f32x4 more = zero4();
 #pragma unroll
-                for (int s = i < 2 ? 0 : 1; s < 2; ++s) {
-                    colk = mm(image(2 * kImage<OWN>, upper_block(i, s)), qb[s], colk);
-                    more = mm(image(3 * kImage<OWN>, upper_block(i, s)), kb[s], more);
+                for (int s = 0; s < 2; ++s) {
+                    const bool low = s < (i < 2 ? 1 : 2), up4 = s >= (i < 2 ? 0 : 1);
+                    Operand<OWN> m[4];
+                    if (low) {
+                        m[0] = image(0, lower_block(i, s), lane);
+                        m[1] = image(kImage<OWN>, lower_block(i, s), lane);
+                    }
+                    if (up4) {
+                        m[2] = image(2 * kImage<OWN>, upper_block(i, s), lane);
+                        m[3] = image(3 * kImage<OWN>, upper_block(i, s), lane);
+                    }
+#pragma unroll
+                    for (int q = OWN - 1; q >= 0; --q)
+#pragma unroll
+                        for (int t = 0; t <= q; ++t) {
+                            const int u = q - t;
+                            if (u >= IN) continue;
+                            if (low) {
+                                q4 = mfma16x16x32(m[0].t[t], kb[s].t[u], q4);
+                                rowk = mfma16x16x32(m[1].t[t], kb[s].t[u], rowk);
+                            }
+                            if (up4) {
+                                colk = mfma16x16x32(m[2].t[t], qb[s].t[u], colk);
+                                more = mfma16x16x32(m[3].t[t], kb[s].t[u], more);
+                            }
+                        }
                 }
                 colk += more;
 #pragma unroll
@@ -318,7 +347,7 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
         if (lane == 0) ends[wave] = along;
         db += __shfl_xor(db, 16);
         db += __shfl_xor(db, 32);
-        if (g == 0) dbs[wave >> 2][mytok] = db;
+        if (g == 0) dbs[wave >> 2][16 * (wave & 3) + l16] = db;
         __syncthreads();
         if (wave == 0) {
             // dG of this lane's token; the chunk's end is its last token's, which
