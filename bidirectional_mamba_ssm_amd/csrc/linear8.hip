@@ -4,15 +4,19 @@
 // order of the products shows in the result; they are converted to fp32 once
 // and scaled there.
 //
-// k_linear8: LDS tiles of 128 bytes of K, two buffers, v_mfma_i32_16x16x64_i8
-// (lane l: row l % 16, bytes 16 (l / 16) .. of K for both operands). w is the
-// first operand, so that a lane's four results lie in one row of out. Rows are
-// copied to LDS without passing through registers (global_load_lds, a wave's 64
-// lanes to consecutive 16-byte places: eight rows of 128 bytes); a row's chunk
-// c is kept at place c ^ (row % 8), which spreads the 16 rows that a fragment
-// read touches over the banks: the copy's lanes read their global chunks in
-// that order. A K that ends inside a step reads zeros there. Rows whose length
-// is no multiple of 16 go through registers (DIRECT = false).
+// k_linear8: v_mfma_i32_16x16x64_i8 (lane l: row l % 16, bytes 16 (l / 16) .. of K
+// for both operands), w the first operand, so that a lane's four results lie in
+// one row of out. Tiles of 64 bytes of K go to LDS without passing through
+// registers (global_load_lds: a wave's lanes to consecutive 16-byte places, 16
+// rows of 64 bytes, which is a fragment of each of the 16-row tiles as it is
+// read, without bank conflicts). Four buffers: while a step's products run, the
+// next step's fragments are read, the one after is landing and a third is asked
+// for, so a load has two steps' time and each step waits for one barrier
+// alone. A K that ends inside a step reads zeros there.
+//
+// k_linear8_rows: rows whose length is no multiple of 16, or that start
+// elsewhere, go through registers byte by byte where they end, in steps of 128
+// bytes and two buffers; chunk c of a row is kept at place c ^ (row % 8).
 //
 // k_linear8_few: up to 64 rows, where the weights' bytes are the work. A
 // workgroup takes 16 output channels; its eight waves split K and read both
@@ -43,45 +47,169 @@ __device__ __forceinline__ void store4(float *p, const float *v) { *(f4_a4 *)p =
 __device__ __forceinline__ void store1(uint16_t *p, float v) { *p = f2bf(v); }
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
 
-template <typename T>
-__device__ __forceinline__ void put(const Linear8Args &a, long long r, float xs, int n, i32x4 acc) {
-    T *out = (T *)a.out + r * a.cout + n;
-    float v[4];
+// Workgroup ids go round the 8 XCDs: each takes a run of tiles, eight row panels
+// under one another before the next channel panel, so that the tiles at work on
+// an XCD share both operands in its L2.
+template <int NT, int MT>
+__device__ __forceinline__ bool place(int ntiles, int mtiles, int &n0, long long &m0) {
+    const long long total = (long long)ntiles * mtiles, per = (total + 7) / 8;
+    const long long tile = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((long long)(blockIdx.x >> 3) >= per || tile >= total) return false;
+    const int band = (int)(tile / (8LL * ntiles)), tall = min(8, mtiles - 8 * band);
+    const long long in = tile - 8LL * band * ntiles;
+    n0 = (int)(in / tall) * NT;
+    m0 = (8LL * band + in % tall) * MT;
+    return true;
+}
+
+// A wave's results: row `row` and every 16th from it, channels n .. n + 3 and every
+// 16th. whole: none of the wave's lies outside.
+template <int TN, int TM, typename T>
+__device__ __forceinline__ void finish(const Linear8Args &a, long long row, int n, bool whole, i32x4 (&acc)[TN][TM]) {
+    float xs[TM];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int c = min(n + j, a.cout - 1);
-        v[j] = fmaf((float)acc[j], xs * a.ws[c], a.bias ? a.bias[c] : 0.f);
-    }
-    if (n + 3 < a.cout) {
-        store4(out, v);
-    } else {
+    for (int j = 0; j < TM; ++j) xs[j] = a.xs[min(row + 16 * j, a.rows - 1)];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (n + j < a.cout) store1(out + j, v[j]);
+    for (int i = 0; i < TN; ++i) {
+        const int c = n + 16 * i;
+        float ws[4], b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int at = min(c + e, a.cout - 1);
+            ws[e] = a.ws[at];
+            b[e] = a.bias ? a.bias[at] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+            T *out = (T *)a.out + (row + 16 * j) * a.cout + c;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = fmaf((float)acc[i][j][e], xs[j] * ws[e], b[e]);
+            if (whole) {
+                store4(out, v);
+            } else if (row + 16 * j < a.rows) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < a.cout) store1(out + e, v[e]);
+            }
+        }
     }
+}
+
+constexpr int KS = 64;   // bytes of K a step
+
+// WN x WM waves of 16 TN output channels by 16 TM rows each
+template <int WN, int WM, int TN, int TM, typename T>
+__global__ __launch_bounds__(64 * WN * WM) void k_linear8(Linear8Args a, int ntiles, int mtiles) {
+    constexpr int NT = 16 * TN * WN, MT = 16 * TM * WM, kWaves = WN * WM, kBufs = 4;
+    constexpr int kGroups = (NT + MT) / 16, kCopies = (kGroups + kWaves - 1) / kWaves;   // 16 rows each
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kBufs][(NT + MT) * KS];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, l16 = lane & 15;
+    int n0;
+    long long m0;
+    if (!place<NT, MT>(ntiles, mtiles, n0, m0)) return;
+    // this lane's 16 bytes of a copied row, and its rows; waves without a last copy
+    // repeat one, so that all have as many loads under way
+    const int chunk = 16 * (lane & 3);
+    const int8_t *src[kCopies];
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+        const int r = min(i * kWaves + wave, kGroups - 1) * 16 + (lane >> 2);
+        src[i] = (r < NT ? a.w + (long long)min(n0 + r, a.cout - 1) * a.cin : a.x + min(m0 + r - NT, a.rows - 1) * a.cin) + chunk;
+    }
+    const int steps = (a.cin + KS - 1) / KS;
+    // whole: the step does not reach past the rows' end
+    auto fetch = [&](int s, bool whole) {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int8_t *p = src[i] + s * KS;
+            if (!whole && s * KS + chunk >= a.cin) p = (const int8_t *)kZeros;
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) void *)p,
+                (__attribute__((address_space(3))) void *)(lds[s % kBufs] + min(i * kWaves + wave, kGroups - 1) * 1024), 16,
+                0, 0);
+        }
+    };
+    const int wn = (wave / WM) * 16 * TN, wm = (wave % WM) * 16 * TM;
+    u32x4 av[2][TN], bv[2][TM];
+    auto read = [&](int s, u32x4 *av, u32x4 *bv) {
+        const uint8_t *p = lds[s % kBufs] + l16 * KS + 16 * g;
+#pragma unroll
+        for (int i = 0; i < TN; ++i) av[i] = *(const u32x4 *)(p + (wn + 16 * i) * KS);
+#pragma unroll
+        for (int j = 0; j < TM; ++j) bv[j] = *(const u32x4 *)(p + (NT + wm + 16 * j) * KS);
+    };
+    i32x4 acc[TN][TM];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    // a barrier that no access of memory moves across (and that waits for none)
+    auto meet = [&]() {
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    };
+    auto products = [&](int cur) {
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int j = 0; j < TM; ++j) acc[i][j] = mfma_i8(av[cur][i], bv[cur][j], acc[i][j]);
+    };
+    // step s: its fragments are in registers, s + 1 landed or landing, s + 2 under
+    // way; after the barrier everybody's part of s + 1 is there, and nobody reads
+    // s - 1 any more
+    auto inner = [&](int s, int cur) {
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCopies) : "memory");
+        meet();
+        fetch(s + 3, true);
+        read(s + 1, av[cur ^ 1], bv[cur ^ 1]);
+        products(cur);
+    };
+    auto outer = [&](int s, int cur) {
+        if (s + 1 < steps) {
+            if (s + 2 < steps) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kCopies) : "memory");
+            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            meet();
+            if (s + 3 < steps) fetch(s + 3, false);
+            read(s + 1, av[cur ^ 1], bv[cur ^ 1]);
+        }
+        products(cur);
+    };
+    fetch(0, false);
+    if (steps > 1) fetch(1, false);
+    if (steps > 2) fetch(2, false);
+    if (steps > 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kCopies) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    meet();
+    read(0, av[0], bv[0]);
+    int s = 0;
+    for (; s + 5 < steps; s += 2) {
+        inner(s, 0);
+        inner(s + 1, 1);
+    }
+    for (; s < steps; s += 2) {
+        outer(s, 0);
+        if (s + 1 < steps) outer(s + 1, 1);
+    }
+    if (n0 + NT <= a.cout && m0 + MT <= a.rows) finish<TN, TM, T>(a, m0 + wm + l16, n0 + wn + 4 * g, true, acc);
+    else finish<TN, TM, T>(a, m0 + wm + l16, n0 + wn + 4 * g, false, acc);
 }
 
 constexpr int KB = 128;   // bytes of K a step
 
 // WN x WM waves of 16 TN output channels by 16 TM rows each
-template <int WN, int WM, int TN, int TM, bool DIRECT, typename T>
-__global__ __launch_bounds__(64 * WN * WM) void k_linear8(Linear8Args a, int ntiles, int mtiles) {
+template <int WN, int WM, int TN, int TM, typename T>
+__global__ __launch_bounds__(64 * WN * WM) void k_linear8_rows(Linear8Args a, int ntiles, int mtiles) {
     constexpr int NT = 16 * TN * WN, MT = 16 * TM * WM;
     constexpr int kCopies = (NT + MT) / 8 / (WN * WM);   // eight rows each, a wave
     static_assert((NT / 8) % (WN * WM) == 0 && (MT / 8) % (WN * WM) == 0, "a copy is of one operand");
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][(NT + MT) * KB];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l16 = lane & 15;
-    // workgroup ids go round the 8 XCDs: each takes a run of tiles, eight row
-    // panels under one another before the next channel panel, so that the
-    // tiles at work on an XCD share both operands in its L2
-    const long long total = (long long)ntiles * mtiles, per = (total + 7) / 8;
-    const long long tile = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((long long)(blockIdx.x >> 3) >= per || tile >= total) return;
-    const int band = (int)(tile / (8LL * ntiles)), tall = min(8, mtiles - 8 * band);
-    const long long in = tile - 8LL * band * ntiles;
-    const int n0 = (int)(in / tall) * NT;
-    const long long m0 = (8LL * band + in % tall) * MT;
+    int n0;
+    long long m0;
+    if (!place<NT, MT>(ntiles, mtiles, n0, m0)) return;
     // this lane's chunk of a copied row, and its rows
     const int row8 = lane >> 3, chunk = 16 * ((lane & 7) ^ row8);
     const int8_t *src[kCopies];
@@ -91,42 +219,26 @@ __global__ __launch_bounds__(64 * WN * WM) void k_linear8(Linear8Args a, int nti
         if (i * WN * WM * 8 < NT) src[i] = a.w + (long long)min(n0 + rg, a.cout - 1) * a.cin;
         else src[i] = a.x + min(m0 + rg - NT, a.rows - 1) * a.cin;
     }
-    u32x4 held[DIRECT ? 1 : kCopies];
-    auto fetch = [&](int k0, int buf) {
-        if constexpr (DIRECT) {
-            const bool ends = k0 + KB > a.cin;
+    u32x4 held[kCopies];
+    auto fetch = [&](int k0) {
 #pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const int8_t *p = src[i] + k0 + chunk;
-                if (ends && k0 + chunk >= a.cin) p = (const int8_t *)kZeros;
-                __builtin_amdgcn_global_load_lds(
-                    (const __attribute__((address_space(1))) void *)p,
-                    (__attribute__((address_space(3))) void *)(lds[buf] + (i * WN * WM + wave) * 1024), 16, 0, 0);
-            }
-        } else {
+        for (int i = 0; i < kCopies; ++i) {
+            const int at = k0 + chunk, left = a.cin - at;
+            if (left >= 16) {
+                held[i] = *(const b16_a1 *)(src[i] + at);
+            } else {
+                u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const int at = k0 + chunk, left = a.cin - at;
-                if (left >= 16) {
-                    held[i] = *(const b16_a1 *)(src[i] + at);
-                } else {
-                    u32x4 v = {0u, 0u, 0u, 0u};
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (j < left) v[j >> 2] |= (uint32_t)(uint8_t)src[i][at + j] << (8 * (j & 3));
-                    held[i] = v;
-                }
+                for (int j = 0; j < 16; ++j)
+                    if (j < left) v[j >> 2] |= (uint32_t)(uint8_t)src[i][at + j] << (8 * (j & 3));
+                held[i] = v;
             }
         }
     };
     auto settle = [&](int buf) {
-        if constexpr (DIRECT) {
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        } else {
 #pragma unroll
-            for (int i = 0; i < kCopies; ++i)
-                *(u32x4 *)(lds[buf] + (i * WN * WM + wave) * 1024 + 16 * lane) = held[i];
-        }
+        for (int i = 0; i < kCopies; ++i)
+            *(u32x4 *)(lds[buf] + (i * WN * WM + wave) * 1024 + 16 * lane) = held[i];
         __syncthreads();
     };
     const int wn = (wave / WM) * 16 * TN, wm = (wave % WM) * 16 * TM;
@@ -135,12 +247,12 @@ __global__ __launch_bounds__(64 * WN * WM) void k_linear8(Linear8Args a, int nti
     for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    fetch(0, 0);
+    fetch(0);
     settle(0);
     const int steps = (a.cin + KB - 1) / KB;
     for (int s = 0; s < steps; ++s) {
         const int cur = s & 1;
-        if (s + 1 < steps) fetch((s + 1) * KB, cur ^ 1);
+        if (s + 1 < steps) fetch((s + 1) * KB);
         const uint8_t *wl = lds[cur], *xl = lds[cur] + NT * KB;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -158,17 +270,8 @@ __global__ __launch_bounds__(64 * WN * WM) void k_linear8(Linear8Args a, int nti
         // the other buffer is complete, and this one read, before either changes
         settle(cur ^ 1);
     }
-#pragma unroll
-    for (int j = 0; j < TM; ++j) {
-        const long long r = m0 + wm + 16 * j + l16;
-        if (r >= a.rows) continue;
-        const float xs = a.xs[r];
-#pragma unroll
-        for (int i = 0; i < TN; ++i) {
-            const int n = n0 + wn + 16 * i + 4 * g;
-            if (n < a.cout) put<T>(a, r, xs, n, acc[i][j]);
-        }
-    }
+    if (n0 + NT <= a.cout && m0 + MT <= a.rows) finish<TN, TM, T>(a, m0 + wm + l16, n0 + wn + 4 * g, true, acc);
+    else finish<TN, TM, T>(a, m0 + wm + l16, n0 + wn + 4 * g, false, acc);
 }
 
 constexpr int kFewWaves = 8;
@@ -213,9 +316,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_linear8_few(Linear8Args a) {
         i32x4 s = sums[0][j][lane];
 #pragma unroll
         for (int i = 1; i < kFewWaves; ++i) s += sums[i][j][lane];
-        const long long r = 16 * j + l16;
-        const int n = n0 + 4 * g;
-        if (r < a.rows && n < a.cout) put<T>(a, r, a.xs[r], n, s);
+        i32x4 one[1][1] = {{s}};
+        finish<1, 1, T>(a, 16 * j + l16, n0 + 4 * g, n0 + 16 <= a.cout && 16 * j + 16 <= a.rows, one);
     }
 }
 
@@ -225,8 +327,9 @@ hipError_t launch_tiles(const Linear8Args &a, hipStream_t s) {
     const int nt = (a.cout + NT - 1) / NT, mt = (int)((a.rows + MT - 1) / MT);
     const long long wgs = ((long long)nt * mt + 7) / 8 * 8;
     if (wgs > (1LL << 24) - 8) return hipErrorInvalidValue;
-    BM_LAUNCH("linear8", (k_linear8<WN, WM, TN, TM, DIRECT, T>), dim3((unsigned)wgs), dim3(64 * WN * WM), 0, s, a, nt,
-              mt);
+    const dim3 grid((unsigned)wgs), block(64 * WN * WM);
+    if constexpr (DIRECT) BM_LAUNCH("linear8", (k_linear8<WN, WM, TN, TM, T>), grid, block, 0, s, a, nt, mt);
+    else BM_LAUNCH("linear8_rows", (k_linear8_rows<WN, WM, TN, TM, T>), grid, block, 0, s, a, nt, mt);
     return hipGetLastError();
 }
 
@@ -243,7 +346,24 @@ hipError_t launch_t(const Linear8Args &a, hipStream_t s) {
     auto tiles = [&](int nt, int mt) { return ((a.cout + nt - 1) / nt) * ((a.rows + mt - 1) / mt); };
     if (!direct) return tiles(128, 128) >= 256 ? launch_tiles<2, 2, 4, 4, false, T>(a, s)
                                                : launch_tiles<2, 2, 2, 2, false, T>(a, s);
-    if (tiles(256, 256) >= 256) return launch_tiles<2, 4, 8, 4, true, T>(a, s);
+    if (tiles(256, 256) >= 200) {
+        // one workgroup a CU: the width whose rounds of 256 tiles take the least time
+        int best = 256;
+        long long least = 0;
+        for (int w = 256; w >= 160; w -= 32) {
+            const long long t = (tiles(w, 256) + 255) / 256 * (w + 16);
+            if (!least || t < least) {
+                least = t;
+                best = w;
+            }
+        }
+        switch (best) {
+            case 160: return launch_tiles<2, 4, 5, 4, true, T>(a, s);
+            case 192: return launch_tiles<2, 4, 6, 4, true, T>(a, s);
+            case 224: return launch_tiles<2, 4, 7, 4, true, T>(a, s);
+        }
+        return launch_tiles<2, 4, 8, 4, true, T>(a, s);
+    }
     if (tiles(128, 128) >= 256) return launch_tiles<2, 2, 4, 4, true, T>(a, s);
     return launch_tiles<2, 2, 2, 2, true, T>(a, s);
 }
