@@ -287,7 +287,6 @@ typedef __attribute__((address_space(3))) v4i16_d lds_v4i16_d;
 struct WalkArgs {
     PrepDir dir[2];
     int ndir;          // FWD: both directions' outputs are added, the reverse one's first
-    int blocks;        // workgroups of a head
 };
 
 // Where element (row, col) of K or Q is in LDS, col a multiple of 4: four
@@ -313,18 +312,19 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
     constexpr int NP = N < 32 ? 32 : N, KS = NP / 32, NT = N / 16;
     constexpr int kRows = C * NP * 2 * IN;              // bytes of K or Q in LDS
     constexpr bool kStaged = sizeof(X) == 2;            // the third input comes through LDS
-    constexpr int kThreads = 64 * W, VS = 16 * W + 16;  // row stride of the third input in LDS, elements
+    constexpr int kThreads = 64 * W;
     constexpr bool kQ = MODE != KEEP;                   // Q read, and a second image
     constexpr int kImages = kQ ? 2 : 1, kImg = kImage<OWN>;
-    constexpr int kBuf = kRows * (kQ ? 2 : 1) + kImg * kImages + kGates * 4 + (kStaged ? C * VS * 2 : 0);
-    __shared__ __attribute__((aligned(16))) uint8_t buf[kBuf];
+    constexpr int kBuf = kRows * (kQ ? 2 : 1) + kImg * kImages + kGates * 4, kOwn = kStaged ? W * C * 32 : 0;
+    // two buffers where one workgroup has the CU, and they fit
+    constexpr bool kTwo = 2 * kBuf + kOwn <= 160 * 1024 && (sizeof(T) == 4 || W == 8);
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kBuf * (kTwo ? 2 : 1) + kOwn];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l16 = lane & 15;
-    const long long work = (long long)args.dir[0].a.units * args.dir[0].a.H * args.blocks, mine = xcd_order(work);
+    const long long work = (long long)args.dir[0].a.units * args.dir[0].a.H, mine = xcd_order(work);
     if (mine >= work) return;
-    const int block = (int)(mine % args.blocks), h = (int)(mine / args.blocks % args.dir[0].a.H);
-    const int u = (int)(mine / args.blocks / args.dir[0].a.H);
-    const int p0 = (block * W + wave) * 16;
+    const int h = (int)(mine % args.dir[0].a.H), u = (int)(mine / args.dir[0].a.H);
+    const int p0 = wave * 16;
     // the wave has columns, those of the walks' own arrays past the head's width among them
     const bool works = p0 < (GRAD ? padded(args.dir[0].a.P) : args.dir[0].a.P);
     // the halves of blocks that lie beyond the diagonal stay zeros
@@ -332,8 +332,10 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
         const int which = i / (2 * OWN * 64), e = i / 64 % (2 * OWN), term = e % OWN, second = e / OWN;
         const int half = MODE == BACK ? 2 * (second ? upper_block(3, 1) : upper_block(1, 0))
                                       : 2 * (second ? lower_block(2, 1) : lower_block(0, 0)) + 1;
-        *(u32x2 *)(buf + (kQ ? 2 : 1) * kRows + which * kImg + ((half >> 1) * OWN + term) * 1024 + 16 * lane +
-                   8 * (half & 1)) = u32x2{0u, 0u};
+#pragma unroll
+        for (int b = 0; b < (kTwo ? 2 : 1); ++b)
+            *(u32x2 *)(lds + b * kBuf + (kQ ? 2 : 1) * kRows + which * kImg + ((half >> 1) * OWN + term) * 1024 +
+                       16 * lane + 8 * (half & 1)) = u32x2{0u, 0u};
     }
     for (int di = args.ndir - 1; di >= 0; --di) {
         const PrepDir &pd = args.dir[di];
@@ -352,7 +354,7 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
             S[t] = zero4();
             if (a.init && own) S[t] = *(const f32x4 *)(a.init + state + 16 * t);
         }
-        // the next chunk on its way: rows of K and Q, images, gates, the third input
+        // chunks on their way: rows of K and Q, images, gates, the third input
         constexpr int V = 16 / sizeof(T), kAll = C * NP / V, kVecs = (kAll + kThreads - 1) / kThreads;
         constexpr int kVi = (kImages * kTiles + W - 1) / W;
         u32x4 nk[kVecs], nq[kQ ? kVecs : 1], ni[kVi], nv[2];
@@ -383,7 +385,7 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
             }
         };
         auto fetch = [&](int chunk) {
-            const int tid = fresh(threadIdx.x), g = (tid & 63) >> 4;
+            const int tid = fresh(threadIdx.x);
             const int first = chunk * C, live = min(C, at.len - first);
             const size_t sh = (size_t)(at.slot + chunk) * a.H + h;
             const __amdgpu_buffer_rsrc_t ir = __builtin_amdgcn_make_buffer_rsrc(
@@ -391,14 +393,14 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
 #pragma unroll
             for (int i = 0; i < kVi; ++i) ni[i] = buf16(ir, 16 * (tid + kThreads * i));
             if (tid < kGates) ngate = pd.gates[sh * kGateFloats + tid];
-            const uint32_t xrow = (uint32_t)(a.H * a.P * sizeof(X));
-            const ChunkRows xr(a.v, at, a.reverse, first, live, xrow, (uint32_t)(h * a.P * sizeof(X)), a.P * sizeof(X));
             if constexpr (kStaged) {
+                const ChunkRows xr(a.v, at, a.reverse, first, live, (uint32_t)(a.H * a.P * sizeof(X)),
+                                   (uint32_t)(h * a.P * sizeof(X)), a.P * sizeof(X));
+                // eight of the wave's columns
+                const int c = p0 + 8 * (tid & 1);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    // eight columns of the workgroup's
-                    const int e = tid + kThreads * i, c = 16 * W * block + e % (2 * W) * 8;
-                    const uint32_t from = xr.offset(e / (2 * W));
+                    const uint32_t from = xr.offset(((tid & 63) >> 1) + 32 * i);
                     if (whole) {
                         nv[i] = buf16(xr.rsrc, from + (c < a.P ? 2 * c : kFar));
                     } else {
@@ -409,7 +411,13 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
                                            << 16;
                     }
                 }
-            } else {
+            }
+        };
+        auto fetch_values = [&](int chunk) {
+            if constexpr (!kStaged) {
+                const int first = chunk * C, live = min(C, at.len - first), g = (fresh(threadIdx.x) & 63) >> 4;
+                const ChunkRows xr(a.v, at, a.reverse, first, live, (uint32_t)(a.H * a.P * sizeof(X)),
+                                   (uint32_t)(h * a.P * sizeof(X)), a.P * sizeof(X));
                 const uint32_t to = xr.offset(4 * g) + (own ? (uint32_t)(p * sizeof(X)) : kFar);
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
@@ -417,7 +425,7 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
                     for (int r = 0; r < 4; ++r) nx[t][r] = buf_value(xr.rsrc, to + (16 * t + r) * xr.step, X());
             }
         };
-        auto stash = [&]() {
+        auto stash = [&](uint8_t *buf) {
             const int tid = fresh(threadIdx.x), lane = tid & 63;
 #pragma unroll
             for (int w = 0; w < (kQ ? 2 : 1); ++w)
@@ -455,29 +463,33 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
             if (tid < kGates) *(float *)(buf + (kQ ? 2 : 1) * kRows + kImages * kImg + 4 * tid) = ngate;
             if constexpr (kStaged) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int e = tid + kThreads * i;
-                    *(u32x4 *)(buf + kBuf - C * VS * 2 + 2 * (e / (2 * W) * VS + e % (2 * W) * 8)) = nv[i];
-                }
+                for (int i = 0; i < 2; ++i) *(u32x4 *)(lds + sizeof(lds) - kOwn + wave * C * 32 + 1024 * i + 16 * lane) = nv[i];
             }
         };
         if (di != args.ndir - 1) __syncthreads();   // the direction before has read its last chunk
         if (chunks > 0) {
             fetch(order(0));
             fetch_rows(order(0));
-            stash();
+            fetch_values(order(0));
+            stash(lds);
+            if (kTwo && chunks > 1) {
+                fetch(order(1));
+                fetch_rows(order(1));
+            }
         }
         for (int step = 0; step < chunks; ++step) {
             const int chunk = order(step), first = chunk * C, live = min(C, at.len - first);
             __syncthreads();
             const int lane = fresh(threadIdx.x & 63), g = lane >> 4, l16 = lane & 15;
+            const int cur = kTwo ? step & 1 : 0;
+            uint8_t *buf = lds + cur * kBuf;
             f32x4 x[4];
             if constexpr (kStaged) {
                 // a tile's columns as lanes, four rows a lane: a result's order
-                const uint16_t *v = (const uint16_t *)(buf + kBuf - C * VS * 2) + (4 * g + (l16 >> 2)) * VS + 16 * wave + 4 * (l16 & 3);
+                const uint16_t *v = (const uint16_t *)(lds + sizeof(lds) - kOwn + wave * C * 32) + 4 * lane;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
-                    const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_d *)(v + 16 * t * VS)));
+                    const u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16_d *)(v + 256 * t)));
                     x[t] = f32x4{__uint_as_float(r[0] << 16), __uint_as_float(r[0] & 0xffff0000u),
                                  __uint_as_float(r[1] << 16), __uint_as_float(r[1] & 0xffff0000u)};
                 }
@@ -488,7 +500,20 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
                     for (int r = 0; r < 4; ++r) x[t][r] = nx[t][r];
             }
             const bool more = step + 1 < chunks;
-            if (more) fetch(order(step + 1));
+            if (more) fetch_values(order(step + 1));
+            if (!kTwo && more) fetch(order(step + 1));
+            // between the chunk's two halves
+            auto middle = [&]() {
+                if constexpr (kTwo) {
+                    if (more) stash(lds + (cur ^ 1) * kBuf);
+                    if (step + 2 < chunks) {
+                        fetch(order(step + 2));
+                        fetch_rows(order(step + 2));
+                    }
+                } else if (more) {
+                    fetch_rows(order(step + 1));
+                }
+            };
             const uint8_t *kl = buf, *ql = buf + kRows;
             const uint8_t *one = buf + (kQ ? 2 : 1) * kRows, *two = one + kImg;
             const float *gate = (const float *)(one + kImages * kImg);
@@ -570,7 +595,7 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
                         mm_tiles(r, sb, out);
                     }
                 }
-                if (more) fetch_rows(order(step + 1));
+                middle();
                 Operand<OWN> b[2], kb[2];   // kb: what K^T multiplies
                 if constexpr (MODE != BACK) {
 #pragma unroll
@@ -633,13 +658,15 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
                     for (int t = 0; t < 4; ++t) out[t] = ks[t];
                 }
             }
-            else if (more) {
-                fetch_rows(order(step + 1));
+            else {
+                middle();
             }
-            __syncthreads();
-            // the next chunk goes to LDS before this one's results go out, so that
-            // nothing waits for stores
-            if (more) stash();
+            if constexpr (!kTwo) {
+                __syncthreads();
+                // the next chunk goes to LDS before this one's results go out, so that
+                // nothing waits for stores
+                if (more) stash(buf);
+            }
             if (works) {
                 const int P = GRAD ? PP : a.P;
                 const ChunkRows yr(a.y, at, a.reverse, first, live, (uint32_t)(a.H * P * 4), (uint32_t)(h * P * 4), P * 4);
@@ -684,7 +711,6 @@ struct Chunked {
         w.dir[1] = d[ndir - 1];
         w.ndir = ndir;
         const DeltaArgs &a = d[0].a;
-        w.blocks = 1;
         const dim3 grid((unsigned)xcd_grid((long long)a.units * a.H));
         if (a.P > 64) BM_LAUNCH(names[MODE], (k_delta_walk<T, N, MODE, 8>), grid, dim3(512), 0, s, w);
         else BM_LAUNCH(names[MODE], (k_delta_walk<T, N, MODE, 4>), grid, dim3(256), 0, s, w);
