@@ -1580,7 +1580,11 @@ int bimamba_delta_workspace_size(const bimamba_shape *s, int has_bwd, int nseq, 
     int rc = check_delta_shape(s, nseq, false);
     if (rc) return rc;
     if (!bytes) return fail(BIMAMBA_EINVAL, "bytes is NULL");
-    *bytes = delta_table(nseq) + (delta_chunked(s, nseq) ? (has_bwd ? 2 : 1) * delta_dir_workspace(s, nseq, false) : 0);
+    *bytes = delta_table(nseq);
+    if (delta_chunked(s, nseq)) {
+        *bytes += (has_bwd ? 2 : 1) * delta_dir_workspace(s, nseq, false);
+        if (has_bwd && delta_apart(nseq ? nseq : s->batch, s->nheads)) *bytes += align256(delta_sizes(s, nseq).y);
+    }
     return BIMAMBA_OK;
 }
 
@@ -1636,6 +1640,10 @@ int bimamba_delta_fwd(const bimamba_shape *s, const bimamba_delta_dir *fwd, cons
         parts[i] = ws + i * part;
     }
     if (delta_chunked(s, packed)) {
+        if (ndir == 2 && delta_apart(a[0].units, s->nheads)) {
+            a[0].add = false;
+            a[1].y = (float *)(ws + 2 * part);
+        }
         e = launch_delta_chunked(a, ndir, bf16, parts, st);
     } else {
         e = ndir == 2 ? launch_delta_seq(a[1], bf16, st) : hipSuccess;
@@ -1656,16 +1664,21 @@ int bimamba_delta_step(const bimamba_shape *s, float *state, const bimamba_delta
 
 namespace {
 
-// The gradient's workspace, one direction at a time: offsets, images and gates,
-// e and z, the chunks' states and their gradients.
+// The gradient's workspace: offsets, then a direction's triangles and gates, e and
+// z, the chunks' states and their gradients, sums over parts of the heads; the reverse direction uses the same,
+// or where the two go side by side its own.
 struct DeltaBwdLayout {
-    size_t chunked, row, states;
+    size_t chunked, row, states, parts;
+    bool apart;
     explicit DeltaBwdLayout(const bimamba_shape *s, int nseq) {
         chunked = delta_dir_workspace(s, nseq, true);
         row = align256(delta_rows_bytes(delta_sized(s, nseq)));
         states = align256(delta_states_bytes(delta_sized(s, nseq)));
+        parts = align256(delta_parts_bytes(delta_sized(s, nseq)));
+        apart = delta_apart(nseq ? nseq : s->batch, s->nheads);
     }
-    size_t total(int nseq) const { return delta_table(nseq) + chunked + 2 * row + 2 * states; }
+    size_t direction() const { return chunked + 2 * row + 2 * states + parts; }
+    size_t total(int nseq) const { return delta_table(nseq) + (apart ? 2 : 1) * direction(); }
 };
 
 }  // namespace
@@ -1744,27 +1757,39 @@ int bimamba_delta_bwd(const bimamba_shape *s, const bimamba_delta_dir *fwd, cons
     }
     ws += delta_table(packed);
     const DeltaBwdLayout lay(s, packed);
-    void *chunked = ws;
-    float *errors = (float *)(ws + lay.chunked), *zs = (float *)((char *)errors + lay.row);
-    float *enter = (float *)((char *)zs + lay.row), *leave = (float *)((char *)enter + lay.states);
-    for (int i = 0; i < (bwd ? 2 : 1); ++i) {
-        DeltaArgs a = delta_args(s, dirs[i], scale, cu, nseq, i == 1);
-        a.init = i ? nullptr : init_state;
-        a.y = errors;
-        a.states = enter;
-        if (!empty && (e = launch_delta_keep(a, bf16, chunked, st)) != hipSuccess)
+    const int ndir = bwd ? 2 : 1, at_once = lay.apart ? ndir : 1;
+    for (int i0 = 0; i0 < ndir; i0 += at_once) {
+        DeltaArgs a[2];
+        DeltaGradArgs o[2];
+        void *chunked[2];
+        for (int j = 0; j < at_once; ++j) {
+            const int i = i0 + j;
+            const bimamba_delta_grad *g = grads[i];
+            a[j] = delta_args(s, dirs[i], scale, cu, nseq, i == 1);
+            char *from = ws + j * lay.direction();
+            chunked[j] = from;
+            float *errors = (float *)(from + lay.chunked), *zs = (float *)((char *)errors + lay.row);
+            float *enter = (float *)((char *)zs + lay.row), *leave = (float *)((char *)enter + lay.states);
+            o[j] = {dy, errors, zs, enter, leave, delta_gates(a[j], from), g->dq, g->dk, g->dv, g->dg, g->dbeta,
+                    (float *)((char *)leave + lay.states)};
+            a[j].init = i ? nullptr : init_state;
+            a[j].y = errors;
+            a[j].states = enter;
+        }
+        if (!empty && (e = launch_delta_keep(a, at_once, bf16, chunked, st)) != hipSuccess)
             return hip_fail(e, "launching the delta rule");
-        a.v = dy;
-        a.init = i ? nullptr : dfinal;
-        a.last = i ? nullptr : dinit;
-        a.y = zs;
-        a.states = leave;
-        if ((!empty || a.last) && (e = launch_delta_back(a, bf16, chunked, st)) != hipSuccess)
+        for (int j = 0; j < at_once; ++j) {
+            const int i = i0 + j;
+            a[j].v = dy;
+            a[j].init = i ? nullptr : dfinal;
+            a[j].last = i ? nullptr : dinit;
+            a[j].y = const_cast<float *>(o[j].z);
+            a[j].states = const_cast<float *>(o[j].leave);
+        }
+        // of an empty problem the state's gradient alone, which is the forward direction's
+        if ((!empty || a[0].last) && (e = launch_delta_back(a, empty ? 1 : at_once, bf16, chunked, st)) != hipSuccess)
             return hip_fail(e, "launching the delta rule's walk back");
-        if (empty) continue;
-        const bimamba_delta_grad *g = grads[i];
-        const DeltaGradArgs o = {dy, errors, zs, enter, leave, delta_gates(a, chunked), g->dq, g->dk, g->dv, g->dg, g->dbeta};
-        if ((e = launch_delta_grad(a, o, bf16, st)) != hipSuccess)
+        if (!empty && (e = launch_delta_grad(a, o, at_once, bf16, st)) != hipSuccess)
             return hip_fail(e, "launching the delta rule's gradient");
     }
     return BIMAMBA_OK;

@@ -37,6 +37,7 @@ struct DeltaGradArgs {
     const float *enter, *leave;      // [slot][H][N][P rounded up]: incoming states, gradients of the outgoing
     const float *gates;              // the preparing kernel's (delta_gates)
     float *dq, *dk, *dv, *dg, *dbeta;
+    float *parts;                    // [delta_grad_parts - 1][dq, dk][tok][G][N]
 };
 
 // A unit's chunk c is kept in slot first_slot + c. Packed units' slots are
@@ -92,12 +93,19 @@ hipError_t launch_delta_seq(const DeltaArgs &a, bool bf16, hipStream_t s);
 // the gradients of the outgoing (with the workspace that the call before filled)
 size_t delta_chunk_workspace(const DeltaArgs &a, bool grad);
 hipError_t launch_delta_chunked(const DeltaArgs *a, int ndir, bool bf16, void *const *ws, hipStream_t s);
-hipError_t launch_delta_keep(const DeltaArgs &a, bool bf16, void *ws, hipStream_t s);
-hipError_t launch_delta_back(const DeltaArgs &a, bool bf16, void *ws, hipStream_t s);
+hipError_t launch_delta_keep(const DeltaArgs *a, int ndir, bool bf16, void *const *ws, hipStream_t s);
+hipError_t launch_delta_back(const DeltaArgs *a, int ndir, bool bf16, void *const *ws, hipStream_t s);
 const float *delta_gates(const DeltaArgs &a, void *ws);
 // delta_grad.hip, and the bytes of e or z, and of the kept states or their gradients
 size_t delta_rows_bytes(const DeltaArgs &a);
+size_t delta_parts_bytes(const DeltaArgs &a);
 size_t delta_states_bytes(const DeltaArgs &a);
-hipError_t launch_delta_grad(const DeltaArgs &a, const DeltaGradArgs &o, bool bf16, hipStream_t s);
+hipError_t launch_delta_grad(const DeltaArgs *a, const DeltaGradArgs *o, int ndir, bool bf16, hipStream_t s);
+
+// A walk keeps one CU a head and unit busy: where both directions' fit on the 256
+// CUs they go side by side, each with arrays of its own (a[1].y is not a[0].y then,
+// and is added to it). One after the other the 66 heads of eleven packed
+// sequences took 73 us, side by side 38.
+inline bool delta_apart(int units, int H) { return 2LL * units * H <= 256; }
 
 }  // namespace bm

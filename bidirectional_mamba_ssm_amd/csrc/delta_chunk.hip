@@ -286,7 +286,9 @@ typedef __attribute__((address_space(3))) v4i16_d lds_v4i16_d;
 
 struct WalkArgs {
     PrepDir dir[2];
-    int ndir;          // FWD: both directions' outputs are added, the reverse one's first
+    int ndir;          // FWD, one after the other: the forward output is added to the reverse one's
+    int blocks;        // workgroups of a head
+    bool apart;        // side by side, blockIdx.y the direction
 };
 
 // Where element (row, col) of K or Q is in LDS, col a multiple of 4: four
@@ -321,10 +323,11 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
     __shared__ __attribute__((aligned(16))) uint8_t lds[kBuf * (kTwo ? 2 : 1) + kOwn];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l16 = lane & 15;
-    const long long work = (long long)args.dir[0].a.units * args.dir[0].a.H, mine = xcd_order(work);
+    const long long work = (long long)args.dir[0].a.units * args.dir[0].a.H * args.blocks, mine = xcd_order(work);
     if (mine >= work) return;
-    const int h = (int)(mine % args.dir[0].a.H), u = (int)(mine / args.dir[0].a.H);
-    const int p0 = wave * 16;
+    const int block = (int)(mine % args.blocks), h = (int)(mine / args.blocks % args.dir[0].a.H);
+    const int u = (int)(mine / args.blocks / args.dir[0].a.H);
+    const int p0 = (block * W + wave) * 16;
     // the wave has columns, those of the walks' own arrays past the head's width among them
     const bool works = p0 < (GRAD ? padded(args.dir[0].a.P) : args.dir[0].a.P);
     // the halves of blocks that lie beyond the diagonal stay zeros
@@ -337,7 +340,8 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
             *(u32x2 *)(lds + b * kBuf + (kQ ? 2 : 1) * kRows + which * kImg + ((half >> 1) * OWN + term) * 1024 +
                        16 * lane + 8 * (half & 1)) = u32x2{0u, 0u};
     }
-    for (int di = args.ndir - 1; di >= 0; --di) {
+    const int d0 = args.apart ? blockIdx.y : 0, d1 = args.apart ? blockIdx.y : args.ndir - 1;
+    for (int di = d1; di >= d0; --di) {
         const PrepDir &pd = args.dir[di];
         const DeltaArgs &a = pd.a;
         const int grp = h / (a.H / a.G), PP = padded(a.P);
@@ -466,7 +470,7 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
                 for (int i = 0; i < 2; ++i) *(u32x4 *)(lds + sizeof(lds) - kOwn + wave * C * 32 + 1024 * i + 16 * lane) = nv[i];
             }
         };
-        if (di != args.ndir - 1) __syncthreads();   // the direction before has read its last chunk
+        if (di != d1) __syncthreads();   // the direction before has read its last chunk
         if (chunks > 0) {
             fetch(order(0));
             fetch_rows(order(0));
@@ -690,6 +694,16 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
     }
 }
 
+// y += other, with both directions' outputs
+__global__ __launch_bounds__(256) void k_delta_join(float *y, const float *other, long long n) {
+    const long long i = 4 * (blockIdx.x * 256LL + threadIdx.x);
+    if (i + 4 <= n) {
+        *(f32x4 *)(y + i) += *(const f32x4 *)(other + i);
+    } else {
+        for (long long j = i; j < n; ++j) y[j] += other[j];
+    }
+}
+
 template <typename T, int N>
 struct Chunked {
     static hipError_t prep(const PrepDir *d, int ndir, bool grad, hipStream_t s) {
@@ -711,8 +725,14 @@ struct Chunked {
         w.dir[1] = d[ndir - 1];
         w.ndir = ndir;
         const DeltaArgs &a = d[0].a;
-        const dim3 grid((unsigned)xcd_grid((long long)a.units * a.H));
-        if (a.P > 64) BM_LAUNCH(names[MODE], (k_delta_walk<T, N, MODE, 8>), grid, dim3(512), 0, s, w);
+        w.apart = ndir == 2 && d[0].a.y != d[1].a.y;
+        const int ny = w.apart ? 2 : 1;
+        // a wide head's 128 columns in one workgroup share its loads, on two CUs they
+        // do not wait for each other (32 heads of 1024 tokens: forward 96 -> 89 us in bf16
+        // and 168 -> 135 in fp32, back 121 -> 98 and 200 -> 149)
+        w.blocks = a.P > 64 && 2LL * a.units * a.H * ny <= 256 ? 2 : 1;
+        const dim3 grid((unsigned)xcd_grid((long long)a.units * a.H * w.blocks), ny);
+        if (a.P > 64 && w.blocks == 1) BM_LAUNCH(names[MODE], (k_delta_walk<T, N, MODE, 8>), grid, dim3(512), 0, s, w);
         else BM_LAUNCH(names[MODE], (k_delta_walk<T, N, MODE, 4>), grid, dim3(256), 0, s, w);
         return hipGetLastError();
     }
@@ -753,23 +773,29 @@ hipError_t launch_delta_chunked(const DeltaArgs *a, int ndir, bool bf16, void *c
     return with_shape(a[0], bf16, [&](auto k) {
         hipError_t e = hipSuccess;
         if (a[0].L > 0) e = k.prep(d, ndir, false, s);
-        return e != hipSuccess ? e : k.template walk<FWD>(d, ndir, s);
+        if (e == hipSuccess) e = k.template walk<FWD>(d, ndir, s);
+        if (e != hipSuccess || ndir == 1 || a[0].y == a[1].y) return e;
+        const long long n = (a[0].cu ? 1LL : a[0].units) * a[0].L * a[0].H * a[0].P;
+        BM_LAUNCH("delta_join", k_delta_join, dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0, s, a[0].y, a[1].y, n);
+        return hipGetLastError();
     });
 }
 
-hipError_t launch_delta_keep(const DeltaArgs &a, bool bf16, void *ws, hipStream_t s) {
-    const PrepDir d = prep_dir(a, ws, true);
-    return with_shape(a, bf16, [&](auto k) {
-        hipError_t e = k.prep(&d, 1, true, s);
-        return e != hipSuccess ? e : k.template walk<KEEP>(&d, 1, s);
+hipError_t launch_delta_keep(const DeltaArgs *a, int ndir, bool bf16, void *const *ws, hipStream_t s) {
+    PrepDir d[2];
+    for (int i = 0; i < ndir; ++i) d[i] = prep_dir(a[i], ws[i], true);
+    return with_shape(a[0], bf16, [&](auto k) {
+        hipError_t e = k.prep(d, ndir, true, s);
+        return e != hipSuccess ? e : k.template walk<KEEP>(d, ndir, s);
     });
 }
 
 const float *delta_gates(const DeltaArgs &a, void *ws) { return prep_dir(a, ws, true).gates; }
 
-hipError_t launch_delta_back(const DeltaArgs &a, bool bf16, void *ws, hipStream_t s) {
-    const PrepDir d = prep_dir(a, ws, true);
-    return with_shape(a, bf16, [&](auto k) { return k.template walk<BACK>(&d, 1, s); });
+hipError_t launch_delta_back(const DeltaArgs *a, int ndir, bool bf16, void *const *ws, hipStream_t s) {
+    PrepDir d[2];
+    for (int i = 0; i < ndir; ++i) d[i] = prep_dir(a[i], ws[i], true);
+    return with_shape(a[0], bf16, [&](auto k) { return k.template walk<BACK>(d, ndir, s); });
 }
 
 }  // namespace bm

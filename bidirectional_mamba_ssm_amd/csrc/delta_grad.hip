@@ -19,7 +19,11 @@
 // dP and dM take their place then, each twice: a result's lanes are the
 // transpose's operand as they come, and the other way goes by halves of a word.
 // Heads that share the group are walked in order, each lane adding to its own
-// elements of dq and dk: no atomics, the same bits every time.
+// elements of dq and dk: no atomics, the same bits every time. Where chunks and
+// groups are few, a group's heads go to several workgroups, whose sums are added
+// in order at the end.
+#include <algorithm>
+
 #include "delta_split.hpp"
 #include "internal.hpp"
 
@@ -28,8 +32,26 @@ namespace {
 
 constexpr int C = kDeltaChunk;
 
+struct GradArgs {
+    DeltaArgs a[2];
+    DeltaGradArgs o[2];
+    int parts;      // workgroups that share a chunk and group
+    long long n;    // elements of dq or dk
+};
+
+// The parts of a group's heads: enough that 256 workgroups, one a CU, have work
+// (32 heads of one group, 1024 tokens: 467 us in one part, 55 in 16 with the sums)
+int grad_parts(const DeltaArgs &a) {
+    const long long work = delta_slots(a.units, a.L, a.cu != nullptr) * a.G * (delta_apart(a.units, a.H) ? 2 : 1);
+    const int heads = a.H / a.G, most = (int)std::min<long long>(heads, (255 + work) / work);
+    const int each = (heads + most - 1) / most;
+    return (heads + each - 1) / each;
+}
+
 template <typename T, int N>
-__global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a, DeltaGradArgs o) {
+__global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(GradArgs args) {
+    const DeltaArgs &a = args.a[blockIdx.y];
+    const DeltaGradArgs &o = args.o[blockIdx.y];
     constexpr int IN = Terms<T>::IN, OWN = 3, W = N == 128 ? 8 : 4, SL = W / 4;   // waves; k steps of a slice
     constexpr int kRow = 4 * OWN * 1024;                   // images of 64 rows, a k step
     constexpr int kSlice = 3 * SL * kRow, kTri = 4 * kImage<OWN>;
@@ -39,8 +61,8 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
     __shared__ float gate[3][C], logs[2][W][C], ends[W], dbs[SL][C];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l16 = lane & 15;
-    const int grp = blockIdx.x % a.G, PP = padded(a.P);
-    const long long slot = blockIdx.x / a.G;
+    const int part = (int)(blockIdx.x % args.parts), grp = (int)(blockIdx.x / args.parts % a.G), PP = padded(a.P);
+    const long long slot = blockIdx.x / args.parts / a.G;
     int chunk;
     const DeltaUnit at = delta_slot(a, slot, chunk);
     const int first = chunk * C, live = min(C, at.len - first);
@@ -95,9 +117,11 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
         return v;
     };
     const uint32_t row4 = (uint32_t)(a.G * N * 4), off4 = (uint32_t)(grp * N * 4);
-    const ChunkRows dqr(o.dq, at, a.reverse, first, live, row4, off4, N * 4);
-    const ChunkRows dkr(o.dk, at, a.reverse, first, live, row4, off4, N * 4);
-    const int h0 = grp * (a.H / a.G), h1 = h0 + a.H / a.G;
+    float *own = o.parts + 2 * (part - 1) * args.n;
+    const ChunkRows dqr(part ? own : o.dq, at, a.reverse, first, live, row4, off4, N * 4);
+    const ChunkRows dkr(part ? own + args.n : o.dk, at, a.reverse, first, live, row4, off4, N * 4);
+    const int heads = a.H / a.G, each = (heads + args.parts - 1) / args.parts;
+    const int h0 = grp * heads + part * each, h1 = min(h0 + each, (grp + 1) * heads);
     // a thread brings eight columns of a token of do, e and z, a wave's lanes their
     // row of S and of D, the first wave's the gates
     const bool whole = a.P % 8 == 0;
@@ -379,12 +403,23 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(DeltaArgs a
     }
 }
 
+// dq and dk (blockIdx.y) of a direction (blockIdx.z): the parts' sums
+__global__ __launch_bounds__(256) void k_delta_parts(GradArgs args) {
+    const DeltaGradArgs &o = args.o[blockIdx.z];
+    const long long i = 4 * (blockIdx.x * 256LL + threadIdx.x);
+    if (i >= args.n) return;
+    f32x4 *to = (f32x4 *)((blockIdx.y ? o.dk : o.dq) + i), v = *to;
+    for (int p = 1; p < args.parts; ++p) v += *(const f32x4 *)(o.parts + (2 * (p - 1) + blockIdx.y) * args.n + i);
+    *to = v;
+}
+
 template <typename T>
-hipError_t launch_t(const DeltaArgs &a, const DeltaGradArgs &o, hipStream_t s) {
-    const dim3 grid((unsigned)(delta_slots(a.units, a.L, a.cu != nullptr) * a.G));
+hipError_t launch_t(const GradArgs &args, int ndir, hipStream_t s) {
+    const DeltaArgs &a = args.a[0];
+    const dim3 grid((unsigned)(delta_slots(a.units, a.L, a.cu != nullptr) * a.G * args.parts), ndir);
 #define GO(n)                                                                                    \
     if (a.N == n) {                                                                              \
-        BM_LAUNCH("delta_grad", (k_delta_grad<T, n>), grid, dim3(n == 128 ? 512 : 256), 0, s, a, o); \
+        BM_LAUNCH("delta_grad", (k_delta_grad<T, n>), grid, dim3(n == 128 ? 512 : 256), 0, s, args); \
         return hipGetLastError();                                                                \
     }
     GO(16) GO(32) GO(64) GO(128)
@@ -394,8 +429,17 @@ hipError_t launch_t(const DeltaArgs &a, const DeltaGradArgs &o, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_delta_grad(const DeltaArgs &a, const DeltaGradArgs &o, bool bf16, hipStream_t s) {
-    return bf16 ? launch_t<uint16_t>(a, o, s) : launch_t<float>(a, o, s);
+hipError_t launch_delta_grad(const DeltaArgs *a, const DeltaGradArgs *o, int ndir, bool bf16, hipStream_t s) {
+    const long long n = (a[0].cu ? 1LL : a[0].units) * a[0].L * a[0].G * a[0].N;
+    const GradArgs args = {{a[0], a[ndir - 1]}, {o[0], o[ndir - 1]}, grad_parts(a[0]), n};
+    const hipError_t e = bf16 ? launch_t<uint16_t>(args, ndir, s) : launch_t<float>(args, ndir, s);
+    if (e != hipSuccess || args.parts == 1) return e;
+    BM_LAUNCH("delta_parts", k_delta_parts, dim3((unsigned)((n / 4 + 255) / 256), 2, ndir), dim3(256), 0, s, args);
+    return hipGetLastError();
+}
+size_t delta_parts_bytes(const DeltaArgs &a) {
+    const size_t tok = a.cu ? (size_t)a.L : (size_t)a.units * a.L;
+    return tok ? (size_t)(grad_parts(a) - 1) * 2 * tok * a.G * a.N * 4 : 0;
 }
 
 // bytes of e or z, and of the kept states or their gradients
