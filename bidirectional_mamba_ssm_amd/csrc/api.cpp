@@ -1561,7 +1561,10 @@ int check_delta_apart(const Array *written, int nw, const Array *read, int nr) {
 
 namespace {
 
-// By chunks, or token by token: short sequences do not fill a chunk
+// By chunks, or token by token where sequences of 16 tokens or fewer (on average)
+// leave a chunk mostly empty. 64 rows x 32 heads of 128 x 128: 16 tokens take 95 us
+// one by one and 121 by chunks, 32 tokens 155 and 124; with 32 x 64 states (fp32)
+// 23 and 71, 39 and 73; one row of 32 heads 13 and 24, 21 and 25.
 bool delta_chunked(const bimamba_shape *s, int nseq) {
     return s->seqlen > 16LL * (nseq ? nseq : 1);
 }

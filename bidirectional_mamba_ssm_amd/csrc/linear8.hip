@@ -19,8 +19,10 @@
 // bytes and two buffers; chunk c of a row is kept at place c ^ (row % 8).
 //
 // k_linear8_few: up to 64 rows, where the weights' bytes are the work. A
-// workgroup takes 16 output channels; its eight waves split K and read both
+// workgroup takes 16 to 48 output channels; its eight waves split K and read both
 // operands from memory straight into the fragments, and their sums meet in LDS.
+#include <algorithm>
+
 #include "common.hpp"
 #include "internal.hpp"
 #include "mfma.hpp"
@@ -276,48 +278,59 @@ __global__ __launch_bounds__(64 * WN * WM) void k_linear8_rows(Linear8Args a, in
 
 constexpr int kFewWaves = 8;
 
-// up to 16 TM rows, cin a multiple of 16
-template <int TM, typename T>
+// up to 16 TM rows, 16 TN channels, cin a multiple of 16
+template <int TN, int TM, typename T>
 __global__ __launch_bounds__(64 * kFewWaves) void k_linear8_few(Linear8Args a) {
-    __shared__ i32x4 sums[kFewWaves][TM][64];
+    __shared__ i32x4 sums[kFewWaves][TN * TM][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, l16 = lane & 15;
-    const int n0 = 16 * blockIdx.x;
-    const int8_t *wp = a.w + (long long)min(n0 + l16, a.cout - 1) * a.cin;
-    const int8_t *xp[TM];
+    const int n0 = 16 * TN * blockIdx.x;
+    const int8_t *wp[TN], *xp[TM];
+#pragma unroll
+    for (int i = 0; i < TN; ++i) wp[i] = a.w + (long long)min(n0 + 16 * i + l16, a.cout - 1) * a.cin;
 #pragma unroll
     for (int j = 0; j < TM; ++j) xp[j] = a.x + min((long long)(16 * j + l16), a.rows - 1) * a.cin;
-    i32x4 acc[TM];
+    i32x4 acc[TN][TM];
 #pragma unroll
-    for (int j = 0; j < TM; ++j) acc[j] = i32x4{0, 0, 0, 0};
-    // four steps' loads at a time; one past the row's end multiplies zeros
-    for (int kb = 64 * wave; kb < a.cin; kb += 4 * 64 * kFewWaves) {
-        u32x4 wv[4], xv[4][TM];
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int j = 0; j < TM; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    // two steps' loads at a time; one past the row's end multiplies zeros
+    constexpr int U = 2;
+    for (int kb = 64 * wave; kb < a.cin; kb += U * 64 * kFewWaves) {
+        u32x4 wv[U][TN], xv[U][TM];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             const int k = kb + 64 * kFewWaves * u + 16 * g;
             const bool in = k < a.cin;
             const int at = in ? k : 0;
-            wv[u] = *(const u32x4 *)(wp + at);
-            if (!in) wv[u] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int i = 0; i < TN; ++i) {
+                wv[u][i] = *(const u32x4 *)(wp[i] + at);
+                if (!in) wv[u][i] = u32x4{0u, 0u, 0u, 0u};
+            }
 #pragma unroll
             for (int j = 0; j < TM; ++j) xv[u][j] = *(const u32x4 *)(xp[j] + at);
         }
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int j = 0; j < TM; ++j) acc[j] = mfma_i8(wv[u], xv[u][j], acc[j]);
+            for (int i = 0; i < TN; ++i)
+#pragma unroll
+                for (int j = 0; j < TM; ++j) acc[i][j] = mfma_i8(wv[u][i], xv[u][j], acc[i][j]);
     }
 #pragma unroll
-    for (int j = 0; j < TM; ++j) sums[wave][j][lane] = acc[j];
-    __syncthreads();
-    for (int e = tid; e < 64 * TM; e += 64 * kFewWaves) {
-        const int j = e >> 6;
-        i32x4 s = sums[0][j][lane];
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
-        for (int i = 1; i < kFewWaves; ++i) s += sums[i][j][lane];
+        for (int j = 0; j < TM; ++j) sums[wave][i * TM + j][lane] = acc[i][j];
+    __syncthreads();
+    for (int e = tid; e < 64 * TN * TM; e += 64 * kFewWaves) {
+        const int i = (e >> 6) / TM, j = (e >> 6) % TM, n = n0 + 16 * i;
+        i32x4 s = sums[0][e >> 6][lane];
+#pragma unroll
+        for (int w = 1; w < kFewWaves; ++w) s += sums[w][e >> 6][lane];
         i32x4 one[1][1] = {{s}};
-        finish<1, 1, T>(a, 16 * j + l16, n0 + 4 * g, n0 + 16 <= a.cout && 16 * j + 16 <= a.rows, one);
+        if (n < a.cout) finish<1, 1, T>(a, 16 * j + l16, n + 4 * g, n + 16 <= a.cout && 16 * j + 16 <= a.rows, one);
     }
 }
 
@@ -337,10 +350,18 @@ template <typename T>
 hipError_t launch_t(const Linear8Args &a, hipStream_t s) {
     const bool direct = a.cin % 16 == 0 && (((uintptr_t)a.x | (uintptr_t)a.w) & 15u) == 0;
     if (a.rows <= 64 && direct) {
-        const dim3 grid((unsigned)((a.cout + 15) / 16)), block(64 * kFewWaves);
-        if (a.rows <= 16) BM_LAUNCH("linear8_few", (k_linear8_few<1, T>), grid, block, 0, s, a);
-        else if (a.rows <= 32) BM_LAUNCH("linear8_few", (k_linear8_few<2, T>), grid, block, 0, s, a);
-        else BM_LAUNCH("linear8_few", (k_linear8_few<4, T>), grid, block, 0, s, a);
+        // Every workgroup reads all of x: with more than 32 rows 16 channels a
+        // workgroup read more of it than of w. Two or three times as many where
+        // that brings the workgroups down to a CU each (64 rows, 2048 -> 8512: 532
+        // workgroups 18.2 us, 178 12.2; 8192 -> 8192: 512 40.3, 256 27.4; 4096 -> 2048:
+        // 128 12.9, 64 14.8; one row, 8192 -> 8192: 512 15.0, 256 20.5).
+        const int tn = a.rows <= 32 ? 1 : std::min(3, (a.cout + 4095) / 4096);
+        const dim3 grid((unsigned)((a.cout + 16 * tn - 1) / (16 * tn))), block(64 * kFewWaves);
+        if (a.rows <= 16) BM_LAUNCH("linear8_few", (k_linear8_few<1, 1, T>), grid, block, 0, s, a);
+        else if (a.rows <= 32) BM_LAUNCH("linear8_few", (k_linear8_few<1, 2, T>), grid, block, 0, s, a);
+        else if (tn == 1) BM_LAUNCH("linear8_few", (k_linear8_few<1, 4, T>), grid, block, 0, s, a);
+        else if (tn == 2) BM_LAUNCH("linear8_few", (k_linear8_few<2, 4, T>), grid, block, 0, s, a);
+        else BM_LAUNCH("linear8_few", (k_linear8_few<3, 4, T>), grid, block, 0, s, a);
         return hipGetLastError();
     }
     auto tiles = [&](int nt, int mt) { return ((a.cout + nt - 1) / nt) * ((a.rows + mt - 1) / mt); };
