@@ -22,6 +22,14 @@
 // elements of dq and dk: no atomics, the same bits every time. Where chunks and
 // groups are few, a group's heads go to several workgroups, whose sums are added
 // in order at the end.
+//
+// Measured, 8 rows of 1024 tokens, 32 heads of 128 x 128 in 16 groups, bf16: 466 us
+// for 1.2 GB (236 us at a copy's rate) and 225 GFLOP of three-term products. A head
+// takes a workgroup 55 000 cycles: two slices 10 000 each, of which 5800 are
+// products and 6900 the LDS's reads of the images, dP and dM 4000, their products
+// 9000, and waits for the slices' arrays. Tried without gain: chunks in
+// a loop with the next one's first slice under way (474), two workgroups of 64 columns a
+// CU (505), tile pairs that share their reads (487).
 #include <algorithm>
 
 #include "delta_split.hpp"

@@ -32,7 +32,9 @@
 // Rows are laid over the lanes as row_form.hpp says.
 //
 // The RMS norm's gradient (rms_norm.hip holds its forward) is the same kernel
-// without the mean: mu = 0, no mean g, no db.
+// without the mean: mu = 0, no mean g, no db (8192 x 2048 bf16, dsum, from the array
+// 22.9 us and 4.4 for the sums, 134 MB at 5.9 TB/s out of the last-level cache;
+// 16 384 x 4096 102 us, 5.3 TB/s).
 #include "row_form.hpp"
 
 namespace bm {

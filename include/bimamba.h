@@ -591,9 +591,8 @@ int bimamba_linear8(long long rows, int cin, int cout, int dtype, const bimamba_
  * direction is given in forward time order, and init_state and final_state
  * are the forward direction's.
  *
- * Accuracy: fp32 inputs are computed in fp32 throughout; with bf16 inputs the
- * operands that the kernels compute enter the matrix cores as two bf16 each (16
- * significant bits, of fp32's range), sums and states are fp32. */
+ * Accuracy: sums and states are fp32; what enters the matrix cores, fp32 inputs
+ * and intermediate results, does so as three bf16 each, which hold its 24 bits. */
 typedef struct {
     const void *q, *k;         /* dtype [batch][seqlen][ngroups][d_state]      */
     const void *v;             /* dtype [batch][seqlen][nheads][headdim]       */
