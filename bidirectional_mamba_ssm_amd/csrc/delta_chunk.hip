@@ -20,8 +20,8 @@
 // tiles' between), both at most 1 where g <= 0; the diagonal tiles' are taken
 // one by one.
 //
-// Bound by its loads' and products' latency: 24 us for 4096 chunks and heads of
-// the layer below (48 with the gradient's triangles).
+// Bound by its loads' and products' latency: 39 us for the 4096 chunks and heads of
+// the layer below, 50 with the gradient's third triangle.
 //
 // k_delta_walk takes a head's chunks in order. A wave owns 16 columns of the
 // state for all N rows; columns never meet. The matrix cores' result order serves
