@@ -402,6 +402,7 @@ class State:
             ch = conv_channels(nheads, headdim, ngroups, d_state)
             self.conv = (ngroups, width, dtype, ch)
         self.shape = (nslots, nheads, headdim, d_state)
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     def ctx_tensor(self):
         """A zero-copy torch view of the convolution context (valid while
@@ -1358,6 +1359,8 @@ def delta_step(state, fwd, bwd=None, commit=True, scale=None, y=None, workspace=
     if isinstance(state, State):
         if tuple(state.shape) != (slots, H, P, N):
             raise ValueError(f"state has shape {tuple(state.shape)}, expected (slots, {H}, {P}, {N})")
+        if state.device != dev:
+            raise ValueError(f"state is on {state.device}, expected {dev}")
         at = state.data_ptr()
     else:
         _check(state, "state", (slots, H, P, N), torch.float32, dev)

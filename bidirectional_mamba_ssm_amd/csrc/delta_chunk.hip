@@ -39,6 +39,8 @@
 // workgroups of 64 columns a CU 160 forward). A chunk takes a wave 3500 cycles of
 // products and about 12 500 in all, since each of its products waits for the one
 // before; with two waves a SIMD the sixteen chunks are 8 us each.
+#include <algorithm>
+
 #include "delta_split.hpp"
 #include "internal.hpp"
 
@@ -707,11 +709,12 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
 
 // y += other, with both directions' outputs
 __global__ __launch_bounds__(256) void k_delta_join(float *y, const float *other, long long n) {
-    const long long i = 4 * (blockIdx.x * 256LL + threadIdx.x);
-    if (i + 4 <= n) {
-        *(f32x4 *)(y + i) += *(const f32x4 *)(other + i);
-    } else {
-        for (long long j = i; j < n; ++j) y[j] += other[j];
+    for (long long i = 4 * (blockIdx.x * 256LL + threadIdx.x); i < n; i += 1024LL * gridDim.x) {
+        if (i + 4 <= n) {
+            *(f32x4 *)(y + i) += *(const f32x4 *)(other + i);
+        } else {
+            for (long long j = i; j < n; ++j) y[j] += other[j];
+        }
     }
 }
 
@@ -787,7 +790,7 @@ hipError_t launch_delta_chunked(const DeltaArgs *a, int ndir, bool bf16, void *c
         if (e == hipSuccess) e = k.template walk<FWD>(d, ndir, s);
         if (e != hipSuccess || ndir == 1 || a[0].y == a[1].y) return e;
         const long long n = (a[0].cu ? 1LL : a[0].units) * a[0].L * a[0].H * a[0].P;
-        BM_LAUNCH("delta_join", k_delta_join, dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0, s, a[0].y, a[1].y, n);
+        BM_LAUNCH("delta_join", k_delta_join, dim3((unsigned)std::min((n + 1023) / 1024, 1LL << 20)), dim3(256), 0, s, a[0].y, a[1].y, n);
         return hipGetLastError();
     });
 }

@@ -592,7 +592,11 @@ int bimamba_linear8(long long rows, int cin, int cout, int dtype, const bimamba_
  * are the forward direction's.
  *
  * Accuracy: sums and states are fp32; what enters the matrix cores, fp32 inputs
- * and intermediate results, does so as three bf16 each, which hold its 24 bits. */
+ * and intermediate results, does so as three bf16 each, which hold its 24 bits.
+ * An infinity or a NaN spoils what it reaches, column by column (v) or in its
+ * group's or head's outputs, and may do so from the first token of its chunk of
+ * 64 on (the reverse direction: from its chunk's last token back), never a chunk
+ * before, another head, group or sequence. */
 typedef struct {
     const void *q, *k;         /* dtype [batch][seqlen][ngroups][d_state]      */
     const void *v;             /* dtype [batch][seqlen][nheads][headdim]       */

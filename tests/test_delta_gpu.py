@@ -200,8 +200,8 @@ def test_large_values_and_equal_keys(dtype):
 
 
 def test_no_number_stays_in_its_head_and_future():
-    """A NaN or an infinity in a value spoils its head from its token on, and
-    no other head, sequence or earlier token."""
+    """A NaN or an infinity in a value spoils its column from its token on, and
+    no other column, head, sequence or earlier chunk."""
     dirs, init, _, _ = _case(9, 1, 300, 4, 64, 2, 128, "bf16", False, 2)
     d, cu = dirs[0], [0, 200, 300]
     clean = bm.delta_fwd(d, cu_seqlens=cu, init_state=init)

@@ -175,6 +175,37 @@ def test_threads():
     assert not bad, bad[:5]
 
 
+def test_state_elsewhere_or_freed():
+    """A State of another device, or one that was freed, is refused."""
+    d = direction(torch.Generator(device=DEV).manual_seed(0), 1, 1, 2, 16, 1, 16, "f32", DEV)
+    st = bm.State(1, 2, 16, 16)
+    st.reset()
+    bm.delta_step(st, d)
+    here, st.device = st.device, torch.device("cuda", 7)
+    with pytest.raises(ValueError, match="state is on cuda:7"):
+        bm.delta_step(st, d)
+    st.device = here
+    st.free()
+    with pytest.raises(bm.BimambaError, match="state is NULL"):
+        bm.delta_step(st, d)
+
+
+def test_no_number_in_queries_and_gates():
+    """Spoils the group's or head's chunk and what follows it; nothing else."""
+    dirs, init, _, _ = _case(61, 1, 300, 4, 32, 2, 64, "f32", False, 2)
+    d, cu = dirs[0], [0, 210, 300]
+    clean = bm.delta_fwd(d, cu_seqlens=cu, init_state=init)
+    for name, heads in (("q", [0, 1]), ("k", [0, 1]), ("g", [0]), ("beta", [0])):
+        for bad in (float("nan"), float("inf")):
+            e = dict(d, **{name: d[name].clone()})
+            e[name][0, 100, 0] = bad
+            y = bm.delta_fwd(e, cu_seqlens=cu, init_state=init)
+            others = [h for h in range(4) if h not in heads]
+            assert torch.equal(y[:, :, others], clean[:, :, others]), name
+            assert torch.equal(y[:, 210:], clean[:, 210:]) and torch.equal(y[:, :64], clean[:, :64]), name
+            assert not torch.isfinite(y[0, 100, heads]).all(), name
+
+
 # ---- arrays beyond 32 bits of elements --------------------------------------------------
 
 def test_rows_beyond_31_bits():
