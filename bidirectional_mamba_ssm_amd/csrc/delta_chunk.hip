@@ -35,7 +35,7 @@
 // CU, and two buffers, filled in the middle of a chunk: one barrier a chunk.
 //
 // Measured, 8 rows of 1024 tokens, 32 heads of 128 x 128, bf16: forward 130 us,
-// keeping the states 112, back 180 (with one buffer 143, 121 and 188; two
+// keeping the states 104, back 180 (with one buffer 143, 121 and 188; two
 // workgroups of 64 columns a CU 160 forward). A chunk takes a wave 3500 cycles of
 // products and about 12 500 in all, since each of its products waits for the one
 // before; with two waves a SIMD the sixteen chunks are 8 us each.
@@ -341,6 +341,10 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
     const int block = (int)(mine % args.blocks), h = (int)(mine / args.blocks % args.dir[0].a.H);
     const int u = (int)(mine / args.blocks / args.dir[0].a.H);
     const int p0 = (block * W + wave) * 16;
+    // Of the two waves of a SIMD one does its share of the copying before its first
+    // products and the other after them (keeping the states 104 us at the layer's
+    // shape, both after 112; forward 150 and 148, back 187 and 178)
+    const bool early = kTwo && W == 8 && MODE == KEEP && wave >= W / 2;
     // the wave has columns, those of the walks' own arrays past the head's width among them
     const bool works = p0 < (GRAD ? padded(args.dir[0].a.P) : args.dir[0].a.P);
     // the halves of blocks that lie beyond the diagonal stay zeros
@@ -595,6 +599,7 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
 #pragma unroll
                         for (int r = 0; r < 4; ++r) buf_store(sr, to + (16 * t + r) * PP * 4, S[t][r]);
                 }
+                if (early) middle();
                 // K S and Q S
                 f32x4 ks[4];
 #pragma unroll
@@ -612,7 +617,7 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
                         mm_tiles(r, sb, out);
                     }
                 }
-                middle();
+                if (!early) middle();
                 Operand<OWN> b[2], kb[2];   // kb: what K^T multiplies
                 if constexpr (MODE != BACK) {
 #pragma unroll
