@@ -384,8 +384,9 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
         const bool whole = a.P % 8 == 0;   // rows of V are 16-byte vectors
         auto order = [&](int i) { return MODE == BACK ? chunks - 1 - i : i; };
         // A lane's own numbers, as a stage of a chunk has them: the compiler would
-        // keep what all stages make of them through the whole walk, more than the
-        // registers hold.
+        // keep what all stages make of them through the whole walk, which in these
+        // forms is more than the registers hold (back 215 us, 190 made anew; forward
+        // of 128 bf16 columns 145 and 149, keeping the states 121 and 131, which fit).
         constexpr bool kCrowded = N == 128 && (MODE == BACK || (MODE == FWD && (W == 4 || IN == 3)));
         auto fresh = [&](int v) {
             if constexpr (kCrowded) asm volatile("" : "+v"(v));
