@@ -250,6 +250,9 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(GradArgs ar
                                 acc[i][2] = mfma16x16x32(m[2].t[t], sb.t[q - t], acc[i][2]);
                             }
                     }
+                } else if (mine && hn < h1 && pn + 32 * s < PP) {
+                    // a head's last slice ends before these columns, the next head's first one has them
+                    fetch_states(hn, pn, s);
                 }
 #pragma unroll
                 for (int t = 0; t < kJobs; ++t) {
