@@ -2,7 +2,8 @@
 //   out[r][n] = xs[r] ws[n] sum_c x[r][c] w[n][c] + bias[n]
 // The sums are whole numbers in int32 (exact: |sum| <= 2^14 cin < 2^31), so no
 // order of the products shows in the result; they are converted to fp32 once
-// and scaled there.
+// and scaled there, or in fp64 where the two scales' product leaves fp32's normal
+// numbers.
 //
 // k_linear8: v_mfma_i32_16x16x64_i8 (lane l: row l % 16, bytes 16 (l / 16) .. of K
 // for both operands), w the first operand, so that a lane's four results lie in
@@ -85,12 +86,25 @@ __device__ __forceinline__ void finish(const Linear8Args &a, long long row, int 
             ws[e] = a.ws[at];
             b[e] = a.bias ? a.bias[at] : 0.f;
         }
+        // A product of two scales that is no normal number (subnormal, overflowed, or
+        // of a row of zeros) has lost what the whole result may still hold
+        bool far = false;
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) far |= !__builtin_isnormal(xs[j] * ws[e]);
+        far = __any(far);
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
             T *out = (T *)a.out + (row + 16 * j) * a.cout + c;
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = fmaf((float)acc[i][j][e], xs[j] * ws[e], b[e]);
+            if (far) {   // of these results alone: the others' bits are what they are beside any
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!__builtin_isnormal(xs[j] * ws[e])) v[e] = (float)((double)acc[i][j][e] * xs[j] * ws[e] + b[e]);
+            }
             if (whole) {
                 store4(out, v);
             } else if (row + 16 * j < a.rows) {
