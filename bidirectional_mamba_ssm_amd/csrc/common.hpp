@@ -15,10 +15,6 @@ __device__ __forceinline__ uint16_t f2bf(float f) {
     u += 0x7fffu + ((u >> 16) & 1u);
     return (uint16_t)(u >> 16);
 }
-// two floats -> packed pair of bf16 (lo in bits 0..15)
-__device__ __forceinline__ uint32_t pack2bf(float lo, float hi) {
-    return (uint32_t)f2bf(lo) | ((uint32_t)f2bf(hi) << 16);
-}
 
 // dt as the scan uses it when a direction carries its pre-activation:
 // softplus(v) = max(v, 0) + log1p(e^{-|v|}) (no overflow, no loss for

@@ -32,9 +32,6 @@ template <int N> struct Operand {
     u32x4 t[N];
 };
 
-__device__ __forceinline__ uint32_t bf_pair(float a, float b) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(rf2{a, b}, rbf2));
-}
 // two numbers as N terms each
 template <int N>
 __device__ __forceinline__ void split2(float a, float b, uint32_t *t) {

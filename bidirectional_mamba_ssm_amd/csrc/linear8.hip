@@ -31,6 +31,7 @@
 #include "common.hpp"
 #include "internal.hpp"
 #include "mfma.hpp"
+#include "rows.hpp"
 
 namespace bm {
 namespace {
@@ -48,10 +49,10 @@ __device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
 
 // four results of one row, channels n .. n + 3
 __device__ __forceinline__ void store4(uint16_t *p, const float *v) {
-    *(h4_a2 *)p = h4_a2{pack2bf(v[0], v[1]), pack2bf(v[2], v[3])};
+    *(h4_a2 *)p = h4_a2{bf_pair(v[0], v[1]), bf_pair(v[2], v[3])};
 }
 __device__ __forceinline__ void store4(float *p, const float *v) { *(f4_a4 *)p = f4_a4{v[0], v[1], v[2], v[3]}; }
-__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = f2bf(v); }
+__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = (uint16_t)bf_pair(v, 0.f); }
 __device__ __forceinline__ void store1(float *p, float v) { *p = v; }
 
 // Workgroup ids go round the 8 XCDs: each takes a run of tiles, eight row panels

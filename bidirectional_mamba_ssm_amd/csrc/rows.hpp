@@ -31,6 +31,12 @@ typedef uint32_t rvec __attribute__((ext_vector_type(4)));
 typedef __bf16 rbf2 __attribute__((ext_vector_type(2)));
 typedef float rf2 __attribute__((ext_vector_type(2)));
 
+// two floats -> bf16, the first in the low half: round to nearest even, a NaN of
+// any bits stays a NaN (hardware conversion)
+__device__ __forceinline__ uint32_t bf_pair(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(rf2{a, b}, rbf2));
+}
+
 // one lane's vector of a row: 16 bytes, V elements
 template <typename T> struct Lane;
 template <> struct Lane<uint16_t> {

@@ -87,3 +87,19 @@ def test_scales_of_zero_and_no_number():
     s[9] = 0
     assert torch.isnan(got[130][s == 0]).all()
     assert torch.equal(got[130][s != 0], torch.sign(s[s != 0]).float() * float("inf"))
+
+
+@pytest.mark.parametrize("rows, cin, cout", FORMS)
+@pytest.mark.parametrize("bits", [0x7fc00000, 0x7fffffff, 0xffffffff, 0x7f800001, 0xffff8000])
+def test_no_number_of_any_bits(rows, cin, cout, bits):
+    """A NaN in a bias or a scale, whatever its bits, is a NaN in bf16, too."""
+    g = _gen(rows + cin)
+    x, w = _pair(g, rows, cin, cout, (-1, 0), (-1, 0))
+    b = torch.randn(cout, generator=g, device=DEV)
+    clean = bm.linear8(x, w, b)
+    nan = torch.tensor(np.array([bits], dtype=np.uint32).view(np.float32), device=DEV)
+    b[cout // 2], w.scale[1], x.scale[rows // 3] = nan[0], nan[0], nan[0]
+    got = bm.linear8(x, w, b)
+    bad = torch.zeros(rows, cout, dtype=torch.bool, device=DEV)
+    bad[:, cout // 2], bad[:, 1], bad[rows // 3] = True, True, True
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], clean[~bad])
