@@ -414,12 +414,15 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(GradArgs ar
     }
 }
 
-// dq and dk (blockIdx.y) of a direction (blockIdx.z): the parts' sums
+// dq and dk (blockIdx.y) of a direction (blockIdx.z): the parts' sums. The caller's
+// arrays are aligned to their elements.
+typedef float f4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 __global__ __launch_bounds__(256) void k_delta_parts(GradArgs args) {
     const DeltaGradArgs &o = args.o[blockIdx.z];
     const long long i = 4 * (blockIdx.x * 256LL + threadIdx.x);
     if (i >= args.n) return;
-    f32x4 *to = (f32x4 *)((blockIdx.y ? o.dk : o.dq) + i), v = *to;
+    f4_a4 *to = (f4_a4 *)((blockIdx.y ? o.dk : o.dq) + i);
+    f32x4 v = *to;
     for (int p = 1; p < args.parts; ++p) v += *(const f32x4 *)(o.parts + (2 * (p - 1) + blockIdx.y) * args.n + i);
     *to = v;
 }

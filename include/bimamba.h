@@ -629,7 +629,9 @@ int bimamba_delta_step(const bimamba_shape *s, float *state, const bimamba_delta
  *  dy          float [batch][seqlen][nheads][headdim]
  *  dfinal      float, the gradient that reaches final_state, or NULL (zeros)
  *  dinit       out float, init_state's gradient, or NULL if not wanted
- * Calls whose outputs or workspace overlap each other or an input are refused. */
+ * Calls whose outputs or workspace overlap each other or an input are refused.
+ * Inputs, states and the workspace are aligned as bimamba_delta_fwd's, dy as y,
+ * dfinal and dinit as states; the arrays of gradients to their elements. */
 typedef struct {
     float *dq, *dk;            /* [batch][seqlen][ngroups][d_state]            */
     float *dv;                 /* [batch][seqlen][nheads][headdim]             */

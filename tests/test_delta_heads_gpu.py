@@ -35,3 +35,26 @@ def test_heads_of_a_group_in_turn(case):
         for n in od.KEYS:
             _close(f"{name} d{n}", got[n], want[n], 2.0, want["gS"] if n == "g" else None)
     _close("dinit", dinit, rd, 2.0)
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+@pytest.mark.parametrize("case", [(1, 300, 8, 40, 1, 128, "bf16", True), (2, 130, 12, 33, 2, 32, "f32", True),
+                                  (130, 65, 2, 80, 1, 128, "f32", False)], ids=lambda c: "-".join(map(str, c)))
+def test_gradients_at_any_element(case, off):
+    """Gradient arrays that start at any element, a group's heads in parts and not:
+    the bits of aligned ones, and nothing around them."""
+    dirs, init, df, dy = _case(case[1] + off, *case)
+    f, b = _pair(dirs)
+    want = bm.delta_bwd(f, b, dy, init_state=init, dfinal=df)
+    bufs, grads = [], []
+    for d in dirs:
+        one = {}
+        for n, t in d.items():
+            bufs.append(torch.full((t.numel() + 8,), 7.0, device="cuda"))
+            one[n] = bufs[-1][off:off + t.numel()].view(t.shape)
+        grads.append(one)
+    got = bm.delta_bwd(f, b, dy, init_state=init, dfinal=df, grads=(grads + [None])[:2])
+    for g, w in zip(got, want):
+        assert w is None or all(torch.equal(g[n], w[n]) for n in od.KEYS)
+    for buf in bufs:
+        assert (buf[:off] == 7).all() and (buf[off - 8:] == 7).all()
