@@ -1300,12 +1300,13 @@ def _delta_workspace(workspace, nbytes, dev):
 def delta_workspace_size(fwd, has_bwd=True, nseq=0):
     """Bytes of workspace of delta_fwd and delta_step for such a direction, or
     for two."""
-    return _delta_size("bimamba_delta_workspace_size", _delta_dims(fwd), fwd["v"].dtype, int(bool(has_bwd)), nseq)[0]
+    return _delta_size("bimamba_delta_workspace_size", _delta_dims(fwd), fwd["v"].dtype, int(bool(has_bwd)),
+                       _int32(nseq, "nseq"))[0]
 
 
 def delta_bwd_workspace_size(fwd, nseq=0):
     """Bytes of workspace of delta_bwd for such a direction."""
-    return _delta_size("bimamba_delta_bwd_workspace_size", _delta_dims(fwd), fwd["v"].dtype, nseq)[0]
+    return _delta_size("bimamba_delta_bwd_workspace_size", _delta_dims(fwd), fwd["v"].dtype, _int32(nseq, "nseq"))[0]
 
 
 def delta_fwd(fwd, bwd=None, scale=None, cu_seqlens=None, init_state=None, final_state=None, y=None,
