@@ -15,9 +15,13 @@
 // of the two products, so one exchange over a row's waves gives both the sum
 // and the largest magnitude: o is taken as (h w) rstd, whose rounding keeps
 // the order of magnitudes, and its largest is exactly round(max |h w| rstd).
+// A row whose mean square leaves fp32 (values from 1e19, or tiny ones with no eps to
+// speak of) is taken once more from its registers, times a power of two.
 //
 // Measured (bf16, residual, 8-bit rows alone): 131 072 x 2048 350 us, 1.88 GB at 5.4
 // TB/s (a copy of that size moves 5.1); 8192 x 4096 51 us, 4.6 TB/s; 64 x 2560 3.5 us.
+#include <type_traits>
+
 #include "row_form.hpp"
 
 namespace bm {
@@ -43,7 +47,7 @@ __global__ __launch_bounds__(G == 0 ? 64 * kMaxWaves : 64 * kRows) void k_rms_no
     constexpr int V = L::V;
     constexpr bool MULTI = G == 0;
     constexpr int kShare = MULTI ? 1 : 64 / G;   // rows of a wave
-    __shared__ float2 part[MULTI ? 2 : 1][MULTI ? kMaxWaves : 1];
+    __shared__ float2 part[MULTI ? 3 : 1][MULTI ? kMaxWaves : 1];
     const int C = a.C;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t = MULTI ? threadIdx.x : threadIdx.x & (G - 1), lanes = MULTI ? blockDim.x : G;
@@ -80,47 +84,69 @@ __global__ __launch_bounds__(G == 0 ? 64 * kMaxWaves : 64 * kRows) void k_rms_no
         }
         if (kAhead && row + step < a.rows) fetch(row + step);
         float o[NV][V];
-        float ss = 0.f;
-        uint32_t top = 0;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            float s = 0.f;
-            uint32_t m = 0;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float h = L::get(r[k], j);
-                if constexpr (NORM) s = fmaf(h, h, s);
-                o[k][j] = NORM ? h * w[k][j] : h;
-                if constexpr (Q8) m = max(m, abs_bits(o[k][j]));
-            }
-            if (NORM && k == at.kt) {
-                s = 0.f;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float h = at.own(k, j, L::get(r[k], j));
-                    s = fmaf(h, h, s);
-                }
-            }
-            // lanes past the row's end hold its last vector again
-            ss += at.has[k] ? s : 0.f;
-            top = max(top, m);
-        }
-        if constexpr (NORM) ss = lanes_total<G>(ss);
-        if constexpr (Q8) top = lanes_max<G>(top);
-        if constexpr (MULTI) {
-            if ((t & 63) == 0) part[flip][wave] = make_float2(ss, __uint_as_float(top));
-            __syncthreads();
+        float ss;
+        uint32_t top;
+        // h w of the lane's elements, and the row's sum of h^2 and largest |h w|, with h
+        // times `by` (a power of two, 1 in the first pass)
+        auto pass = [&](auto first, float by) {
+            constexpr bool kFirst = decltype(first)::value;
+            auto value = [&](int k, int j) { return kFirst ? L::get(r[k], j) : L::get(r[k], j) * by; };
             ss = 0.f;
             top = 0;
-            for (int i = 0; i < (lanes >> 6); ++i) {
-                const float2 p = part[flip][i];
-                ss += p.x;
-                top = max(top, __float_as_uint(p.y));
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                float s = 0.f;
+                uint32_t m = 0;
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float h = value(k, j);
+                    if constexpr (NORM) s = fmaf(h, h, s);
+                    o[k][j] = NORM ? h * w[k][j] : h;
+                    if constexpr (Q8) m = max(m, abs_bits(o[k][j]));
+                }
+                if (NORM && k == at.kt) {
+                    s = 0.f;
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const float h = at.own(k, j, value(k, j));
+                        s = fmaf(h, h, s);
+                    }
+                }
+                // lanes past the row's end hold its last vector again
+                ss += at.has[k] ? s : 0.f;
+                top = max(top, m);
             }
-        }
-        float rstd = 1.f;
+            if constexpr (NORM) ss = lanes_total<G>(ss);
+            if constexpr (Q8) top = lanes_max<G>(top);
+            if constexpr (MULTI) {
+                // the second pass has a place of its own, which the next row's barrier frees
+                float2 *const p = part[kFirst ? flip : 2];
+                if ((t & 63) == 0) p[wave] = make_float2(ss, __uint_as_float(top));
+                __syncthreads();
+                ss = 0.f;
+                top = 0;
+                for (int i = 0; i < (lanes >> 6); ++i) {
+                    ss += p[i].x;
+                    top = max(top, __float_as_uint(p[i].y));
+                }
+            }
+        };
+        pass(std::true_type(), 1.f);
+        float rstd = 1.f, by = 1.f;   // of h times `by`
         if constexpr (NORM) {
-            rstd = 1.0f / sqrtf(fmaf(ss, inv, a.eps));
+            float mean = fmaf(ss, inv, a.eps);
+            // Squares that overflow, or underflow where eps lets them count: once more,
+            // with the row scaled to where they do neither
+            if (!(mean >= 0x1p-100f && mean < __builtin_inff())) {
+                by = mean < 1.f ? 0x1p100f : 0x1p-80f;
+                // (the compiler would keep the first pass's values for it: of 2048 channels
+                // to 8 bits 110 registers and 361 us, so 94 and 354)
+#pragma unroll
+                for (int k = 0; k < NV; ++k) asm volatile("" : "+v"(r[k]));
+                pass(std::false_type(), by);
+                mean = fmaf(ss, inv, a.eps * by * by);
+            }
+            rstd = 1.0f / sqrtf(mean);
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -154,7 +180,7 @@ __global__ __launch_bounds__(G == 0 ? 64 * kMaxWaves : 64 * kRows) void k_rms_no
         }
         if (t == 0) {
             if constexpr (NORM) {
-                if (a.rstd) a.rstd[row] = rstd;
+                if (a.rstd) a.rstd[row] = rstd * by;
             }
             if constexpr (Q8) a.scale[row] = scale;
         }

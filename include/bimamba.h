@@ -545,7 +545,9 @@ int bimamba_rows8_pack(long long rows, int channels, int dtype, const void *x, c
  *            8-bit rows, in the same pass
  * out and sum may each be x or residual itself; calls whose outputs overlap
  * each other, or an input in any other way, are refused. Arrays are aligned
- * to their elements. Computed in fp32. */
+ * to their elements. Computed in fp32; rows whose squares leave its range are
+ * scaled by a power of two for it (out is right also where rstd, at 2^128 and
+ * more, is an infinity). */
 int bimamba_rms_norm(long long rows, int channels, int dtype, const void *x, const void *residual,
                      const float *weight, float eps, void *out, void *sum, float *rstd, const bimamba_rows8 *out8,
                      bimamba_stream stream);
