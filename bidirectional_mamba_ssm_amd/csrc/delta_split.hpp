@@ -2,7 +2,11 @@
 //
 // bf16 inputs are one term, exactly; fp32 inputs and everything the kernels
 // compute (states, errors, the chunk's inverse) are three terms, bf16(v), bf16 of
-// what is left and bf16 of what is left then: all 24 bits over fp32's range. A
+// what is left and bf16 of what is left then: all 24 bits of a magnitude from 2^-110
+// up to bf16's largest number. Below, what is left ends at bf16's last step, 2^-133;
+// the numbers above (from 3.396e38 on, the last 1 in 256 of the top binade) round to
+// an infinity (a first term held at the largest number would keep them, and cost
+// the layer's forward 154 -> 159 us and its gradient 806 -> 819). A
 // product of operands keeps the pairs of terms that reach its last one: 3 for one
 // by three, 6 for three by three, each a v_mfma_f32_16x16x32_bf16 summed in
 // fp32, the smallest first. (Two terms, 2 and 3 products, are off by 5e-6 of a

@@ -595,7 +595,9 @@ int bimamba_linear8(long long rows, int cin, int cout, int dtype, const bimamba_
  * are the forward direction's.
  *
  * Accuracy: sums and states are fp32; what enters the matrix cores, fp32 inputs
- * and intermediate results, does so as three bf16 each, which hold its 24 bits.
+ * and intermediate results, does so as three bf16 each, which hold its 24 bits
+ * (down to 2^-133; a number from 3.396e38 on, which bf16 rounds to an infinity,
+ * counts as one).
  * An infinity or a NaN spoils what it reaches, column by column (v) or in its
  * group's or head's outputs, and may do so from the first token of its chunk of
  * 64 on (the reverse direction: from its chunk's last token back), never a chunk
