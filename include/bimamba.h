@@ -633,6 +633,8 @@ int bimamba_delta_step(const bimamba_shape *s, float *state, const bimamba_delta
  *  dy          float [batch][seqlen][nheads][headdim]
  *  dfinal      float, the gradient that reaches final_state, or NULL (zeros)
  *  dinit       out float, init_state's gradient, or NULL if not wanted
+ * An infinity or a NaN stays in its sequence, its direction and its head (dq and
+ * dk: its group); one in dy or dfinal goes back from its chunk's end.
  * Calls whose outputs or workspace overlap each other or an input are refused.
  * Inputs, states and the workspace are aligned as bimamba_delta_fwd's, dy as y,
  * dfinal and dinit as states; the arrays of gradients to their elements. */

@@ -81,3 +81,23 @@ def test_infinities_and_nan_stay_what_they_were(C):
     assert torch.isnan(s[1:4]).all() and (q[1:4] == 0).all() and (q[[0, 4, 5]] == 127).all()
     assert (o["rstd"][[1, 3]] == 0).all() and torch.isnan(o["rstd"][2])
     assert torch.isnan(o["out"][1, 3]) and torch.isnan(o["out"][2]).all() and (o["out"][0] == 1).all()
+
+
+@pytest.mark.parametrize("C, rows", [(64, 70000), (300, 17000), (1500, 6300), (9000, 4200)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_in_turns(C, rows, dtype):
+    """Such rows in a workgroup's several turns, one after the other and between
+    ordinary ones: what each is in a short batch."""
+    g = _gen(rows)
+    k = torch.randint(0, 3, (rows, 1), generator=g, device=DEV)
+    x = _randn(g, rows, C) * torch.tensor([1.0, 1e25, 1e-25], device=DEV)[k]
+    x, w = x.to(DT[dtype]), _randn(g, C)
+    o = bm.rms_norm(x, w, eps=0.0, rows8=True, dense=True)
+    for a in range(0, rows, 1500):
+        b = bm.rms_norm(x[a:a + 1500], w, eps=0.0, rows8=True, dense=True)
+        for n in ("out", "rstd"):
+            assert torch.equal(o[n][a:a + 1500], b[n]), (a, n)
+        assert torch.equal(o["rows8"].q[a:a + 1500], b["rows8"].q)
+        assert torch.equal(o["rows8"].scale[a:a + 1500], b["rows8"].scale)
+    _, rstd = orows.rms_norm(x[-500:], w, 0.0)
+    _close("rstd", o["rstd"][-500:], rstd, rstd, REL)
