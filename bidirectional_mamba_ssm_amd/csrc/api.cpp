@@ -1562,9 +1562,12 @@ int check_delta_apart(const Array *written, int nw, const Array *read, int nr) {
 namespace {
 
 // By chunks, or token by token where sequences of 16 tokens or fewer (on average)
-// leave a chunk mostly empty. 64 rows x 32 heads of 128 x 128: 16 tokens take 95 us
-// one by one and 121 by chunks, 32 tokens 155 and 124; with 32 x 64 states (fp32)
-// 23 and 71, 39 and 73; one row of 32 heads 13 and 24, 21 and 25.
+// leave a chunk mostly empty. 64 rows x 32 heads of 128 x 128: 16 tokens take 98 us
+// one by one and 119 by chunks, 32 tokens 148 and 121; with 32 x 64 states (fp32)
+// 21 and 67, 35 and 70; one row of 32 heads 11 and 19, 18 and 19; 600 packed
+// sequences, 4 heads of 64 x 128, 68 and 97, 103 and 100. The average says nothing
+// of uneven lengths: one of 4000 tokens beside 300 of one token goes one by one,
+// 1820 us, and would take 352 by chunks.
 bool delta_chunked(const bimamba_shape *s, int nseq) {
     return s->seqlen > 16LL * (nseq ? nseq : 1);
 }

@@ -30,15 +30,18 @@
 // waits for another wave. K and Q come to LDS row by row (read as rows for
 // K S and Q S, transposed by ds_read_b64_tr_b16 for K^T E), the triangles as
 // operand images; the next chunk's loads are under way meanwhile, in
-// registers. A head's waves share both. Heads up to 64 wide take one buffer, so
-// that two workgroups share a CU and hide each other's waits; wider ones have the
-// CU, and two buffers, filled in the middle of a chunk: one barrier a chunk.
+// registers. A head's waves share both. A workgroup that has the CU (of eight
+// waves, or in fp32) takes two buffers where they fit into LDS, filled in the
+// middle of a chunk: one barrier a chunk. The others take one: bf16 walks of 64
+// columns, two of whose workgroups share a CU and hide each other's waits, and
+// fp32 ones forward and back with d_state 64 and 128.
 //
-// Measured, 8 rows of 1024 tokens, 32 heads of 128 x 128, bf16: forward 130 us,
-// keeping the states 104, back 180 (with one buffer 143, 121 and 188; two
-// workgroups of 64 columns a CU 160 forward). A chunk takes a wave 3500 cycles of
-// products and about 12 500 in all, since each of its products waits for the one
-// before; with two waves a SIMD the sixteen chunks are 8 us each.
+// Measured, 8 rows of 1024 tokens, 32 heads of 128 x 128, bf16, in a row of calls:
+// forward 117 us, keeping the states 109, back 177 (with one buffer 125, 116 and
+// 183; two workgroups of 64 columns a CU 147, 125 and 201); in fp32 211, 161 and
+// 258. A chunk takes a wave 3500 cycles of products and some 12 500 in all, since
+// each of its products waits for the one before; with two waves a SIMD the sixteen
+// chunks are 7 us each.
 #include <algorithm>
 
 #include "delta_split.hpp"
@@ -342,8 +345,8 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
     const int u = (int)(mine / args.blocks / args.dir[0].a.H);
     const int p0 = (block * W + wave) * 16;
     // Of the two waves of a SIMD one does its share of the copying before its first
-    // products and the other after them (keeping the states 104 us at the layer's
-    // shape, both after 112; forward 150 and 148, back 187 and 178)
+    // products and the other after them (keeping the states 109 us at the layer's
+    // shape, both after 113; forward it is 124 and 117 so, back 187 and 177)
     const bool early = kTwo && W == 8 && MODE == KEEP && wave >= W / 2;
     // the wave has columns, those of the walks' own arrays past the head's width among them
     const bool works = p0 < (GRAD ? padded(args.dir[0].a.P) : args.dir[0].a.P);
@@ -385,8 +388,11 @@ __global__ __launch_bounds__(64 * W, sizeof(T) == 2 || W == 8 ? 2 : 1) void k_de
         auto order = [&](int i) { return MODE == BACK ? chunks - 1 - i : i; };
         // A lane's own numbers, as a stage of a chunk has them: the compiler would
         // keep what all stages make of them through the whole walk, which in these
-        // forms is more than the registers hold (back 215 us, 190 made anew; forward
-        // of 128 bf16 columns 145 and 149, keeping the states 121 and 131, which fit).
+        // forms is more than the registers hold (back 224 us, 177 made anew, in fp32 420
+        // and 258, of 64 columns 277 and 136). What fits is kept: forward of 128 bf16
+        // columns 117 us and 123 made anew, keeping the states 109 and 115. The other
+        // forwards put 20 bytes a lane into scratch if kept, which costs them nothing:
+        // of 64 bf16 columns 104 and 111, of 128 in fp32 207 and 211.
         constexpr bool kCrowded = N == 128 && (MODE == BACK || (MODE == FWD && (W == 4 || IN == 3)));
         auto fresh = [&](int v) {
             if constexpr (kCrowded) asm volatile("" : "+v"(v));

@@ -23,13 +23,14 @@
 // groups are few, a group's heads go to several workgroups, whose sums are added
 // in order at the end.
 //
-// Measured, 8 rows of 1024 tokens, 32 heads of 128 x 128 in 16 groups, bf16: 466 us
-// for 1.2 GB (236 us at a copy's rate) and 225 GFLOP of three-term products. A head
+// Measured, 8 rows of 1024 tokens, 32 heads of 128 x 128 in 16 groups, bf16: 470 us
+// for 1.2 GB (236 us at a copy's rate) and 225 GFLOP of three-term products; heads
+// 96 wide 440; fp32 590. A head
 // takes a workgroup 55 000 cycles: two slices 10 000 each, of which 5800 are
 // products and 6900 the LDS's reads of the images, dP and dM 4000, their products
-// 9000, and waits for the slices' arrays. Tried without gain: chunks in
-// a loop with the next one's first slice under way (474), two workgroups of 64 columns a
-// CU (505), tile pairs that share their reads (487).
+// 9000, and waits for the slices' arrays. Tried without gain (466 at
+// the time): chunks in a loop with the next one's first slice under way (474), two
+// workgroups of 64 columns a CU (505), tile pairs that share their reads (487).
 #include <algorithm>
 
 #include "delta_split.hpp"
@@ -77,7 +78,8 @@ __global__ __launch_bounds__(N == 128 ? 512 : 256) void k_delta_grad(GradArgs ar
     if (live <= 0) return;
     // A lane's own number, as a stage of a head's work has it: the compiler would
     // keep what all stages make of it through the whole walk, far more than the
-    // registers hold (58 of them went to memory, 590 us at the layer's shape).
+    // registers hold (58 of them went to memory, 590 us at the layer's shape). With
+    // d_state 128 10 still do, and 57 in fp32, whose K and Q are three terms each.
     auto fresh = [&]() {
         int l = lane;
         asm volatile("" : "+v"(l));

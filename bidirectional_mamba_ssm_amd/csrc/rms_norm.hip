@@ -19,7 +19,8 @@
 // speak of) is taken once more from its registers, times a power of two.
 //
 // Measured (bf16, residual, 8-bit rows alone): 131 072 x 2048 350 us, 1.88 GB at 5.4
-// TB/s (a copy of that size moves 5.1); 8192 x 4096 51 us, 4.6 TB/s; 64 x 2560 3.5 us.
+// TB/s (a copy of that size moves 5.1); 8192 x 4096 36 us, 6.5 TB/s, some of it out of
+// the last-level cache; 64 x 2560 3.6 us. To bf16 alone: 131 072 x 2048 396 us, 5.4 TB/s.
 #include <type_traits>
 
 #include "row_form.hpp"

@@ -570,8 +570,10 @@ int bimamba_rms_norm_bwd(long long rows, int channels, int dtype, const void *x,
  *  out       dtype [rows][cout], which may not overlap an input
  * The sums are exact (int32), whatever the order; scaled and rounded in fp32
  * (fp64 where the product of the two scales leaves fp32's normal numbers, which
- * the result need not do), bf16 to nearest even. Arrays are aligned to their elements (16-byte
- * aligned rows, cin a multiple of 16, are read faster). */
+ * the result need not do), bf16 to nearest even. Arrays are aligned to their
+ * elements (16-byte aligned rows, cin a multiple of 16, are read faster).
+ * bimamba_rows8_pack makes rows of up to 16384; longer ones are the caller's to
+ * make. */
 int bimamba_linear8(long long rows, int cin, int cout, int dtype, const bimamba_rows8 *x,
                     const bimamba_rows8 *weight, const float *bias, void *out, bimamba_stream stream);
 
